@@ -233,6 +233,155 @@ int nvfp4_scale_from_amax(const float *amax, float *ts, void *hip_stream);
 int nvfp4_gemm_w4a16(const void *a, int a_dtype, int64_t m, int64_t lda, const nvfp4_tensor *b, void *c,
                      int c_dtype, int64_t ldc, void *hip_stream);
 
+/* ---- The block around the quantized products ---------------------------------------------------------
+ * The recipe keeps part of a model out of NVFP4: selective layers stay in higher precision
+ * (aissential.tech article, Method), and the Nemotron 3 Ultra checkpoint mixes NVFP4 with 8- and
+ * 16-bit layers around its routed experts (hyper.ai (de) story).  The entry points below are what such
+ * a block needs next to the NVFP4 products: routing tokens to experts, products of 8-bit integers
+ * (plain, for few tokens, and by expert), the sum of the experts' rows, and the norms before and after
+ * a block.  They follow the conventions at the top of this file, except that routing accepts
+ * infinities and NaN in its logits (see nvfp4_moe_route).  None of them uses floating-point atomics
+ * across workgroups: the same input gives the same bits on every call. */
+
+enum {
+  NVFP4_ROUTE_SIGMOID = 1u << 0,    /* scores 1 / (1 + exp(-l)); without it, softmax over the experts  */
+  NVFP4_ROUTE_RENORM = 1u << 1,     /* weights s / (sum of the chosen s + 1e-20)                       */
+  NVFP4_ROUTE_GROUP_SUM2 = 1u << 2  /* a group's key is the sum of its two largest keys, not its largest */
+};
+enum {
+  NVFP4_NORM_ONE_PLUS = 1u << 0,   /* norm weights are stored as w - 1 (a zero weight scales by one)    */
+  NVFP4_NORM_TOKEN_GATE = 1u << 1  /* the gate is [tokens x d] in y's dtype, not float[d]               */
+};
+
+/* Bytes of device workspace nvfp4_moe_route (with a plan) and nvfp4_moe_plan need.  Fully rewritten by
+ * every call before it is read; calls that may overlap must use distinct workspaces. */
+size_t nvfp4_moe_workspace_size(int64_t tokens, int64_t experts, int32_t top_k);
+
+/* Routing of tokens to experts.  logits [tokens x experts] (dtype NVFP4_F32 or NVFP4_BF16, leading
+ * dimension ld elements, element-aligned).  Per token, all in fp32:
+ *   - an expert whose logit is -inf or NaN is closed to the token; other logits are capped at FLT_MAX;
+ *   - score: exp(l - max l) / sum, the sum taken pairwise, neighbours first, over the experts padded
+ *     with zeros to a power of two (one order on every device); or 1 / (1 + exp(-l)) with
+ *     NVFP4_ROUTE_SIGMOID;
+ *   - key = score + bias[e] (bias: nullable device float[experts], e.g. a load-balancing bias; it
+ *     decides the choice and never enters a weight).  A key that is -inf or NaN closes the expert;
+ *   - with group_top_k < num_groups: the experts form num_groups equal consecutive groups; a group's
+ *     key is its largest key, or with NVFP4_ROUTE_GROUP_SUM2 the sum of its two largest (a missing
+ *     second counts as zero); only the group_top_k groups with the largest keys stay open;
+ *   - the top_k largest keys are chosen in falling order; ties go to the lower index, for groups too;
+ *   - weight = score, divided by (sum of the chosen scores + 1e-20) with NVFP4_ROUTE_RENORM, times scale.
+ * ids, weights: device [tokens][top_k].  A token with fewer than top_k open experts has id -1 and
+ * weight 0 in its last slots.
+ * offsets, rows, pos: all NULL, or all device buffers for the plan of nvfp4_moe_plan, made in the same
+ * call (workspace then as for nvfp4_moe_plan, else ignored).
+ * experts 1 .. 512, top_k 1 .. min(32, experts), num_groups 1 .. 16 dividing experts, group_top_k
+ * 1 .. num_groups with group_top_k * (experts / num_groups) >= top_k, tokens * top_k < 2^31 (else
+ * NVFP4_ERR_SHAPE). */
+int nvfp4_moe_route(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t ld, const float *bias,
+                    int32_t num_groups, int32_t group_top_k, int32_t top_k, uint32_t flags, float scale, int32_t *ids,
+                    float *weights, int32_t *offsets, int32_t *rows, int32_t *pos, void *workspace, void *hip_stream);
+
+/* Gradient of nvfp4_moe_route's weights with respect to the logits, for the ids it chose (the choice
+ * itself has no gradient, and the bias none at all): dlogits [tokens x experts] in the logits' dtype
+ * (leading dimension ldd), from dweights [tokens][top_k].  Scores are computed again from the logits.
+ * flags (NVFP4_ROUTE_SIGMOID, NVFP4_ROUTE_RENORM; others ignored) and scale as in the forward call.
+ * Slots whose id is not in [0, experts) have no gradient; a closed expert's gradient is 0. */
+int nvfp4_moe_route_backward(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t ld,
+                             const int32_t *ids, const float *dweights, int32_t top_k, uint32_t flags, float scale,
+                             void *dlogits, int64_t ldd, void *hip_stream);
+
+/* Plan of a grouped product: the slots (token t, choice j; slot t * top_k + j) in order of their
+ * expert, each expert's slots in rising order.  ids: device [tokens][top_k]; an id outside
+ * [0, experts) means no expert.
+ *   offsets [experts + 1]: expert e has the rows offsets[e] .. offsets[e + 1] - 1
+ *   rows [tokens * top_k]: the slot of each row; -1 from offsets[experts] on
+ *   pos [tokens][top_k]:   the row of each slot; -1 without an expert
+ * experts 1 .. 512, top_k 1 .. 32, tokens * top_k < 2^31.  workspace: device,
+ * nvfp4_moe_workspace_size() bytes, 16-byte aligned. */
+int nvfp4_moe_plan(const int32_t *ids, int64_t tokens, int32_t top_k, int64_t experts, int32_t *offsets, int32_t *rows,
+                   int32_t *pos, void *workspace, void *hip_stream);
+
+/* y[r] = x[rows[r] / top_k]: the tokens' rows in the plan's order (what a product with rows sorted by
+ * expert reads); a row without a slot (-1) is zero.  x [tokens x d], y [tokens * top_k x d], both
+ * of dtype NVFP4_F32 or NVFP4_BF16, leading dimensions ldx, ldy.  d * sizeof(dtype), ldx and ldy in
+ * bytes multiples of 16; x, y 16-byte aligned. */
+int nvfp4_moe_gather(const void *x, int dtype, int64_t tokens, int64_t d, int64_t ldx, const int32_t *rows,
+                     int32_t top_k, void *y, int64_t ldy, void *hip_stream);
+
+/* out[t] = sum over j of weights[t][j] * y[pos[t][j]] in fp32, in the order of j, rounded once (weights
+ * NULL: all one, the gradient of nvfp4_moe_gather).  Slots with pos outside [0, tokens * top_k) add
+ * nothing.  y [tokens * top_k x d] and out [tokens x d] of one dtype; shapes and alignment as
+ * nvfp4_moe_gather. */
+int nvfp4_moe_combine(const void *y, int dtype, int64_t tokens, int64_t d, int64_t ldy, const int32_t *pos,
+                      const float *weights, int32_t top_k, void *out, int64_t ldo, void *hip_stream);
+
+/* Gradients of nvfp4_moe_combine: dy[pos[t][j]] = weights[t][j] * dout[t] and dweights[t][j] =
+ * sum_d dout[t][d] * y[pos[t][j]][d] (0 for a slot without a row).  rows: the plan's rows; rows of dy without a
+ * slot (-1) are zero.  dy has y's dtype, leading dimension lddy. */
+int nvfp4_moe_combine_backward(const void *dout, int64_t ldo, const void *y, int64_t ldy, int dtype, int64_t tokens,
+                               int64_t d, const int32_t *pos, const int32_t *rows, const float *weights, int32_t top_k,
+                               void *dy, int64_t lddy, float *dweights, void *hip_stream);
+
+/* Quantize the rows of x [rows x cols] (NVFP4_F32 or NVFP4_BF16, leading dimension ldx) to 8-bit
+ * integers with one fp32 scale a row (a token's, or a weight's output channel): s = RN(amax / 127),
+ * q = the nearest integer (ties to even) to RN(x * RN(1 / s)), so |q| <= 127 and x ~ q * s.  A row
+ * whose s would be below 2^-126 becomes zeros with s = 0.  q: device int8 [rows][cols] (no padding);
+ * scales: device float[rows].  cols % 16 == 0; x and q 16-byte aligned, ldx * sizeof(dtype) a multiple
+ * of 16. */
+int nvfp4_int8_quantize(const void *x, int dtype, int64_t rows, int64_t cols, int64_t ldx, int8_t *q, float *scales,
+                        void *hip_stream);
+
+/* Product of 8-bit integers with a scale for each token and each channel:
+ *   C[i][j] = (a_scales[i] * b_scales[j]) * sum_k a[i][k] * b[j][k],
+ * the sum exact in 32-bit integers, the scale product and its multiply in fp32, one rounding to a
+ * bf16 C.  a: int8 [a_rows][K], b: int8 [N][K], both without padding; c [M x N], dtype NVFP4_F32 or
+ * NVFP4_BF16, leading dimension ldc >= N.  Values -128 are allowed.
+ * Plain form (offsets NULL, num_groups 1, rows NULL): M == a_rows.
+ * By expert: offsets is a DEVICE array of num_groups + 1 row offsets (a plan's offsets; offsets[0]
+ * = 0, rising, at most M); rows offsets[g] .. offsets[g + 1] - 1 of C use weight g of b's num_groups
+ * consecutive [N x K] weights and of b_scales' num_groups * N floats.  Rows of C from
+ * offsets[num_groups] on are not written.  rows: nullable device int32[M] (a plan's rows): row r of C
+ * then takes row rows[r] / row_div of a and a_scales (row_div = top_k reads a token's row for each of
+ * its slots, without a gathered copy); rows outside a are read as row 0.  Without rows, M == a_rows.
+ * K % 16 == 0 and K < 2^17 (so that no sum overflows); N * K < 2^32 and, with rows, a_rows * K < 2^32;
+ * M < 2^31; num_groups 1 .. 512 (else NVFP4_ERR_SHAPE); a and b 16-byte aligned, the other arrays
+ * aligned to their element size. */
+int nvfp4_int8_gemm(const int8_t *a, const float *a_scales, int64_t a_rows, const int8_t *b, const float *b_scales,
+                    int64_t M, int64_t N, int64_t K, void *c, int c_dtype, int64_t ldc, int32_t num_groups,
+                    const int32_t *offsets, const int32_t *rows, int32_t row_div, void *hip_stream);
+
+/* The norms between two blocks, with the block's gate and residual scale, in one pass over the rows:
+ *   p = y * rstd_post * w_post,  rstd_post = 1 / sqrt(mean(y^2) + eps)   (w_post NULL: p = y)
+ *   x' = x + alpha * gate * p                                            (gate NULL: 1)
+ *   n = x' * rstd_pre * w_pre,   rstd_pre = 1 / sqrt(mean(x'^2) + eps)   (w_pre NULL: no n)
+ * x: the residual stream [tokens x d]; y: the block's output (NULL: x' = x, the second norm alone; w_post
+ * and gate are then NULL).  All in fp32 from the inputs; x' enters the second norm before its rounding to
+ * x's dtype.  x_dtype is the dtype of x and x_out, y_dtype that of y, n and a gate by token (each NVFP4_F32
+ * or NVFP4_BF16).  w_post, w_pre: device float[d]; with NVFP4_NORM_ONE_PLUS the factors are 1 + w.  gate:
+ * device float[d], or [tokens x d] of y_dtype with NVFP4_NORM_TOKEN_GATE.  x_out: given exactly with y
+ * (may be x); n: given exactly with w_pre; rstd_post, rstd_pre: nullable float[tokens], for the
+ * backward call.  Matrices have no padding.  d % 8 == 0, 8 <= d <= 16384 (else NVFP4_ERR_SHAPE); eps a
+ * normal positive number (else NVFP4_ERR_UNSUPPORTED); pointers 16-byte aligned. */
+int nvfp4_block_norm(const void *x, int x_dtype, const void *y, int y_dtype, int64_t tokens, int64_t d,
+                     const float *w_post, const void *gate, const float *w_pre, float alpha, float eps,
+                     uint32_t flags, void *x_out, void *n, float *rstd_post, float *rstd_pre, void *hip_stream);
+
+/* Bytes of device workspace nvfp4_block_norm_backward needs (partial column sums; fully rewritten before
+ * it is read). */
+size_t nvfp4_block_norm_workspace_size(int64_t tokens, int64_t d);
+
+/* Gradients of nvfp4_block_norm from those of its outputs, dx_out (NULL: zero) and dn (given exactly with
+ * w_pre), and its inputs and rstd values (rstd_post given exactly with w_post, rstd_pre with w_pre); x' is
+ * formed again from x and y.  Outputs: dx (x_dtype), dy (y_dtype, exactly with y), dw_post and dw_pre
+ * (float[d], exactly with w_post / w_pre), dgate (exactly with gate: float[d], or [tokens x d] of y_dtype with
+ * NVFP4_NORM_TOKEN_GATE).  Column sums run in fp32 in one fixed order.  Outputs must not overlap inputs.
+ * workspace: device, nvfp4_block_norm_workspace_size() bytes, 16-byte aligned. */
+int nvfp4_block_norm_backward(const void *dx_out, const void *dn, const void *x, int x_dtype, const void *y,
+                              int y_dtype, int64_t tokens, int64_t d, const float *w_post, const void *gate,
+                              const float *w_pre, float alpha, uint32_t flags, const float *rstd_post,
+                              const float *rstd_pre, void *dx, void *dy, float *dw_post, void *dgate, float *dw_pre,
+                              void *workspace, void *hip_stream);
+
 /* Static, human-readable text for a status code. */
 const char *nvfp4_status_string(int status);
 

@@ -25,12 +25,18 @@ __all__ = [
     "NVFP4_FOUR_OVER_SIX", "NVFP4_TS_FOR_FOUR", "NVFP4_SCALE_SEARCH", "NVFP4Error", "NVFP4Tensor", "library_path", "lib",
     "nvfp4_workspace_size", "nvfp4_quantize", "nvfp4_quantize_noalloc", "nvfp4_rht_quantize", "nvfp4_dequantize",
     "nvfp4_gemm", "nvfp4_gemm_nvfp4_out", "nvfp4_scale_from_amax", "nvfp4_gemm_w4a16", "nvfp4_transpose", "nvfp4_status_string", "empty_like_quantized",
+    "NVFP4_ROUTE_SIGMOID", "NVFP4_ROUTE_RENORM", "NVFP4_ROUTE_GROUP_SUM2", "NVFP4_NORM_ONE_PLUS", "MoEPlan", "Int8Tensor",
+    "BlockNorm", "BlockNormGrads", "nvfp4_moe_route", "nvfp4_moe_route_backward", "nvfp4_moe_plan", "nvfp4_moe_gather",
+    "nvfp4_moe_combine", "nvfp4_moe_combine_backward", "nvfp4_int8_quantize", "nvfp4_int8_gemm", "nvfp4_block_norm",
+    "nvfp4_block_norm_backward",
 ]
 
 NVFP4_OK, NVFP4_ERR_NULL, NVFP4_ERR_SHAPE, NVFP4_ERR_ALIGN, NVFP4_ERR_UNSUPPORTED, NVFP4_ERR_HIP = range(6)
 NVFP4_F32, NVFP4_BF16 = 0, 1
 NVFP4_COLWISE, NVFP4_BLOCK2D, NVFP4_SR, NVFP4_FOUR_OVER_SIX = 1, 2, 4, 8
 NVFP4_TS_FOR_FOUR, NVFP4_SCALE_SEARCH = 16, 32
+NVFP4_ROUTE_SIGMOID, NVFP4_ROUTE_RENORM, NVFP4_ROUTE_GROUP_SUM2 = 1, 2, 4
+NVFP4_NORM_ONE_PLUS, NVFP4_NORM_TOKEN_GATE = 1, 2
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -78,6 +84,22 @@ def lib():
         L.nvfp4_gemm_w4a16.restype = ctypes.c_int
         L.nvfp4_transpose.argtypes = [TP, TP, P]
         L.nvfp4_transpose.restype = ctypes.c_int
+        i, f32, size = ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+        for name, res, args in (
+                ("nvfp4_moe_workspace_size", size, [i64, i64, i32]),
+                ("nvfp4_moe_route", i, [P, i, i64, i64, i64, P, i32, i32, i32, u32, f32, P, P, P, P, P, P, P]),
+                ("nvfp4_moe_route_backward", i, [P, i, i64, i64, i64, P, P, i32, u32, f32, P, i64, P]),
+                ("nvfp4_moe_plan", i, [P, i64, i32, i64, P, P, P, P, P]),
+                ("nvfp4_moe_gather", i, [P, i, i64, i64, i64, P, i32, P, i64, P]),
+                ("nvfp4_moe_combine", i, [P, i, i64, i64, i64, P, P, i32, P, i64, P]),
+                ("nvfp4_moe_combine_backward", i, [P, i64, P, i64, i, i64, i64, P, P, P, i32, P, i64, P, P]),
+                ("nvfp4_int8_quantize", i, [P, i, i64, i64, i64, P, P, P]),
+                ("nvfp4_int8_gemm", i, [P, P, i64, P, P, i64, i64, i64, P, i, i64, i32, P, P, i32, P]),
+                ("nvfp4_block_norm", i, [P, i, P, i, i64, i64, P, P, P, f32, f32, u32, P, P, P, P, P]),
+                ("nvfp4_block_norm_workspace_size", size, [i64, i64]),
+                ("nvfp4_block_norm_backward", i,
+                 [P, P, P, i, P, i, i64, i64, P, P, P, f32, u32, P, P, P, P, P, P, P, P, P])):
+            getattr(L, name).argtypes, getattr(L, name).restype = args, res
         L.nvfp4_status_string.argtypes = [ctypes.c_int]
         L.nvfp4_status_string.restype = ctypes.c_char_p
         _LIB = L
@@ -317,3 +339,343 @@ def nvfp4_transpose(t: NVFP4Tensor, out: Optional[NVFP4Tensor] = None) -> NVFP4T
     st = lib().nvfp4_transpose(ctypes.byref(din), ctypes.byref(dout), _stream_handle(t.data.device))
     _check(st, "nvfp4_transpose")
     return out
+
+
+# ---- the block around the quantized products ----------------------------------------------------------
+@dataclass
+class MoEPlan:
+    """The order of a grouped product's rows (see nvfp4_moe_plan): slot t * top_k + j is token t's choice j."""
+    offsets: torch.Tensor  # int32 [experts + 1], first row of each expert
+    rows: torch.Tensor     # int32 [tokens * top_k], the slot of each row (-1: none)
+    pos: torch.Tensor      # int32 [tokens, top_k], the row of each slot (-1: none)
+
+    @property
+    def experts(self) -> int:
+        return self.offsets.shape[0] - 1
+
+    @property
+    def top_k(self) -> int:
+        return self.pos.shape[1]
+
+
+@dataclass
+class Int8Tensor:
+    """8-bit integers with one scale a row (logical [rows x k], k contiguous); a grouped product's weight
+    holds `groups` consecutive tensors of `rows` rows each."""
+    data: torch.Tensor    # int8 [groups*rows, k]
+    scales: torch.Tensor  # float32 [groups*rows]
+    rows: int
+    k: int
+    groups: int = 1
+
+
+@dataclass
+class BlockNorm:
+    """What nvfp4_block_norm gives."""
+    x: torch.Tensor                    # the residual stream after the block
+    n: Optional[torch.Tensor]          # its norm, the next block's input
+    rstd_post: Optional[torch.Tensor]  # float32 [tokens], for the backward call
+    rstd_pre: Optional[torch.Tensor]
+
+
+@dataclass
+class BlockNormGrads:
+    """What nvfp4_block_norm_backward gives (None where the forward call had no such input)."""
+    dx: torch.Tensor
+    dy: Optional[torch.Tensor]
+    dw_post: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+    dw_pre: Optional[torch.Tensor]
+
+
+def _raw_stream(t: torch.Tensor):
+    return torch._C._cuda_getCurrentRawStream(t.device.index) if t.is_cuda else None
+
+
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _want(where: str, name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape, like: torch.Tensor):
+    """A contiguous tensor of this dtype and shape on the device of `like`."""
+    if t is None:
+        return
+    if t.dtype != dtype:
+        raise TypeError(f"{where}: {name} must be {dtype}, is {t.dtype}")
+    if t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{where}: {name} must be a contiguous {list(shape)}, is {list(t.shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{where}: {name} is on {t.device}, not {like.device}")
+
+
+def _matrix(where: str, name: str, t: torch.Tensor) -> int:
+    """Leading dimension of a matrix with unit column stride."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{where}: {name} must be 2-D with unit column stride")
+    cols = t.shape[1]
+    if t.shape[0] <= 1:
+        return cols
+    ld = t.stride(0)
+    if ld < cols:
+        raise ValueError(f"{where}: rows of {name} overlap")
+    return ld
+
+
+def _empty_plan(tokens: int, top_k: int, experts: int, device) -> MoEPlan:
+    slots = tokens * top_k
+    buf = torch.empty(2 * slots + experts + 1, dtype=torch.int32, device=device)
+    return MoEPlan(buf[2 * slots:], buf[:slots], buf[slots:2 * slots].view(tokens, top_k))
+
+
+def _moe_workspace(tokens: int, experts: int, top_k: int, device) -> torch.Tensor:
+    return torch.empty(lib().nvfp4_moe_workspace_size(tokens, experts, top_k) // 4, dtype=torch.int32, device=device)
+
+
+def nvfp4_moe_route(logits: torch.Tensor, top_k: int, flags: int = 0, bias: Optional[torch.Tensor] = None,
+                    num_groups: int = 1, group_top_k: int = 1, scale: float = 1.0, with_plan: bool = True,
+                    workspace: Optional[torch.Tensor] = None):
+    """Route tokens to experts from logits [tokens, experts] (float32 / bfloat16, unit column stride);
+    returns (ids int32 [tokens, top_k], weights float32 [tokens, top_k], MoEPlan or None).  See
+    include/nvfp4.h for the scores, groups, ties and closed experts."""
+    ld = _matrix("nvfp4_moe_route", "logits", logits)
+    T, E = logits.shape
+    _want("nvfp4_moe_route", "bias", bias, torch.float32, (E,), logits)
+    dev = logits.device
+    ids = torch.empty((T, max(top_k, 0)), dtype=torch.int32, device=dev)
+    weights = torch.empty((T, max(top_k, 0)), dtype=torch.float32, device=dev)
+    plan = None
+    if with_plan:
+        plan = _empty_plan(T, max(top_k, 0), E, dev)
+        if workspace is None:
+            workspace = _moe_workspace(T, E, top_k, dev)
+    st = lib().nvfp4_moe_route(logits.data_ptr(), _dtype_code(logits.dtype), T, E, ld, _addr(bias), num_groups, group_top_k,
+                               top_k, flags, scale, ids.data_ptr(), weights.data_ptr(),
+                               plan.offsets.data_ptr() if plan else None, plan.rows.data_ptr() if plan else None,
+                               plan.pos.data_ptr() if plan else None, _addr(workspace), _raw_stream(logits))
+    _check(st, "nvfp4_moe_route")
+    return ids, weights, plan
+
+
+def nvfp4_moe_route_backward(logits: torch.Tensor, ids: torch.Tensor, dweights: torch.Tensor, flags: int = 0,
+                             scale: float = 1.0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of nvfp4_moe_route's weights with respect to the logits, for the ids it chose."""
+    where = "nvfp4_moe_route_backward"
+    ld = _matrix(where, "logits", logits)
+    T, E = logits.shape
+    _want(where, "ids", ids, torch.int32, (T, ids.shape[-1]), logits)
+    _want(where, "dweights", dweights, torch.float32, ids.shape, logits)
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    elif out.shape != logits.shape or out.dtype != logits.dtype or out.device != logits.device:
+        raise ValueError(f"{where}: out must match the logits")
+    st = lib().nvfp4_moe_route_backward(logits.data_ptr(), _dtype_code(logits.dtype), T, E, ld, ids.data_ptr(),
+                                        dweights.data_ptr(), ids.shape[1], flags, scale, out.data_ptr(),
+                                        _matrix(where, "out", out), _raw_stream(logits))
+    _check(st, where)
+    return out
+
+
+def nvfp4_moe_plan(ids: torch.Tensor, experts: int, workspace: Optional[torch.Tensor] = None) -> MoEPlan:
+    """The plan of a grouped product over ids [tokens, top_k] (int32; ids outside [0, experts) have no
+    expert)."""
+    if ids.dim() != 2:
+        raise ValueError("nvfp4_moe_plan: ids must be 2-D")
+    _want("nvfp4_moe_plan", "ids", ids, torch.int32, ids.shape, ids)
+    T, k = ids.shape
+    plan = _empty_plan(T, k, max(experts, 0), ids.device)
+    if workspace is None:
+        workspace = _moe_workspace(T, experts, k, ids.device)
+    st = lib().nvfp4_moe_plan(ids.data_ptr(), T, k, experts, plan.offsets.data_ptr(), plan.rows.data_ptr(),
+                              plan.pos.data_ptr(), workspace.data_ptr(), _raw_stream(ids))
+    _check(st, "nvfp4_moe_plan")
+    return plan
+
+
+def nvfp4_moe_gather(x: torch.Tensor, plan: MoEPlan, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x[rows / top_k]: the tokens' rows in the plan's order (zero rows where the plan has no slot)."""
+    where = "nvfp4_moe_gather"
+    ldx = _matrix(where, "x", x)
+    T, D = x.shape
+    _want(where, "plan.rows", plan.rows, torch.int32, (T * plan.top_k,), x)
+    if out is None:
+        out = torch.empty((T * plan.top_k, D), dtype=x.dtype, device=x.device)
+    elif out.shape != (T * plan.top_k, D) or out.dtype != x.dtype or out.device != x.device:
+        raise ValueError(f"{where}: out must be [{T * plan.top_k}, {D}] like x")
+    st = lib().nvfp4_moe_gather(x.data_ptr(), _dtype_code(x.dtype), T, D, ldx, plan.rows.data_ptr(), plan.top_k,
+                                out.data_ptr(), _matrix(where, "out", out), _raw_stream(x))
+    _check(st, where)
+    return out
+
+
+def nvfp4_moe_combine(y: torch.Tensor, plan: MoEPlan, weights: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """sum over a token's slots of weight * y[row of the slot] ([tokens * top_k, d] -> [tokens, d]);
+    without weights the plain sum, the gradient of nvfp4_moe_gather."""
+    where = "nvfp4_moe_combine"
+    ldy = _matrix(where, "y", y)
+    T, k = plan.pos.shape
+    D = y.shape[1]
+    if y.shape[0] != T * k:
+        raise ValueError(f"{where}: y has {y.shape[0]} rows, the plan {T * k}")
+    _want(where, "plan.pos", plan.pos, torch.int32, (T, k), y)
+    _want(where, "weights", weights, torch.float32, (T, k), y)
+    if out is None:
+        out = torch.empty((T, D), dtype=y.dtype, device=y.device)
+    elif out.shape != (T, D) or out.dtype != y.dtype or out.device != y.device:
+        raise ValueError(f"{where}: out must be [{T}, {D}] like y")
+    st = lib().nvfp4_moe_combine(y.data_ptr(), _dtype_code(y.dtype), T, D, ldy, plan.pos.data_ptr(), _addr(weights), k,
+                                 out.data_ptr(), _matrix(where, "out", out), _raw_stream(y))
+    _check(st, where)
+    return out
+
+
+def nvfp4_moe_combine_backward(dout: torch.Tensor, y: torch.Tensor, plan: MoEPlan, weights: torch.Tensor):
+    """Gradients (dy, dweights) of nvfp4_moe_combine with weights."""
+    where = "nvfp4_moe_combine_backward"
+    ldo, ldy = _matrix(where, "dout", dout), _matrix(where, "y", y)
+    T, k = plan.pos.shape
+    D = y.shape[1]
+    if y.shape[0] != T * k or dout.shape != (T, D) or dout.dtype != y.dtype or dout.device != y.device:
+        raise ValueError(f"{where}: dout must be [{T}, {D}] like y [{T * k}, {D}]")
+    _want(where, "plan.pos", plan.pos, torch.int32, (T, k), y)
+    _want(where, "plan.rows", plan.rows, torch.int32, (T * k,), y)
+    _want(where, "weights", weights, torch.float32, (T, k), y)
+    dy = torch.empty((T * k, D), dtype=y.dtype, device=y.device)
+    dweights = torch.empty((T, k), dtype=torch.float32, device=y.device)
+    st = lib().nvfp4_moe_combine_backward(dout.data_ptr(), ldo, y.data_ptr(), ldy, _dtype_code(y.dtype), T, D,
+                                          plan.pos.data_ptr(), plan.rows.data_ptr(), weights.data_ptr(), k, dy.data_ptr(), D,
+                                          dweights.data_ptr(), _raw_stream(y))
+    _check(st, where)
+    return dy, dweights
+
+
+def nvfp4_int8_quantize(x: torch.Tensor, out: Optional[Int8Tensor] = None) -> Int8Tensor:
+    """Rows of x (float32 / bfloat16 [rows, cols]) to 8-bit integers with one scale a row."""
+    where = "nvfp4_int8_quantize"
+    ld = _matrix(where, "x", x)
+    R, K = x.shape
+    if out is None:
+        out = Int8Tensor(torch.empty((R, K), dtype=torch.int8, device=x.device),
+                         torch.empty((R,), dtype=torch.float32, device=x.device), R, K)
+    else:
+        _want(where, "out.data", out.data, torch.int8, (R, K), x)
+        _want(where, "out.scales", out.scales, torch.float32, (R,), x)
+    st = lib().nvfp4_int8_quantize(x.data_ptr(), _dtype_code(x.dtype), R, K, ld, out.data.data_ptr(),
+                                   out.scales.data_ptr(), _raw_stream(x))
+    _check(st, where)
+    return out
+
+
+def nvfp4_int8_gemm(a: Int8Tensor, b: Int8Tensor, out_dtype: torch.dtype = torch.bfloat16, plan: Optional[MoEPlan] = None,
+                    gather: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """C = (a * scales) @ (b * scales)^T with exact integer sums.  With a plan: by expert, b holding one
+    weight for each; a's rows are in the plan's order, or with gather=True a has one row a token and is
+    read through the plan.  Rows of C that the plan gives no expert are not written."""
+    where = "nvfp4_int8_gemm"
+    if a.k != b.k:
+        raise ValueError(f"{where}: a has K={a.k}, b has K={b.k}")
+    _want(where, "a.data", a.data, torch.int8, (a.rows, a.k), a.data)
+    _want(where, "a.scales", a.scales, torch.float32, (a.rows,), a.data)
+    _want(where, "b.data", b.data, torch.int8, (b.groups * b.rows, b.k), a.data)
+    _want(where, "b.scales", b.scales, torch.float32, (b.groups * b.rows,), a.data)
+    M, offsets, rows, div = a.rows, None, None, 1
+    if plan is not None:
+        if plan.experts != b.groups:
+            raise ValueError(f"{where}: the plan has {plan.experts} experts, b {b.groups}")
+        _want(where, "plan.offsets", plan.offsets, torch.int32, (b.groups + 1,), a.data)
+        offsets, M = plan.offsets.data_ptr(), plan.rows.shape[0]
+        if gather:
+            _want(where, "plan.rows", plan.rows, torch.int32, (a.rows * plan.top_k,), a.data)
+            rows, div = plan.rows.data_ptr(), plan.top_k
+        elif M != a.rows:
+            raise ValueError(f"{where}: a has {a.rows} rows, the plan {M}")
+    elif gather or b.groups != 1:
+        raise ValueError(f"{where}: a grouped product needs a plan")
+    if out is None:
+        out = torch.empty((M, b.rows), dtype=out_dtype, device=a.data.device)
+    elif out.shape != (M, b.rows) or out.device != a.data.device:
+        raise ValueError(f"{where}: out must be [{M}, {b.rows}] on {a.data.device}")
+    st = lib().nvfp4_int8_gemm(a.data.data_ptr(), a.scales.data_ptr(), a.rows, b.data.data_ptr(), b.scales.data_ptr(), M,
+                               b.rows, b.k, out.data_ptr(), _dtype_code(out.dtype), max(_matrix(where, "out", out), 1),
+                               b.groups, offsets, rows, div, _raw_stream(a.data))
+    _check(st, where)
+    return out
+
+
+def _norm_inputs(where, x, y, w_post, gate, w_pre, flags):
+    if x.dim() != 2:
+        raise ValueError(f"{where}: x must be [tokens, d]")
+    T, D = x.shape
+    _want(where, "x", x, x.dtype, (T, D), x)
+    if y is not None:
+        _want(where, "y", y, y.dtype, (T, D), x)
+    elif w_post is not None or gate is not None:
+        raise ValueError(f"{where}: w_post and gate go with y")
+    _want(where, "w_post", w_post, torch.float32, (D,), x)
+    _want(where, "w_pre", w_pre, torch.float32, (D,), x)
+    if gate is not None and gate.dim() == 2:
+        _want(where, "gate", gate, y.dtype, (T, D), x)
+        flags |= NVFP4_NORM_TOKEN_GATE
+    else:
+        _want(where, "gate", gate, torch.float32, (D,), x)
+    return T, D, flags
+
+
+def nvfp4_block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, w_post: Optional[torch.Tensor] = None,
+                     gate: Optional[torch.Tensor] = None, w_pre: Optional[torch.Tensor] = None, alpha: float = 1.0,
+                     eps: float = 1e-6, flags: int = 0, n_dtype: Optional[torch.dtype] = None,
+                     x_out: Optional[torch.Tensor] = None) -> BlockNorm:
+    """x + alpha * gate * norm(y) * w_post and its own norm * w_pre, in one pass (see include/nvfp4.h).
+    gate is float32 [d] or [tokens, d] in y's dtype; x_out may be x.  Without y only the second norm (n in
+    n_dtype, default x's)."""
+    where = "nvfp4_block_norm"
+    T, D, flags = _norm_inputs(where, x, y, w_post, gate, w_pre, flags)
+    dev = x.device
+    y_dtype = y.dtype if y is not None else (n_dtype or x.dtype)
+    if y is None:
+        if x_out is not None:
+            raise ValueError(f"{where}: without y the residual stream does not change")
+    elif x_out is None:
+        x_out = torch.empty_like(x)
+    else:
+        _want(where, "x_out", x_out, x.dtype, (T, D), x)
+    n = torch.empty((T, D), dtype=y_dtype, device=dev) if w_pre is not None else None
+    rstd_post = torch.empty(T, dtype=torch.float32, device=dev) if w_post is not None else None
+    rstd_pre = torch.empty(T, dtype=torch.float32, device=dev) if w_pre is not None else None
+    st = lib().nvfp4_block_norm(x.data_ptr(), _dtype_code(x.dtype), _addr(y), _dtype_code(y_dtype), T, D, _addr(w_post),
+                                _addr(gate), _addr(w_pre), alpha, eps, flags, _addr(x_out), _addr(n), _addr(rstd_post),
+                                _addr(rstd_pre), _raw_stream(x))
+    _check(st, where)
+    return BlockNorm(x if y is None else x_out, n, rstd_post, rstd_pre)
+
+
+def nvfp4_block_norm_backward(dx_out: Optional[torch.Tensor], dn: Optional[torch.Tensor], x: torch.Tensor,
+                              y: Optional[torch.Tensor] = None, rstd_post: Optional[torch.Tensor] = None,
+                              rstd_pre: Optional[torch.Tensor] = None, w_post: Optional[torch.Tensor] = None,
+                              gate: Optional[torch.Tensor] = None, w_pre: Optional[torch.Tensor] = None, alpha: float = 1.0,
+                              flags: int = 0, workspace: Optional[torch.Tensor] = None) -> BlockNormGrads:
+    """Gradients of nvfp4_block_norm from dx_out (None: zero) and dn, its inputs (x as it was before the
+    call) and its rstd values."""
+    where = "nvfp4_block_norm_backward"
+    T, D, flags = _norm_inputs(where, x, y, w_post, gate, w_pre, flags)
+    dev = x.device
+    if (dn is None) != (w_pre is None):
+        raise ValueError(f"{where}: dn goes with w_pre")
+    y_dtype = y.dtype if y is not None else (dn.dtype if dn is not None else x.dtype)
+    _want(where, "dx_out", dx_out, x.dtype, (T, D), x)
+    _want(where, "dn", dn, y_dtype, (T, D), x)
+    _want(where, "rstd_post", rstd_post, torch.float32, (T,), x)
+    _want(where, "rstd_pre", rstd_pre, torch.float32, (T,), x)
+    dx = torch.empty_like(x)
+    dy = torch.empty_like(y) if y is not None else None
+    dw_post = torch.empty(D, dtype=torch.float32, device=dev) if w_post is not None else None
+    dgate = torch.empty_like(gate) if gate is not None else None
+    dw_pre = torch.empty(D, dtype=torch.float32, device=dev) if w_pre is not None else None
+    if workspace is None:
+        workspace = torch.empty(lib().nvfp4_block_norm_workspace_size(T, D) // 4, dtype=torch.float32, device=dev)
+    st = lib().nvfp4_block_norm_backward(_addr(dx_out), _addr(dn), x.data_ptr(), _dtype_code(x.dtype), _addr(y),
+                                         _dtype_code(y_dtype), T, D, _addr(w_post), _addr(gate), _addr(w_pre), alpha, flags,
+                                         _addr(rstd_post), _addr(rstd_pre), dx.data_ptr(), _addr(dy), _addr(dw_post),
+                                         _addr(dgate), _addr(dw_pre), _addr(workspace), _raw_stream(x))
+    _check(st, where)
+    return BlockNormGrads(dx, dy, dw_post, dgate, dw_pre)

@@ -33,7 +33,8 @@ DEVICE = ["-x", "hip", f"--offload-arch={ARCH}", "-Xclang", "-target-feature", "
 def units():
     """(source, object name, extra flags) of every translation unit."""
     u = [(s, s + ".o", []) for s in ["nvfp4_api.cpp", "quantize.hip", "dequant.hip", "gemm.hip",
-                                      "gemm_w4a16.hip", "transpose.hip"]]
+                                      "gemm_w4a16.hip", "transpose.hip", "block_api.cpp", "moe_route.hip",
+                                      "moe_rows.hip", "int8_quantize.hip", "gemm_int8.hip", "block_norm.hip"]]
     for out in (0, 1, 2):
         for a2d in (0, 1):
             for b2d in (0, 1):

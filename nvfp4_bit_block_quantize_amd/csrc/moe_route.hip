@@ -1,0 +1,697 @@
+// moe_route.hip -- routing of tokens to experts, its gradient, and the plan of a grouped product.
+//
+// Routing.  Sixteen lanes (one DPP row) own a token and hold its P = 16 EPL >= E experts, lane i the
+// experts [i EPL, (i + 1) EPL): reductions over a token are four DPP steps, and a wave routes four
+// tokens at once.  The softmax sum is one fixed order -- neighbours first -- which this layout gives
+// for free (the lane's own EPL values pairwise, then lanes 1, 2, 4, 8 apart), so scores, and with them
+// every choice, are the same bits in any implementation of that order.  top_k rounds then each take
+// the largest key of the row (a DPP maximum, a ballot for the lowest lane that holds it).
+//
+// Plan.  A counting sort, stable in the slots: each chunk of tokens counts its experts (the routing
+// kernel does so itself), and a second kernel gives every slot its row: the experts' totals and the
+// counts of the chunks before it, then the slot's rank among its chunk's equal ids, found with ballots
+// over the id's bits.  Up to 64 tokens (one chunk) the routing workgroup does all of it: one launch.
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "nvfp4_internal.h"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kMaxExperts = 512;
+constexpr int kPlanThreads = 1024;     // 16 waves
+constexpr int kOneBlockTokens = 64;    // routed and planned by one workgroup
+constexpr int kOneBlockSlots = 4096;   // planned from given ids by one workgroup
+constexpr int64_t kMaxBlocks = int64_t(1) << 20;  // of a launch (2^32 threads or more do not launch)
+constexpr size_t kOneBlockKeys = 60 * 1024;
+constexpr float kNegInf = -__builtin_huge_valf();
+
+// Value of the lane CTRL away in the DPP row of 16 lanes.
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  const int b = __float_as_int(v);
+  return __int_as_float(__builtin_amdgcn_update_dpp(b, b, CTRL, 0xF, 0xF, false));
+}
+constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
+
+// Over the 16 lanes of a row; every lane has the result.  (After the first two steps the lanes of a
+// quad agree, so the mirrors are exchanges 4 and 8 apart: the sum's order is neighbours first.)
+__device__ __forceinline__ float row_sum(float v) {
+  v += dpp<kXor1>(v);
+  v += dpp<kXor2>(v);
+  v += dpp<kHalfMirror>(v);
+  v += dpp<kMirror>(v);
+  return v;
+}
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, dpp<kXor1>(v));
+  v = fmaxf(v, dpp<kXor2>(v));
+  v = fmaxf(v, dpp<kHalfMirror>(v));
+  v = fmaxf(v, dpp<kMirror>(v));
+  return v;
+}
+
+// The lane's EPL logits from expert e0 on, as routing takes them: closed experts (-inf, NaN, beyond E)
+// are -inf, others capped at FLT_MAX.  vec: the row is 16-byte aligned.
+template <int EPL, bool BF16>
+__device__ __forceinline__ void load_logits(const uint8_t *row, int e0, int E, bool vec, float (&l)[EPL]) {
+  constexpr int ES = BF16 ? 2 : 4, BYTES = EPL * ES;
+  if (vec && BYTES % 4 == 0 && e0 + EPL <= E) {
+    uint32_t w[BYTES < 4 ? 1 : BYTES / 4];
+    if constexpr (BYTES % 16 == 0) {
+#pragma unroll
+      for (int i = 0; i < BYTES / 16; ++i) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(row + e0 * ES + 16 * i);
+        w[4 * i] = v.x;
+        w[4 * i + 1] = v.y;
+        w[4 * i + 2] = v.z;
+        w[4 * i + 3] = v.w;
+      }
+    } else if constexpr (BYTES == 8) {
+      const uint2 v = *reinterpret_cast<const uint2 *>(row + e0 * ES);
+      w[0] = v.x;
+      w[1] = v.y;
+    } else if constexpr (BYTES == 4) {
+      w[0] = *reinterpret_cast<const uint32_t *>(row + e0 * ES);
+    }
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      if constexpr (BF16)
+        l[j] = __uint_as_float(j & 1 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+      else
+        l[j] = __uint_as_float(w[j]);
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      l[j] = kNegInf;
+      if (e0 + j < E) {
+        if constexpr (BF16)
+          l[j] = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[e0 + j]) << 16);
+        else
+          l[j] = reinterpret_cast<const float *>(row)[e0 + j];
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) l[j] = l[j] > kNegInf ? fminf(l[j], 3.402823466e+38f) : kNegInf;  // NaN -> -inf
+}
+
+// Scores of the lane's logits (0 where closed); (top, total) are the row's softmax maximum and sum.
+__device__ __forceinline__ float softmax_score(float l, float top, float total) {
+  return l > kNegInf ? expf(l - top) / total : 0.0f;
+}
+__device__ __forceinline__ float sigmoid_score(float l) { return l > kNegInf ? 1.0f / (1.0f + expf(-l)) : 0.0f; }
+
+template <int EPL, bool SIGMOID>
+__device__ __forceinline__ void row_scores(const float (&l)[EPL], float (&s)[EPL], float &top, float &total) {
+  top = 0.0f;
+  total = 1.0f;
+  if constexpr (SIGMOID) {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) s[j] = sigmoid_score(l[j]);
+  } else {
+    top = l[0];
+#pragma unroll
+    for (int j = 1; j < EPL; ++j) top = fmaxf(top, l[j]);
+    top = row_max(top);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) s[j] = l[j] > kNegInf ? expf(l[j] - top) : 0.0f;
+    float t[EPL];
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) t[j] = s[j];
+#pragma unroll
+    for (int n = EPL; n > 1; n /= 2)
+#pragma unroll
+      for (int j = 0; j < n / 2; ++j) t[j] = t[2 * j] + t[2 * j + 1];
+    total = row_sum(t[0]);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) s[j] = l[j] > kNegInf ? s[j] / total : 0.0f;
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ float load_logit(const uint8_t *row, int e) {
+  float v;
+  if constexpr (BF16)
+    v = __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[e]) << 16);
+  else
+    v = reinterpret_cast<const float *>(row)[e];
+  return v > kNegInf ? fminf(v, 3.402823466e+38f) : kNegInf;
+}
+
+// ---- plan ----------------------------------------------------------------------------------------
+struct PlanLds {
+  int32_t base[kMaxExperts];                // next row of each expert for this chunk
+  int32_t wave_count[16][kMaxExperts];      // of the current tile of 1024 slots
+  int32_t part[kMaxExperts];
+  int32_t scan[16];
+};
+
+// Exclusive scan of v over the first 512 threads of a workgroup of 1024; total of all in *total.
+__device__ __forceinline__ int32_t scan512(int32_t v, int32_t *scratch, int32_t *total) {
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+  int32_t s = v;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int32_t o = __shfl_up(s, d);
+    if (lane >= d) s += o;
+  }
+  if (lane == 63) scratch[wave] = s;
+  __syncthreads();
+  int32_t before = 0, all = 0;
+#pragma unroll
+  for (uint32_t w = 0; w < 8; ++w) {
+    const int32_t c = scratch[w];
+    before += w < wave ? c : 0;
+    all += c;
+  }
+  *total = all;
+  return before + s - v;
+}
+
+// Rows of the slots [slot0, slot1) of one chunk, in order; lds.base holds each expert's next row.
+// Called by a whole workgroup of 1024; base is complete and synchronised.
+__device__ __forceinline__ void place_slots(PlanLds &lds, const int32_t *ids, int64_t slot0, int64_t slot1, int E,
+                                            int bits, int64_t total, int32_t *rows, int32_t *pos) {
+  const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
+  for (int64_t s0 = slot0; s0 < slot1; s0 += kPlanThreads) {
+    for (int e = tid; e < 16 * kMaxExperts; e += kPlanThreads) (&lds.wave_count[0][0])[e] = 0;
+    __syncthreads();
+    const int64_t slot = s0 + tid;
+    int32_t id = slot < slot1 ? ids[slot] : -1;
+    const bool live = id >= 0 && id < E;
+    // the lanes of this wave with the same id
+    uint64_t same = __ballot(live);
+    for (int b = 0; b < bits; ++b) {
+      const uint64_t m = __ballot((id >> b) & 1);
+      same &= ((id >> b) & 1) ? m : ~m;
+    }
+    const uint32_t rank = __popcll(same & ((1ull << lane) - 1));
+    if (live && rank == 0) lds.wave_count[wave][id] = __popcll(same);
+    __syncthreads();
+    if (tid < kMaxExperts && static_cast<int>(tid) < E) {
+      int32_t at = lds.base[tid];
+#pragma unroll
+      for (int w = 0; w < 16; ++w) {
+        const int32_t c = lds.wave_count[w][tid];
+        lds.wave_count[w][tid] = at;
+        at += c;
+      }
+      lds.base[tid] = at;
+    }
+    __syncthreads();
+    if (slot < slot1) {
+      int32_t p = -1;
+      if (live) {
+        p = lds.wave_count[wave][id] + static_cast<int32_t>(rank);
+        rows[p] = static_cast<int32_t>(slot);
+      }
+      pos[slot] = p;
+      if (slot >= total) rows[slot] = -1;  // rows beyond the last expert's (no slot is placed there)
+    }
+    __syncthreads();
+  }
+}
+
+// counts: [chunks][E] from the first kernel; chunk c has the slots [c * per, min((c + 1) * per, slots)).
+__global__ __launch_bounds__(kPlanThreads) void place_kernel(const int32_t *ids, const int32_t *counts, int chunks,
+                                                             int64_t per, int64_t slots, int E, int bits,
+                                                             int32_t *offsets, int32_t *rows, int32_t *pos) {
+  __shared__ PlanLds lds;
+  const uint32_t tid = threadIdx.x;
+  const int c = blockIdx.x;
+  // two threads an expert: chunks before and from this one on... summed over strided chunks
+  const int e = tid & (kMaxExperts - 1), half = tid / kMaxExperts;
+  int32_t before = 0, all = 0;
+  if (e < E) {
+    for (int i = half; i < chunks; i += 2) {
+      const int32_t n = counts[static_cast<int64_t>(i) * E + e];
+      all += n;
+      before += i < c ? n : 0;
+    }
+  }
+  if (half == 1) {
+    lds.base[e] = before;
+    lds.part[e] = all;
+  }
+  __syncthreads();
+  if (half == 0) {
+    before += lds.base[e];
+    all += lds.part[e];
+  }
+  int32_t total;
+  const int32_t first = scan512(half == 0 ? all : 0, lds.scan, &total);
+  __syncthreads();
+  if (half == 0) {
+    lds.base[e] = first + before;
+    if (c == 0 && e < E) offsets[e] = first;
+    if (c == 0 && e == 0) offsets[E] = total;
+  }
+  __syncthreads();
+  const int64_t slot0 = c * per;
+  place_slots(lds, ids, slot0, min(slot0 + per, slots), E, bits, total, rows, pos);
+}
+
+// The whole plan of at most kOneBlockSlots slots by one workgroup of 1024.
+__device__ __forceinline__ void plan_block(PlanLds &lds, const int32_t *ids, int64_t slots, int E, int bits,
+                                           int32_t *offsets, int32_t *rows, int32_t *pos) {
+  const uint32_t tid = threadIdx.x;
+  if (tid < kMaxExperts) lds.base[tid] = 0;
+  __syncthreads();
+  for (int64_t s = tid; s < slots; s += kPlanThreads) {
+    const int32_t id = ids[s];
+    if (id >= 0 && id < E) atomicAdd(&lds.base[id], 1);
+  }
+  __syncthreads();
+  const int32_t n = tid < kMaxExperts ? lds.base[tid] : 0;
+  int32_t total;
+  const int32_t first = scan512(n, lds.scan, &total);
+  if (tid < kMaxExperts) lds.base[tid] = first;
+  if (static_cast<int>(tid) < E) offsets[tid] = first;
+  if (tid == 0) offsets[E] = total;
+  __syncthreads();
+  place_slots(lds, ids, 0, slots, E, bits, total, rows, pos);
+}
+
+__global__ __launch_bounds__(kPlanThreads) void plan_one_kernel(const int32_t *ids, int64_t slots, int E, int bits,
+                                                                int32_t *offsets, int32_t *rows, int32_t *pos) {
+  __shared__ PlanLds lds;
+  plan_block(lds, ids, slots, E, bits, offsets, rows, pos);
+}
+
+// counts[c][e] of the slots of chunk c.
+__global__ __launch_bounds__(256) void count_kernel(const int32_t *ids, int64_t per, int64_t slots, int E,
+                                                    int32_t *counts) {
+  __shared__ int32_t hist[kMaxExperts];
+  for (int e = threadIdx.x; e < E; e += 256) hist[e] = 0;
+  __syncthreads();
+  const int64_t s0 = blockIdx.x * per, s1 = min(s0 + per, slots);
+  for (int64_t s = s0 + threadIdx.x; s < s1; s += 256) {
+    const int32_t id = ids[s];
+    if (id >= 0 && id < E) atomicAdd(&hist[id], 1);
+  }
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += 256) counts[static_cast<int64_t>(blockIdx.x) * E + e] = hist[e];
+}
+
+// ---- routing --------------------------------------------------------------------------------------
+struct RouteArgs {
+  const uint8_t *logits;
+  int64_t row_bytes;
+  int64_t tokens, per;  // tokens of a workgroup: [b * per, (b + 1) * per)
+  int E, G, GS, group_k, k;
+  bool sum2, renorm, vec;
+  float scale;
+  const float *bias;
+  int32_t *ids;
+  float *weights;
+  int32_t *counts;  // nullable [blocks][E]
+  int32_t *offsets, *rows, *pos;  // the whole plan (one workgroup of 1024), else NULL
+  int bits;
+};
+
+// Closes the experts of the groups that are not among the row's group_k best.  keys: this row's LDS
+// copy of its keys.
+template <int EPL>
+__device__ __forceinline__ void keep_groups(float (&key)[EPL], float *keys, const RouteArgs &p, uint32_t lane) {
+  const int l16 = lane & 15;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) keys[l16 * EPL + j] = key[j];
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  // lane g of the row: its group's best two keys, each lane starting elsewhere in its group
+  float m1 = kNegInf, m2 = kNegInf;
+  if (l16 < p.G) {
+    int at = l16 < p.GS ? l16 : l16 % p.GS;
+    for (int i = 0; i < p.GS; ++i) {
+      const float v = keys[l16 * p.GS + at];
+      m2 = fmaxf(m2, fminf(m1, v));
+      m1 = fmaxf(m1, v);
+      at = at + 1 == p.GS ? 0 : at + 1;
+    }
+  }
+  float value = m1;
+  if (p.sum2 && m2 > kNegInf) value = m1 + m2;
+  // the group's place: how many groups come before it
+  int place = 0;
+  for (int g = 0; g < p.G; ++g) {
+    const float o = __shfl(value, (lane & 48) + g);
+    place += (o > value || (o == value && g < l16)) ? 1 : 0;
+  }
+  const uint32_t kept = static_cast<uint32_t>(__ballot(l16 < p.G && place < p.group_k) >> (lane & 48)) & 0xFFFFu;
+  int g = l16 * EPL / p.GS, left = (g + 1) * p.GS - l16 * EPL;
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    if (!((kept >> g) & 1u)) key[j] = kNegInf;
+    if (--left == 0) {
+      ++g;
+      left = p.GS;
+    }
+  }
+}
+
+template <int EPL, bool BF16, bool SIGMOID>
+__global__ __launch_bounds__(kPlanThreads) void route_kernel(RouteArgs p) {
+  constexpr int P = 16 * EPL;
+  __shared__ int32_t hist[kMaxExperts];
+  // with groups: P keys a token; then, where this workgroup makes the plan, the plan's
+  extern __shared__ __attribute__((aligned(16))) uint8_t area[];
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+  const int l16 = lane & 15;
+  if (p.counts) {
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
+    __syncthreads();
+  }
+  const int64_t t1 = min(p.tokens, (blockIdx.x + 1) * p.per);
+  const int step = blockDim.x / 16;
+  for (int64_t tb = blockIdx.x * p.per; tb < t1; tb += step) {
+    if (tb + 4 * wave >= t1) continue;  // (no workgroup barrier inside)
+    const int64_t t = tb + (threadIdx.x >> 4);
+    const bool exists = t < t1;
+    const uint8_t *row = p.logits + (exists ? t : t1 - 1) * p.row_bytes;
+    float l[EPL], key[EPL], top, total;
+    load_logits<EPL, BF16>(row, l16 * EPL, p.E, p.vec, l);
+    row_scores<EPL, SIGMOID>(l, key, top, total);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      const int e = l16 * EPL + j;
+      float v = key[j];
+      if (p.bias && e < p.E) v += p.bias[e];
+      // (+ 0 so that a key of -0 is +0; a NaN key closes)
+      key[j] = l[j] > kNegInf && v > kNegInf ? v + 0.0f : kNegInf;
+    }
+    if (p.group_k < p.G) keep_groups<EPL>(key, reinterpret_cast<float *>(area) + (threadIdx.x >> 4) * P, p, lane);
+
+    float best = key[0];
+#pragma unroll
+    for (int j = 1; j < EPL; ++j) best = fmaxf(best, key[j]);
+    int id_lo = -1, id_hi = -1;  // slots l16 and 16 + l16
+    for (int r = 0; r < p.k; ++r) {
+      const float m = row_max(best);
+      const uint32_t holds = static_cast<uint32_t>(__ballot(best == m) >> (lane & 48)) & 0xFFFFu;
+      const int owner = __ffs(holds) - 1;
+      // the lane's first expert with that key; the owner closes it
+      int at = 0;
+#pragma unroll
+      for (int j = EPL - 1; j >= 0; --j) at = key[j] == m ? j : at;
+      const int mine = l16 == owner ? at : -1;
+      best = kNegInf;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) {
+        key[j] = j == mine ? kNegInf : key[j];
+        best = fmaxf(best, key[j]);
+      }
+      const int id = m > kNegInf ? owner * EPL + __shfl(at, (lane & 48) + owner) : -1;
+      if (l16 == (r & 15)) {
+        if (r < 16)
+          id_lo = id;
+        else
+          id_hi = id;
+      }
+    }
+    // the chosen experts' scores, formed again from their logits (the same operations, the same bits)
+    auto score_of = [&](int id) {
+      if (id < 0) return 0.0f;
+      const float v = load_logit<BF16>(row, id);
+      return SIGMOID ? sigmoid_score(v) : softmax_score(v, top, total);
+    };
+    float w_lo = score_of(id_lo), w_hi = p.k > 16 ? score_of(id_hi) : 0.0f;
+    if (p.renorm) {
+      const float sum = row_sum(w_lo + w_hi) + 1e-20f;
+      w_lo /= sum;
+      w_hi /= sum;
+    }
+    if (exists) {
+      if (l16 < p.k) {
+        p.ids[t * p.k + l16] = id_lo;
+        p.weights[t * p.k + l16] = w_lo * p.scale;
+        if (p.counts && id_lo >= 0) atomicAdd(&hist[id_lo], 1);
+      }
+      if (16 + l16 < p.k) {
+        p.ids[t * p.k + 16 + l16] = id_hi;
+        p.weights[t * p.k + 16 + l16] = w_hi * p.scale;
+        if (p.counts && id_hi >= 0) atomicAdd(&hist[id_hi], 1);
+      }
+    }
+  }
+  if (p.counts) {
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.E; e += blockDim.x) p.counts[static_cast<int64_t>(blockIdx.x) * p.E + e] = hist[e];
+  }
+  if (p.offsets) {
+    __syncthreads();  // the ids are in global memory for the whole workgroup
+    plan_block(*reinterpret_cast<PlanLds *>(area), p.ids, p.tokens * p.k, p.E, p.bits, p.offsets, p.rows, p.pos);
+  }
+}
+
+// ---- gradient of the weights -------------------------------------------------------------------------
+struct RouteBwdArgs {
+  const uint8_t *logits;
+  int64_t row_bytes;
+  int64_t tokens;
+  int E, k;
+  bool renorm, vec, vec_out;
+  float scale;
+  const int32_t *ids;
+  const float *dweights;
+  uint8_t *dlogits;
+  int64_t out_row_bytes;
+  int64_t first_block;  // of this launch
+};
+
+__device__ __forceinline__ uint32_t bf16_of(float v) {
+  return static_cast<uint32_t>(__builtin_bit_cast(uint16_t, static_cast<__bf16>(v)));
+}
+
+template <int EPL, bool BF16, bool SIGMOID>
+__global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs p) {
+  constexpr int P = 16 * EPL;
+  __shared__ float ds_lds[16][P];  // gradient of each expert's score, a row a token
+  const uint32_t lane = threadIdx.x & 63u;
+  const int l16 = lane & 15;
+  const int64_t t = (p.first_block + blockIdx.x) * 16 + (threadIdx.x >> 4);
+  const bool exists = t < p.tokens;
+  const int64_t tr = exists ? t : p.tokens - 1;
+  const uint8_t *row = p.logits + tr * p.row_bytes;
+  float l[EPL], s[EPL], top, total;
+  load_logits<EPL, BF16>(row, l16 * EPL, p.E, p.vec, l);
+  row_scores<EPL, SIGMOID>(l, s, top, total);
+
+  // the row's slots l16 and 16 + l16: score and gradient
+  float picked[2] = {0.0f, 0.0f}, g[2] = {0.0f, 0.0f};
+  int id[2] = {-1, -1};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int j = 16 * h + l16;
+    if (j < p.k) {
+      const int e = p.ids[tr * p.k + j];
+      if (e >= 0 && e < p.E) {
+        const float v = load_logit<BF16>(row, e);
+        id[h] = e;
+        picked[h] = SIGMOID ? sigmoid_score(v) : softmax_score(v, top, total);
+        g[h] = p.dweights[tr * p.k + j] * p.scale;
+      }
+    }
+  }
+  // sum over the chosen of (gradient * score): the normaliser's own gradient, and the softmax's
+  float gs = row_sum(fmaf(g[0], picked[0], g[1] * picked[1]));
+  if (p.renorm) {
+    const float sum = row_sum(picked[0] + picked[1]) + 1e-20f;
+    const float mean = gs / sum;
+    g[0] = (g[0] - mean) / sum;
+    g[1] = (g[1] - mean) / sum;
+    if (id[0] < 0) g[0] = 0.0f;
+    if (id[1] < 0) g[1] = 0.0f;
+    if (!SIGMOID) gs = row_sum(fmaf(g[0], picked[0], g[1] * picked[1]));
+  }
+  float *ds = ds_lds[threadIdx.x >> 4];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) ds[l16 * EPL + j] = 0.0f;
+  __syncthreads();
+  // (an atomic add only so that an id given twice counts twice; distinct ids add to zero)
+  if (id[0] >= 0) atomicAdd(&ds[id[0]], g[0]);
+  if (id[1] >= 0) atomicAdd(&ds[id[1]], g[1]);
+  __syncthreads();
+  float d[EPL];
+#pragma unroll
+  for (int j = 0; j < EPL; ++j) {
+    const float v = ds[l16 * EPL + j];
+    d[j] = SIGMOID ? (v * s[j]) * (1.0f - s[j]) : s[j] * (v - gs);
+  }
+  if (!exists) return;
+  uint8_t *out = p.dlogits + t * p.out_row_bytes;
+  constexpr int ES = BF16 ? 2 : 4, BYTES = EPL * ES;
+  const int e0 = l16 * EPL;
+  if (p.vec_out && BYTES % 16 == 0 && e0 + EPL <= p.E) {
+#pragma unroll
+    for (int i = 0; i < BYTES / 16; ++i) {
+      uint4 v;
+      uint32_t *w = reinterpret_cast<uint32_t *>(&v);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        w[q] = BF16 ? bf16_of(d[(8 * i + 2 * q) % EPL]) | bf16_of(d[(8 * i + 2 * q + 1) % EPL]) << 16
+                    : __float_as_uint(d[(4 * i + q) % EPL]);
+      *reinterpret_cast<uint4 *>(out + e0 * ES + 16 * i) = v;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j)
+      if (e0 + j < p.E) {
+        if constexpr (BF16)
+          reinterpret_cast<uint16_t *>(out)[e0 + j] = static_cast<uint16_t>(bf16_of(d[j]));
+        else
+          reinterpret_cast<float *>(out)[e0 + j] = d[j];
+      }
+  }
+}
+
+int id_bits(int64_t E) {
+  int b = 0;
+  while ((int64_t(1) << b) < E) ++b;
+  return b;
+}
+
+// Experts a lane holds: the power of two that gives 16 lanes all of them.
+int experts_per_lane(int64_t E) {
+  int epl = 1;
+  while (16 * epl < E) epl *= 2;
+  return epl;
+}
+
+bool rows_aligned16(const void *p, int64_t row_bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && row_bytes % 16 == 0;
+}
+
+template <int EPL>
+hipError_t run_route(const RouteArgs &p, bool bf16, bool sigmoid, int blocks, int threads, size_t lds,
+                     hipStream_t stream) {
+  auto *kernel = bf16 ? (sigmoid ? route_kernel<EPL, true, true> : route_kernel<EPL, true, false>)
+                      : (sigmoid ? route_kernel<EPL, false, true> : route_kernel<EPL, false, false>);
+  kernel<<<dim3(blocks), dim3(threads), lds, stream>>>(p);
+  return hipGetLastError();
+}
+
+template <int EPL>
+hipError_t run_route_backward(RouteBwdArgs p, bool bf16, bool sigmoid, hipStream_t stream) {
+  auto *kernel = bf16 ? (sigmoid ? route_backward_kernel<EPL, true, true> : route_backward_kernel<EPL, true, false>)
+                      : (sigmoid ? route_backward_kernel<EPL, false, true> : route_backward_kernel<EPL, false, false>);
+  const int64_t blocks = (p.tokens + 15) / 16;
+  for (p.first_block = 0; p.first_block < blocks; p.first_block += kMaxBlocks) {
+    const int64_t n = blocks - p.first_block < kMaxBlocks ? blocks - p.first_block : kMaxBlocks;
+    kernel<<<dim3(static_cast<uint32_t>(n)), dim3(256), 0, stream>>>(p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+size_t moe_workspace_bytes(int64_t experts) { return static_cast<size_t>(kPlanChunks) * experts * sizeof(int32_t); }
+
+hipError_t launch_moe_plan(const int32_t *ids, int64_t slots, int64_t experts, int32_t *offsets, int32_t *rows,
+                           int32_t *pos, int32_t *counts, hipStream_t stream) {
+  const int E = static_cast<int>(experts), bits = id_bits(E);
+  if (slots <= kOneBlockSlots) {
+    plan_one_kernel<<<dim3(1), dim3(kPlanThreads), 0, stream>>>(ids, slots, E, bits, offsets, rows, pos);
+    return hipGetLastError();
+  }
+  const int64_t per = ((slots + kPlanChunks - 1) / kPlanChunks + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
+  const int chunks = static_cast<int>((slots + per - 1) / per);
+  count_kernel<<<dim3(chunks), dim3(256), 0, stream>>>(ids, per, slots, E, counts);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  place_kernel<<<dim3(chunks), dim3(kPlanThreads), 0, stream>>>(ids, counts, chunks, per, slots, E, bits, offsets,
+                                                                rows, pos);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_route(const MoeRouteArgs &a) {
+  RouteArgs p{};
+  p.logits = static_cast<const uint8_t *>(a.logits);
+  p.row_bytes = a.ld * (a.dtype == 1 ? 2 : 4);
+  p.tokens = a.tokens;
+  p.E = static_cast<int>(a.experts);
+  p.G = a.num_groups;
+  p.GS = p.E / p.G;
+  p.group_k = a.group_top_k;
+  p.k = a.top_k;
+  p.sum2 = a.sum2;
+  p.renorm = a.renorm;
+  p.vec = rows_aligned16(a.logits, p.row_bytes);
+  p.scale = a.scale;
+  p.bias = a.bias;
+  p.ids = a.ids;
+  p.weights = a.weights;
+  p.bits = id_bits(p.E);
+  const bool plan = a.offsets != nullptr;
+  if (a.tokens == 0)
+    return plan ? launch_moe_plan(a.ids, 0, a.experts, a.offsets, a.rows, a.pos, a.workspace, a.stream) : hipSuccess;
+  // keys of the tokens that a workgroup holds at once (whole waves of four), for the choice of groups
+  const int epl = experts_per_lane(p.E);
+  const bool groups = p.group_k < p.G;
+  size_t lds = groups ? static_cast<size_t>((a.tokens + 3) / 4 * 4) * 16 * epl * sizeof(float) : 0;
+  const bool one = plan && a.tokens <= kOneBlockTokens && lds <= kOneBlockKeys;
+  int blocks, threads;
+  if (one) {
+    p.offsets = a.offsets;
+    p.rows = a.rows;
+    p.pos = a.pos;
+    p.per = a.tokens;
+    blocks = 1;
+    threads = kPlanThreads;
+    if (lds < sizeof(PlanLds)) lds = sizeof(PlanLds);
+  } else {
+    lds = groups ? static_cast<size_t>(256) * epl * sizeof(float) : 0;
+    // chunks of whole 16-token workgroup steps, at most kPlanChunks of them when they are counted
+    threads = 256;
+    const int64_t most = plan ? kPlanChunks : kMaxBlocks;
+    if (plan) p.counts = a.workspace;
+    p.per = ((a.tokens + most - 1) / most + 15) / 16 * 16;
+    blocks = static_cast<int>((a.tokens + p.per - 1) / p.per);
+  }
+  hipError_t e;
+  switch (epl) {
+    case 1: e = run_route<1>(p, a.dtype == 1, a.sigmoid, blocks, threads, lds, a.stream); break;
+    case 2: e = run_route<2>(p, a.dtype == 1, a.sigmoid, blocks, threads, lds, a.stream); break;
+    case 4: e = run_route<4>(p, a.dtype == 1, a.sigmoid, blocks, threads, lds, a.stream); break;
+    case 8: e = run_route<8>(p, a.dtype == 1, a.sigmoid, blocks, threads, lds, a.stream); break;
+    case 16: e = run_route<16>(p, a.dtype == 1, a.sigmoid, blocks, threads, lds, a.stream); break;
+    default: e = run_route<32>(p, a.dtype == 1, a.sigmoid, blocks, threads, lds, a.stream); break;
+  }
+  if (e != hipSuccess || !plan || one) return e;
+  place_kernel<<<dim3(blocks), dim3(kPlanThreads), 0, a.stream>>>(a.ids, a.workspace, blocks, p.per * p.k,
+                                                                  a.tokens * p.k, p.E, p.bits, a.offsets, a.rows, a.pos);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_route_backward(const MoeRouteBackwardArgs &a) {
+  RouteBwdArgs p{};
+  const int es = a.dtype == 1 ? 2 : 4;
+  p.logits = static_cast<const uint8_t *>(a.logits);
+  p.row_bytes = a.ld * es;
+  p.tokens = a.tokens;
+  p.E = static_cast<int>(a.experts);
+  p.k = a.top_k;
+  p.renorm = a.renorm;
+  p.vec = rows_aligned16(a.logits, p.row_bytes);
+  p.vec_out = rows_aligned16(a.dlogits, a.ldd * es);
+  p.scale = a.scale;
+  p.ids = a.ids;
+  p.dweights = a.dweights;
+  p.dlogits = static_cast<uint8_t *>(a.dlogits);
+  p.out_row_bytes = a.ldd * es;
+  switch (experts_per_lane(p.E)) {
+    case 1: return run_route_backward<1>(p, a.dtype == 1, a.sigmoid, a.stream);
+    case 2: return run_route_backward<2>(p, a.dtype == 1, a.sigmoid, a.stream);
+    case 4: return run_route_backward<4>(p, a.dtype == 1, a.sigmoid, a.stream);
+    case 8: return run_route_backward<8>(p, a.dtype == 1, a.sigmoid, a.stream);
+    case 16: return run_route_backward<16>(p, a.dtype == 1, a.sigmoid, a.stream);
+    default: return run_route_backward<32>(p, a.dtype == 1, a.sigmoid, a.stream);
+  }
+}
+
+}  // namespace nvfp4

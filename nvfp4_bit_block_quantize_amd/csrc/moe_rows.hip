@@ -1,0 +1,225 @@
+// moe_rows.hip -- rows between tokens and experts: the gather into a plan's order, the weighted sum of
+// the experts' rows, and its gradients.  All three move rows once (HBM-bound): a lane owns 16 bytes of
+// a row's columns and walks the token's slots, so the k loads of a lane are independent and a token's
+// own row (dout) is read once for all of its slots.  A token's sums run in the order of its slots.
+#include "nvfp4_internal.h"
+#include "vec_io.hpp"
+
+namespace nvfp4 {
+namespace {
+
+constexpr int kRowThreads = 256;
+// Workgroups of a launch; each walks its share of a larger problem (a grid of 2^32 threads or more does
+// not launch).
+constexpr int64_t kMaxBlocks = int64_t(1) << 20;
+
+struct RowsArgs {
+  const uint8_t *x;
+  int64_t ldx;  // bytes
+  const uint8_t *dout;
+  int64_t ld_dout;  // bytes
+  int64_t tokens;
+  int pieces;  // 16-byte pieces of a row
+  int col_blocks;
+  const int32_t *pos, *rows;
+  const float *weights;
+  int k;
+  int64_t blocks;  // (row, column block) pairs, or tokens
+  uint8_t *out;
+  int64_t ldo;  // bytes
+  float *dweights;
+};
+
+template <bool BF16>
+__device__ __forceinline__ void unpack16(const uint4 &v, float (&f)[BF16 ? 8 : 4]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (BF16) {
+      f[2 * q] = __uint_as_float(w[q] << 16);
+      f[2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+    } else {
+      f[q] = __uint_as_float(w[q]);
+    }
+  }
+}
+template <bool BF16>
+__device__ __forceinline__ uint4 pack16(const float (&f)[BF16 ? 8 : 4]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    if constexpr (BF16)
+      w[q] = pack_bf16(f[2 * q], f[2 * q + 1]);
+    else
+      w[q] = __float_as_uint(f[q]);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// y[r] = x[rows[r] / k]; the dtype does not matter.
+__global__ __launch_bounds__(kRowThreads) void gather_kernel(RowsArgs p) {
+  for (int64_t b = blockIdx.x; b < p.blocks; b += gridDim.x) {
+    const int64_t r = b / p.col_blocks;
+    const int c = static_cast<int>(b % p.col_blocks) * kRowThreads + threadIdx.x;
+    if (c >= p.pieces) continue;
+    const int64_t slot = p.rows[r];
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (slot >= 0 && slot < p.tokens * p.k) v = *reinterpret_cast<const uint4 *>(p.x + slot / p.k * p.ldx + 16ll * c);
+    *reinterpret_cast<uint4 *>(p.out + r * p.ldo + 16ll * c) = v;
+  }
+}
+
+template <bool BF16>
+__global__ __launch_bounds__(kRowThreads) void combine_kernel(RowsArgs p) {
+  constexpr int V = BF16 ? 8 : 4;
+  for (int64_t b = blockIdx.x; b < p.blocks; b += gridDim.x) {
+    const int64_t t = b / p.col_blocks;
+    const int c = static_cast<int>(b % p.col_blocks) * kRowThreads + threadIdx.x;
+    if (c >= p.pieces) continue;
+    const uint32_t slots = static_cast<uint32_t>(p.tokens * p.k);
+    float acc[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.0f;
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+      uint4 v[8];
+      float w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[j] = make_uint4(0, 0, 0, 0);
+        w[j] = 0.0f;
+        if (j0 + j < p.k) {
+          const uint32_t row = static_cast<uint32_t>(p.pos[t * p.k + j0 + j]);
+          if (row < slots) {  // (-1 is beyond)
+            v[j] = *reinterpret_cast<const uint4 *>(p.x + row * p.ldx + 16ll * c);
+            w[j] = p.weights ? p.weights[t * p.k + j0 + j] : 1.0f;
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j0 + j >= p.k) break;
+        float f[V];
+        unpack16<BF16>(v[j], f);
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(w[j], f[i], acc[i]);
+      }
+    }
+    *reinterpret_cast<uint4 *>(p.out + t * p.ldo + 16ll * c) = pack16<BF16>(acc);
+  }
+}
+
+// One workgroup a token; its lanes' partial dot products of eight slots at a time meet in LDS.
+template <bool BF16>
+__global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(RowsArgs p) {
+  constexpr int V = BF16 ? 8 : 4;
+  __shared__ float part[4][8];
+  const int64_t slots = p.tokens * p.k;
+  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
+  for (int64_t t = blockIdx.x; t < p.blocks; t += gridDim.x) {
+    const uint8_t *dout = p.dout + t * p.ld_dout;
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+      float dot[8], w[8];
+      int64_t row[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        dot[j] = 0.0f;
+        w[j] = 0.0f;
+        row[j] = -1;
+        if (j0 + j < p.k) {
+          const int64_t r = p.pos[t * p.k + j0 + j];
+          row[j] = r < slots ? r : -1;
+          w[j] = p.weights[t * p.k + j0 + j];
+        }
+      }
+      for (int c = threadIdx.x; c < p.pieces; c += kRowThreads) {
+        uint4 v[8];
+        const uint4 dv = *reinterpret_cast<const uint4 *>(dout + 16ll * c);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[j] = make_uint4(0, 0, 0, 0);
+          if (row[j] >= 0) v[j] = *reinterpret_cast<const uint4 *>(p.x + row[j] * p.ldx + 16ll * c);
+        }
+        float d[V];
+        unpack16<BF16>(dv, d);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (row[j] < 0) continue;
+          float f[V], g[V];
+          unpack16<BF16>(v[j], f);
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            dot[j] = fmaf(d[i], f[i], dot[j]);
+            g[i] = w[j] * d[i];
+          }
+          *reinterpret_cast<uint4 *>(p.out + row[j] * p.ldo + 16ll * c) = pack16<BF16>(g);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float s = wave_sum(dot[j]);
+        if (lane == 0) part[wave][j] = s;
+      }
+      __syncthreads();
+      if (threadIdx.x < 8 && j0 + static_cast<int>(threadIdx.x) < p.k)
+        p.dweights[t * p.k + j0 + threadIdx.x] =
+            (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
+      __syncthreads();
+    }
+    // rows that no slot has: this workgroup looks after rows [t k, (t + 1) k)
+    for (int j = 0; j < p.k; ++j) {
+      const int64_t r = t * p.k + j;
+      if (p.rows[r] < 0)
+        for (int c = threadIdx.x; c < p.pieces; c += kRowThreads)
+          *reinterpret_cast<uint4 *>(p.out + r * p.ldo + 16ll * c) = make_uint4(0, 0, 0, 0);
+    }
+  }
+}
+
+RowsArgs rows_args(const MoeRowsArgs &a) {
+  const int es = a.dtype == 1 ? 2 : 4;
+  RowsArgs p{};
+  p.x = static_cast<const uint8_t *>(a.x);
+  p.ldx = a.ldx * es;
+  p.dout = static_cast<const uint8_t *>(a.dout);
+  p.ld_dout = a.ld_dout * es;
+  p.tokens = a.tokens;
+  p.pieces = static_cast<int>(a.d * es / 16);
+  p.col_blocks = (p.pieces + kRowThreads - 1) / kRowThreads;
+  p.pos = a.pos;
+  p.rows = a.rows;
+  p.weights = a.weights;
+  p.k = a.top_k;
+  p.out = static_cast<uint8_t *>(a.out);
+  p.ldo = a.ldo * es;
+  p.dweights = a.dweights;
+  return p;
+}
+
+dim3 grid_of(const RowsArgs &p) { return dim3(static_cast<uint32_t>(p.blocks < kMaxBlocks ? p.blocks : kMaxBlocks)); }
+
+}  // namespace
+
+hipError_t launch_moe_gather(const MoeRowsArgs &a) {
+  RowsArgs p = rows_args(a);
+  p.blocks = a.tokens * a.top_k * p.col_blocks;
+  gather_kernel<<<grid_of(p), dim3(kRowThreads), 0, a.stream>>>(p);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_combine(const MoeRowsArgs &a) {
+  RowsArgs p = rows_args(a);
+  p.blocks = a.tokens * p.col_blocks;
+  auto *kernel = a.dtype == 1 ? combine_kernel<true> : combine_kernel<false>;
+  kernel<<<grid_of(p), dim3(kRowThreads), 0, a.stream>>>(p);
+  return hipGetLastError();
+}
+
+hipError_t launch_moe_combine_backward(const MoeRowsArgs &a) {
+  RowsArgs p = rows_args(a);
+  p.blocks = a.tokens;
+  auto *kernel = a.dtype == 1 ? combine_backward_kernel<true> : combine_backward_kernel<false>;
+  kernel<<<grid_of(p), dim3(kRowThreads), 0, a.stream>>>(p);
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4

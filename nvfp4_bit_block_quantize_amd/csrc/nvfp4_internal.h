@@ -84,7 +84,111 @@ struct TransposeLaunch {
   hipStream_t stream;
 };
 
+// Chunks of the counting sort behind a plan: at most one row of counts each in the workspace.
+constexpr int kPlanChunks = 256;
+
+struct MoeRouteArgs {
+  const void *logits;
+  int dtype;
+  int64_t tokens, experts, ld;
+  const float *bias;
+  int32_t num_groups, group_top_k, top_k;
+  bool sigmoid, renorm, sum2;
+  float scale;
+  int32_t *ids;
+  float *weights;
+  int32_t *offsets, *rows, *pos;  // all or none
+  int32_t *workspace;
+  hipStream_t stream;
+};
+
+struct MoeRouteBackwardArgs {
+  const void *logits;
+  int dtype;
+  int64_t tokens, experts, ld;
+  const int32_t *ids;
+  const float *dweights;
+  int32_t top_k;
+  bool sigmoid, renorm;
+  float scale;
+  void *dlogits;
+  int64_t ldd;
+  hipStream_t stream;
+};
+
+struct MoeRowsArgs {  // gather, combine and combine's gradient
+  const void *x;       // gather: x; combine: y; gradient: y
+  int64_t ldx;
+  const void *dout;    // gradient only
+  int64_t ld_dout;
+  int dtype;
+  int64_t tokens, d;
+  const int32_t *pos, *rows;
+  const float *weights;
+  int32_t top_k;
+  void *out;           // gather: y; combine: out; gradient: dy
+  int64_t ldo;
+  float *dweights;
+  hipStream_t stream;
+};
+
+struct Int8QuantArgs {
+  const void *x;
+  int dtype;
+  int64_t rows, cols, ldx;
+  int8_t *q;
+  float *scales;
+  hipStream_t stream;
+};
+
+struct Int8GemmArgs {
+  const int8_t *a;
+  const float *a_scales;
+  int64_t a_rows;
+  const int8_t *b;
+  const float *b_scales;
+  int64_t M, N, K;
+  void *c;
+  int c_dtype;
+  int64_t ldc;
+  int32_t num_groups;
+  const int32_t *offsets, *rows;  // device
+  int32_t row_div;
+  hipStream_t stream;
+};
+
+struct BlockNormArgs {
+  const void *x, *y;
+  int x_dtype, y_dtype;
+  int64_t tokens, d;
+  const float *w_post;
+  const void *gate;
+  const float *w_pre;
+  float alpha, eps;
+  bool one_plus, token_gate;
+  void *x_out, *n;              // forward
+  float *rstd_post, *rstd_pre;  // forward: written; backward: read
+  const void *dx_out, *dn;      // backward
+  void *dx, *dy, *dgate;
+  float *dw_post, *dw_pre;
+  float *workspace;
+  hipStream_t stream;
+};
+
 // Each returns hipSuccess or the launch error.
+hipError_t launch_moe_route(const MoeRouteArgs &a);
+hipError_t launch_moe_route_backward(const MoeRouteBackwardArgs &a);
+hipError_t launch_moe_plan(const int32_t *ids, int64_t slots, int64_t experts, int32_t *offsets, int32_t *rows,
+                           int32_t *pos, int32_t *counts, hipStream_t stream);
+size_t moe_workspace_bytes(int64_t experts);
+hipError_t launch_moe_gather(const MoeRowsArgs &a);
+hipError_t launch_moe_combine(const MoeRowsArgs &a);
+hipError_t launch_moe_combine_backward(const MoeRowsArgs &a);
+hipError_t launch_int8_quantize(const Int8QuantArgs &a);
+hipError_t launch_int8_gemm(const Int8GemmArgs &a);
+hipError_t launch_block_norm(const BlockNormArgs &a);
+hipError_t launch_block_norm_backward(const BlockNormArgs &a);
+size_t block_norm_workspace_bytes(int64_t tokens, int64_t d);
 hipError_t launch_quantize(const QuantArgs &a);
 hipError_t launch_dequantize(const DequantArgs &a);
 hipError_t launch_gemm(const GemmArgs &a);

@@ -13,6 +13,8 @@
 // By expert.  The row offsets live on the device, so the launch has as many workgroups as any offsets
 // could need (a partial tile more for every expert), and each finds its tile by a scan over the experts'
 // tile counts; those beyond the last tile leave.  A's rows may be read through the plan's slots.
+#include <type_traits>
+
 #include "gemm_common.hpp"
 #include "nvfp4_internal.h"
 
@@ -37,18 +39,20 @@ struct I8Args {
   uint8_t *c;
   int64_t ldc;
   int32_t tiles_n;
-  int32_t tiles;  // plain form: all tiles
+  int32_t tiles_m;  // plain form
   int32_t groups;
   const int32_t *offsets;  // NULL: one group of M rows
   const int32_t *rows;     // NULL: row r of C is row r of A
   int32_t row_div;
-  int32_t vec_store;
+  int32_t vec_store, vec_scales;
 };
 
 // What A reads beyond K in the last step.
 __device__ const uint4 kZeros = {0u, 0u, 0u, 0u};
 
-__device__ __forceinline__ uint32_t swz(uint32_t r) { return (r + ((r >> 3) & 3u)) & 7u; }
+// 128-byte rows: a ds_read_b128 serves sixteen lanes a pass, lanes 0-3, 12-15 and 20-27 together and so on;
+// with this swizzle the fragment rows of each such set cover all 64 banks once.
+__device__ __forceinline__ uint32_t swz(uint32_t r) { return (r >> 1) & 7u; }
 
 // The rows of C of a tile row: rows [m0, m_end) of group g.
 struct TileRows {
@@ -96,7 +100,7 @@ __device__ __forceinline__ int32_t count_rows(const int32_t *offsets, int groups
   }
 #pragma unroll
   for (int d = 32; d > 0; d /= 2) n += __shfl_xor(n, d);
-  return n;
+  return __builtin_amdgcn_readfirstlane(n);
 }
 
 // Row of A behind row r of C.
@@ -104,6 +108,40 @@ __device__ __forceinline__ int64_t a_row(const I8Args &p, int64_t r) {
   if (!p.rows) return r;
   const int64_t s = p.rows[r] / p.row_div;
   return s >= 0 && s < p.a_rows ? s : 0;
+}
+
+// The tiles of a launch, dealt so that each XCD (workgroup i runs on XCD i mod 8) gets a contiguous range of
+// them, walked in bands of tile rows (band_tile).
+struct Tiles {
+  int32_t rows, total, per;  // tile rows, tiles, tiles of an XCD
+};
+template <int BM>
+__device__ __forceinline__ Tiles all_tiles(const I8Args &p) {
+  Tiles w;
+  w.rows = p.offsets ? count_rows<BM>(p.offsets, p.groups) : p.tiles_m;
+  w.total = w.rows * p.tiles_n;
+  w.per = (w.total + 7) >> 3;
+  return w;
+}
+// The tile of workgroup number `id`; false where there is none.
+template <int BM>
+__device__ __forceinline__ bool find_tile(const I8Args &p, const Tiles &w, int32_t id, TileRows &t, int32_t &tn) {
+  const int32_t tile = (id & 7) * w.per + (id >> 3);
+  if ((id >> 3) >= w.per || tile >= w.total) return false;
+  int32_t tm;
+  band_tile(tile, p.tiles_n, w.rows, tm, tn);
+  if (p.offsets) {
+    if (!find_rows<BM>(p.offsets, p.groups, tm, t)) return false;
+    t.group = __builtin_amdgcn_readfirstlane(t.group);
+    t.m0 = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(t.m0));
+    t.m_end = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(t.m_end));
+    t.m_end = t.m_end < p.M ? t.m_end : p.M;
+    return t.m0 >= 0 && t.m0 < t.m_end;
+  }
+  t.group = 0;
+  t.m0 = static_cast<int64_t>(tm) * BM;
+  t.m_end = p.M;
+  return true;
 }
 
 template <int FM, int FN, int STAGES, bool OUT_BF16>
@@ -118,29 +156,9 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_int8_kernel(I8Args p) {
   const uint32_t h = lane >> 5, l32 = lane & 31u;
   const uint32_t wm = (wave >> 1) * 32 * FM, wn = (wave & 1) * 32 * FN;
 
-  // ---- this workgroup's tile
   TileRows t;
   int32_t tn;
-  if (p.offsets) {
-    const int32_t tiles_m = count_rows<TM>(p.offsets, p.groups);
-    const int32_t total = tiles_m * p.tiles_n;
-    // each XCD (workgroup i runs on XCD i mod 8) gets a contiguous range of tiles
-    const int32_t per = (total + 7) >> 3, tile = (blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    if (static_cast<int32_t>(blockIdx.x >> 3) >= per || tile >= total) return;
-    int32_t tm;
-    band_tile(tile, p.tiles_n, tiles_m, tm, tn);
-    if (!find_rows<TM>(p.offsets, p.groups, tm, t)) return;
-    t.group = __builtin_amdgcn_readfirstlane(t.group);
-    t.m_end = t.m_end < p.M ? t.m_end : p.M;
-    if (t.m0 < 0 || t.m0 >= t.m_end) return;
-  } else {
-    const int32_t tile = xcd_tile(blockIdx.x, p.tiles);
-    int32_t tm;
-    band_tile(tile, p.tiles_n, p.tiles / p.tiles_n, tm, tn);
-    t.group = 0;
-    t.m0 = static_cast<int64_t>(tm) * TM;
-    t.m_end = p.M;
-  }
+  if (!find_tile<TM>(p, all_tiles<TM>(p), blockIdx.x, t, tn)) return;
   const int64_t n0 = static_cast<int64_t>(tn) * TN;
   const uint8_t *const b = p.b + static_cast<int64_t>(t.group) * p.N * p.K;
 
@@ -260,20 +278,295 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_int8_kernel(I8Args p) {
   }
 }
 
-template <int FM, int FN, int STAGES>
-hipError_t run_tiles(const Int8GemmArgs &a, I8Args p) {
-  constexpr int TM = 64 * FM, TN = 64 * FN;
+// Buffer descriptor over the bytes from p on (raw 32-bit data format, no limit below 4 GiB).
+// The same in every lane: the read of lane 0's pointer only tells the compiler so.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const uint8_t *p) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  const uint64_t u = static_cast<uint64_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a >> 32))) << 32 |
+                     static_cast<uint32_t>(__builtin_amdgcn_readfirstlane(static_cast<uint32_t>(a)));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<uint8_t *>(u), 0, -1, 0x00020000);
+}
+// As lds_load16, from byte `off` (a lane's) + `step` (the wave's) of a buffer.
+__device__ __forceinline__ void lds_buffer16(__amdgpu_buffer_rsrc_t rs, uint32_t off, uint32_t step, uint8_t *lds_base) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_void *)lds_base, 16, off, step, 0, 0);
+}
+
+// ---- many rows: 256 x 256 tiles ---------------------------------------------------------------------
+// Four waves of 128 x 128 (16 MFMA tiles, 256 accumulators a lane), one a SIMD.  K advances 128 bytes a
+// step through two 64 KB stages: whole 128-byte lines, since the L2 serves one request a clock and
+// channel whatever its size (with 64-byte rows its request rate was the bound).  A step has four
+// sub-steps of 16 MFMAs; the fragments of the next sub-step are read under the MFMAs of this one, and
+// the step's one barrier follows sub-step 2: there every fragment of the stage is in registers, so
+// behind it the stage takes the loads of the step after next, and the next stage, whose loads this
+// wave has waited for, is read.
+constexpr int kBigB = 256 * kStep, kBigStage = 512 * kStep;
+
+// C of a wave's quarter of a tile, 32 rows and (in fp32) 64 columns at a time through 8 KB of the wave's own LDS:
+// lane (h, l32) holds row l32 of tile (i, j), columns 8 q + 4 h + e; staged rows leave as whole 256-byte
+// segments, 16-byte chunk c of row r at c ^ (r mod 16).  Tiles cut by N, or C without 16-byte aligned rows,
+// take element stores.  Waits for this wave's loads in flight.
+template <bool OUT_BF16>
+__device__ __forceinline__ void store_big_tile(const I8Args &p, const intx16 (&acc)[4][4], uint8_t *region, const TileRows &t,
+                                               int64_t n0, uint32_t wm, uint32_t wn, uint32_t lane) {
+  constexpr int64_t ES = OUT_BF16 ? 2 : 4;
+  // (an opaque copy: the per-lane addresses are formed here and not carried through the tile loop)
+  asm volatile("" : "+v"(lane));
+  const uint32_t h = lane >> 5, l32 = lane & 31u;
+  const float *sb = p.b_scales + static_cast<int64_t>(t.group) * p.N;
+  const bool whole = n0 + 256 <= p.N;
+  float s[4][4][4], sa[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int64_t col = n0 + wn + 32 * j + 8 * q + 4 * h;
+      if (p.vec_scales && whole) {
+        const float4 v = *reinterpret_cast<const float4 *>(sb + col);
+        s[j][q][0] = v.x;
+        s[j][q][1] = v.y;
+        s[j][q][2] = v.z;
+        s[j][q][3] = v.w;
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[j][q][e] = sb[min(col + e, p.N - 1)];
+      }
+    }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) sa[i] = p.a_scales[a_row(p, min(t.m0 + wm + 32 * i + l32, t.m_end - 1))];
+  wait_vmcnt<0>();
+  const int64_t rows_left = t.m_end - (t.m0 + wm);
+  uint8_t *const out = p.c + ((t.m0 + wm) * p.ldc + n0 + wn) * ES;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (32 * i >= rows_left) break;  // (the same in every lane)
+    if (p.vec_store && whole) {
+      constexpr int JP = OUT_BF16 ? 4 : 2;  // B fragments a pass: 256 bytes a row
+#pragma unroll
+      for (int j0 = 0; j0 < 4; j0 += JP) {
+#pragma unroll
+        for (int jj = 0; jj < JP; ++jj)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int j = j0 + jj;
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = static_cast<float>(acc[j][i][4 * q + e]) * (sa[i] * s[j][q][e]);
+            if constexpr (OUT_BF16) {
+              const bf16x2v lo = __builtin_convertvector((float2v){v[0], v[1]}, bf16x2v);
+              const bf16x2v hi = __builtin_convertvector((float2v){v[2], v[3]}, bf16x2v);
+              *reinterpret_cast<uint2 *>(region + l32 * 256 + (((4 * jj + q) ^ (l32 & 15)) * 16 + 8 * h)) =
+                  make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+            } else {
+              *reinterpret_cast<float4 *>(region + l32 * 256 + ((8 * jj + 2 * q + h) ^ (l32 & 15)) * 16) =
+                  make_float4(v[0], v[1], v[2], v[3]);
+            }
+          }
+        // the wave reads back its own rows (LDS accesses of one wave complete in order)
+#pragma unroll
+        for (uint32_t u = 0; u < 8; ++u) {
+          const uint32_t row = 4 * u + (lane >> 4), c = lane & 15u;
+          const uint4 v = *reinterpret_cast<const uint4 *>(region + row * 256 + ((c ^ (row & 15)) * 16));
+          if (32 * i + row < rows_left)
+            *reinterpret_cast<uint4 *>(out + (32 * i + row) * p.ldc * ES + j0 * 32 * ES + c * 16) = v;
+        }
+      }
+    } else if (32 * i + l32 < rows_left) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t col = 32 * j + 8 * q + 4 * h + e;
+            if (n0 + wn + col >= p.N) continue;
+            const float v = static_cast<float>(acc[j][i][4 * q + e]) * (sa[i] * s[j][q][e]);
+            uint8_t *at = out + ((32 * i + l32) * p.ldc + col) * ES;
+            if constexpr (OUT_BF16)
+              *reinterpret_cast<uint16_t *>(at) = static_cast<uint16_t>(bf16_rne(v));
+            else
+              *reinterpret_cast<float *>(at) = v;
+          }
+    }
+  }
+}
+
+template <bool OUT_BF16>
+__global__ __launch_bounds__(kThreads, 1) void gemm_int8_big_kernel(I8Args p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kBigStage];
+  const uint32_t lane = threadIdx.x & 63u;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t h = lane >> 5, l32 = lane & 31u;
+  const uint32_t wm = (wave >> 1) * 128, wn = (wave & 1) * 128;
+
+  TileRows t;
+  int32_t tn;
+  if (!find_tile<256>(p, all_tiles<256>(p), blockIdx.x, t, tn)) return;
+  const int64_t n0 = static_cast<int64_t>(tn) * 256;
+  // direct loads: wave w fetches rows [64 w, 64 w + 64) of A and of B, 8 rows a load; rows beyond the
+  // operand read its last one (their products are never stored).  Buffer loads: a lane's offset within
+  // the operand stays in one register and the step's advance is a scalar, so a load takes no vector
+  // arithmetic.  (Every address is inside the operand: the range check is not relied on.)
+  const __amdgpu_buffer_rsrc_t rsA = buffer_of(p.rows ? p.a : p.a + t.m0 * p.K);
+  const __amdgpu_buffer_rsrc_t rsB = buffer_of(p.b + (static_cast<int64_t>(t.group) * p.N + n0) * p.K);
+  uint32_t off[16];  // A, then B
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t R = 64 * wave + 8 * i + (lane >> 3);
+    const uint32_t chunk = ((lane & 7u) ^ swz(R)) * 16;
+    const int64_t r = min(t.m0 + R, t.m_end - 1);
+    off[i] = static_cast<uint32_t>(p.rows ? a_row(p, r) : r - t.m0) * p.K + chunk;
+    off[8 + i] = static_cast<uint32_t>(min(n0 + R, p.N - 1) - n0) * p.K + chunk;
+  }
+  const int32_t steps = static_cast<int32_t>((p.K + kStep - 1) / kStep);
+  const uint32_t rest = p.K - (steps - 1) * kStep;  // bytes of K in the last step
+  auto load = [&](uint8_t *st, int32_t kt, int q) {
+    lds_buffer16(q < 8 ? rsA : rsB, off[q], kt * kStep,
+                 st + (q < 8 ? 0 : kBigB) + (64 * wave + 8 * (q & 7)) * kStep);
+  };
+  // before the loads of a last step that K does not fill: chunks beyond K read its last one (their A
+  // fragments are cleared)
+  auto end_of_k = [&](int32_t kt) {
+    if (kt == steps - 1 && rest < kStep) {
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const uint32_t R = 64 * wave + 8 * (q & 7) + (lane >> 3);
+        const uint32_t chunk = ((lane & 7u) ^ swz(R)) * 16;
+        off[q] -= chunk > rest - 16 ? chunk - (rest - 16) : 0;
+      }
+    }
+  };
+
+  intx16 acc[4][4];  // [B fragment][A fragment]
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[j][i][r] = 0;
+
+  const uint32_t rdA = (wm + l32) * kStep, rdB = kBigB + (wn + l32) * kStep, sw = swz(l32);
+  intx4 a0[4], b0[4], a1[4], b1[4];  // fragments of the even and the odd sub-steps
+  auto read = [&](const uint8_t *st, int s, intx4 (&af)[4], intx4 (&bf)[4]) {
+    const uint32_t pos = 16 * ((2 * s + h) ^ sw);
+#pragma unroll
+    for (int f = 0; f < 4; ++f) {
+      af[f] = *reinterpret_cast<const intx4 *>(st + rdA + 32 * kStep * f + pos);
+      bf[f] = *reinterpret_cast<const intx4 *>(st + rdB + 32 * kStep * f + pos);
+    }
+  };
+  auto multiply = [&](const intx4 (&af)[4], const intx4 (&bf)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(bf[j], af[i], acc[j][i], 0, 0, 0);
+  };
+  // clears the A fragments of K beyond the end
+  auto clear = [&](int32_t kt, int s, intx4 (&af)[4]) {
+    const bool in = static_cast<uint32_t>(kt) * kStep + 16 * (2 * s + h) < p.K;
+#pragma unroll
+    for (int f = 0; f < 4; ++f)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) af[f][e] = in ? af[f][e] : 0;
+  };
+  // an MFMA, then a fragment read, eight times, and eight MFMAs under which the reads land
+  auto order = [&]() {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+    }
+    __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
+  };
+
+  if (steps > 0) {
+    end_of_k(0);
+#pragma unroll
+    for (int q = 0; q < 16; ++q) load(smem, 0, q);
+    if (steps > 1) {
+      end_of_k(1);
+#pragma unroll
+      for (int q = 0; q < 16; ++q) load(smem + kBigStage, 1, q);
+      wait_vmcnt<16>();
+    } else {
+      wait_vmcnt<0>();
+    }
+    lds_barrier();
+    read(smem, 0, a0, b0);
+  }
+  // One step out of stage cur, whose sub-step 0 is in a0, b0; then cur takes the loads of step kt + 2.
+  auto step = [&](uint8_t *__restrict__ cur, const uint8_t *__restrict__ nxt, int32_t kt) {
+    end_of_k(kt + 2);
+    read(cur, 1, a1, b1);
+    multiply(a0, b0);
+    order();
+    read(cur, 2, a0, b0);
+    multiply(a1, b1);
+    order();
+    read(cur, 3, a1, b1);
+    multiply(a0, b0);
+    order();
+    wait_vmcnt<0>();
+    wait_lgkmcnt0();
+    lds_barrier();
+    read(nxt, 0, a0, b0);
+#pragma unroll
+    for (int q = 0; q < 16; ++q) load(cur, kt + 2, q);
+    multiply(a1, b1);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // a direct load
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    }
+  };
+  int32_t kt = 0;
+  uint32_t cur = 0;
+  for (; kt + 2 < steps; ++kt) {
+    step(smem + cur, smem + (cur ^ kBigStage), kt);
+    cur ^= kBigStage;
+  }
+  // the last two steps: nothing left to load
+  for (; kt < steps; ++kt) {
+    const uint8_t *const st = smem + cur;
+    read(st, 1, a1, b1);
+    clear(kt, 0, a0);
+    multiply(a0, b0);
+    read(st, 2, a0, b0);
+    clear(kt, 1, a1);
+    multiply(a1, b1);
+    read(st, 3, a1, b1);
+    clear(kt, 2, a0);
+    multiply(a0, b0);
+    wait_vmcnt<0>();
+    wait_lgkmcnt0();
+    lds_barrier();
+    cur ^= kBigStage;
+    if (kt + 1 < steps) read(smem + cur, 0, a0, b0);
+    clear(kt, 3, a1);
+    multiply(a1, b1);
+  }
+
+  // every wave is done with the stages
+  lds_barrier();
+  store_big_tile<OUT_BF16>(p, acc, smem + wave * 8192, t, n0, wm, wn, lane);
+}
+
+template <int TM, int TN>
+hipError_t run_tiles(const Int8GemmArgs &a, I8Args p, int64_t most, void (*bf16_kernel)(I8Args),
+                     void (*f32_kernel)(I8Args)) {
   p.tiles_n = static_cast<int32_t>((a.N + TN - 1) / TN);
   // by expert: every group may have one partial tile row
-  const int64_t most = (a.M + TM - 1) / TM + (a.offsets ? a.num_groups : 0);
-  const int64_t tiles = most * p.tiles_n;
+  const int64_t rows = (a.M + TM - 1) / TM + (a.offsets ? a.num_groups : 0);
+  p.tiles_m = static_cast<int32_t>(rows);
+  const int64_t tiles = (rows * p.tiles_n + 7) / 8 * 8;
   if (tiles > (int64_t(1) << 23)) return hipErrorInvalidValue;
-  p.tiles = static_cast<int32_t>(tiles);
-  const uint32_t grid = static_cast<uint32_t>(a.offsets ? (tiles + 7) / 8 * 8 : tiles);
-  if (a.c_dtype == 1)
-    gemm_int8_kernel<FM, FN, STAGES, true><<<dim3(grid), dim3(kThreads), 0, a.stream>>>(p);
-  else
-    gemm_int8_kernel<FM, FN, STAGES, false><<<dim3(grid), dim3(kThreads), 0, a.stream>>>(p);
+  const uint32_t grid = static_cast<uint32_t>(tiles < most ? tiles : most);
+  (a.c_dtype == 1 ? bf16_kernel : f32_kernel)<<<dim3(grid), dim3(kThreads), 0, a.stream>>>(p);
   return hipGetLastError();
 }
 
@@ -296,10 +589,14 @@ hipError_t launch_int8_gemm(const Int8GemmArgs &a) {
   p.rows = a.rows;
   p.row_div = a.row_div;
   const int64_t es = a.c_dtype == 1 ? 2 : 4;
-  p.vec_store = (reinterpret_cast<uintptr_t>(a.c) % (4 * es)) == 0 && a.ldc % 4 == 0;
   const int64_t rows_each = a.M / a.num_groups;
-  if (rows_each >= 256) return run_tiles<4, 4, 2>(a, p);
-  return run_tiles<1, 1, 4>(a, p);
+  if (rows_each >= 256 && a.K > kStep) {
+    p.vec_store = (reinterpret_cast<uintptr_t>(a.c) & 15u) == 0 && (a.ldc * es) % 16 == 0;
+    p.vec_scales = (reinterpret_cast<uintptr_t>(a.b_scales) & 15u) == 0 && a.N % 4 == 0;
+    return run_tiles<256, 256>(a, p, int64_t(1) << 23, gemm_int8_big_kernel<true>, gemm_int8_big_kernel<false>);
+  }
+  p.vec_store = (reinterpret_cast<uintptr_t>(a.c) % (4 * es)) == 0 && a.ldc % 4 == 0;
+  return run_tiles<64, 64>(a, p, int64_t(1) << 23, gemm_int8_kernel<1, 1, 4, true>, gemm_int8_kernel<1, 1, 4, false>);
 }
 
 }  // namespace nvfp4

@@ -331,6 +331,10 @@ int nvfp4_moe_combine_backward(const void *dout, int64_t ldo, const void *y, int
 int nvfp4_int8_quantize(const void *x, int dtype, int64_t rows, int64_t cols, int64_t ldx, int8_t *q, float *scales,
                         void *hip_stream);
 
+/* Bytes of device workspace with which the plain form of nvfp4_int8_gemm splits a long K of a product of few
+ * rows over more of the GPU (0: it would not).  Fully rewritten before it is read. */
+size_t nvfp4_int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
+
 /* Product of 8-bit integers with a scale for each token and each channel:
  *   C[i][j] = (a_scales[i] * b_scales[j]) * sum_k a[i][k] * b[j][k],
  * the sum exact in 32-bit integers, the scale product and its multiply in fp32, one rounding to a
@@ -345,10 +349,11 @@ int nvfp4_int8_quantize(const void *x, int dtype, int64_t rows, int64_t cols, in
  * its slots, without a gathered copy); rows outside a are read as row 0.  Without rows, M == a_rows.
  * K % 16 == 0 and K < 2^17 (so that no sum overflows); N * K < 2^32 and, with rows, a_rows * K < 2^32;
  * M < 2^31; num_groups 1 .. 512 (else NVFP4_ERR_SHAPE); a and b 16-byte aligned, the other arrays
- * aligned to their element size. */
+ * aligned to their element size.  workspace: nullable (the result is the same without it), device,
+ * nvfp4_int8_gemm_workspace_size() bytes, 16-byte aligned; calls that may overlap need distinct ones. */
 int nvfp4_int8_gemm(const int8_t *a, const float *a_scales, int64_t a_rows, const int8_t *b, const float *b_scales,
                     int64_t M, int64_t N, int64_t K, void *c, int c_dtype, int64_t ldc, int32_t num_groups,
-                    const int32_t *offsets, const int32_t *rows, int32_t row_div, void *hip_stream);
+                    const int32_t *offsets, const int32_t *rows, int32_t row_div, void *workspace, void *hip_stream);
 
 /* The norms between two blocks, with the block's gate and residual scale, in one pass over the rows:
  *   p = y * rstd_post * w_post,  rstd_post = 1 / sqrt(mean(y^2) + eps)   (w_post NULL: p = y)

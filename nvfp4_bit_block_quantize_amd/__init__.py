@@ -94,7 +94,8 @@ def lib():
                 ("nvfp4_moe_combine", i, [P, i, i64, i64, i64, P, P, i32, P, i64, P]),
                 ("nvfp4_moe_combine_backward", i, [P, i64, P, i64, i, i64, i64, P, P, P, i32, P, i64, P, P]),
                 ("nvfp4_int8_quantize", i, [P, i, i64, i64, i64, P, P, P]),
-                ("nvfp4_int8_gemm", i, [P, P, i64, P, P, i64, i64, i64, P, i, i64, i32, P, P, i32, P]),
+                ("nvfp4_int8_gemm_workspace_size", size, [i64, i64, i64]),
+                ("nvfp4_int8_gemm", i, [P, P, i64, P, P, i64, i64, i64, P, i, i64, i32, P, P, i32, P, P]),
                 ("nvfp4_block_norm", i, [P, i, P, i, i64, i64, P, P, P, f32, f32, u32, P, P, P, P, P]),
                 ("nvfp4_block_norm_workspace_size", size, [i64, i64]),
                 ("nvfp4_block_norm_backward", i,
@@ -567,7 +568,8 @@ def nvfp4_int8_quantize(x: torch.Tensor, out: Optional[Int8Tensor] = None) -> In
 
 
 def nvfp4_int8_gemm(a: Int8Tensor, b: Int8Tensor, out_dtype: torch.dtype = torch.bfloat16, plan: Optional[MoEPlan] = None,
-                    gather: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+                    gather: bool = False, out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """C = (a * scales) @ (b * scales)^T with exact integer sums.  With a plan: by expert, b holding one
     weight for each; a's rows are in the plan's order, or with gather=True a has one row a token and is
     read through the plan.  Rows of C that the plan gives no expert are not written."""
@@ -595,9 +597,13 @@ def nvfp4_int8_gemm(a: Int8Tensor, b: Int8Tensor, out_dtype: torch.dtype = torch
         out = torch.empty((M, b.rows), dtype=out_dtype, device=a.data.device)
     elif out.shape != (M, b.rows) or out.device != a.data.device:
         raise ValueError(f"{where}: out must be [{M}, {b.rows}] on {a.data.device}")
+    if workspace is None and plan is None:
+        size = lib().nvfp4_int8_gemm_workspace_size(M, b.rows, b.k)
+        if size:
+            workspace = torch.empty(size // 4, dtype=torch.int32, device=a.data.device)
     st = lib().nvfp4_int8_gemm(a.data.data_ptr(), a.scales.data_ptr(), a.rows, b.data.data_ptr(), b.scales.data_ptr(), M,
                                b.rows, b.k, out.data_ptr(), _dtype_code(out.dtype), max(_matrix(where, "out", out), 1),
-                               b.groups, offsets, rows, div, _raw_stream(a.data))
+                               b.groups, offsets, rows, div, _addr(workspace), _raw_stream(a.data))
     _check(st, where)
     return out
 

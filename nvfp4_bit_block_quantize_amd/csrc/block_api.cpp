@@ -264,9 +264,13 @@ int nvfp4_int8_quantize(const void *x, int dtype, int64_t rows, int64_t cols, in
   return status_of(nvfp4::launch_int8_quantize(a));
 }
 
+size_t nvfp4_int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K) {
+  return M < 1 || N < 1 || K < 1 || N >= kMaxSlots ? 0 : (nvfp4::int8_gemm_workspace_bytes(M, N, K) + 15) / 16 * 16;
+}
+
 int nvfp4_int8_gemm(const int8_t *a, const float *a_scales, int64_t a_rows, const int8_t *b, const float *b_scales,
                     int64_t M, int64_t N, int64_t K, void *c, int c_dtype, int64_t ldc, int32_t num_groups,
-                    const int32_t *offsets, const int32_t *rows, int32_t row_div, void *hip_stream) {
+                    const int32_t *offsets, const int32_t *rows, int32_t row_div, void *workspace, void *hip_stream) {
   const int es = dtype_size(c_dtype);
   if (es == 0) return NVFP4_ERR_UNSUPPORTED;
   if (M < 0 || N < 0 || K < 0 || a_rows < 0 || K % 16 != 0 || K >= (int64_t(1) << 17) || M >= kMaxSlots ||
@@ -278,7 +282,7 @@ int nvfp4_int8_gemm(const int8_t *a, const float *a_scales, int64_t a_rows, cons
   if (a_rows == 0) return NVFP4_ERR_SHAPE;
   if (!a_scales || !b_scales || !c || (K > 0 && (!a || !b))) return NVFP4_ERR_NULL;
   if (!aligned(a, 16) || !aligned(b, 16) || !aligned(a_scales, 4) || !aligned(b_scales, 4) || !aligned(c, es) ||
-      !aligned(offsets, 4) || !aligned(rows, 4))
+      !aligned(offsets, 4) || !aligned(rows, 4) || !aligned(workspace, 16))
     return NVFP4_ERR_ALIGN;
   nvfp4::Int8GemmArgs g{};
   g.a = a;
@@ -296,6 +300,7 @@ int nvfp4_int8_gemm(const int8_t *a, const float *a_scales, int64_t a_rows, cons
   g.offsets = offsets;
   g.rows = rows;
   g.row_div = row_div;
+  g.workspace = static_cast<int32_t *>(workspace);
   g.stream = stream_of(hip_stream);
   return status_of(nvfp4::launch_int8_gemm(g));
 }

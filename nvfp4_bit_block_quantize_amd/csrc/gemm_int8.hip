@@ -13,8 +13,6 @@
 // By expert.  The row offsets live on the device, so the launch has as many workgroups as any offsets
 // could need (a partial tile more for every expert), and each finds its tile by a scan over the experts'
 // tile counts; those beyond the last tile leave.  A's rows may be read through the plan's slots.
-#include <type_traits>
-
 #include "gemm_common.hpp"
 #include "nvfp4_internal.h"
 
@@ -44,7 +42,9 @@ struct I8Args {
   const int32_t *offsets;  // NULL: one group of M rows
   const int32_t *rows;     // NULL: row r of C is row r of A
   int32_t row_div;
-  int32_t vec_store, vec_scales;
+  int32_t splits, split_steps;  // few rows, plain form: K split over workgroups
+  int32_t *partial;             // [splits][M][partial_ld]
+  int64_t partial_ld;
 };
 
 // What A reads beyond K in the last step.
@@ -144,6 +144,128 @@ __device__ __forceinline__ bool find_tile(const I8Args &p, const Tiles &w, int32
   return true;
 }
 
+// 16 bytes at an address aligned to an element only (rows of C may start anywhere).
+struct __attribute__((packed, aligned(2))) Bytes16 {
+  uint32_t v[4];
+};
+struct __attribute__((packed, aligned(4))) Floats4 {
+  float v[4];
+};
+struct __attribute__((packed, aligned(2))) Bytes8 {
+  uint32_t v[2];
+};
+
+// Four consecutive values of a row of C, cut by N.
+template <bool OUT_BF16>
+__device__ __forceinline__ void store4(const I8Args &p, int64_t row, int64_t col, const float (&v)[4]) {
+  uint8_t *out = p.c + (row * p.ldc + col) * (OUT_BF16 ? 2 : 4);
+  if (col + 4 <= p.N) {
+    if constexpr (OUT_BF16) {
+      const bf16x2v lo = __builtin_convertvector((float2v){v[0], v[1]}, bf16x2v);
+      const bf16x2v hi = __builtin_convertvector((float2v){v[2], v[3]}, bf16x2v);
+      *reinterpret_cast<Bytes8 *>(out) = Bytes8{{__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi)}};
+    } else {
+      *reinterpret_cast<Floats4 *>(out) = Floats4{{v[0], v[1], v[2], v[3]}};
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (col + e < p.N) {
+        if constexpr (OUT_BF16)
+          reinterpret_cast<uint16_t *>(out)[e] = static_cast<uint16_t>(bf16_rne(v[e]));
+        else
+          reinterpret_cast<float *>(out)[e] = v[e];
+      }
+  }
+}
+
+// C of a wave's FM x FN fragments (32 x 32 each) at rows t.m0 + wm, columns n0 on, 32 rows and at most 256
+// bytes of a row at a time through the wave's own LDS (32 rows of kRowBytes): lane (h, l32) holds row l32 of
+// fragment (i, j), columns 8 q + 4 h + e; staged rows leave in 16-byte pieces of whole row segments, piece
+// c of row r staged at c ^ (r mod pieces).  The columns' scales take the region's last 512 bytes.  No other
+// wave may still read the region.
+constexpr uint32_t kRegion = 8192 + 512;
+template <int FM, int FN, bool OUT_BF16>
+__device__ __forceinline__ void store_tile(const I8Args &p, const intx16 (&acc)[FN][FM], uint8_t *region, const TileRows &t,
+                                           int64_t n0, uint32_t wm, uint32_t lane) {
+  constexpr int ES = OUT_BF16 ? 2 : 4, V = 16 / ES;          // element size, elements of a piece
+  constexpr int JP = FN * 32 * ES > 256 ? 256 / (32 * ES) : FN;  // fragments a pass
+  constexpr uint32_t kRowBytes = JP * 32 * ES, NP = kRowBytes / 16;
+  // (an opaque copy: the per-lane addresses are formed here and not held through the products)
+  asm volatile("" : "+v"(lane));
+  const uint32_t h = lane >> 5, l32 = lane & 31u;
+  const float *sb = p.b_scales + static_cast<int64_t>(t.group) * p.N;
+  float s[FN][4][4], sa[FM];
+  float *const staged = reinterpret_cast<float *>(region + 8192);
+#pragma unroll
+  for (uint32_t c = 0; c < 32 * FN; c += 64)
+    if (c + lane < 32 * FN) staged[c + lane] = sb[min(n0 + c + lane, p.N - 1)];
+#pragma unroll
+  for (int i = 0; i < FM; ++i) sa[i] = p.a_scales[a_row(p, min(t.m0 + wm + 32 * i + l32, t.m_end - 1))];
+#pragma unroll
+  for (int j = 0; j < FN; ++j)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const float4 v = *reinterpret_cast<const float4 *>(staged + 32 * j + 8 * q + 4 * h);
+      s[j][q][0] = v.x;
+      s[j][q][1] = v.y;
+      s[j][q][2] = v.z;
+      s[j][q][3] = v.w;
+    }
+  const int64_t rows_left = t.m_end - (t.m0 + wm), cols_left = p.N - n0;
+  uint8_t *const out = p.c + ((t.m0 + wm) * p.ldc + n0) * ES;
+#pragma unroll
+  for (int i = 0; i < FM; ++i) {
+    if (32 * i >= rows_left) break;  // (the same in every lane)
+#pragma unroll
+    for (int j0 = 0; j0 < FN; j0 += JP) {
+#pragma unroll
+      for (int jj = 0; jj < JP; ++jj)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int j = j0 + jj;
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = static_cast<float>(acc[j][i][4 * q + e]) * (sa[i] * s[j][q][e]);
+          if constexpr (OUT_BF16) {
+            const bf16x2v lo = __builtin_convertvector((float2v){v[0], v[1]}, bf16x2v);
+            const bf16x2v hi = __builtin_convertvector((float2v){v[2], v[3]}, bf16x2v);
+            *reinterpret_cast<uint2 *>(region + l32 * kRowBytes + (((4 * jj + q) ^ (l32 & (NP - 1))) * 16 + 8 * h)) =
+                make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+          } else {
+            *reinterpret_cast<float4 *>(region + l32 * kRowBytes + ((8 * jj + 2 * q + h) ^ (l32 & (NP - 1))) * 16) =
+                make_float4(v[0], v[1], v[2], v[3]);
+          }
+        }
+      // the wave reads back its own rows (LDS accesses of one wave complete in order)
+#pragma unroll
+      for (uint32_t u = 0; u < 32 * NP / 64; ++u) {
+        const uint32_t row = u * (64 / NP) + lane / NP, c = lane % NP;
+        const uint4 v = *reinterpret_cast<const uint4 *>(region + row * kRowBytes + ((c ^ (row & (NP - 1))) * 16));
+        const int64_t col = j0 * 32 + c * V;
+        if (32 * i + row >= rows_left || col >= cols_left) continue;
+        uint8_t *at = out + ((32 * i + row) * p.ldc + col) * ES;
+        if (col + V <= cols_left) {
+          *reinterpret_cast<Bytes16 *>(at) = Bytes16{{v.x, v.y, v.z, v.w}};
+        } else {
+          // (a loop, to keep this rare path's code short)
+          uint64_t lo = v.x | static_cast<uint64_t>(v.y) << 32, hi = v.z | static_cast<uint64_t>(v.w) << 32;
+#pragma clang loop unroll(disable)
+          for (int64_t e = col; e < cols_left; ++e) {
+            if constexpr (OUT_BF16)
+              *reinterpret_cast<uint16_t *>(at) = static_cast<uint16_t>(lo);
+            else
+              *reinterpret_cast<uint32_t *>(at) = static_cast<uint32_t>(lo);
+            at += ES;
+            lo = lo >> (8 * ES) | hi << (64 - 8 * ES);
+            hi >>= 8 * ES;
+          }
+        }
+      }
+    }
+  }
+}
+
 template <int FM, int FN, int STAGES, bool OUT_BF16>
 __global__ __launch_bounds__(kThreads, 1) void gemm_int8_kernel(I8Args p) {
   constexpr int TM = 64 * FM, TN = 64 * FN;  // the workgroup's tile; a wave has 32 FM x 32 FN
@@ -221,61 +343,31 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_int8_kernel(I8Args p) {
     const int nxt = cur == 0 ? STAGES - 1 : cur - 1;
     if (kt + kAhead < steps) load(smem + nxt * kStage, kt + kAhead);
     const uint8_t *st = smem + cur * kStage;
+    // all of the step's fragment reads go out before its first MFMA, which then waits for its own alone
+    intx4 af[4][FM], bf[4][FN];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       const uint32_t pos = 16 * ((2 * s + h) ^ sw);
-      intx4 af[FM], bf[FN];
 #pragma unroll
-      for (int i = 0; i < FM; ++i) af[i] = *reinterpret_cast<const intx4 *>(st + rdA + 4096 * i + pos);
+      for (int i = 0; i < FM; ++i) af[s][i] = *reinterpret_cast<const intx4 *>(st + rdA + 4096 * i + pos);
 #pragma unroll
-      for (int j = 0; j < FN; ++j) bf[j] = *reinterpret_cast<const intx4 *>(st + rdB + 4096 * j + pos);
+      for (int j = 0; j < FN; ++j) bf[s][j] = *reinterpret_cast<const intx4 *>(st + rdB + 4096 * j + pos);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
 #pragma unroll
       for (int j = 0; j < FN; ++j)
 #pragma unroll
-        for (int i = 0; i < FM; ++i) acc[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(bf[j], af[i], acc[j][i], 0, 0, 0);
-    }
+        for (int i = 0; i < FM; ++i)
+          acc[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(bf[s][j], af[s][i], acc[j][i], 0, 0, 0);
     cur = cur + 1 == STAGES ? 0 : cur + 1;
   }
 
-  // ---- epilogue: lane (h, l32) holds row l32 of tile (i, j), columns 8 (r >> 2) + 4 h + (r & 3)
-  const float *sb = p.b_scales + static_cast<int64_t>(t.group) * p.N;
-#pragma unroll
-  for (int i = 0; i < FM; ++i) {
-    const int64_t row = t.m0 + wm + 32 * i + l32;
-    if (row >= t.m_end) continue;
-    const float sa = p.a_scales[a_row(p, row)];
-#pragma unroll
-    for (int j = 0; j < FN; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t col = n0 + wn + 32 * j + 8 * q + 4 * h;
-        if (col >= p.N) continue;
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          v[e] = static_cast<float>(acc[j][i][4 * q + e]) * (sa * sb[min(col + e, p.N - 1)]);
-        uint8_t *out = p.c + (row * p.ldc + col) * (OUT_BF16 ? 2 : 4);
-        if (p.vec_store && col + 4 <= p.N) {
-          if constexpr (OUT_BF16) {
-            const bf16x2v lo = __builtin_convertvector((float2v){v[0], v[1]}, bf16x2v);
-            const bf16x2v hi = __builtin_convertvector((float2v){v[2], v[3]}, bf16x2v);
-            *reinterpret_cast<uint2 *>(out) =
-                make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
-          } else {
-            *reinterpret_cast<float4 *>(out) = make_float4(v[0], v[1], v[2], v[3]);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (col + e < p.N) {
-              if constexpr (OUT_BF16)
-                reinterpret_cast<uint16_t *>(out)[e] = static_cast<uint16_t>(bf16_rne(v[e]));
-              else
-                reinterpret_cast<float *>(out)[e] = v[e];
-            }
-        }
-      }
-  }
+  // every wave is done with the stages
+  wait_lgkmcnt0();
+  lds_barrier();
+  store_tile<FM, FN, OUT_BF16>(p, acc, smem + wave * kRegion, t, n0 + wn, wm, lane);
 }
 
 // Buffer descriptor over the bytes from p on (raw 32-bit data format, no limit below 4 GiB).
@@ -300,95 +392,6 @@ __device__ __forceinline__ void lds_buffer16(__amdgpu_buffer_rsrc_t rs, uint32_t
 // behind it the stage takes the loads of the step after next, and the next stage, whose loads this
 // wave has waited for, is read.
 constexpr int kBigB = 256 * kStep, kBigStage = 512 * kStep;
-
-// C of a wave's quarter of a tile, 32 rows and (in fp32) 64 columns at a time through 8 KB of the wave's own LDS:
-// lane (h, l32) holds row l32 of tile (i, j), columns 8 q + 4 h + e; staged rows leave as whole 256-byte
-// segments, 16-byte chunk c of row r at c ^ (r mod 16).  Tiles cut by N, or C without 16-byte aligned rows,
-// take element stores.  Waits for this wave's loads in flight.
-template <bool OUT_BF16>
-__device__ __forceinline__ void store_big_tile(const I8Args &p, const intx16 (&acc)[4][4], uint8_t *region, const TileRows &t,
-                                               int64_t n0, uint32_t wm, uint32_t wn, uint32_t lane) {
-  constexpr int64_t ES = OUT_BF16 ? 2 : 4;
-  // (an opaque copy: the per-lane addresses are formed here and not carried through the tile loop)
-  asm volatile("" : "+v"(lane));
-  const uint32_t h = lane >> 5, l32 = lane & 31u;
-  const float *sb = p.b_scales + static_cast<int64_t>(t.group) * p.N;
-  const bool whole = n0 + 256 <= p.N;
-  float s[4][4][4], sa[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int64_t col = n0 + wn + 32 * j + 8 * q + 4 * h;
-      if (p.vec_scales && whole) {
-        const float4 v = *reinterpret_cast<const float4 *>(sb + col);
-        s[j][q][0] = v.x;
-        s[j][q][1] = v.y;
-        s[j][q][2] = v.z;
-        s[j][q][3] = v.w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[j][q][e] = sb[min(col + e, p.N - 1)];
-      }
-    }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) sa[i] = p.a_scales[a_row(p, min(t.m0 + wm + 32 * i + l32, t.m_end - 1))];
-  wait_vmcnt<0>();
-  const int64_t rows_left = t.m_end - (t.m0 + wm);
-  uint8_t *const out = p.c + ((t.m0 + wm) * p.ldc + n0 + wn) * ES;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    if (32 * i >= rows_left) break;  // (the same in every lane)
-    if (p.vec_store && whole) {
-      constexpr int JP = OUT_BF16 ? 4 : 2;  // B fragments a pass: 256 bytes a row
-#pragma unroll
-      for (int j0 = 0; j0 < 4; j0 += JP) {
-#pragma unroll
-        for (int jj = 0; jj < JP; ++jj)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int j = j0 + jj;
-            float v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = static_cast<float>(acc[j][i][4 * q + e]) * (sa[i] * s[j][q][e]);
-            if constexpr (OUT_BF16) {
-              const bf16x2v lo = __builtin_convertvector((float2v){v[0], v[1]}, bf16x2v);
-              const bf16x2v hi = __builtin_convertvector((float2v){v[2], v[3]}, bf16x2v);
-              *reinterpret_cast<uint2 *>(region + l32 * 256 + (((4 * jj + q) ^ (l32 & 15)) * 16 + 8 * h)) =
-                  make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
-            } else {
-              *reinterpret_cast<float4 *>(region + l32 * 256 + ((8 * jj + 2 * q + h) ^ (l32 & 15)) * 16) =
-                  make_float4(v[0], v[1], v[2], v[3]);
-            }
-          }
-        // the wave reads back its own rows (LDS accesses of one wave complete in order)
-#pragma unroll
-        for (uint32_t u = 0; u < 8; ++u) {
-          const uint32_t row = 4 * u + (lane >> 4), c = lane & 15u;
-          const uint4 v = *reinterpret_cast<const uint4 *>(region + row * 256 + ((c ^ (row & 15)) * 16));
-          if (32 * i + row < rows_left)
-            *reinterpret_cast<uint4 *>(out + (32 * i + row) * p.ldc * ES + j0 * 32 * ES + c * 16) = v;
-        }
-      }
-    } else if (32 * i + l32 < rows_left) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t col = 32 * j + 8 * q + 4 * h + e;
-            if (n0 + wn + col >= p.N) continue;
-            const float v = static_cast<float>(acc[j][i][4 * q + e]) * (sa[i] * s[j][q][e]);
-            uint8_t *at = out + ((32 * i + l32) * p.ldc + col) * ES;
-            if constexpr (OUT_BF16)
-              *reinterpret_cast<uint16_t *>(at) = static_cast<uint16_t>(bf16_rne(v));
-            else
-              *reinterpret_cast<float *>(at) = v;
-          }
-    }
-  }
-}
 
 template <bool OUT_BF16>
 __global__ __launch_bounds__(kThreads, 1) void gemm_int8_big_kernel(I8Args p) {
@@ -526,11 +529,13 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_int8_big_kernel(I8Args p) {
   };
   int32_t kt = 0;
   uint32_t cur = 0;
+#pragma clang loop unroll(disable)
   for (; kt + 2 < steps; ++kt) {
     step(smem + cur, smem + (cur ^ kBigStage), kt);
     cur ^= kBigStage;
   }
   // the last two steps: nothing left to load
+#pragma clang loop unroll(disable)
   for (; kt < steps; ++kt) {
     const uint8_t *const st = smem + cur;
     read(st, 1, a1, b1);
@@ -552,22 +557,207 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_int8_big_kernel(I8Args p) {
   }
 
   // every wave is done with the stages
+  wait_lgkmcnt0();
   lds_barrier();
-  store_big_tile<OUT_BF16>(p, acc, smem + wave * 8192, t, n0, wm, wn, lane);
+  store_tile<4, 4, OUT_BF16>(p, acc, smem + wave * kRegion, t, n0 + wn, wm, lane);
 }
 
+// ---- few rows: weight streaming -------------------------------------------------------------------------
+// With few rows the product is bound by reading the weight once.  A workgroup owns 64 weight rows and
+// 16 MT rows of its expert: both pass through a deep LDS ring of whole 128-byte lines (direct loads, so
+// that the bytes in flight cost no registers), wave w multiplying weight rows [16 w, 16 w + 16) by all rows
+// (v_mfma_i32_16x16x64_i8; lane l: row l mod 16, bytes 16 (l / 16) of every 64).  Where that leaves compute
+// units without work (the plain form), the steps of K are split over grid.z, each split's integer sums go to the
+// workspace, and a second kernel adds and scales them.
+template <int MT>
+struct Few {
+  static constexpr int kRows = 16 * MT;
+  static constexpr int kA = MT < 2 ? 1 : MT / 2;  // direct loads of A a wave and step (MT 1: two waves load the same)
+  static constexpr int kLoads = kA + 2;
+  static constexpr int kB = kRows * kStep, kStage = (kRows + 64) * kStep;
+  static constexpr int kStages = MT <= 2 ? 6 : MT == 4 ? 5 : 6;  // MT <= 4: two workgroups share a compute unit's LDS
+};
+
+template <int MT, bool OUT_BF16>
+__global__ __launch_bounds__(kThreads) void gemm_int8_few_kernel(I8Args p) {
+  using F = Few<MT>;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[F::kStages * F::kStage];
+  const uint32_t lane = threadIdx.x & 63u;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t r16 = lane & 15u, g = lane >> 4;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 64;
+  const int32_t group = p.offsets ? blockIdx.z : 0;
+  int64_t m0 = static_cast<int64_t>(blockIdx.y) * F::kRows, m_end = p.M;
+  if (p.offsets) {
+    const int64_t lo = p.offsets[group], hi = p.offsets[group + 1];
+    m0 += lo;
+    m_end = min(hi, p.M);
+    if (lo < 0 || m0 >= m_end) return;
+  }
+  // this split's steps
+  const int32_t all = static_cast<int32_t>((p.K + kStep - 1) / kStep);
+  const int32_t kt0 = p.splits > 1 ? static_cast<int32_t>(blockIdx.z) * p.split_steps : 0;
+  const int32_t steps = p.splits > 1 ? min(p.split_steps, all - kt0) : all;
+
+  const uint8_t *srcA[F::kA], *srcB[2];
+  uint32_t chunkA[F::kA], chunkB[2], dstA[F::kA];
+#pragma unroll
+  for (int i = 0; i < F::kA; ++i) {
+    const uint32_t R0 = (8 * (F::kA * wave + i)) % F::kRows, R = R0 + (lane >> 3);
+    dstA[i] = R0 * kStep;
+    chunkA[i] = ((lane & 7u) ^ swz(R)) * 16;
+    srcA[i] = p.a + a_row(p, min(m0 + R, m_end - 1)) * p.K;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t R = 16 * wave + 8 * i + (lane >> 3);
+    chunkB[i] = ((lane & 7u) ^ swz(R)) * 16;
+    srcB[i] = p.b + (static_cast<int64_t>(group) * p.N + min(n0 + R, p.N - 1)) * p.K;
+  }
+  auto load = [&](uint8_t *st, int32_t kt) {
+    const uint32_t k0 = static_cast<uint32_t>(kt0 + kt) * kStep;
+    const bool whole = k0 + kStep <= p.K;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      lds_load16(srcB[i] + (whole || k0 + chunkB[i] < p.K ? k0 + chunkB[i] : 0), st + F::kB + (16 * wave + 8 * i) * kStep);
+#pragma unroll
+    for (int i = 0; i < F::kA; ++i)
+      lds_load16(whole || k0 + chunkA[i] < p.K ? srcA[i] + (k0 + chunkA[i]) : reinterpret_cast<const uint8_t *>(&kZeros),
+                 st + dstA[i]);
+  };
+  intx4 acc[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i] = (intx4){0, 0, 0, 0};
+  constexpr int kAhead = F::kStages - 1;
+  for (int s = 0; s < kAhead && s < steps; ++s) load(smem + s * F::kStage, s);
+  const uint32_t rdA = r16 * kStep, rdB = F::kB + (16 * wave + r16) * kStep, sw = swz(r16);
+  int cur = 0;
+  for (int32_t kt = 0; kt < steps; ++kt) {
+    // this wave's loads of step kt have landed; after the barrier everyone's have, and the stage of
+    // step kt - 1 is free
+    if (kt + kAhead <= steps)
+      wait_vmcnt<(kAhead - 1) * F::kLoads>();
+    else
+      wait_vmcnt<0>();
+    wait_lgkmcnt0();
+    lds_barrier();
+    const int nxt = cur == 0 ? F::kStages - 1 : cur - 1;
+    if (kt + kAhead < steps) load(smem + nxt * F::kStage, kt + kAhead);
+    const uint8_t *st = smem + cur * F::kStage;
+    intx4 w[2], a[2][MT];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const uint32_t pos = 16 * ((4 * s + g) ^ sw);
+      w[s] = *reinterpret_cast<const intx4 *>(st + rdB + pos);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) a[s][i] = *reinterpret_cast<const intx4 *>(st + rdA + 16 * kStep * i + pos);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < 2; ++s)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[s], a[s][i], acc[i], 0, 0, 0);
+    cur = cur + 1 == F::kStages ? 0 : cur + 1;
+  }
+  // lane (r16, g) of tile i holds row 16 i + r16, columns 4 g + e
+  const int64_t col = n0 + 16 * wave + 4 * g;
+  if (col >= p.N) return;
+  const float *sb = p.b_scales + static_cast<int64_t>(group) * p.N;
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int64_t row = m0 + 16 * i + r16;
+    if (row >= m_end) continue;
+    if (p.splits > 1) {
+      // (the workspace's rows are padded to 64 columns)
+      *reinterpret_cast<intx4 *>(p.partial + (static_cast<int64_t>(blockIdx.z) * p.M + row) * p.partial_ld + col) = acc[i];
+      continue;
+    }
+    const float sa = p.a_scales[a_row(p, row)];
+    float v[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = static_cast<float>(acc[i][e]) * (sa * sb[min(col + e, p.N - 1)]);
+    store4<OUT_BF16>(p, row, col, v);
+  }
+}
+
+// C from the splits' sums: four columns a lane.
+template <bool OUT_BF16>
+__global__ __launch_bounds__(kThreads) void int8_sum_kernel(I8Args p) {
+  const int64_t u = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, per_row = p.partial_ld / 4;
+  const int64_t row = u / per_row, col = u % per_row * 4;
+  if (row >= p.M || col >= p.N) return;
+  intx4 t = {0, 0, 0, 0};
+#pragma unroll 4
+  for (int s = 0; s < p.splits; ++s)
+    t += *reinterpret_cast<const intx4 *>(p.partial + (s * p.M + row) * p.partial_ld + col);
+  const float sa = p.a_scales[row];
+  float v[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = static_cast<float>(t[e]) * (sa * p.b_scales[min(col + e, p.N - 1)]);
+  store4<OUT_BF16>(p, row, col, v);
+}
+
+constexpr int64_t kMaxTiles = int64_t(1) << 23;  // workgroups of a launch
+
 template <int TM, int TN>
-hipError_t run_tiles(const Int8GemmArgs &a, I8Args p, int64_t most, void (*bf16_kernel)(I8Args),
-                     void (*f32_kernel)(I8Args)) {
+hipError_t run_tiles(const Int8GemmArgs &a, I8Args p, void (*bf16_kernel)(I8Args), void (*f32_kernel)(I8Args)) {
   p.tiles_n = static_cast<int32_t>((a.N + TN - 1) / TN);
   // by expert: every group may have one partial tile row
   const int64_t rows = (a.M + TM - 1) / TM + (a.offsets ? a.num_groups : 0);
   p.tiles_m = static_cast<int32_t>(rows);
   const int64_t tiles = (rows * p.tiles_n + 7) / 8 * 8;
-  if (tiles > (int64_t(1) << 23)) return hipErrorInvalidValue;
-  const uint32_t grid = static_cast<uint32_t>(tiles < most ? tiles : most);
-  (a.c_dtype == 1 ? bf16_kernel : f32_kernel)<<<dim3(grid), dim3(kThreads), 0, a.stream>>>(p);
+  if (tiles > kMaxTiles) return hipErrorInvalidValue;
+  (a.c_dtype == 1 ? bf16_kernel : f32_kernel)<<<dim3(static_cast<uint32_t>(tiles)), dim3(kThreads), 0, a.stream>>>(p);
   return hipGetLastError();
+}
+
+// The tile for these sizes: 256 (256 x 256), 128 (128 x 128 in two stages, two workgroups a compute unit),
+// 129 (128 x 128 in four stages, one workgroup a compute unit) or 64 (64 x 64).  The estimates are lines
+// through measured times in us (fixed costs, and a time for every step of 128 bytes of K and every 256 tiles,
+// e.g. 8192 x 4096 x 4096: 123 / 152 / 191 / 236; 1024 x 4096 x 14336: 160 / 103 / 81 / 117; 512 x 4096 x
+// 4096: 48 / 27 / 24 / 18), within about a fifth of the measured times over such sizes.
+int pick_tile(const Int8GemmArgs &a) {
+  const double steps = static_cast<double>((a.K + kStep - 1) / kStep);
+  const auto tiles = [&](int64_t t) {
+    const int64_t rows = (a.M + t - 1) / t + (a.offsets ? a.num_groups / 2 : 0);
+    return rows * ((a.N + t - 1) / t);
+  };
+  const auto rounds = [](int64_t t) { return static_cast<double>((t + 255) / 256); };
+  const double t64 = rounds(tiles(64)) * (0.21 * steps + 0.5) + 3.5;
+  const bool one = tiles(128) <= 256;
+  const double t128 = one ? 0.65 * steps + 4 : rounds(tiles(128)) * (0.5 * steps + 2) + 3;
+  const double t256 = rounds(tiles(256)) * (1.2 * steps + 6) + 6;
+  // (a launch's tiles are bounded; larger tiles are fewer)
+  const bool large = tiles(64) + (a.num_groups + 1) * ((a.N + 63) / 64) > kMaxTiles;
+  if (large || (t256 < t128 && t256 < t64)) return 256;
+  return t128 < t64 ? (one ? 129 : 128) : 64;
+}
+
+template <int MT>
+hipError_t run_few(const Int8GemmArgs &a, const I8Args &p, int64_t most) {
+  const uint32_t tiles_n = static_cast<uint32_t>((a.N + 63) / 64), rows = static_cast<uint32_t>((most + 16 * MT - 1) / (16 * MT));
+  const dim3 grid(tiles_n, rows, a.offsets ? a.num_groups : p.splits);
+  if (a.c_dtype == 1)
+    gemm_int8_few_kernel<MT, true><<<grid, dim3(kThreads), 0, a.stream>>>(p);
+  else
+    gemm_int8_few_kernel<MT, false><<<grid, dim3(kThreads), 0, a.stream>>>(p);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.splits == 1) return e;
+  const dim3 sums(static_cast<uint32_t>((a.M * p.partial_ld / 4 + kThreads - 1) / kThreads));
+  if (a.c_dtype == 1)
+    int8_sum_kernel<true><<<sums, dim3(kThreads), 0, a.stream>>>(p);
+  else
+    int8_sum_kernel<false><<<sums, dim3(kThreads), 0, a.stream>>>(p);
+  return hipGetLastError();
+}
+
+// Splits of K of the few-row kernel: towards one workgroup a compute unit, at least eight steps each, and only
+// where the steps saved (0.28 us each) are worth the second kernel (3 us).
+int few_splits(int64_t M, int64_t N, int64_t K) {
+  const int64_t steps = (K + kStep - 1) / kStep, tiles = (N + 63) / 64;
+  if (M > 128 || steps < 24 || tiles > 128) return 1;
+  const int64_t s = 256 / tiles, most = steps / 8;
+  return static_cast<int>(s < most ? s : most);
 }
 
 }  // namespace
@@ -588,15 +778,32 @@ hipError_t launch_int8_gemm(const Int8GemmArgs &a) {
   p.offsets = a.offsets;
   p.rows = a.rows;
   p.row_div = a.row_div;
-  const int64_t es = a.c_dtype == 1 ? 2 : 4;
-  const int64_t rows_each = a.M / a.num_groups;
-  if (rows_each >= 256 && a.K > kStep) {
-    p.vec_store = (reinterpret_cast<uintptr_t>(a.c) & 15u) == 0 && (a.ldc * es) % 16 == 0;
-    p.vec_scales = (reinterpret_cast<uintptr_t>(a.b_scales) & 15u) == 0 && a.N % 4 == 0;
-    return run_tiles<256, 256>(a, p, int64_t(1) << 23, gemm_int8_big_kernel<true>, gemm_int8_big_kernel<false>);
+  // rows an expert can have
+  const int64_t most = a.rows && a.a_rows < a.M ? a.a_rows : a.M;
+  const int splits = !a.offsets && a.workspace ? few_splits(a.M, a.N, a.K) : 1;
+  // (from 65 to 128 rows the few-row kernel pays only where it splits K: 100 x 4096 x 14336 24.5 us against 36
+  // in 64 x 64 tiles, but 100 x 1000 x 1008 9.2 against 5.8)
+  if (most <= 64 || splits > 1) {
+    const int steps = static_cast<int>((a.K + kStep - 1) / kStep);
+    p.split_steps = (steps + splits - 1) / splits;
+    p.splits = steps > 0 ? (steps + p.split_steps - 1) / p.split_steps : 1;
+    p.partial = a.workspace;
+    p.partial_ld = (a.N + 63) / 64 * 64;
+    if (most <= 16) return run_few<1>(a, p, most);
+    if (most <= 32) return run_few<2>(a, p, most);
+    if (most <= 64) return run_few<4>(a, p, most);
+    return run_few<8>(a, p, most);
   }
-  p.vec_store = (reinterpret_cast<uintptr_t>(a.c) % (4 * es)) == 0 && a.ldc % 4 == 0;
-  return run_tiles<64, 64>(a, p, int64_t(1) << 23, gemm_int8_kernel<1, 1, 4, true>, gemm_int8_kernel<1, 1, 4, false>);
+  const int tile = pick_tile(a);
+  if (tile == 256) return run_tiles<256, 256>(a, p, gemm_int8_big_kernel<true>, gemm_int8_big_kernel<false>);
+  if (tile == 129) return run_tiles<128, 128>(a, p, gemm_int8_kernel<2, 2, 4, true>, gemm_int8_kernel<2, 2, 4, false>);
+  if (tile == 128) return run_tiles<128, 128>(a, p, gemm_int8_kernel<2, 2, 2, true>, gemm_int8_kernel<2, 2, 2, false>);
+  return run_tiles<64, 64>(a, p, gemm_int8_kernel<1, 1, 4, true>, gemm_int8_kernel<1, 1, 4, false>);
+}
+
+size_t int8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  const int splits = few_splits(M, N, K);
+  return splits > 1 ? static_cast<size_t>(splits) * M * ((N + 63) / 64 * 64) * sizeof(int32_t) : 0;
 }
 
 }  // namespace nvfp4

@@ -154,6 +154,7 @@ struct Int8GemmArgs {
   int32_t num_groups;
   const int32_t *offsets, *rows;  // device
   int32_t row_div;
+  int32_t *workspace;  // int8_gemm_workspace_bytes() of the plain form (nullptr: none)
   hipStream_t stream;
 };
 
@@ -186,6 +187,7 @@ hipError_t launch_moe_combine(const MoeRowsArgs &a);
 hipError_t launch_moe_combine_backward(const MoeRowsArgs &a);
 hipError_t launch_int8_quantize(const Int8QuantArgs &a);
 hipError_t launch_int8_gemm(const Int8GemmArgs &a);
+size_t int8_gemm_workspace_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_block_norm(const BlockNormArgs &a);
 hipError_t launch_block_norm_backward(const BlockNormArgs &a);
 size_t block_norm_workspace_bytes(int64_t tokens, int64_t d);

@@ -88,7 +88,7 @@ def test_rows(name, args, changes, status):
 
 QUANT = dict(x=P, dtype=nv.NVFP4_BF16, rows=8, cols=64, ldx=64, q=P, scales=P, stream=None)
 GEMM = dict(a=P, a_scales=P, a_rows=8, b=P, b_scales=P, M=8, N=64, K=64, c=P, c_dtype=nv.NVFP4_BF16, ldc=64, num_groups=1,
-            offsets=None, rows=None, row_div=1, stream=None)
+            offsets=None, rows=None, row_div=1, workspace=None, stream=None)
 
 
 @pytest.mark.parametrize("changes,status", [

@@ -3,7 +3,8 @@
 //   p = y r_y w_post,  x' = x + alpha g p,  n = x' r_x w_pre,  r_v = 1 / sqrt(mean(v^2) + eps)
 //
 // HBM-bound: a row of x and y is read once and stays in registers through both sums; x', n and the
-// gradients are written once.  A row belongs to a wave (up to 1024 columns), to 256 or to 512 threads.
+// gradients are written once.  A row belongs to a workgroup of 64 to 512 threads with one
+// 8-column piece each (two above 4096 columns, four above 8192).
 //
 // Gradients, with yh = y r_y, xh = x' r_x, d = dL/dx' through both uses of x':
 //   d  = dx' + r_x (w_pre dn - xh mean(w_pre dn xh)),          dx = d
@@ -35,132 +36,144 @@ struct NormArgs {
   float *parts;  // [2][parts][d]
 };
 
-// Sum over the T threads of a row (T == 64: a wave; else the workgroup, through `part`, which must not
-// be in use by an earlier sum).
-template <int T>
-__device__ __forceinline__ float row_total(float v, float *part) {
-  v = wave_sum(v);
+// Sums over the workgroup's T threads (one row), in one fixed order.  `part` must not be in use by earlier sums.
+template <int T, int N>
+__device__ __forceinline__ void row_totals(float (&v)[N], float (*part)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
   if constexpr (T > 64) {
-    if ((threadIdx.x & 63u) == 0) part[threadIdx.x >> 6] = v;
+    if ((threadIdx.x & 63u) == 0)
+#pragma unroll
+      for (int i = 0; i < N; ++i) part[threadIdx.x >> 6][i] = v[i];
     __syncthreads();
-    v = 0.0f;
 #pragma unroll
-    for (int w = 0; w < T / 64; w += 4) v += (part[w] + part[w + 1]) + (part[w + 2] + part[w + 3]);
-  }
-  return v;
-}
-
-__device__ __forceinline__ void load_factors(const float *w, int c, float shift, float (&f)[8]) {
-  unpack8<false>(load8<false>(w, 8ll * c), f);
+    for (int i = 0; i < N; ++i) {
+      v[i] = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) f[i] += shift;
-}
-
-// Factors of a lane's columns, loaded at once where they fit in registers (EARLY: their latency then
-// hides behind the row's own loads) or when they are used.
-template <int T, int NV, bool EARLY>
-struct Factors {
-  float v[EARLY ? NV : 1][8];
-  const float *p;
-  float shift;
-  __device__ __forceinline__ Factors(const float *w, float s, int pieces) : p(w), shift(s) {
-    if constexpr (EARLY) {
-      const int tid = threadIdx.x % T;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (p && tid + T * i < pieces) load_factors(p, tid + T * i, shift, v[i]);
+      for (int w = 0; w < T / 64; w += 2) v[i] += part[w][i] + part[w + 1][i];
     }
   }
-  __device__ __forceinline__ void get(int i, int c, float (&f)[8]) const {
-    if constexpr (EARLY) {
+}
+
+// Factors of a lane's columns: in registers for the whole call (EARLY, one piece a lane) or loaded at each use.
+template <int T, int NV>
+struct Factors {
+  static constexpr bool kEarly = NV == 1;
+  float v[8];
+  const float *p;
+  float shift;
+  __device__ __forceinline__ void load(int c, float (&f)[8]) const {
+    unpack8<false>(load8<false>(p, 8ll * c), f);
 #pragma unroll
-      for (int q = 0; q < 8; ++q) f[q] = v[i][q];
+    for (int i = 0; i < 8; ++i) f[i] += shift;
+  }
+  __device__ __forceinline__ Factors(const float *w, float s, int pieces) : p(w), shift(s) {
+    if constexpr (kEarly)
+      if (p && static_cast<int>(threadIdx.x) < pieces) load(threadIdx.x, v);
+  }
+  __device__ __forceinline__ void get(int c, float (&f)[8]) const {
+    if constexpr (kEarly) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) f[q] = v[q];
     } else {
-      load_factors(p, c, shift, f);
+      load(c, f);
     }
   }
 };
 
+// y (a piece of the block's output) to its share of x' - x without alpha: gate (y r_post w_post); yh: y r_post.
+template <bool YB, class F>
+__device__ __forceinline__ void block_output(const NormArgs &p, const F &w_post, const F &gate, const Raw8<YB> &gr, int c,
+                                             float r_post, float (&y)[8]) {
+  float f[8];
+  if (p.w_post) {
+    w_post.get(c, f);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) y[q] = (y[q] * r_post) * f[q];
+  }
+  if (p.gate_t) {
+    unpack8<YB>(gr, f);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) y[q] *= f[q];
+  } else if (p.gate_c) {
+    gate.get(c, f);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) y[q] *= f[q];
+  }
+}
+
+// A workgroup a row at a time, NV pieces of 8 columns a thread; with one piece a thread the next row's loads go
+// out before this row's sums.
 template <bool XB, bool YB, int T, int NV>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void block_norm_kernel(NormArgs p) {
-  constexpr bool kEarly = NV <= 2 && T <= 256;
-  constexpr int kRows = T < 256 ? 256 / T : 1;
-  __shared__ float part[2][16];
-  const int tid = threadIdx.x % T;
-  const Factors<T, NV, kEarly> w_post(p.w_post, p.shift, p.pieces), gate(p.gate_c, 0.0f, p.pieces),
+__global__ __launch_bounds__(T) void block_norm_kernel(NormArgs p) {
+  __shared__ float part[2][16][1];
+  const int tid = threadIdx.x;
+  const Factors<T, NV> w_post(p.w_post, p.shift, p.pieces), gate(p.gate_c, 0.0f, p.pieces),
       w_pre(p.w_pre, p.shift, p.pieces);
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows; r0 < p.tokens; r0 += gridDim.x * static_cast<int64_t>(kRows)) {
-    const int64_t r = r0 + threadIdx.x / T;
-    const bool live = r < p.tokens;
-    const int64_t base = (live ? r : p.tokens - 1) * p.d;
-    Raw8<XB> xr[NV];
-    Raw8<YB> yr[NV], gr[NV];
+  auto fetch = [&](int64_t row, Raw8<XB> (&a)[NV], Raw8<YB> (&b)[NV], Raw8<YB> (&g)[NV]) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = tid + T * i;
       if (c < p.pieces) {
-        xr[i] = load8<XB>(p.x, base + 8ll * c);
-        if (p.y) yr[i] = load8<YB>(p.y, base + 8ll * c);
-        if (p.gate_t) gr[i] = load8<YB>(p.gate_t, base + 8ll * c);
+        if (p.y) b[i] = load8<YB>(p.y, row * p.d + 8ll * c);
+        a[i] = load8<XB>(p.x, row * p.d + 8ll * c);
+        if (p.gate_t) g[i] = load8<YB>(p.gate_t, row * p.d + 8ll * c);
       }
     }
+  };
+  Raw8<XB> xr[NV];
+  Raw8<YB> yr[NV], gr[NV];
+  fetch(blockIdx.x, xr, yr, gr);
+  for (int64_t r = blockIdx.x; r < p.tokens; r += gridDim.x) {
+    const int64_t base = r * p.d;
+    const bool more = NV == 1 && r + gridDim.x < p.tokens;
+    Raw8<XB> nx[NV];
+    Raw8<YB> ny[NV], ng[NV];
+    if (more) fetch(r + gridDim.x, nx, ny, ng);
     float r_post = 1.0f;
     if (p.w_post) {
-      float ss = 0.0f;
+      float ss[1] = {0.0f};
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         if (tid + T * i < p.pieces) {
           float y[8];
           unpack8<YB>(yr[i], y);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) ss = fmaf(y[q], y[q], ss);
+          for (int q = 0; q < 8; ++q) ss[0] = fmaf(y[q], y[q], ss[0]);
         }
       }
-      ss = row_total<T>(ss, part[0]);
-      r_post = 1.0f / sqrtf(ss / static_cast<float>(p.d) + p.eps);
-      if (p.rstd_post && live && tid == 0) p.rstd_post[r] = r_post;
+      row_totals<T>(ss, part[0]);
+      r_post = 1.0f / sqrtf(ss[0] / static_cast<float>(p.d) + p.eps);
+      if (p.rstd_post && tid == 0) p.rstd_post[r] = r_post;
     }
-    float x1[NV][8], ss = 0.0f;
+    float x1[NV][8], ss[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = tid + T * i;
       if (c < p.pieces) {
         unpack8<XB>(xr[i], x1[i]);
         if (p.y) {
-          float y[8], f[8];
+          float y[8];
           unpack8<YB>(yr[i], y);
-          if (p.w_post) {
-            w_post.get(i, c, f);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) y[q] = (y[q] * r_post) * f[q];
-          }
-          if (p.gate_t) {
-            unpack8<YB>(gr[i], f);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) y[q] *= f[q];
-          } else if (p.gate_c) {
-            gate.get(i, c, f);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) y[q] *= f[q];
-          }
+          block_output<YB>(p, w_post, gate, gr[i], c, r_post, y);
 #pragma unroll
           for (int q = 0; q < 8; ++q) x1[i][q] = fmaf(p.alpha, y[q], x1[i][q]);
-          if (live) store8<XB>(p.x_out, base + 8ll * c, x1[i]);
+          store8<XB>(p.x_out, base + 8ll * c, x1[i]);
         }
 #pragma unroll
-        for (int q = 0; q < 8; ++q) ss = fmaf(x1[i][q], x1[i][q], ss);
+        for (int q = 0; q < 8; ++q) ss[0] = fmaf(x1[i][q], x1[i][q], ss[0]);
       }
     }
     if (p.w_pre) {
-      ss = row_total<T>(ss, part[1]);
-      const float r_pre = 1.0f / sqrtf(ss / static_cast<float>(p.d) + p.eps);
-      if (p.rstd_pre && live && tid == 0) p.rstd_pre[r] = r_pre;
+      row_totals<T>(ss, part[1]);
+      const float r_pre = 1.0f / sqrtf(ss[0] / static_cast<float>(p.d) + p.eps);
+      if (p.rstd_pre && tid == 0) p.rstd_pre[r] = r_pre;
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = tid + T * i;
-        if (c < p.pieces && live) {
+        if (c < p.pieces) {
           float f[8], n[8];
-          w_pre.get(i, c, f);
+          w_pre.get(c, f);
 #pragma unroll
           for (int q = 0; q < 8; ++q) n[q] = (x1[i][q] * r_pre) * f[q];
           store8<YB>(p.n, base + 8ll * c, n);
@@ -168,178 +181,181 @@ __global__ __launch_bounds__(T < 256 ? 256 : T) void block_norm_kernel(NormArgs 
       }
     }
     if constexpr (T > 64) __syncthreads();  // the next row's sums reuse `part`
+    if (more) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        xr[i] = nx[i];
+        yr[i] = ny[i];
+        gr[i] = ng[i];
+      }
+    } else if (r + gridDim.x < p.tokens) {
+      fetch(r + gridDim.x, xr, yr, gr);
+    }
   }
 }
 
+// A row's inputs of the backward pass.
+template <bool XB, bool YB, int NV>
+struct BackwardRow {
+  Raw8<XB> x[NV], dx[NV];
+  Raw8<YB> y[NV], dn[NV], gate[NV];
+  float r_post, r_pre;
+};
 template <bool XB, bool YB, int T, int NV>
-__global__ __launch_bounds__(T < 256 ? 256 : T) void block_norm_backward_kernel(NormArgs p) {
-  constexpr int kRows = T < 256 ? 256 / T : 1;
-  constexpr bool kEarly = NV <= 2 && T <= 256;
-  __shared__ float part[2][16];
-  const int tid = threadIdx.x % T;
-  const Factors<T, NV, kEarly> w_post(p.w_post, p.shift, p.pieces), gate(p.gate_c, 0.0f, p.pieces),
+__device__ __forceinline__ void load_row(const NormArgs &p, int64_t r, BackwardRow<XB, YB, NV> &v) {
+  v.r_post = p.w_post ? p.rstd_post[r] : 1.0f;
+  v.r_pre = p.w_pre ? p.rstd_pre[r] : 0.0f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = threadIdx.x + T * i;
+    if (c < p.pieces) {
+      const int64_t at = r * p.d + 8ll * c;
+      if (p.w_pre) {
+        v.x[i] = load8<XB>(p.x, at);
+        v.dn[i] = load8<YB>(p.dn, at);
+      }
+      if (p.y) v.y[i] = load8<YB>(p.y, at);
+      if (p.dx_out) v.dx[i] = load8<XB>(p.dx_out, at);
+      if (p.gate_t) v.gate[i] = load8<YB>(p.gate_t, at);
+    }
+  }
+}
+
+// One barrier a row: with a = alpha g w_post yh, the second sum mean(a d) follows from three sums that need no
+// other, mean(a d) = mean(a (dx' + r_x w_pre dn)) - r_x mean(w_pre dn xh) mean(a xh).  The loads
+// of the next row (bf16: of the next two, for as many bytes in flight) go out before this row's sums, up to 4096
+// columns; more would not fit in registers.  8192 x 4096 bf16: 84 us with the column sums, 4.8 TB/s (97 us with
+// one row ahead, 190 us with none and 16 columns a thread).
+template <bool XB, bool YB, int T, int NV>
+__global__ __launch_bounds__(T) void block_norm_backward_kernel(NormArgs p) {
+  constexpr int kAhead = NV > 1 ? 0 : XB && YB ? 2 : 1;
+  __shared__ float part[2][16][3];
+  const int tid = threadIdx.x;
+  const Factors<T, NV> w_post(p.w_post, p.shift, p.pieces), gate(p.gate_c, 0.0f, p.pieces),
       w_pre(p.w_pre, p.shift, p.pieces);
-  float s_pre[NV][8], s_post[NV][8];  // column sums of this workgroup's (wave's) rows
+  float s_pre[NV][8], s_post[NV][8];  // column sums of this workgroup's rows
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int q = 0; q < 8; ++q) s_pre[i][q] = s_post[i][q] = 0.0f;
 
   const float inv_d = 1.0f / static_cast<float>(p.d);
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows; r0 < p.tokens; r0 += gridDim.x * static_cast<int64_t>(kRows)) {
-    const int64_t r = r0 + threadIdx.x / T;
-    if (T == 64 && r >= p.tokens) break;  // (a wave of its own: nothing waits for it)
+  BackwardRow<XB, YB, NV> row, next, after;
+  int64_t r = blockIdx.x;  // (there are no more workgroups than rows)
+  load_row<XB, YB, T, NV>(p, r, row);
+  if constexpr (kAhead == 2)
+    if (r + gridDim.x < p.tokens) load_row<XB, YB, T, NV>(p, r + gridDim.x, next);
+  for (int turn = 0; r < p.tokens; r += gridDim.x, turn ^= 1) {
     const int64_t base = r * p.d;
-    Raw8<XB> xr[NV], dr[NV];
-    Raw8<YB> yr[NV], nr[NV], gr[NV];
+    const bool more = r + gridDim.x < p.tokens;
+    if constexpr (kAhead == 1)
+      if (more) load_row<XB, YB, T, NV>(p, r + gridDim.x, next);
+    if constexpr (kAhead == 2)
+      if (r + 2ll * gridDim.x < p.tokens) load_row<XB, YB, T, NV>(p, r + 2ll * gridDim.x, after);
+    const float r_post = row.r_post, r_pre = row.r_pre;
+    float xh[NV][8], d[NV][8];  // x' r_pre; dx' + r_pre w_pre dn
+    float sums[3] = {0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = tid + T * i;
       if (c < p.pieces) {
-        const int64_t at = base + 8ll * c;
-        if (p.w_pre) {
-          xr[i] = load8<XB>(p.x, at);
-          nr[i] = load8<YB>(p.dn, at);
-        }
-        if (p.dx_out) dr[i] = load8<XB>(p.dx_out, at);
-        if (p.y) yr[i] = load8<YB>(p.y, at);
-        if (p.gate_t) gr[i] = load8<YB>(p.gate_t, at);
-      }
-    }
-    const float r_post = p.w_post ? p.rstd_post[r] : 1.0f, r_pre = p.w_pre ? p.rstd_pre[r] : 0.0f;
-
-    // the lane's factors of y: alpha g w_post, then the second norm's sum
-    float xh[NV][8], c1 = 0.0f;
-    if (p.w_pre) {
+        float f[8], a[8];
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = tid + T * i;
-        if (c < p.pieces) {
-          float f[8], dn[8];
-          unpack8<XB>(xr[i], xh[i]);
-          if (p.y) {
-            float y[8];
-            unpack8<YB>(yr[i], y);
-            if (p.w_post) {
-              w_post.get(i, c, f);
+        for (int q = 0; q < 8; ++q) d[i][q] = a[q] = 0.0f;
+        if (p.dx_out) unpack8<XB>(row.dx[i], d[i]);
+        if (p.y) {
+          unpack8<YB>(row.y[i], a);
+          block_output<YB>(p, w_post, gate, row.gate[i], c, r_post, a);
 #pragma unroll
-              for (int q = 0; q < 8; ++q) y[q] = (y[q] * r_post) * f[q];
-            }
-            if (p.gate_t) {
-              unpack8<YB>(gr[i], f);
-#pragma unroll
-              for (int q = 0; q < 8; ++q) y[q] *= f[q];
-            } else if (p.gate_c) {
-              gate.get(i, c, f);
-#pragma unroll
-              for (int q = 0; q < 8; ++q) y[q] *= f[q];
-            }
-#pragma unroll
-            for (int q = 0; q < 8; ++q) xh[i][q] = fmaf(p.alpha, y[q], xh[i][q]);
-          }
-          unpack8<YB>(nr[i], dn);
-          w_pre.get(i, c, f);
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            xh[i][q] *= r_pre;
-            s_pre[i][q] = fmaf(dn[q], xh[i][q], s_pre[i][q]);
-            c1 = fmaf(dn[q] * f[q], xh[i][q], c1);
-          }
-        }
-      }
-      c1 = row_total<T>(c1, part[0]) * inv_d;
-    }
-    float d[NV][8], c2 = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int c = tid + T * i;
-      if (c < p.pieces) {
-        float f[8];
-        if (p.dx_out) {
-          unpack8<XB>(dr[i], d[i]);
-        } else {
-#pragma unroll
-          for (int q = 0; q < 8; ++q) d[i][q] = 0.0f;
+          for (int q = 0; q < 8; ++q) a[q] *= p.alpha;
         }
         if (p.w_pre) {
           float dn[8];
-          unpack8<YB>(nr[i], dn);
-          w_pre.get(i, c, f);
+          unpack8<XB>(row.x[i], xh[i]);
+          unpack8<YB>(row.dn[i], dn);
+          w_pre.get(c, f);
 #pragma unroll
-          for (int q = 0; q < 8; ++q) d[i][q] = fmaf(r_pre, dn[q] * f[q] - xh[i][q] * c1, d[i][q]);
+          for (int q = 0; q < 8; ++q) {
+            xh[i][q] = (xh[i][q] + a[q]) * r_pre;
+            s_pre[i][q] = fmaf(dn[q], xh[i][q], s_pre[i][q]);
+            const float u = dn[q] * f[q];
+            sums[0] = fmaf(u, xh[i][q], sums[0]);
+            d[i][q] = fmaf(r_pre, u, d[i][q]);
+            sums[2] = fmaf(a[q], xh[i][q], sums[2]);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sums[1] = fmaf(a[q], d[i][q], sums[1]);
+      }
+    }
+    row_totals<T>(sums, part[turn]);  // (the other half of `part` may still be read)
+    const float c1 = sums[0] * inv_d * r_pre, c2 = (sums[1] - c1 * sums[2]) * inv_d;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = tid + T * i;
+      if (c < p.pieces) {
+        if (p.w_pre) {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) d[i][q] = fmaf(-c1, xh[i][q], d[i][q]);
         }
         store8<XB>(p.dx, base + 8ll * c, d[i]);
         if (p.y) {
-          // d becomes q = alpha g d, and with the first norm w_post q
-          float yh[8], g[8], w[8];
-          unpack8<YB>(yr[i], yh);
+          // d becomes q = alpha g d, then the gradient of y
+          float yh[8], f[8];
+          unpack8<YB>(row.y[i], yh);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             yh[q] *= r_post;
             d[i][q] *= p.alpha;
-            w[q] = 1.0f;
           }
-          if (p.w_post) w_post.get(i, c, w);
           if (p.gate_t) {
             float dg[8];
-            unpack8<YB>(gr[i], g);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              dg[q] = d[i][q] * (yh[q] * w[q]);
-              d[i][q] *= g[q];
-              s_post[i][q] = fmaf(d[i][q], yh[q], s_post[i][q]);
+            for (int q = 0; q < 8; ++q) dg[q] = d[i][q] * yh[q];
+            if (p.w_post) {
+              w_post.get(c, f);
+#pragma unroll
+              for (int q = 0; q < 8; ++q) dg[q] *= f[q];
             }
             store8<YB>(p.dgate_t, base + 8ll * c, dg);
-          } else {
+            unpack8<YB>(row.gate[i], f);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) s_post[i][q] = fmaf(d[i][q], yh[q], s_post[i][q]);
-            if (p.gate_c) {
-              gate.get(i, c, g);
+            for (int q = 0; q < 8; ++q) d[i][q] *= f[q];
+          }
 #pragma unroll
-              for (int q = 0; q < 8; ++q) d[i][q] *= g[q];
-            }
+          for (int q = 0; q < 8; ++q) s_post[i][q] = fmaf(d[i][q], yh[q], s_post[i][q]);
+          if (p.gate_c) {
+            gate.get(c, f);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) d[i][q] *= f[q];
           }
           if (p.w_post) {
+            w_post.get(c, f);
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              d[i][q] *= w[q];
-              c2 = fmaf(d[i][q], yh[q], c2);
-            }
-          }
-        }
-      }
-    }
-    if (p.y) {
-      if (p.w_post) c2 = row_total<T>(c2, part[1]) * inv_d;
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = tid + T * i;
-        if (c < p.pieces) {
-          if (p.w_post) {
-            float yh[8];
-            unpack8<YB>(yr[i], yh);
-#pragma unroll
-            for (int q = 0; q < 8; ++q) d[i][q] = r_post * (d[i][q] - (yh[q] * r_post) * c2);
+            for (int q = 0; q < 8; ++q) d[i][q] = r_post * fmaf(-c2, yh[q], d[i][q] * f[q]);
           }
           store8<YB>(p.dy, base + 8ll * c, d[i]);
         }
       }
     }
-    if constexpr (T > 64) __syncthreads();
+    if constexpr (kAhead > 0) {
+      row = next;
+      if constexpr (kAhead == 2) next = after;
+    } else {
+      if (more) load_row<XB, YB, T, NV>(p, r + gridDim.x, row);
+    }
   }
-  const int64_t parts = static_cast<int64_t>(gridDim.x) * kRows;
-  const int64_t mine = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / T;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = tid + T * i;
     if (c < p.pieces) {
-      if (p.w_pre) store8<false>(p.parts, mine * p.d + 8ll * c, s_pre[i]);
-      if (p.y) store8<false>(p.parts, (parts + mine) * p.d + 8ll * c, s_post[i]);
+      if (p.w_pre) store8<false>(p.parts, blockIdx.x * static_cast<int64_t>(p.d) + 8ll * c, s_pre[i]);
+      if (p.y) store8<false>(p.parts, (static_cast<int64_t>(gridDim.x) + blockIdx.x) * p.d + 8ll * c, s_post[i]);
     }
   }
 }
 
-// Column sums of the partial rows: 16 lanes of four columns by 16 groups of rows, whose sums are added
+// Column sums of the partial rows: 16 lanes of four columns by 64 groups of rows, whose sums are added
 // in the order of the groups.  grid.y = 0: dw_pre, 1: dw_post and dgate.
 struct NormSumArgs {
   const float *parts;
@@ -349,16 +365,16 @@ struct NormSumArgs {
   const float *w_post, *gate_c;
   float shift;
 };
-__global__ __launch_bounds__(256) void block_norm_sum_kernel(NormSumArgs p) {
-  __shared__ float4 part[16][16];
+__global__ __launch_bounds__(1024) void block_norm_sum_kernel(NormSumArgs p) {
+  __shared__ float4 part[64][16];
   const int c = (blockIdx.x * 16 + (threadIdx.x & 15)) * 4, g = threadIdx.x >> 4;
   const bool second = blockIdx.y == 1;
   if (second ? (!p.dw_post && !p.dgate_c) : !p.dw_pre) return;
   const float *src = p.parts + (second ? p.count * p.d : 0);
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (c < p.d) {
-#pragma unroll 4
-    for (int64_t r = g; r < p.count; r += 16) {
+#pragma unroll 8
+    for (int64_t r = g; r < p.count; r += 64) {
       const float4 v = *reinterpret_cast<const float4 *>(src + r * p.d + c);
       s.x += v.x;
       s.y += v.y;
@@ -368,14 +384,19 @@ __global__ __launch_bounds__(256) void block_norm_sum_kernel(NormSumArgs p) {
   }
   part[g][threadIdx.x & 15] = s;
   __syncthreads();
-  if (g != 0 || c >= p.d) return;
-  for (int i = 1; i < 16; ++i) {
-    const float4 v = part[i][threadIdx.x & 15];
-    s.x += v.x;
-    s.y += v.y;
-    s.z += v.z;
-    s.w += v.w;
+  // the groups' sums in a tree
+  for (int n = 32; n > 0; n /= 2) {
+    if (g < n) {
+      const float4 v = part[g + n][threadIdx.x & 15];
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+      part[g][threadIdx.x & 15] = s;
+    }
+    __syncthreads();
   }
+  if (g != 0 || c >= p.d) return;
   const float v[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -416,32 +437,31 @@ NormArgs norm_args(const BlockNormArgs &a) {
 }
 
 constexpr int64_t kForwardBlocks = int64_t(1) << 20;
-constexpr int64_t kBackwardBlocks = 256;
 
-// Rows a workgroup works on at once: four of up to 1024 columns.
-int64_t rows_at_once(int64_t d) { return d <= 1024 ? 4 : 1; }
+// Workgroups of the backward pass: what the compute units hold at once (8 waves each), since each leaves a
+// partial row that is written and read again (8192 x 4096: 96 us with 256, 98 with 512 before rows were
+// fetched two ahead).
 int64_t backward_blocks(int64_t tokens, int64_t d) {
-  const int64_t n = (tokens + rows_at_once(d) - 1) / rows_at_once(d);
-  return n < kBackwardBlocks ? n : kBackwardBlocks;
+  const int64_t n = d <= 512 ? 2048 : d <= 1024 ? 1024 : d <= 2048 ? 512 : 256;
+  return tokens < n ? tokens : n;
 }
 
 template <bool BWD, bool XB, bool YB, int T, int NV>
 hipError_t go(const NormArgs &p, int64_t blocks, hipStream_t stream) {
   if constexpr (BWD)
-    block_norm_backward_kernel<XB, YB, T, NV>
-        <<<dim3(static_cast<uint32_t>(blocks)), dim3(T < 256 ? 256 : T), 0, stream>>>(p);
+    block_norm_backward_kernel<XB, YB, T, NV><<<dim3(static_cast<uint32_t>(blocks)), dim3(T), 0, stream>>>(p);
   else
-    block_norm_kernel<XB, YB, T, NV><<<dim3(static_cast<uint32_t>(blocks)), dim3(T < 256 ? 256 : T), 0, stream>>>(p);
+    block_norm_kernel<XB, YB, T, NV><<<dim3(static_cast<uint32_t>(blocks)), dim3(T), 0, stream>>>(p);
   return hipGetLastError();
 }
 
 template <bool BWD, bool XB, bool YB>
 hipError_t run(const NormArgs &p, int64_t blocks, hipStream_t stream) {
   if (p.pieces <= 64) return go<BWD, XB, YB, 64, 1>(p, blocks, stream);
-  if (p.pieces <= 128) return go<BWD, XB, YB, 64, 2>(p, blocks, stream);
+  if (p.pieces <= 128) return go<BWD, XB, YB, 128, 1>(p, blocks, stream);
   if (p.pieces <= 256) return go<BWD, XB, YB, 256, 1>(p, blocks, stream);
-  if (p.pieces <= 512) return go<BWD, XB, YB, 256, 2>(p, blocks, stream);
-  if (p.pieces <= 1024) return go<BWD, XB, YB, 256, 4>(p, blocks, stream);
+  if (p.pieces <= 512) return go<BWD, XB, YB, 512, 1>(p, blocks, stream);
+  if (p.pieces <= 1024) return go<BWD, XB, YB, 512, 2>(p, blocks, stream);
   return go<BWD, XB, YB, 512, 4>(p, blocks, stream);
 }
 
@@ -455,12 +475,15 @@ hipError_t run_types(const BlockNormArgs &a, const NormArgs &p, int64_t blocks) 
 }  // namespace
 
 hipError_t launch_block_norm(const BlockNormArgs &a) {
-  const int64_t n = (a.tokens + rows_at_once(a.d) - 1) / rows_at_once(a.d);
-  return run_types<false>(a, norm_args(a), n < kForwardBlocks ? n : kForwardBlocks);
+  // bf16 rows above 2048 columns: three workgroups a compute unit, which then fetch their next row ahead (8192 x
+  // 4096: 50 us, 5.3 TB/s; a workgroup a row 59 us).  fp32 rows keep enough in flight by themselves (102 us
+  // against 112), and shorter rows run more workgroups at once.
+  const int64_t most = a.x_dtype == 1 && a.y_dtype == 1 && a.d > 2048 ? 768 : kForwardBlocks;
+  return run_types<false>(a, norm_args(a), a.tokens < most ? a.tokens : most);
 }
 
 size_t block_norm_workspace_bytes(int64_t tokens, int64_t d) {
-  return static_cast<size_t>(2 * backward_blocks(tokens, d) * rows_at_once(d) * d) * sizeof(float);
+  return static_cast<size_t>(2 * backward_blocks(tokens, d) * d) * sizeof(float);
 }
 
 hipError_t launch_block_norm_backward(const BlockNormArgs &a) {
@@ -472,7 +495,7 @@ hipError_t launch_block_norm_backward(const BlockNormArgs &a) {
   }
   NormSumArgs s{};
   s.parts = a.workspace;
-  s.count = blocks * rows_at_once(a.d);  // (no rows: the sums are zero)
+  s.count = blocks;  // (no rows: the sums are zero)
   s.d = p.d;
   s.dw_pre = a.dw_pre;
   s.dw_post = a.dw_post;
@@ -481,7 +504,7 @@ hipError_t launch_block_norm_backward(const BlockNormArgs &a) {
   s.gate_c = p.gate_c;
   s.shift = p.shift;
   if (!s.dw_pre && !s.dw_post && !s.dgate_c) return hipSuccess;
-  block_norm_sum_kernel<<<dim3((p.d + 63) / 64, 2), dim3(256), 0, a.stream>>>(s);
+  block_norm_sum_kernel<<<dim3((p.d + 63) / 64, 2), dim3(1024), 0, a.stream>>>(s);
   return hipGetLastError();
 }
 

@@ -31,8 +31,7 @@ constexpr float kNegInf = -__builtin_huge_valf();
 // Value of the lane CTRL away in the DPP row of 16 lanes.
 template <int CTRL>
 __device__ __forceinline__ float dpp(float v) {
-  const int b = __float_as_int(v);
-  return __int_as_float(__builtin_amdgcn_update_dpp(b, b, CTRL, 0xF, 0xF, false));
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, true));
 }
 constexpr int kXor1 = 0xB1, kXor2 = 0x4E, kHalfMirror = 0x141, kMirror = 0x140;
 
@@ -52,6 +51,26 @@ __device__ __forceinline__ float row_max(float v) {
   v = fmaxf(v, dpp<kMirror>(v));
   return v;
 }
+
+template <int CTRL>
+__device__ __forceinline__ int dpp(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, true);
+}
+__device__ __forceinline__ int row_max(int v) {
+  v = max(v, dpp<kXor1>(v));
+  v = max(v, dpp<kXor2>(v));
+  v = max(v, dpp<kHalfMirror>(v));
+  v = max(v, dpp<kMirror>(v));
+  return v;
+}
+
+// Keys as integers of the same order (no NaN arithmetic in the maxima); kClosed is below every key.
+constexpr int kClosed = -2147483647 - 1;
+__device__ __forceinline__ int order_of(float v) {
+  const int b = __float_as_int(v);
+  return b ^ ((b >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float value_of(int k) { return __int_as_float(k ^ ((k >> 31) & 0x7FFFFFFF)); }
 
 // The lane's EPL logits from expert e0 on, as routing takes them: closed experts (-inf, NaN, beyond E)
 // are -inf, others capped at FLT_MAX.  vec: the row is 16-byte aligned.
@@ -99,36 +118,69 @@ __device__ __forceinline__ void load_logits(const uint8_t *row, int e0, int E, b
   for (int j = 0; j < EPL; ++j) l[j] = l[j] > kNegInf ? fminf(l[j], 3.402823466e+38f) : kNegInf;  // NaN -> -inf
 }
 
-// Scores of the lane's logits (0 where closed); (top, total) are the row's softmax maximum and sum.
-__device__ __forceinline__ float softmax_score(float l, float top, float total) {
-  return l > kNegInf ? expf(l - top) / total : 0.0f;
+// Correctly rounded 1 / x and e / total without the general division's range handling: the hardware's
+// reciprocal and one Newton step, then (Markstein) one corrected quotient, each with a fused remainder.  For
+// 1 <= x < 2^126 and, in the quotient, 1 <= total <= 512 and e = 0 or 2^-100 <= e <= 1 (`plain`): no step under-
+// or overflows there.  Elsewhere the general division.
+__device__ __forceinline__ float recip(float x) {
+  const float r = __builtin_amdgcn_rcpf(x);
+  return fmaf(fmaf(-x, r, 1.0f), r, r);
 }
-__device__ __forceinline__ float sigmoid_score(float l) { return l > kNegInf ? 1.0f / (1.0f + expf(-l)) : 0.0f; }
+__device__ __forceinline__ float quotient(float e, float total, float r) {
+  const float q = e * r;
+  return fmaf(fmaf(-q, total, e), r, q);
+}
+constexpr float kPlainMost = 0x1p125f, kPlainLeast = 0x1p-100f;
+
+// Scores (0 where closed: exp(-inf) = 0 and 1 / inf = 0).  (top, total): the row's softmax maximum and sum, 0
+// and 1 for a row without an open expert.
+__device__ __forceinline__ float softmax_score(float l, float top, float total) { return expf(l - top) / total; }
+__device__ __forceinline__ float sigmoid_score(float l) { return 1.0f / (1.0f + expf(-l)); }
 
 template <int EPL, bool SIGMOID>
 __device__ __forceinline__ void row_scores(const float (&l)[EPL], float (&s)[EPL], float &top, float &total) {
   top = 0.0f;
   total = 1.0f;
   if constexpr (SIGMOID) {
+    float most = 0.0f;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) s[j] = sigmoid_score(l[j]);
+    for (int j = 0; j < EPL; ++j) {
+      s[j] = 1.0f + expf(-l[j]);
+      most = fmaxf(most, s[j]);
+    }
+    if (__ballot(most > kPlainMost)) {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) s[j] = 1.0f / s[j];
+    } else {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) s[j] = recip(s[j]);
+    }
   } else {
     top = l[0];
 #pragma unroll
     for (int j = 1; j < EPL; ++j) top = fmaxf(top, l[j]);
     top = row_max(top);
-#pragma unroll
-    for (int j = 0; j < EPL; ++j) s[j] = l[j] > kNegInf ? expf(l[j] - top) : 0.0f;
+    top = top > kNegInf ? top : 0.0f;
     float t[EPL];
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) t[j] = s[j];
+    for (int j = 0; j < EPL; ++j) t[j] = s[j] = expf(l[j] - top);
 #pragma unroll
     for (int n = EPL; n > 1; n /= 2)
 #pragma unroll
       for (int j = 0; j < n / 2; ++j) t[j] = t[2 * j] + t[2 * j + 1];
     total = row_sum(t[0]);
+    total = total > 0.0f ? total : 1.0f;
+    bool small = false;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) s[j] = l[j] > kNegInf ? s[j] / total : 0.0f;
+    for (int j = 0; j < EPL; ++j) small |= s[j] < kPlainLeast && s[j] > 0.0f;
+    if (__ballot(small)) {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) s[j] = s[j] / total;
+    } else {
+      const float r = recip(total);
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) s[j] = quotient(s[j], total, r);
+    }
   }
 }
 
@@ -146,7 +198,6 @@ __device__ __forceinline__ float load_logit(const uint8_t *row, int e) {
 struct PlanLds {
   int32_t base[kMaxExperts];                // next row of each expert for this chunk
   int32_t wave_count[16][kMaxExperts];      // of the current tile of 1024 slots
-  int32_t part[kMaxExperts];
   int32_t scan[16];
 };
 
@@ -223,36 +274,80 @@ __global__ __launch_bounds__(kPlanThreads) void place_kernel(const int32_t *ids,
   __shared__ PlanLds lds;
   const uint32_t tid = threadIdx.x;
   const int c = blockIdx.x;
-  // two threads an expert: chunks before and from this one on... summed over strided chunks
-  const int e = tid & (kMaxExperts - 1), half = tid / kMaxExperts;
+  // each expert's counts of all chunks and of those before this one: the threads of an expert (two at
+  // least) take every parts-th chunk, eight loads in flight
+  const int width = 1 << (bits < 6 ? 6 : bits), parts = kPlanThreads / width;
+  const int e = tid & (width - 1), part = tid / width;
   int32_t before = 0, all = 0;
   if (e < E) {
-    for (int i = half; i < chunks; i += 2) {
-      const int32_t n = counts[static_cast<int64_t>(i) * E + e];
+    const int32_t *column = counts + e;
+#pragma unroll 8
+    for (int i = part; i < chunks; i += parts) {
+      const int32_t n = column[static_cast<int64_t>(i) * E];
       all += n;
       before += i < c ? n : 0;
     }
   }
-  if (half == 1) {
-    lds.base[e] = before;
-    lds.part[e] = all;
-  }
+  int32_t *const sums = &lds.wave_count[0][0];  // [2][1024]
+  sums[tid] = all;
+  sums[kPlanThreads + tid] = before;
   __syncthreads();
-  if (half == 0) {
-    before += lds.base[e];
-    all += lds.part[e];
-  }
   int32_t total;
-  const int32_t first = scan512(half == 0 ? all : 0, lds.scan, &total);
-  __syncthreads();
-  if (half == 0) {
-    lds.base[e] = first + before;
-    if (c == 0 && e < E) offsets[e] = first;
-    if (c == 0 && e == 0) offsets[E] = total;
+  all = before = 0;
+  if (tid < static_cast<uint32_t>(width))
+    for (int i = 0; i < parts; ++i) {
+      all += sums[i * width + tid];
+      before += sums[kPlanThreads + i * width + tid];
+    }
+  const int32_t first = scan512(all, lds.scan, &total);
+  if (tid < kMaxExperts) lds.base[tid] = first + before;
+  if (c == 0) {
+    if (static_cast<int>(tid) < E) offsets[tid] = first;
+    if (tid == 0) offsets[E] = total;
   }
   __syncthreads();
   const int64_t slot0 = c * per;
   place_slots(lds, ids, slot0, min(slot0 + per, slots), E, bits, total, rows, pos);
+}
+
+// The whole plan of at most 64 slots by one workgroup of 512 or more: each lane of the first wave compares its
+// slot's id with all others bit by bit, and the offsets are found in the sorted ids.
+__device__ __forceinline__ void plan_wave(PlanLds &lds, const int32_t *ids, int slots, int E, int bits,
+                                          int32_t *offsets, int32_t *rows, int32_t *pos) {
+  const uint32_t tid = threadIdx.x;
+  if (tid < 64) {
+    const int lane = tid;
+    const int32_t id = lane < slots ? ids[lane] : -1;
+    const bool live = id >= 0 && id < E;
+    const uint64_t all = __ballot(live);
+    uint64_t same = all, less = 0;  // slots whose id agrees with this one's so far; whose id is smaller
+    for (int b = bits - 1; b >= 0; --b) {
+      const bool one = (id >> b) & 1;
+      const uint64_t ones = __ballot(one);
+      less |= one ? same & ~ones : 0ull;
+      same &= one ? ones : ~ones;
+    }
+    const int p = __popcll(less) + __popcll(same & ((1ull << lane) - 1));
+    lds.base[lane] = E;  // (beyond the placed slots)
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (live) {
+      rows[p] = lane;
+      lds.base[p] = id;
+    }
+    if (lane < slots) {
+      pos[lane] = live ? p : -1;
+      if (lane >= __popcll(all)) rows[lane] = -1;
+    }
+  }
+  __syncthreads();
+  for (int e = tid; e <= E; e += blockDim.x) {
+    int lo = 0;  // slots with an id below e
+#pragma unroll
+    for (int n = 32; n > 0; n /= 2) lo += lds.base[lo + n - 1] < e ? n : 0;
+    lo += lo < 64 && lds.base[lo < 64 ? lo : 63] < e ? 1 : 0;
+    offsets[e] = lo;
+  }
 }
 
 // The whole plan of at most kOneBlockSlots slots by one workgroup of 1024.
@@ -303,7 +398,8 @@ struct RouteArgs {
   int64_t row_bytes;
   int64_t tokens, per;  // tokens of a workgroup: [b * per, (b + 1) * per)
   int E, G, GS, group_k, k;
-  bool sum2, renorm, vec;
+  int group_lanes;  // lanes of a group, where groups are whole lanes and a power of two of them (else 0)
+  bool sum2, renorm, vec, vec_bias;
   float scale;
   const float *bias;
   int32_t *ids;
@@ -313,39 +409,85 @@ struct RouteArgs {
   int bits;
 };
 
-// Closes the experts of the groups that are not among the row's group_k best.  keys: this row's LDS
-// copy of its keys.
+// (m1, m2): the two largest of both pairs.
+__device__ __forceinline__ void merge_two(int &m1, int &m2, int o1, int o2) {
+  m2 = max(min(m1, o1), max(m2, o2));
+  m1 = max(m1, o1);
+}
+template <int CTRL>
+__device__ __forceinline__ void merge_two(int &m1, int &m2) {
+  const int o1 = dpp<CTRL>(m1), o2 = dpp<CTRL>(m2);
+  merge_two(m1, m2, o1, o2);
+}
+
+// Closes the experts of the groups that are not among the row's group_k best.  Where a group is 1, 2, 4, 8 or
+// 16 whole lanes (group_lanes) its two best keys meet by lane exchanges; else through `keys`, the row's copy in
+// LDS, which lane g reads for group g.
 template <int EPL>
-__device__ __forceinline__ void keep_groups(float (&key)[EPL], float *keys, const RouteArgs &p, uint32_t lane) {
-  const int l16 = lane & 15;
+__device__ __forceinline__ void keep_groups(int (&key)[EPL], int *keys, const RouteArgs &p, uint32_t lane) {
+  const int l16 = lane & 15, W = p.group_lanes;
+  int m1 = kClosed, m2 = kClosed;
+  int mine, stride;  // the group whose value this lane holds, lanes between the groups' values
+  if (W > 0) {
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) keys[l16 * EPL + j] = key[j];
-  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  // lane g of the row: its group's best two keys, each lane starting elsewhere in its group
-  float m1 = kNegInf, m2 = kNegInf;
-  if (l16 < p.G) {
-    int at = l16 < p.GS ? l16 : l16 % p.GS;
-    for (int i = 0; i < p.GS; ++i) {
-      const float v = keys[l16 * p.GS + at];
-      m2 = fmaxf(m2, fminf(m1, v));
-      m1 = fmaxf(m1, v);
-      at = at + 1 == p.GS ? 0 : at + 1;
+    for (int j = 0; j < EPL; ++j) {
+      m2 = max(m2, min(m1, key[j]));
+      m1 = max(m1, key[j]);
+    }
+    if (W > 1) merge_two<kXor1>(m1, m2);
+    if (W > 2) merge_two<kXor2>(m1, m2);
+    if (W > 4) merge_two<kHalfMirror>(m1, m2);
+    if (W > 8) merge_two<kMirror>(m1, m2);
+    mine = l16 / W;
+    stride = W;
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) keys[l16 * EPL + j] = key[j];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    mine = l16;
+    stride = 1;
+    if (l16 < p.G) {
+      int at = l16 % p.GS;  // (each lane starts elsewhere in its group: other banks)
+      for (int i = 0; i < p.GS; i += 4) {
+        int v[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          v[u] = i + u < p.GS ? keys[l16 * p.GS + at] : kClosed;
+          at = at + 1 == p.GS ? 0 : at + 1;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          m2 = max(m2, min(m1, v[u]));
+          m1 = max(m1, v[u]);
+        }
+      }
     }
   }
-  float value = m1;
-  if (p.sum2 && m2 > kNegInf) value = m1 + m2;
+  int value = m1;
+  if (p.sum2 && m2 != kClosed) value = order_of((value_of(m1) + value_of(m2)) + 0.0f);
+  if (mine >= p.G) value = kClosed;
   // the group's place: how many groups come before it
   int place = 0;
-  for (int g = 0; g < p.G; ++g) {
-    const float o = __shfl(value, (lane & 48) + g);
-    place += (o > value || (o == value && g < l16)) ? 1 : 0;
+  for (int g0 = 0; g0 < p.G; g0 += 4) {
+    int o[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) o[u] = __shfl(value, (lane & 48) + min(g0 + u, p.G - 1) * stride);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (g0 + u < p.G) place += (o[u] > value || (o[u] == value && g0 + u < mine)) ? 1 : 0;
   }
-  const uint32_t kept = static_cast<uint32_t>(__ballot(l16 < p.G && place < p.group_k) >> (lane & 48)) & 0xFFFFu;
+  const bool stays = place < p.group_k;
+  if (W > 0) {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) key[j] = stays ? key[j] : kClosed;
+    return;
+  }
+  const uint32_t kept = static_cast<uint32_t>(__ballot(stays) >> (lane & 48)) & 0xFFFFu;
   int g = l16 * EPL / p.GS, left = (g + 1) * p.GS - l16 * EPL;
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
-    if (!((kept >> g) & 1u)) key[j] = kNegInf;
+    if (!((kept >> g) & 1u)) key[j] = kClosed;
     if (--left == 0) {
       ++g;
       left = p.GS;
@@ -357,10 +499,9 @@ template <int EPL, bool BF16, bool SIGMOID>
 __global__ __launch_bounds__(kPlanThreads) void route_kernel(RouteArgs p) {
   constexpr int P = 16 * EPL;
   __shared__ int32_t hist[kMaxExperts];
-  // with groups: P keys a token; then, where this workgroup makes the plan, the plan's
+  // with groups that are not whole lanes: P keys a token; then, where this workgroup makes the plan, the plan's
   extern __shared__ __attribute__((aligned(16))) uint8_t area[];
-  const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-  const int l16 = lane & 15;
+  const uint32_t wave = threadIdx.x >> 6;
   if (p.counts) {
     for (int e = threadIdx.x; e < p.E; e += blockDim.x) hist[e] = 0;
     __syncthreads();
@@ -369,42 +510,75 @@ __global__ __launch_bounds__(kPlanThreads) void route_kernel(RouteArgs p) {
   const int step = blockDim.x / 16;
   for (int64_t tb = blockIdx.x * p.per; tb < t1; tb += step) {
     if (tb + 4 * wave >= t1) continue;  // (no workgroup barrier inside)
+    // (an opaque copy: nothing that depends on the lane is computed ahead of the loop, for paths not taken)
+    uint32_t lane = threadIdx.x & 63u;
+    asm volatile("" : "+v"(lane));
+    const int l16 = lane & 15;
     const int64_t t = tb + (threadIdx.x >> 4);
     const bool exists = t < t1;
     const uint8_t *row = p.logits + (exists ? t : t1 - 1) * p.row_bytes;
-    float l[EPL], key[EPL], top, total;
+    float l[EPL], s[EPL], top, total;
     load_logits<EPL, BF16>(row, l16 * EPL, p.E, p.vec, l);
-    row_scores<EPL, SIGMOID>(l, key, top, total);
+    row_scores<EPL, SIGMOID>(l, s, top, total);
+    if (p.bias) {
+      float b[EPL];
+      if (EPL >= 4 && p.vec_bias && l16 * EPL + EPL <= p.E) {
+#pragma unroll
+        for (int j = 0; j + 4 <= EPL; j += 4) {
+          const float4 v = *reinterpret_cast<const float4 *>(p.bias + l16 * EPL + j);
+          b[j] = v.x;
+          b[(j + 1) % EPL] = v.y;
+          b[(j + 2) % EPL] = v.z;
+          b[(j + 3) % EPL] = v.w;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < EPL; ++j) b[j] = p.bias[min(l16 * EPL + j, p.E - 1)];
+      }
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) s[j] += b[j];
+    }
+    // (a NaN key closes too; + 0 so that a key of -0 is +0)
+    int key[EPL];
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-      const int e = l16 * EPL + j;
-      float v = key[j];
-      if (p.bias && e < p.E) v += p.bias[e];
-      // (+ 0 so that a key of -0 is +0; a NaN key closes)
-      key[j] = l[j] > kNegInf && v > kNegInf ? v + 0.0f : kNegInf;
+      const bool is_open = (l[j] > kNegInf) & (s[j] > kNegInf);
+      key[j] = is_open ? order_of(s[j] + 0.0f) : kClosed;
     }
-    if (p.group_k < p.G) keep_groups<EPL>(key, reinterpret_cast<float *>(area) + (threadIdx.x >> 4) * P, p, lane);
+    if (p.group_k < p.G) keep_groups<EPL>(key, reinterpret_cast<int *>(area) + (threadIdx.x >> 4) * P, p, lane);
 
-    float best = key[0];
+    int best = key[0];
 #pragma unroll
-    for (int j = 1; j < EPL; ++j) best = fmaxf(best, key[j]);
+    for (int j = 1; j < EPL; ++j) best = max(best, key[j]);
     int id_lo = -1, id_hi = -1;  // slots l16 and 16 + l16
     for (int r = 0; r < p.k; ++r) {
-      const float m = row_max(best);
+      const int m = row_max(best);
       const uint32_t holds = static_cast<uint32_t>(__ballot(best == m) >> (lane & 48)) & 0xFFFFu;
       const int owner = __ffs(holds) - 1;
-      // the lane's first expert with that key; the owner closes it
-      int at = 0;
-#pragma unroll
-      for (int j = EPL - 1; j >= 0; --j) at = key[j] == m ? j : at;
-      const int mine = l16 == owner ? at : -1;
-      best = kNegInf;
+      // the lowest lane that holds the key closes it, and gets a bit for every expert of its that has it, the
+      // first expert's the highest.  In integer arithmetic, since a lane mask for every compare costs wait
+      // states: t is 0 for the key and -1 for a smaller one (other lanes want a key above all).
+      const int want = l16 == owner ? m : 2147483647;
+      int misses = 0;
+      best = kClosed;
 #pragma unroll
       for (int j = 0; j < EPL; ++j) {
-        key[j] = j == mine ? kNegInf : key[j];
-        best = fmaxf(best, key[j]);
+        int t = __builtin_elementwise_sub_sat(key[j], want) >> 31;
+        asm("" : "+v"(t));  // (else the compiler goes back to compares)
+        misses = (misses << 1) + t;
+        key[j] = (key[j] & t) | (kClosed & ~t);
+        best = max(best, key[j]);
       }
-      const int id = m > kNegInf ? owner * EPL + __shfl(at, (lane & 48) + owner) : -1;
+      const uint32_t hits = static_cast<uint32_t>(misses) + (EPL == 32 ? 0xFFFFFFFFu : (1u << (EPL & 31)) - 1u);
+      const uint32_t others = hits & ((1u << (31 - __clz(hits | 1u))) - 1u);
+      if (__ballot(others != 0 && m != kClosed)) {  // equal keys in one lane: all but the first come back
+#pragma unroll
+        for (int j = 0; j < EPL; ++j)
+          if ((others >> (EPL - 1 - j)) & 1u) key[j] = m;
+        best = others ? m : best;
+      }
+      const int at = __clz(hits) - (32 - EPL);
+      const int id = m != kClosed ? owner * EPL + __shfl(at, (lane & 48) + owner) : -1;
       if (l16 == (r & 15)) {
         if (r < 16)
           id_lo = id;
@@ -443,7 +617,11 @@ __global__ __launch_bounds__(kPlanThreads) void route_kernel(RouteArgs p) {
   }
   if (p.offsets) {
     __syncthreads();  // the ids are in global memory for the whole workgroup
-    plan_block(*reinterpret_cast<PlanLds *>(area), p.ids, p.tokens * p.k, p.E, p.bits, p.offsets, p.rows, p.pos);
+    PlanLds &lds = *reinterpret_cast<PlanLds *>(area);
+    if (p.tokens * p.k <= 64)
+      plan_wave(lds, p.ids, static_cast<int>(p.tokens * p.k), p.E, p.bits, p.offsets, p.rows, p.pos);
+    else
+      plan_block(lds, p.ids, p.tokens * p.k, p.E, p.bits, p.offsets, p.rows, p.pos);
   }
 }
 
@@ -624,6 +802,7 @@ hipError_t launch_moe_route(const MoeRouteArgs &a) {
   p.vec = rows_aligned16(a.logits, p.row_bytes);
   p.scale = a.scale;
   p.bias = a.bias;
+  p.vec_bias = (reinterpret_cast<uintptr_t>(a.bias) & 15u) == 0;
   p.ids = a.ids;
   p.weights = a.weights;
   p.bits = id_bits(p.E);
@@ -632,7 +811,9 @@ hipError_t launch_moe_route(const MoeRouteArgs &a) {
     return plan ? launch_moe_plan(a.ids, 0, a.experts, a.offsets, a.rows, a.pos, a.workspace, a.stream) : hipSuccess;
   // keys of the tokens that a workgroup holds at once (whole waves of four), for the choice of groups
   const int epl = experts_per_lane(p.E);
-  const bool groups = p.group_k < p.G;
+  const int lanes = p.GS % epl == 0 ? p.GS / epl : 0;
+  p.group_lanes = (lanes & (lanes - 1)) == 0 ? lanes : 0;
+  const bool groups = p.group_k < p.G && p.group_lanes == 0;  // (through LDS)
   size_t lds = groups ? static_cast<size_t>((a.tokens + 3) / 4 * 4) * 16 * epl * sizeof(float) : 0;
   const bool one = plan && a.tokens <= kOneBlockTokens && lds <= kOneBlockKeys;
   int blocks, threads;
@@ -642,15 +823,18 @@ hipError_t launch_moe_route(const MoeRouteArgs &a) {
     p.pos = a.pos;
     p.per = a.tokens;
     blocks = 1;
-    threads = kPlanThreads;
+    threads = a.tokens * a.top_k <= 64 ? 512 : kPlanThreads;
     if (lds < sizeof(PlanLds)) lds = sizeof(PlanLds);
   } else {
-    lds = groups ? static_cast<size_t>(256) * epl * sizeof(float) : 0;
-    // chunks of whole 16-token workgroup steps, at most kPlanChunks of them when they are counted
-    threads = 256;
+
+    // chunks of whole workgroup steps (64 tokens where they are counted, in at most kPlanChunks chunks)
+    // (with groups, fewer tokens at once where their keys would pass 32 KB)
+    threads = !plan ? 256 : groups && epl >= 16 ? 8192 / epl : kPlanThreads;
     const int64_t most = plan ? kPlanChunks : kMaxBlocks;
     if (plan) p.counts = a.workspace;
-    p.per = ((a.tokens + most - 1) / most + 15) / 16 * 16;
+    const int64_t at_once = threads / 16;
+    p.per = ((a.tokens + most - 1) / most + at_once - 1) / at_once * at_once;
+    lds = groups ? static_cast<size_t>(threads) * epl * sizeof(float) : 0;
     blocks = static_cast<int>((a.tokens + p.per - 1) / p.per);
   }
   hipError_t e;

@@ -253,8 +253,9 @@ enum {
   NVFP4_NORM_TOKEN_GATE = 1u << 1  /* the gate is [tokens x d] in y's dtype, not float[d]               */
 };
 
-/* Bytes of device workspace nvfp4_moe_route (with a plan) and nvfp4_moe_plan need.  Fully rewritten by
- * every call before it is read; calls that may overlap must use distinct workspaces. */
+/* Bytes of device workspace nvfp4_moe_route (with a plan) and nvfp4_moe_plan need (0 for up to 16 tokens:
+ * workspace may then be NULL).  Fully rewritten by every call before it is read; calls that may overlap must
+ * use distinct workspaces. */
 size_t nvfp4_moe_workspace_size(int64_t tokens, int64_t experts, int32_t top_k);
 
 /* Routing of tokens to experts.  logits [tokens x experts] (dtype NVFP4_F32 or NVFP4_BF16, leading
@@ -323,7 +324,7 @@ int nvfp4_moe_combine_backward(const void *dout, int64_t ldo, const void *y, int
                                void *dy, int64_t lddy, float *dweights, void *hip_stream);
 
 /* Quantize the rows of x [rows x cols] (NVFP4_F32 or NVFP4_BF16, leading dimension ldx) to 8-bit
- * integers with one fp32 scale a row (a token's, or a weight's output channel): s = RN(amax / 127),
+ * integers with one fp32 scale a row (a token's, or a weight's output channel): s = RN(amax * RN(1 / 127)),
  * q = the nearest integer (ties to even) to RN(x * RN(1 / s)), so |q| <= 127 and x ~ q * s.  A row
  * whose s would be below 2^-126 becomes zeros with s = 0.  q: device int8 [rows][cols] (no padding);
  * scales: device float[rows].  cols % 16 == 0; x and q 16-byte aligned, ldx * sizeof(dtype) a multiple

@@ -373,10 +373,19 @@ class Int8Tensor:
 @dataclass
 class BlockNorm:
     """What nvfp4_block_norm gives."""
-    x: torch.Tensor                    # the residual stream after the block
-    n: Optional[torch.Tensor]          # its norm, the next block's input
-    rstd_post: Optional[torch.Tensor]  # float32 [tokens], for the backward call
-    rstd_pre: Optional[torch.Tensor]
+    x: torch.Tensor            # the residual stream after the block
+    n: Optional[torch.Tensor]  # its norm, the next block's input
+    rstd: torch.Tensor         # float32 [2, tokens]: of the block's output and of x, where they are normed
+    has_post: bool
+
+    @property
+    def rstd_post(self) -> Optional[torch.Tensor]:
+        """float32 [tokens], for the backward call."""
+        return self.rstd[0] if self.has_post else None
+
+    @property
+    def rstd_pre(self) -> Optional[torch.Tensor]:
+        return self.rstd[1] if self.n is not None else None
 
 
 @dataclass
@@ -401,7 +410,7 @@ def _want(where: str, name: str, t: Optional[torch.Tensor], dtype: torch.dtype, 
     """A contiguous tensor of this dtype and shape on the device of `like`."""
     if t is None:
         return
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{where}: {name} must be {dtype}, is {t.dtype}")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{where}: {name} must be a contiguous {list(shape)}, is {list(t.shape)}")
@@ -423,13 +432,14 @@ def _matrix(where: str, name: str, t: torch.Tensor) -> int:
 
 
 def _empty_plan(tokens: int, top_k: int, experts: int, device) -> MoEPlan:
-    slots = tokens * top_k
-    buf = torch.empty(2 * slots + experts + 1, dtype=torch.int32, device=device)
-    return MoEPlan(buf[2 * slots:], buf[:slots], buf[slots:2 * slots].view(tokens, top_k))
+    i32 = torch.int32
+    return MoEPlan(torch.empty(experts + 1, dtype=i32, device=device), torch.empty(tokens * top_k, dtype=i32, device=device),
+                   torch.empty((tokens, top_k), dtype=i32, device=device))
 
 
-def _moe_workspace(tokens: int, experts: int, top_k: int, device) -> torch.Tensor:
-    return torch.empty(lib().nvfp4_moe_workspace_size(tokens, experts, top_k) // 4, dtype=torch.int32, device=device)
+def _moe_workspace(tokens: int, experts: int, top_k: int, device) -> Optional[torch.Tensor]:
+    size = lib().nvfp4_moe_workspace_size(tokens, experts, top_k)
+    return torch.empty(size // 4, dtype=torch.int32, device=device) if size else None
 
 
 def nvfp4_moe_route(logits: torch.Tensor, top_k: int, flags: int = 0, bias: Optional[torch.Tensor] = None,
@@ -487,7 +497,7 @@ def nvfp4_moe_plan(ids: torch.Tensor, experts: int, workspace: Optional[torch.Te
     if workspace is None:
         workspace = _moe_workspace(T, experts, k, ids.device)
     st = lib().nvfp4_moe_plan(ids.data_ptr(), T, k, experts, plan.offsets.data_ptr(), plan.rows.data_ptr(),
-                              plan.pos.data_ptr(), workspace.data_ptr(), _raw_stream(ids))
+                              plan.pos.data_ptr(), _addr(workspace), _raw_stream(ids))
     _check(st, "nvfp4_moe_plan")
     return plan
 
@@ -646,13 +656,13 @@ def nvfp4_block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, w_post: 
     else:
         _want(where, "x_out", x_out, x.dtype, (T, D), x)
     n = torch.empty((T, D), dtype=y_dtype, device=dev) if w_pre is not None else None
-    rstd_post = torch.empty(T, dtype=torch.float32, device=dev) if w_post is not None else None
-    rstd_pre = torch.empty(T, dtype=torch.float32, device=dev) if w_pre is not None else None
+    rstd = torch.empty((2, T), dtype=torch.float32, device=dev)
+    at = rstd.data_ptr()
     st = lib().nvfp4_block_norm(x.data_ptr(), _dtype_code(x.dtype), _addr(y), _dtype_code(y_dtype), T, D, _addr(w_post),
-                                _addr(gate), _addr(w_pre), alpha, eps, flags, _addr(x_out), _addr(n), _addr(rstd_post),
-                                _addr(rstd_pre), _raw_stream(x))
+                                _addr(gate), _addr(w_pre), alpha, eps, flags, _addr(x_out), _addr(n), at, at + 4 * T,
+                                _raw_stream(x))
     _check(st, where)
-    return BlockNorm(x if y is None else x_out, n, rstd_post, rstd_pre)
+    return BlockNorm(x if y is None else x_out, n, rstd, w_post is not None)
 
 
 def nvfp4_block_norm_backward(dx_out: Optional[torch.Tensor], dn: Optional[torch.Tensor], x: torch.Tensor,

@@ -62,8 +62,10 @@ int check_route_common(const void *logits, int dtype, int64_t tokens, int64_t ex
   return aligned(logits, es) ? NVFP4_OK : NVFP4_ERR_ALIGN;
 }
 
-int check_plan(int64_t slots, const int32_t *offsets, const int32_t *rows, const int32_t *pos, const void *workspace) {
-  if (!offsets || (slots > 0 && (!rows || !pos || !workspace))) return NVFP4_ERR_NULL;
+int check_plan(int64_t tokens, int64_t experts, const int32_t *offsets, const int32_t *rows, const int32_t *pos,
+               const void *workspace) {
+  if (!offsets || (tokens > 0 && (!rows || !pos))) return NVFP4_ERR_NULL;
+  if (nvfp4::moe_workspace_bytes(tokens, experts) > 0 && !workspace) return NVFP4_ERR_NULL;
   return aligned(offsets, 4) && aligned(rows, 4) && aligned(pos, 4) && aligned(workspace, 16) ? NVFP4_OK
                                                                                                : NVFP4_ERR_ALIGN;
 }
@@ -86,9 +88,10 @@ int check_norm(const void *x, int x_dtype, const void *y, int y_dtype, int64_t t
 extern "C" {
 
 size_t nvfp4_moe_workspace_size(int64_t tokens, int64_t experts, int32_t top_k) {
-  (void)tokens;
   (void)top_k;
-  return experts < 1 || experts > kMaxExperts ? 0 : (nvfp4::moe_workspace_bytes(experts) + 15) / 16 * 16;
+  return tokens < 0 || experts < 1 || experts > kMaxExperts
+             ? 0
+             : (nvfp4::moe_workspace_bytes(tokens, experts) + 15) / 16 * 16;
 }
 
 int nvfp4_moe_route(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t ld, const float *bias,
@@ -103,7 +106,7 @@ int nvfp4_moe_route(const void *logits, int dtype, int64_t tokens, int64_t exper
   if (tokens > 0 && (!ids || !weights)) return NVFP4_ERR_NULL;
   if (!aligned(ids, 4) || !aligned(weights, 4) || !aligned(bias, 4)) return NVFP4_ERR_ALIGN;
   if (offsets || rows || pos) {
-    st = check_plan(tokens * top_k, offsets, rows, pos, workspace);
+    st = check_plan(tokens, experts, offsets, rows, pos, workspace);
     if (st != NVFP4_OK) return st;
   }
   nvfp4::MoeRouteArgs a{};
@@ -164,7 +167,7 @@ int nvfp4_moe_plan(const int32_t *ids, int64_t tokens, int32_t top_k, int64_t ex
   if (st != NVFP4_OK) return st;
   if (tokens > 0 && !ids) return NVFP4_ERR_NULL;
   if (!aligned(ids, 4)) return NVFP4_ERR_ALIGN;
-  st = check_plan(tokens * top_k, offsets, rows, pos, workspace);
+  st = check_plan(tokens, experts, offsets, rows, pos, workspace);
   if (st != NVFP4_OK) return st;
   return status_of(nvfp4::launch_moe_plan(ids, tokens * top_k, experts, offsets, rows, pos,
                                           static_cast<int32_t *>(workspace), stream_of(hip_stream)));

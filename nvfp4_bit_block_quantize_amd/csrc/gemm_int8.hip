@@ -391,75 +391,85 @@ __device__ __forceinline__ void lds_buffer16(__amdgpu_buffer_rsrc_t rs, uint32_t
 // the step's one barrier follows sub-step 2: there every fragment of the stage is in registers, so
 // behind it the stage takes the loads of the step after next, and the next stage, whose loads this
 // wave has waited for, is read.
-constexpr int kBigB = 256 * kStep, kBigStage = 512 * kStep;
+constexpr int kBigLds = 3 * 384 * kStep;  // three stages of half tiles, or two of full ones
 
-template <bool OUT_BF16>
-__global__ __launch_bounds__(kThreads, 1) void gemm_int8_big_kernel(I8Args p) {
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[2 * kBigStage];
+//
+// HALF: 128 x 256 tiles, each wave all 128 rows by 64 columns (eight MFMAs a sub-step): half the work where a
+// group's (or the matrix's) last tile row has at most 128 rows.  Such a tile has half the time a step to cover
+// its loads: three stages of 48 KB, loaded two to three steps ahead.  (32768 x 1536 x 4096 over 64 experts:
+// 256 us, against 183 us for one expert; the last, partly filled round is what is left.  Half tiles after all
+// full ones 247-262 us; lines fetched into the L2 some steps ahead 263-305 us.)
+template <bool OUT_BF16, bool HALF>
+__device__ __forceinline__ void big_tile(const I8Args &p, uint8_t *smem, const TileRows &t, int32_t tn) {
+  constexpr int FN = HALF ? 2 : 4;                       // B fragments a wave
+  constexpr int NA = HALF ? 4 : 8, NL = NA + 8;          // direct loads a wave and step: of A, all
+  constexpr int S = HALF ? 3 : 2;                        // stages
+  constexpr uint32_t kB = 32 * NA * kStep, kStage = kB + 256 * kStep;
   const uint32_t lane = threadIdx.x & 63u;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t h = lane >> 5, l32 = lane & 31u;
-  const uint32_t wm = (wave >> 1) * 128, wn = (wave & 1) * 128;
-
-  TileRows t;
-  int32_t tn;
-  if (!find_tile<256>(p, all_tiles<256>(p), blockIdx.x, t, tn)) return;
+  const uint32_t wm = HALF ? 0 : (wave >> 1) * 128, wn = HALF ? 64 * wave : (wave & 1) * 128;
   const int64_t n0 = static_cast<int64_t>(tn) * 256;
-  // direct loads: wave w fetches rows [64 w, 64 w + 64) of A and of B, 8 rows a load; rows beyond the
+  // direct loads: wave w fetches rows [8 NA w, 8 NA (w + 1)) of A and [64 w, 64 w + 64) of B, 8 rows a load; rows beyond the
   // operand read its last one (their products are never stored).  Buffer loads: a lane's offset within
   // the operand stays in one register and the step's advance is a scalar, so a load takes no vector
   // arithmetic.  (Every address is inside the operand: the range check is not relied on.)
   const __amdgpu_buffer_rsrc_t rsA = buffer_of(p.rows ? p.a : p.a + t.m0 * p.K);
   const __amdgpu_buffer_rsrc_t rsB = buffer_of(p.b + (static_cast<int64_t>(t.group) * p.N + n0) * p.K);
-  uint32_t off[16];  // A, then B
+  uint32_t off[NL];  // A, then B
+  const auto row_of = [&](int q) { return (q < NA ? 8 * NA * wave + 8 * q : 64 * wave + 8 * (q - NA)) + (lane >> 3); };
+  const auto chunk_of = [&](int q) { return ((lane & 7u) ^ swz(row_of(q))) * 16; };
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t R = 64 * wave + 8 * i + (lane >> 3);
-    const uint32_t chunk = ((lane & 7u) ^ swz(R)) * 16;
+  for (int q = 0; q < NL; ++q) {
+    const uint32_t R = row_of(q);
     const int64_t r = min(t.m0 + R, t.m_end - 1);
-    off[i] = static_cast<uint32_t>(p.rows ? a_row(p, r) : r - t.m0) * p.K + chunk;
-    off[8 + i] = static_cast<uint32_t>(min(n0 + R, p.N - 1) - n0) * p.K + chunk;
+    off[q] = (q < NA ? static_cast<uint32_t>(p.rows ? a_row(p, r) : r - t.m0)
+                     : static_cast<uint32_t>(min(n0 + R, p.N - 1) - n0)) * p.K + chunk_of(q);
   }
   const int32_t steps = static_cast<int32_t>((p.K + kStep - 1) / kStep);
   const uint32_t rest = p.K - (steps - 1) * kStep;  // bytes of K in the last step
+  // Each group starts elsewhere in K (integer sums have no order): tiles that began together would all read the
+  // same columns of their weights, rows a power of two apart, from the same memory channels (42 experts of
+  // 128 x 1536 x 4096: 73 -> 57 us).  Not where K ends within a step.
+  const uint32_t turn = steps > 0 && rest == kStep ? static_cast<uint32_t>(t.group) * 7u % static_cast<uint32_t>(steps) : 0u;
   auto load = [&](uint8_t *st, int32_t kt, int q) {
-    lds_buffer16(q < 8 ? rsA : rsB, off[q], kt * kStep,
-                 st + (q < 8 ? 0 : kBigB) + (64 * wave + 8 * (q & 7)) * kStep);
+    const int32_t at = kt + static_cast<int32_t>(turn);
+    lds_buffer16(q < NA ? rsA : rsB, off[q], (at < steps ? at : at - steps) * kStep,
+                 st + (q < NA ? (8 * NA * wave + 8 * q) * kStep : kB + (64 * wave + 8 * (q - NA)) * kStep));
   };
   // before the loads of a last step that K does not fill: chunks beyond K read its last one (their A
   // fragments are cleared)
   auto end_of_k = [&](int32_t kt) {
     if (kt == steps - 1 && rest < kStep) {
 #pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const uint32_t R = 64 * wave + 8 * (q & 7) + (lane >> 3);
-        const uint32_t chunk = ((lane & 7u) ^ swz(R)) * 16;
+      for (int q = 0; q < NL; ++q) {
+        const uint32_t chunk = chunk_of(q);
         off[q] -= chunk > rest - 16 ? chunk - (rest - 16) : 0;
       }
     }
   };
 
-  intx16 acc[4][4];  // [B fragment][A fragment]
+  intx16 acc[FN][4];  // [B fragment][A fragment]
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
+  for (int j = 0; j < FN; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) acc[j][i][r] = 0;
 
-  const uint32_t rdA = (wm + l32) * kStep, rdB = kBigB + (wn + l32) * kStep, sw = swz(l32);
-  intx4 a0[4], b0[4], a1[4], b1[4];  // fragments of the even and the odd sub-steps
-  auto read = [&](const uint8_t *st, int s, intx4 (&af)[4], intx4 (&bf)[4]) {
+  const uint32_t rdA = (wm + l32) * kStep, rdB = kB + (wn + l32) * kStep, sw = swz(l32);
+  intx4 a0[4], b0[FN], a1[4], b1[FN];  // fragments of the even and the odd sub-steps
+  auto read = [&](const uint8_t *st, int s, intx4 (&af)[4], intx4 (&bf)[FN]) {
     const uint32_t pos = 16 * ((2 * s + h) ^ sw);
 #pragma unroll
     for (int f = 0; f < 4; ++f) {
       af[f] = *reinterpret_cast<const intx4 *>(st + rdA + 32 * kStep * f + pos);
-      bf[f] = *reinterpret_cast<const intx4 *>(st + rdB + 32 * kStep * f + pos);
+      if (f < FN) bf[f] = *reinterpret_cast<const intx4 *>(st + rdB + 32 * kStep * f + pos);
     }
   };
-  auto multiply = [&](const intx4 (&af)[4], const intx4 (&bf)[4]) {
+  auto multiply = [&](const intx4 (&af)[4], const intx4 (&bf)[FN]) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < FN; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[j][i] = __builtin_amdgcn_mfma_i32_32x32x32_i8(bf[j], af[i], acc[j][i], 0, 0, 0);
   };
@@ -471,34 +481,35 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_int8_big_kernel(I8Args p) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) af[f][e] = in ? af[f][e] : 0;
   };
-  // an MFMA, then a fragment read, eight times, and eight MFMAs under which the reads land
+  // an MFMA, then a fragment read, for every read, and the other MFMAs, under which the reads land
   auto order = [&]() {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < 4 + FN; ++q) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
     }
-    __builtin_amdgcn_sched_group_barrier(0x008, 8, 0);
+    __builtin_amdgcn_sched_group_barrier(0x008, HALF ? 2 : 8, 0);
   };
 
   if (steps > 0) {
-    end_of_k(0);
 #pragma unroll
-    for (int q = 0; q < 16; ++q) load(smem, 0, q);
-    if (steps > 1) {
-      end_of_k(1);
+    for (int s = 0; s < S; ++s) {
+      if (s < steps) {
+        end_of_k(s);
 #pragma unroll
-      for (int q = 0; q < 16; ++q) load(smem + kBigStage, 1, q);
-      wait_vmcnt<16>();
-    } else {
-      wait_vmcnt<0>();
+        for (int q = 0; q < NL; ++q) load(smem + s * kStage, s, q);
+      }
     }
+    if (steps >= S)
+      wait_vmcnt<(S - 1) * NL>();
+    else
+      wait_vmcnt<0>();
     lds_barrier();
     read(smem, 0, a0, b0);
   }
-  // One step out of stage cur, whose sub-step 0 is in a0, b0; then cur takes the loads of step kt + 2.
+  // One step out of stage cur, whose sub-step 0 is in a0, b0; then cur takes the loads of step kt + S.
   auto step = [&](uint8_t *__restrict__ cur, const uint8_t *__restrict__ nxt, int32_t kt) {
-    end_of_k(kt + 2);
+    end_of_k(kt + S);
     read(cur, 1, a1, b1);
     multiply(a0, b0);
     order();
@@ -508,33 +519,30 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_int8_big_kernel(I8Args p) {
     read(cur, 3, a1, b1);
     multiply(a0, b0);
     order();
-    wait_vmcnt<0>();
+    wait_vmcnt<(S - 2) * NL>();
     wait_lgkmcnt0();
     lds_barrier();
     read(nxt, 0, a0, b0);
 #pragma unroll
-    for (int q = 0; q < 16; ++q) load(cur, kt + 2, q);
+    for (int q = 0; q < NL; ++q) load(cur, kt + S, q);
     multiply(a1, b1);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
+    for (int q = 0; q < 4 * FN; ++q) {
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      if (q < 4 + FN) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);  // a direct load
-    }
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      if (HALF && q < 4) __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
     }
   };
   int32_t kt = 0;
   uint32_t cur = 0;
+  const auto after = [](uint32_t st) { return st == (S - 1) * kStage ? 0 : st + kStage; };
 #pragma clang loop unroll(disable)
-  for (; kt + 2 < steps; ++kt) {
-    step(smem + cur, smem + (cur ^ kBigStage), kt);
-    cur ^= kBigStage;
+  for (; kt + S < steps; ++kt) {
+    step(smem + cur, smem + after(cur), kt);
+    cur = after(cur);
   }
-  // the last two steps: nothing left to load
+  // the last S steps: nothing left to load
 #pragma clang loop unroll(disable)
   for (; kt < steps; ++kt) {
     const uint8_t *const st = smem + cur;
@@ -547,10 +555,13 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_int8_big_kernel(I8Args p) {
     read(st, 3, a1, b1);
     clear(kt, 2, a0);
     multiply(a0, b0);
-    wait_vmcnt<0>();
+    if (S > 2 && kt + 2 < steps)
+      wait_vmcnt<NL>();
+    else
+      wait_vmcnt<0>();
     wait_lgkmcnt0();
     lds_barrier();
-    cur ^= kBigStage;
+    cur = after(cur);
     if (kt + 1 < steps) read(smem + cur, 0, a0, b0);
     clear(kt, 3, a1);
     multiply(a1, b1);
@@ -559,7 +570,19 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_int8_big_kernel(I8Args p) {
   // every wave is done with the stages
   wait_lgkmcnt0();
   lds_barrier();
-  store_tile<4, 4, OUT_BF16>(p, acc, smem + wave * kRegion, t, n0 + wn, wm, lane);
+  store_tile<4, FN, OUT_BF16>(p, acc, smem + wave * kRegion, t, n0 + wn, wm, lane);
+}
+
+template <bool OUT_BF16>
+__global__ __launch_bounds__(kThreads, 1) void gemm_int8_big_kernel(I8Args p) {
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kBigLds];
+  TileRows t;
+  int32_t tn;
+  if (!find_tile<256>(p, all_tiles<256>(p), blockIdx.x, t, tn)) return;
+  if (t.m_end - t.m0 > 128)
+    big_tile<OUT_BF16, false>(p, smem, t, tn);
+  else
+    big_tile<OUT_BF16, true>(p, smem, t, tn);
 }
 
 // ---- few rows: weight streaming -------------------------------------------------------------------------

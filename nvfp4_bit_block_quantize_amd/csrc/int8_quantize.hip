@@ -1,4 +1,4 @@
-// int8_quantize.hip -- rows of fp32 / bf16 to 8-bit integers, one fp32 scale a row: s = RN(amax / 127),
+// int8_quantize.hip -- rows of fp32 / bf16 to 8-bit integers, one fp32 scale a row: s = RN(amax * RN(1 / 127)),
 // q = rint(RN(x * RN(1 / s))).  HBM-bound: a row is read once and stays in registers between its
 // maximum and its encode (rows too long for that are read again, from the cache).  Rounding to the
 // nearest integer, ties to even, is the addition of 1.5 * 2^23, whose sum holds q in its low byte
@@ -75,7 +75,7 @@ __global__ __launch_bounds__(256) void int8_quantize_kernel(const void *x, int64
       __syncthreads();
     }
     if (!live) continue;  // (only with T == 64, where nothing waits for this wave)
-    const float s = m / 127.0f;
+    const float s = m * (1.0f / 127.0f);
     const bool zero = !(s >= kTiny);
     const float inv = zero ? 0.0f : 1.0f / s;
     if (tid == 0) scales[r] = zero ? 0.0f : s;

@@ -26,6 +26,9 @@ constexpr int kOneBlockTokens = 64;    // routed and planned by one workgroup
 constexpr int kOneBlockSlots = 4096;   // planned from given ids by one workgroup
 constexpr int64_t kMaxBlocks = int64_t(1) << 20;  // of a launch (2^32 threads or more do not launch)
 constexpr size_t kOneBlockKeys = 60 * 1024;
+// Up to this many tokens one workgroup suffices whatever the other sizes (16 x 512 keys are 32 KB, 16 x 32 slots
+// less than kOneBlockSlots), and no workspace is needed.
+constexpr int64_t kAlwaysOneBlock = 16;
 constexpr float kNegInf = -__builtin_huge_valf();
 
 // Value of the lane CTRL away in the DPP row of 16 lanes.
@@ -768,7 +771,9 @@ hipError_t run_route_backward(RouteBwdArgs p, bool bf16, bool sigmoid, hipStream
 
 }  // namespace
 
-size_t moe_workspace_bytes(int64_t experts) { return static_cast<size_t>(kPlanChunks) * experts * sizeof(int32_t); }
+size_t moe_workspace_bytes(int64_t tokens, int64_t experts) {
+  return tokens <= kAlwaysOneBlock ? 0 : static_cast<size_t>(kPlanChunks) * experts * sizeof(int32_t);
+}
 
 hipError_t launch_moe_plan(const int32_t *ids, int64_t slots, int64_t experts, int32_t *offsets, int32_t *rows,
                            int32_t *pos, int32_t *counts, hipStream_t stream) {

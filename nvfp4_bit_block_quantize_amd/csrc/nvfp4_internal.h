@@ -181,7 +181,7 @@ hipError_t launch_moe_route(const MoeRouteArgs &a);
 hipError_t launch_moe_route_backward(const MoeRouteBackwardArgs &a);
 hipError_t launch_moe_plan(const int32_t *ids, int64_t slots, int64_t experts, int32_t *offsets, int32_t *rows,
                            int32_t *pos, int32_t *counts, hipStream_t stream);
-size_t moe_workspace_bytes(int64_t experts);
+size_t moe_workspace_bytes(int64_t tokens, int64_t experts);
 hipError_t launch_moe_gather(const MoeRowsArgs &a);
 hipError_t launch_moe_combine(const MoeRowsArgs &a);
 hipError_t launch_moe_combine_backward(const MoeRowsArgs &a);

@@ -93,7 +93,7 @@ def plan(ids, E):
 def int8_rows(x):
     """8-bit rows by the definition (scale, reciprocal and product are 32-bit numbers)."""
     x = np.asarray(x, dtype=np.float32)
-    s = (np.abs(x).max(axis=1) / np.float32(127)).astype(np.float32)
+    s = (np.abs(x).max(axis=1) * (np.float32(1) / np.float32(127))).astype(np.float32)
     s = np.where(s >= np.finfo(np.float32).tiny, s, np.float32(0)).astype(np.float32)
     with np.errstate(divide="ignore"):
         inv = np.where(s > 0, np.float32(1) / s, np.float32(0)).astype(np.float32)

@@ -20,7 +20,7 @@ def _call(name, defaults, **changes):
     return getattr(nv.lib(), name)(*args.values())
 
 
-ROUTE = dict(logits=P, dtype=nv.NVFP4_F32, tokens=8, experts=64, ld=64, bias=None, num_groups=1, group_top_k=1, top_k=4,
+ROUTE = dict(logits=P, dtype=nv.NVFP4_F32, tokens=80, experts=64, ld=64, bias=None, num_groups=1, group_top_k=1, top_k=4,
              flags=0, scale=1.0, ids=P, weights=P, offsets=P, rows=P, pos=P, workspace=P, stream=None)
 
 
@@ -55,7 +55,7 @@ def test_route_backward(changes, status):
     assert _call("nvfp4_moe_route_backward", BWD, **changes) == status
 
 
-PLAN = dict(ids=P, tokens=8, top_k=4, experts=64, offsets=P, rows=P, pos=P, workspace=P, stream=None)
+PLAN = dict(ids=P, tokens=80, top_k=4, experts=64, offsets=P, rows=P, pos=P, workspace=P, stream=None)
 
 
 @pytest.mark.parametrize("changes,status", [
@@ -139,6 +139,7 @@ def test_block_norm_backward(changes, status):
 def test_workspace_sizes():
     L = nv.lib()
     assert L.nvfp4_moe_workspace_size(100, 64, 4) >= 64 * 4 and L.nvfp4_moe_workspace_size(100, 0, 4) == 0
+    assert L.nvfp4_moe_workspace_size(16, 512, 32) == 0
     assert L.nvfp4_block_norm_workspace_size(4, 64) >= 2 * 4 * 64 * 4 and L.nvfp4_block_norm_workspace_size(4, 0) == 0
 
 

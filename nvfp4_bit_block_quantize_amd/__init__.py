@@ -399,6 +399,7 @@ class BlockNormGrads:
 
 
 def _raw_stream(t: torch.Tensor):
+    """The current stream of t's device, as a number (torch.cuda.current_stream builds an object first)."""
     return torch._C._cuda_getCurrentRawStream(t.device.index) if t.is_cuda else None
 
 
@@ -408,27 +409,27 @@ def _addr(t: Optional[torch.Tensor]):
 
 def _want(where: str, name: str, t: Optional[torch.Tensor], dtype: torch.dtype, shape, like: torch.Tensor):
     """A contiguous tensor of this dtype and shape on the device of `like`."""
-    if t is None:
+    if t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == like.device):
         return
     if t.dtype is not dtype:
         raise TypeError(f"{where}: {name} must be {dtype}, is {t.dtype}")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{where}: {name} must be a contiguous {list(shape)}, is {list(t.shape)}")
-    if t.device != like.device:
-        raise ValueError(f"{where}: {name} is on {t.device}, not {like.device}")
+    raise ValueError(f"{where}: {name} is on {t.device}, not {like.device}")
 
 
 def _matrix(where: str, name: str, t: torch.Tensor) -> int:
     """Leading dimension of a matrix with unit column stride."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{where}: {name} must be 2-D with unit column stride")
-    cols = t.shape[1]
-    if t.shape[0] <= 1:
-        return cols
-    ld = t.stride(0)
-    if ld < cols:
-        raise ValueError(f"{where}: rows of {name} overlap")
-    return ld
+    if t.dim() == 2:
+        rows, cols = t.shape
+        ld, unit = t.stride()
+        if unit == 1 or cols <= 1:
+            if rows <= 1:
+                return cols
+            if ld >= cols:
+                return ld
+            raise ValueError(f"{where}: rows of {name} overlap")
+    raise ValueError(f"{where}: {name} must be 2-D with unit column stride")
 
 
 def _empty_plan(tokens: int, top_k: int, experts: int, device) -> MoEPlan:
@@ -530,12 +531,15 @@ def nvfp4_moe_combine(y: torch.Tensor, plan: MoEPlan, weights: Optional[torch.Te
         raise ValueError(f"{where}: y has {y.shape[0]} rows, the plan {T * k}")
     _want(where, "plan.pos", plan.pos, torch.int32, (T, k), y)
     _want(where, "weights", weights, torch.float32, (T, k), y)
+    ldo = D
     if out is None:
         out = torch.empty((T, D), dtype=y.dtype, device=y.device)
     elif out.shape != (T, D) or out.dtype != y.dtype or out.device != y.device:
         raise ValueError(f"{where}: out must be [{T}, {D}] like y")
+    else:
+        ldo = _matrix(where, "out", out)
     st = lib().nvfp4_moe_combine(y.data_ptr(), _dtype_code(y.dtype), T, D, ldy, plan.pos.data_ptr(), _addr(weights), k,
-                                 out.data_ptr(), _matrix(where, "out", out), _raw_stream(y))
+                                 out.data_ptr(), ldo, _raw_stream(y))
     _check(st, where)
     return out
 
@@ -566,8 +570,9 @@ def nvfp4_int8_quantize(x: torch.Tensor, out: Optional[Int8Tensor] = None) -> In
     ld = _matrix(where, "x", x)
     R, K = x.shape
     if out is None:
-        out = Int8Tensor(torch.empty((R, K), dtype=torch.int8, device=x.device),
-                         torch.empty((R,), dtype=torch.float32, device=x.device), R, K)
+        # (empty_like is the cheapest way to a tensor, and a few tokens' call is mostly that)
+        out = Int8Tensor(torch.empty_like(x, dtype=torch.int8, memory_format=torch.contiguous_format),
+                         torch.empty(R, dtype=torch.float32, device=x.device), R, K)
     else:
         _want(where, "out.data", out.data, torch.int8, (R, K), x)
         _want(where, "out.scales", out.scales, torch.float32, (R,), x)
@@ -586,10 +591,11 @@ def nvfp4_int8_gemm(a: Int8Tensor, b: Int8Tensor, out_dtype: torch.dtype = torch
     where = "nvfp4_int8_gemm"
     if a.k != b.k:
         raise ValueError(f"{where}: a has K={a.k}, b has K={b.k}")
-    _want(where, "a.data", a.data, torch.int8, (a.rows, a.k), a.data)
-    _want(where, "a.scales", a.scales, torch.float32, (a.rows,), a.data)
-    _want(where, "b.data", b.data, torch.int8, (b.groups * b.rows, b.k), a.data)
-    _want(where, "b.scales", b.scales, torch.float32, (b.groups * b.rows,), a.data)
+    ad, asc, bd, bsc, n = a.data, a.scales, b.data, b.scales, b.groups * b.rows
+    _want(where, "a.data", ad, torch.int8, (a.rows, a.k), ad)
+    _want(where, "a.scales", asc, torch.float32, (a.rows,), ad)
+    _want(where, "b.data", bd, torch.int8, (n, b.k), ad)
+    _want(where, "b.scales", bsc, torch.float32, (n,), ad)
     M, offsets, rows, div = a.rows, None, None, 1
     if plan is not None:
         if plan.experts != b.groups:
@@ -604,16 +610,18 @@ def nvfp4_int8_gemm(a: Int8Tensor, b: Int8Tensor, out_dtype: torch.dtype = torch
     elif gather or b.groups != 1:
         raise ValueError(f"{where}: a grouped product needs a plan")
     if out is None:
-        out = torch.empty((M, b.rows), dtype=out_dtype, device=a.data.device)
-    elif out.shape != (M, b.rows) or out.device != a.data.device:
-        raise ValueError(f"{where}: out must be [{M}, {b.rows}] on {a.data.device}")
+        out = torch.empty((M, b.rows), dtype=out_dtype, device=ad.device)
+        ldc = b.rows
+    elif out.shape != (M, b.rows) or out.device != ad.device:
+        raise ValueError(f"{where}: out must be [{M}, {b.rows}] on {ad.device}")
+    else:
+        ldc = _matrix(where, "out", out)
     if workspace is None and plan is None:
         size = lib().nvfp4_int8_gemm_workspace_size(M, b.rows, b.k)
         if size:
-            workspace = torch.empty(size // 4, dtype=torch.int32, device=a.data.device)
-    st = lib().nvfp4_int8_gemm(a.data.data_ptr(), a.scales.data_ptr(), a.rows, b.data.data_ptr(), b.scales.data_ptr(), M,
-                               b.rows, b.k, out.data_ptr(), _dtype_code(out.dtype), max(_matrix(where, "out", out), 1),
-                               b.groups, offsets, rows, div, _addr(workspace), _raw_stream(a.data))
+            workspace = torch.empty(size // 4, dtype=torch.int32, device=ad.device)
+    st = lib().nvfp4_int8_gemm(ad.data_ptr(), asc.data_ptr(), a.rows, bd.data_ptr(), bsc.data_ptr(), M, b.rows, b.k,
+                               out.data_ptr(), _dtype_code(out.dtype), max(ldc, 1), b.groups, offsets, rows, div, _addr(workspace), _raw_stream(ad))
     _check(st, where)
     return out
 
@@ -655,7 +663,7 @@ def nvfp4_block_norm(x: torch.Tensor, y: Optional[torch.Tensor] = None, w_post: 
         x_out = torch.empty_like(x)
     else:
         _want(where, "x_out", x_out, x.dtype, (T, D), x)
-    n = torch.empty((T, D), dtype=y_dtype, device=dev) if w_pre is not None else None
+    n = torch.empty_like(x, dtype=y_dtype) if w_pre is not None else None
     rstd = torch.empty((2, T), dtype=torch.float32, device=dev)
     at = rstd.data_ptr()
     st = lib().nvfp4_block_norm(x.data_ptr(), _dtype_code(x.dtype), _addr(y), _dtype_code(y_dtype), T, D, _addr(w_post),

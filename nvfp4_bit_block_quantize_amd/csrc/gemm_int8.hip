@@ -703,12 +703,11 @@ __global__ __launch_bounds__(kThreads) void gemm_int8_few_kernel(I8Args p) {
   }
 }
 
-// C from the splits' sums: four columns a lane.
+// C from the splits' sums: four columns a lane, a row of the grid a row.
 template <bool OUT_BF16>
 __global__ __launch_bounds__(kThreads) void int8_sum_kernel(I8Args p) {
-  const int64_t u = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x, per_row = p.partial_ld / 4;
-  const int64_t row = u / per_row, col = u % per_row * 4;
-  if (row >= p.M || col >= p.N) return;
+  const int64_t row = blockIdx.y, col = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * 4;
+  if (col >= p.N) return;
   intx4 t = {0, 0, 0, 0};
 #pragma unroll 4
   for (int s = 0; s < p.splits; ++s)
@@ -766,7 +765,7 @@ hipError_t run_few(const Int8GemmArgs &a, const I8Args &p, int64_t most) {
     gemm_int8_few_kernel<MT, false><<<grid, dim3(kThreads), 0, a.stream>>>(p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
-  const dim3 sums(static_cast<uint32_t>((a.M * p.partial_ld / 4 + kThreads - 1) / kThreads));
+  const dim3 sums(static_cast<uint32_t>((p.partial_ld / 4 + kThreads - 1) / kThreads), static_cast<uint32_t>(a.M));
   if (a.c_dtype == 1)
     int8_sum_kernel<true><<<sums, dim3(kThreads), 0, a.stream>>>(p);
   else

@@ -32,14 +32,16 @@ __device__ __forceinline__ uint2 encode8(const float (&f)[8], float inv) {
   return make_uint2(w[0], w[1]);
 }
 
-// T threads a row, NV pieces of 8 elements a thread in registers (NV == 0: any row length, read twice).
+// T threads a row (64: four rows a workgroup), NV pieces of 8 elements a thread in registers (NV == 0: any row
+// length, read twice).
 template <bool BF16, int T, int NV>
-__global__ __launch_bounds__(256) void int8_quantize_kernel(const void *x, int64_t rows, int64_t cols, int64_t ldx,
+__global__ __launch_bounds__(T < 256 ? 256 : T) void int8_quantize_kernel(const void *x, int64_t rows, int64_t cols, int64_t ldx,
                                                             int8_t *q, float *scales) {
-  __shared__ float part[4];
+  constexpr int kRows = T < 256 ? 256 / T : 1;
+  __shared__ float part[16];
   const uint32_t tid = threadIdx.x % T;
   const int pieces = static_cast<int>(cols / 8);
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * (256 / T); r0 < rows; r0 += gridDim.x * (256ll / T)) {
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * kRows; r0 < rows; r0 += gridDim.x * static_cast<int64_t>(kRows)) {
     const int64_t r = r0 + threadIdx.x / T;
     const bool live = r < rows;
     const int64_t row = live ? r : rows - 1;
@@ -68,10 +70,11 @@ __global__ __launch_bounds__(256) void int8_quantize_kernel(const void *x, int64
       }
     }
     m = wave_max(m);
-    if constexpr (T == 256) {
+    if constexpr (T >= 256) {
       if ((threadIdx.x & 63u) == 0) part[threadIdx.x >> 6] = m;
       __syncthreads();
-      m = fmaxf(fmaxf(part[0], part[1]), fmaxf(part[2], part[3]));
+#pragma unroll
+      for (int w = 0; w < T / 64; ++w) m = fmaxf(m, part[w]);
       __syncthreads();
     }
     if (!live) continue;  // (only with T == 64, where nothing waits for this wave)
@@ -104,13 +107,19 @@ template <bool BF16>
 hipError_t run(const Int8QuantArgs &a) {
   const int64_t pieces = a.cols / 8;
   auto go = [&](auto *kernel, int threads_per_row) {
-    const int64_t per_block = 256 / threads_per_row;
+    const int64_t per_block = threads_per_row < 256 ? 256 / threads_per_row : 1;
     const int64_t blocks = (a.rows + per_block - 1) / per_block;
     // (a grid of 2^32 threads or more does not launch: a workgroup walks several rows then)
-    kernel<<<dim3(static_cast<uint32_t>(blocks < (1 << 20) ? blocks : 1 << 20)), dim3(256), 0, a.stream>>>(
-        a.x, a.rows, a.cols, a.ldx, a.q, a.scales);
+    kernel<<<dim3(static_cast<uint32_t>(blocks < (1 << 20) ? blocks : 1 << 20)),
+             dim3(threads_per_row < 256 ? 256 : threads_per_row), 0, a.stream>>>(a.x, a.rows, a.cols, a.ldx, a.q, a.scales);
     return hipGetLastError();
   };
+  // a few long rows: as many threads a row as there are, since only the latency of a row counts
+  if (a.rows <= 256 && pieces > 256) {
+    if (pieces <= 1024) return go(int8_quantize_kernel<BF16, 1024, 1>, 1024);
+    if (pieces <= 2048) return go(int8_quantize_kernel<BF16, 1024, 2>, 1024);
+    if (pieces <= 4096) return go(int8_quantize_kernel<BF16, 1024, 4>, 1024);
+  }
   // rows of up to 1024 elements: a wave each, so that short rows still fill their lanes
   if (pieces <= 64) return go(int8_quantize_kernel<BF16, 64, 1>, 64);
   if (pieces <= 128) return go(int8_quantize_kernel<BF16, 64, 2>, 64);

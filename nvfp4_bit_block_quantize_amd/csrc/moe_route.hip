@@ -10,7 +10,7 @@
 // Plan.  A counting sort, stable in the slots: each chunk of tokens counts its experts (the routing
 // kernel does so itself), and a second kernel gives every slot its row: the experts' totals and the
 // counts of the chunks before it, then the slot's rank among its chunk's equal ids, found with ballots
-// over the id's bits.  Up to 64 tokens (one chunk) the routing workgroup does all of it: one launch.
+// over the id's bits.  Up to 16 tokens (one chunk) the routing workgroup does all of it: one launch.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -22,13 +22,11 @@ namespace {
 
 constexpr int kMaxExperts = 512;
 constexpr int kPlanThreads = 1024;     // 16 waves
-constexpr int kOneBlockTokens = 64;    // routed and planned by one workgroup
 constexpr int kOneBlockSlots = 4096;   // planned from given ids by one workgroup
 constexpr int64_t kMaxBlocks = int64_t(1) << 20;  // of a launch (2^32 threads or more do not launch)
-constexpr size_t kOneBlockKeys = 60 * 1024;
-// Up to this many tokens one workgroup suffices whatever the other sizes (16 x 512 keys are 32 KB, 16 x 32 slots
-// less than kOneBlockSlots), and no workspace is needed.
-constexpr int64_t kAlwaysOneBlock = 16;
+// Tokens that one workgroup routes and plans (no workspace then): more would share its four SIMDs, and two
+// launches are faster (64 tokens over 256 experts: 19 us in one launch, 13 in two).
+constexpr int64_t kOneBlockTokens = 16;
 constexpr float kNegInf = -__builtin_huge_valf();
 
 // Value of the lane CTRL away in the DPP row of 16 lanes.
@@ -772,7 +770,7 @@ hipError_t run_route_backward(RouteBwdArgs p, bool bf16, bool sigmoid, hipStream
 }  // namespace
 
 size_t moe_workspace_bytes(int64_t tokens, int64_t experts) {
-  return tokens <= kAlwaysOneBlock ? 0 : static_cast<size_t>(kPlanChunks) * experts * sizeof(int32_t);
+  return tokens <= kOneBlockTokens ? 0 : static_cast<size_t>(kPlanChunks) * experts * sizeof(int32_t);
 }
 
 hipError_t launch_moe_plan(const int32_t *ids, int64_t slots, int64_t experts, int32_t *offsets, int32_t *rows,
@@ -819,8 +817,8 @@ hipError_t launch_moe_route(const MoeRouteArgs &a) {
   const int lanes = p.GS % epl == 0 ? p.GS / epl : 0;
   p.group_lanes = (lanes & (lanes - 1)) == 0 ? lanes : 0;
   const bool groups = p.group_k < p.G && p.group_lanes == 0;  // (through LDS)
-  size_t lds = groups ? static_cast<size_t>((a.tokens + 3) / 4 * 4) * 16 * epl * sizeof(float) : 0;
-  const bool one = plan && a.tokens <= kOneBlockTokens && lds <= kOneBlockKeys;
+  const bool one = plan && a.tokens <= kOneBlockTokens;
+  size_t lds = 0;
   int blocks, threads;
   if (one) {
     p.offsets = a.offsets;
@@ -829,13 +827,16 @@ hipError_t launch_moe_route(const MoeRouteArgs &a) {
     p.per = a.tokens;
     blocks = 1;
     threads = a.tokens * a.top_k <= 64 ? 512 : kPlanThreads;
-    if (lds < sizeof(PlanLds)) lds = sizeof(PlanLds);
+    lds = sizeof(PlanLds);
+    if (groups && lds < static_cast<size_t>(kOneBlockTokens) * 16 * epl * sizeof(float))
+      lds = static_cast<size_t>(kOneBlockTokens) * 16 * epl * sizeof(float);
   } else {
-
-    // chunks of whole workgroup steps (64 tokens where they are counted, in at most kPlanChunks chunks)
-    // (with groups, fewer tokens at once where their keys would pass 32 KB)
-    threads = !plan ? 256 : groups && epl >= 16 ? 8192 / epl : kPlanThreads;
+    // Chunks of whole workgroup steps, in at most kPlanChunks chunks where they are counted.  16 tokens a
+    // workgroup (a wave a SIMD) as long as there are compute units for them, then 32 and 64: a wave's latency
+    // is its instructions', so four waves a SIMD take four times as long.  With keys in LDS, at most 32 KB.
     const int64_t most = plan ? kPlanChunks : kMaxBlocks;
+    threads = !plan || a.tokens <= 16 * most ? 256 : a.tokens <= 32 * most ? 512 : kPlanThreads;
+    if (groups && threads * epl > 8192) threads = 8192 / epl;
     if (plan) p.counts = a.workspace;
     const int64_t at_once = threads / 16;
     p.per = ((a.tokens + most - 1) / most + at_once - 1) / at_once * at_once;

@@ -2,7 +2,8 @@
 // q = rint(RN(x * RN(1 / s))).  HBM-bound: a row is read once and stays in registers between its
 // maximum and its encode (rows too long for that are read again, from the cache).  Rounding to the
 // nearest integer, ties to even, is the addition of 1.5 * 2^23, whose sum holds q in its low byte
-// (|x / s| < 128, so the addition is exact up to that rounding).
+// (|x / s| < 128, so the addition is exact up to that rounding).  8192 x 4096 bf16 from HBM: 20 us, 5.0 TB/s (a 1
+// GiB copy: 5.1), 8192 x 14336: 71 us, 4.9 TB/s; 65536 x 512: 21 us, 4.8 TB/s.
 #include "nvfp4_internal.h"
 #include "vec_io.hpp"
 
@@ -114,7 +115,8 @@ hipError_t run(const Int8QuantArgs &a) {
              dim3(threads_per_row < 256 ? 256 : threads_per_row), 0, a.stream>>>(a.x, a.rows, a.cols, a.ldx, a.q, a.scales);
     return hipGetLastError();
   };
-  // a few long rows: as many threads a row as there are, since only the latency of a row counts
+  // a few long rows: as many threads a row as there are, since only the latency of a row counts (37 x 14336: 3.5 us,
+  // with 256 threads a row 6.0)
   if (a.rows <= 256 && pieces > 256) {
     if (pieces <= 1024) return go(int8_quantize_kernel<BF16, 1024, 1>, 1024);
     if (pieces <= 2048) return go(int8_quantize_kernel<BF16, 1024, 2>, 1024);

@@ -15,6 +15,7 @@
 // tile counts; those beyond the last tile leave.  A's rows may be read through the plan's slots.
 #include "gemm_common.hpp"
 #include "nvfp4_internal.h"
+#include "vec_io.hpp"
 
 namespace nvfp4 {
 namespace {
@@ -145,9 +146,7 @@ __device__ __forceinline__ bool find_tile(const I8Args &p, const Tiles &w, int32
 }
 
 // 16 bytes at an address aligned to an element only (rows of C may start anywhere).
-struct __attribute__((packed, aligned(2))) Bytes16 {
-  uint32_t v[4];
-};
+typedef uint32_t any_u32x4 __attribute__((ext_vector_type(4), aligned(2)));
 struct __attribute__((packed, aligned(4))) Floats4 {
   float v[4];
 };
@@ -246,7 +245,7 @@ __device__ __forceinline__ void store_tile(const I8Args &p, const intx16 (&acc)[
         if (32 * i + row >= rows_left || col >= cols_left) continue;
         uint8_t *at = out + ((32 * i + row) * p.ldc + col) * ES;
         if (col + V <= cols_left) {
-          *reinterpret_cast<Bytes16 *>(at) = Bytes16{{v.x, v.y, v.z, v.w}};
+          __builtin_nontemporal_store((any_u32x4){v.x, v.y, v.z, v.w}, reinterpret_cast<any_u32x4 *>(at));
         } else {
           // (a loop, to keep this rare path's code short)
           uint64_t lo = v.x | static_cast<uint64_t>(v.y) << 32, hi = v.z | static_cast<uint64_t>(v.w) << 32;
@@ -601,7 +600,7 @@ struct Few {
   static constexpr int kStages = MT <= 2 ? 6 : MT == 4 ? 5 : 6;  // MT <= 4: two workgroups share a compute unit's LDS
 };
 
-template <int MT, bool OUT_BF16>
+template <int MT, bool OUT_BF16, bool ONCE>
 __global__ __launch_bounds__(kThreads) void gemm_int8_few_kernel(I8Args p) {
   using F = Few<MT>;
   __shared__ __attribute__((aligned(1024))) uint8_t smem[F::kStages * F::kStage];
@@ -641,8 +640,14 @@ __global__ __launch_bounds__(kThreads) void gemm_int8_few_kernel(I8Args p) {
     const uint32_t k0 = static_cast<uint32_t>(kt0 + kt) * kStep;
     const bool whole = k0 + kStep <= p.K;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      lds_load16(srcB[i] + (whole || k0 + chunkB[i] < p.K ? k0 + chunkB[i] : 0), st + F::kB + (16 * wave + 8 * i) * kStep);
+    for (int i = 0; i < 2; ++i) {
+      const uint8_t *from = srcB[i] + (whole || k0 + chunkB[i] < p.K ? k0 + chunkB[i] : 0);
+      uint8_t *to = st + F::kB + (16 * wave + 8 * i) * kStep;
+      if constexpr (ONCE)
+        __builtin_amdgcn_global_load_lds((global_void *)from, (lds_void *)to, 16, 0, 2);  // (2: non-temporal)
+      else
+        lds_load16(from, to);
+    }
 #pragma unroll
     for (int i = 0; i < F::kA; ++i)
       lds_load16(whole || k0 + chunkA[i] < p.K ? srcA[i] + (k0 + chunkA[i]) : reinterpret_cast<const uint8_t *>(&kZeros),
@@ -755,14 +760,16 @@ int pick_tile(const Int8GemmArgs &a) {
   return t128 < t64 ? (one ? 129 : 128) : 64;
 }
 
-template <int MT>
+// ONCE: the weights are too large for the cache, so they are read past it (8 tokens, 8 of 64 experts of 1536 x 4096,
+// 403 MB, about 40 of them read: 46 -> 40 us; 59 MB of weights with non-temporal loads 12.2 -> 13.1).
+template <int MT, bool ONCE>
 hipError_t run_few(const Int8GemmArgs &a, const I8Args &p, int64_t most) {
   const uint32_t tiles_n = static_cast<uint32_t>((a.N + 63) / 64), rows = static_cast<uint32_t>((most + 16 * MT - 1) / (16 * MT));
   const dim3 grid(tiles_n, rows, a.offsets ? a.num_groups : p.splits);
   if (a.c_dtype == 1)
-    gemm_int8_few_kernel<MT, true><<<grid, dim3(kThreads), 0, a.stream>>>(p);
+    gemm_int8_few_kernel<MT, true, ONCE><<<grid, dim3(kThreads), 0, a.stream>>>(p);
   else
-    gemm_int8_few_kernel<MT, false><<<grid, dim3(kThreads), 0, a.stream>>>(p);
+    gemm_int8_few_kernel<MT, false, ONCE><<<grid, dim3(kThreads), 0, a.stream>>>(p);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.splits == 1) return e;
   const dim3 sums(static_cast<uint32_t>((p.partial_ld / 4 + kThreads - 1) / kThreads), static_cast<uint32_t>(a.M));
@@ -811,10 +818,14 @@ hipError_t launch_int8_gemm(const Int8GemmArgs &a) {
     p.splits = steps > 0 ? (steps + p.split_steps - 1) / p.split_steps : 1;
     p.partial = a.workspace;
     p.partial_ld = (a.N + 63) / 64 * 64;
-    if (most <= 16) return run_few<1>(a, p, most);
-    if (most <= 32) return run_few<2>(a, p, most);
-    if (most <= 64) return run_few<4>(a, p, most);
-    return run_few<8>(a, p, most);
+    const auto few = [&](auto once) {
+      constexpr bool kOnce = decltype(once)::value;
+      if (most <= 16) return run_few<1, kOnce>(a, p, most);
+      if (most <= 32) return run_few<2, kOnce>(a, p, most);
+      if (most <= 64) return run_few<4, kOnce>(a, p, most);
+      return run_few<8, kOnce>(a, p, most);
+    };
+    return a.num_groups * a.N * a.K >= kStreamBytes ? few(std::true_type{}) : few(std::false_type{});
   }
   const int tile = pick_tile(a);
   if (tile == 256) return run_tiles<256, 256>(a, p, gemm_int8_big_kernel<true>, gemm_int8_big_kernel<false>);

@@ -16,17 +16,33 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((vec_f32x2){lo, hi}, vec_bf16x2));
 }
 
+// From this many bytes on (the Infinity Cache's 256 MiB) data cannot stay in it: what a call reads or multiplies of
+// such data goes through non-temporal loads, which keep it from pushing out what the call writes.  Below, those
+// loads cost time where the data is still cached.
+constexpr int64_t kStreamBytes = int64_t(256) << 20;
+
+typedef uint32_t vec_u32x4 __attribute__((ext_vector_type(4)));
+template <bool ONCE>
+__device__ __forceinline__ uint4 load16(const uint8_t *p) {
+  if constexpr (ONCE) {
+    const vec_u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const vec_u32x4 *>(p));
+    return make_uint4(v.x, v.y, v.z, v.w);
+  } else {
+    return *reinterpret_cast<const uint4 *>(p);
+  }
+}
+
 // Eight consecutive elements from element index i (a multiple of 8) on.
 template <bool BF16>
 struct Raw8 {
   uint4 v[BF16 ? 1 : 2];
 };
-template <bool BF16>
+template <bool BF16, bool ONCE = false>
 __device__ __forceinline__ Raw8<BF16> load8(const void *base, int64_t i) {
   Raw8<BF16> r;
-  const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(base) + i * (BF16 ? 2 : 4));
-  r.v[0] = p[0];
-  if constexpr (!BF16) r.v[1] = p[1];
+  const uint8_t *p = static_cast<const uint8_t *>(base) + i * (BF16 ? 2 : 4);
+  r.v[0] = load16<ONCE>(p);
+  if constexpr (!BF16) r.v[1] = load16<ONCE>(p + 16);
   return r;
 }
 template <bool BF16>

@@ -11,8 +11,8 @@
 //   dy = r_y (w_post q - yh mean(w_post q yh)),   q = alpha g d  (w_post NULL: dy = q)
 //   dw_pre = sum dn xh,  dw_post = sum q yh,  dgate = sum alpha d p
 // With a gate by channel both dw_post = g S and dgate = w_post S for S = sum alpha d yh, so two column
-// sums serve three gradients.  A workgroup walks rows with its column sums in registers and leaves
-// one partial row a sum; a second kernel adds the partial rows in order (no atomics: the bits do not
+// sums serve three gradients.  A workgroup walks rows with its column sums in registers (LDS above
+// 4096 columns) and leaves one partial row a sum; a second kernel adds the partial rows in order (no atomics: the bits do not
 // depend on the schedule).
 #include "nvfp4_internal.h"
 #include "vec_io.hpp"
@@ -55,11 +55,11 @@ __device__ __forceinline__ void row_totals(float (&v)[N], float (*part)[N]) {
   }
 }
 
-// Factors of a lane's columns: in registers for the whole call (EARLY, one piece a lane) or loaded at each use.
-template <int T, int NV>
+// Factors of a lane's columns: in registers for the whole call (EARLY pieces a lane at most) or loaded at each use.
+template <int T, int NV, int EARLY>
 struct Factors {
-  static constexpr bool kEarly = NV == 1;
-  float v[8];
+  static constexpr bool kEarly = NV <= EARLY;
+  float v[kEarly ? NV : 1][8];
   const float *p;
   float shift;
   __device__ __forceinline__ void load(int c, float (&f)[8]) const {
@@ -69,25 +69,27 @@ struct Factors {
   }
   __device__ __forceinline__ Factors(const float *w, float s, int pieces) : p(w), shift(s) {
     if constexpr (kEarly)
-      if (p && static_cast<int>(threadIdx.x) < pieces) load(threadIdx.x, v);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (p && static_cast<int>(threadIdx.x) + T * i < pieces) load(threadIdx.x + T * i, v[i]);
   }
-  __device__ __forceinline__ void get(int c, float (&f)[8]) const {
+  __device__ __forceinline__ void get(int i, float (&f)[8]) const {
     if constexpr (kEarly) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) f[q] = v[q];
+      for (int q = 0; q < 8; ++q) f[q] = v[i][q];
     } else {
-      load(c, f);
+      load(threadIdx.x + T * i, f);
     }
   }
 };
 
 // y (a piece of the block's output) to its share of x' - x without alpha: gate (y r_post w_post); yh: y r_post.
 template <bool YB, class F>
-__device__ __forceinline__ void block_output(const NormArgs &p, const F &w_post, const F &gate, const Raw8<YB> &gr, int c,
+__device__ __forceinline__ void block_output(const NormArgs &p, const F &w_post, const F &gate, const Raw8<YB> &gr, int i,
                                              float r_post, float (&y)[8]) {
   float f[8];
   if (p.w_post) {
-    w_post.get(c, f);
+    w_post.get(i, f);
 #pragma unroll
     for (int q = 0; q < 8; ++q) y[q] = (y[q] * r_post) * f[q];
   }
@@ -96,7 +98,7 @@ __device__ __forceinline__ void block_output(const NormArgs &p, const F &w_post,
 #pragma unroll
     for (int q = 0; q < 8; ++q) y[q] *= f[q];
   } else if (p.gate_c) {
-    gate.get(c, f);
+    gate.get(i, f);
 #pragma unroll
     for (int q = 0; q < 8; ++q) y[q] *= f[q];
   }
@@ -104,20 +106,20 @@ __device__ __forceinline__ void block_output(const NormArgs &p, const F &w_post,
 
 // A workgroup a row at a time, NV pieces of 8 columns a thread; with one piece a thread the next row's loads go
 // out before this row's sums.
-template <bool XB, bool YB, int T, int NV>
+template <bool XB, bool YB, int T, int NV, bool ONCE>
 __global__ __launch_bounds__(T) void block_norm_kernel(NormArgs p) {
   __shared__ float part[2][16][1];
   const int tid = threadIdx.x;
-  const Factors<T, NV> w_post(p.w_post, p.shift, p.pieces), gate(p.gate_c, 0.0f, p.pieces),
+  const Factors<T, NV, 1> w_post(p.w_post, p.shift, p.pieces), gate(p.gate_c, 0.0f, p.pieces),
       w_pre(p.w_pre, p.shift, p.pieces);
   auto fetch = [&](int64_t row, Raw8<XB> (&a)[NV], Raw8<YB> (&b)[NV], Raw8<YB> (&g)[NV]) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = tid + T * i;
       if (c < p.pieces) {
-        if (p.y) b[i] = load8<YB>(p.y, row * p.d + 8ll * c);
-        a[i] = load8<XB>(p.x, row * p.d + 8ll * c);
-        if (p.gate_t) g[i] = load8<YB>(p.gate_t, row * p.d + 8ll * c);
+        if (p.y) b[i] = load8<YB, ONCE>(p.y, row * p.d + 8ll * c);
+        a[i] = load8<XB, ONCE>(p.x, row * p.d + 8ll * c);
+        if (p.gate_t) g[i] = load8<YB, ONCE>(p.gate_t, row * p.d + 8ll * c);
       }
     }
   };
@@ -155,7 +157,7 @@ __global__ __launch_bounds__(T) void block_norm_kernel(NormArgs p) {
         if (p.y) {
           float y[8];
           unpack8<YB>(yr[i], y);
-          block_output<YB>(p, w_post, gate, gr[i], c, r_post, y);
+          block_output<YB>(p, w_post, gate, gr[i], i, r_post, y);
 #pragma unroll
           for (int q = 0; q < 8; ++q) x1[i][q] = fmaf(p.alpha, y[q], x1[i][q]);
           store8<XB>(p.x_out, base + 8ll * c, x1[i]);
@@ -173,7 +175,7 @@ __global__ __launch_bounds__(T) void block_norm_kernel(NormArgs p) {
         const int c = tid + T * i;
         if (c < p.pieces) {
           float f[8], n[8];
-          w_pre.get(c, f);
+          w_pre.get(i, f);
 #pragma unroll
           for (int q = 0; q < 8; ++q) n[q] = (x1[i][q] * r_pre) * f[q];
           store8<YB>(p.n, base + 8ll * c, n);
@@ -201,7 +203,7 @@ struct BackwardRow {
   Raw8<YB> y[NV], dn[NV], gate[NV];
   float r_post, r_pre;
 };
-template <bool XB, bool YB, int T, int NV>
+template <bool ONCE, int T, bool XB, bool YB, int NV>
 __device__ __forceinline__ void load_row(const NormArgs &p, int64_t r, BackwardRow<XB, YB, NV> &v) {
   v.r_post = p.w_post ? p.rstd_post[r] : 1.0f;
   v.r_pre = p.w_pre ? p.rstd_pre[r] : 0.0f;
@@ -211,47 +213,96 @@ __device__ __forceinline__ void load_row(const NormArgs &p, int64_t r, BackwardR
     if (c < p.pieces) {
       const int64_t at = r * p.d + 8ll * c;
       if (p.w_pre) {
-        v.x[i] = load8<XB>(p.x, at);
-        v.dn[i] = load8<YB>(p.dn, at);
+        v.x[i] = load8<XB, ONCE>(p.x, at);
+        v.dn[i] = load8<YB, ONCE>(p.dn, at);
       }
-      if (p.y) v.y[i] = load8<YB>(p.y, at);
-      if (p.dx_out) v.dx[i] = load8<XB>(p.dx_out, at);
-      if (p.gate_t) v.gate[i] = load8<YB>(p.gate_t, at);
+      if (p.y) v.y[i] = load8<YB, ONCE>(p.y, at);
+      if (p.dx_out) v.dx[i] = load8<XB, ONCE>(p.dx_out, at);
+      if (p.gate_t) v.gate[i] = load8<YB, ONCE>(p.gate_t, at);
     }
   }
 }
 
+// Sums over a workgroup's rows of a lane's columns, two kinds: in registers with one piece a lane, else each lane's own
+// 16-byte pieces in LDS, whose traffic is an eighth of what a row's time has room for.
+template <int T, int NV>
+struct ColumnSums {
+  static constexpr bool kLds = NV > 1;
+  static constexpr int kBytes = kLds ? 2 * NV * T * 32 : 16;
+  float v[2][8];
+  float4 *lds;
+  __device__ __forceinline__ float4 &piece(int kind, int i, int half) const {
+    return lds[((kind * NV + i) * 2 + half) * T + threadIdx.x];
+  }
+  __device__ __forceinline__ explicit ColumnSums(uint8_t *area) : lds(reinterpret_cast<float4 *>(area)) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[k][q] = 0.0f;
+      if constexpr (kLds)
+#pragma unroll
+        for (int i = 0; i < 2 * NV; ++i) piece(k, i / 2, i & 1) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+  }
+  __device__ __forceinline__ void get(int kind, int i, float (&s)[8]) const {
+    if constexpr (kLds) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float4 w = piece(kind, i, h);
+        s[4 * h] = w.x;
+        s[4 * h + 1] = w.y;
+        s[4 * h + 2] = w.z;
+        s[4 * h + 3] = w.w;
+      }
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) s[q] = v[kind][q];
+    }
+  }
+  __device__ __forceinline__ void add(int kind, int i, const float (&a)[8], const float (&b)[8]) {
+    float s[8];
+    get(kind, i, s);
+#pragma unroll
+    for (int q = 0; q < 8; ++q) s[q] = fmaf(a[q], b[q], s[q]);
+    if constexpr (kLds) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) piece(kind, i, h) = make_float4(s[4 * h], s[4 * h + 1], s[4 * h + 2], s[4 * h + 3]);
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) v[kind][q] = s[q];
+    }
+  }
+};
+
 // One barrier a row: with a = alpha g w_post yh, the second sum mean(a d) follows from three sums that need no
 // other, mean(a d) = mean(a (dx' + r_x w_pre dn)) - r_x mean(w_pre dn xh) mean(a xh).  The loads
-// of the next row (bf16: of the next two, for as many bytes in flight) go out before this row's sums, up to 4096
-// columns; more would not fit in registers.  8192 x 4096 bf16: 84 us with the column sums, 4.8 TB/s (97 us with
-// one row ahead, 190 us with none and 16 columns a thread).
-template <bool XB, bool YB, int T, int NV>
+// of the next row (bf16 up to 4096 columns: of the next two, for as many bytes in flight) go out before this row's
+// sums, up to 8192 columns; more would not fit in registers.  Measured with the column sums: 8192 x 4096 bf16 72 us,
+// 5.6 TB/s (84 us before the loads were non-temporal, 97 us with one row ahead, 190 us with none and 16 columns a
+// thread); 4096 x 8192 93 us, 4.3 TB/s (factors loaded at each use 105); 2048 x 16384 118 us, 3.4 TB/s (187 us with
+// the column sums in registers, which spilled); fp32 4096 x 8192 174 us, 4.6 TB/s (factors in registers spill: 264).
+template <bool XB, bool YB, int T, int NV, bool ONCE>
 __global__ __launch_bounds__(T) void block_norm_backward_kernel(NormArgs p) {
-  constexpr int kAhead = NV > 1 ? 0 : XB && YB ? 2 : 1;
+  constexpr int kAhead = NV > 2 ? 0 : XB && YB && NV == 1 ? 2 : 1;
   __shared__ float part[2][16][3];
+  __shared__ __attribute__((aligned(16))) uint8_t column_area[ColumnSums<T, NV>::kBytes];
   const int tid = threadIdx.x;
-  const Factors<T, NV> w_post(p.w_post, p.shift, p.pieces), gate(p.gate_c, 0.0f, p.pieces),
+  const Factors<T, NV, XB && YB ? 2 : 1> w_post(p.w_post, p.shift, p.pieces), gate(p.gate_c, 0.0f, p.pieces),
       w_pre(p.w_pre, p.shift, p.pieces);
-  float s_pre[NV][8], s_post[NV][8];  // column sums of this workgroup's rows
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int q = 0; q < 8; ++q) s_pre[i][q] = s_post[i][q] = 0.0f;
-
+  ColumnSums<T, NV> columns(column_area);  // 0: of dn xh, 1: of q yh
   const float inv_d = 1.0f / static_cast<float>(p.d);
   BackwardRow<XB, YB, NV> row, next, after;
   int64_t r = blockIdx.x;  // (there are no more workgroups than rows)
-  load_row<XB, YB, T, NV>(p, r, row);
+  load_row<ONCE, T>(p, r, row);
   if constexpr (kAhead == 2)
-    if (r + gridDim.x < p.tokens) load_row<XB, YB, T, NV>(p, r + gridDim.x, next);
+    if (r + gridDim.x < p.tokens) load_row<ONCE, T>(p, r + gridDim.x, next);
   for (int turn = 0; r < p.tokens; r += gridDim.x, turn ^= 1) {
     const int64_t base = r * p.d;
     const bool more = r + gridDim.x < p.tokens;
     if constexpr (kAhead == 1)
-      if (more) load_row<XB, YB, T, NV>(p, r + gridDim.x, next);
+      if (more) load_row<ONCE, T>(p, r + gridDim.x, next);
     if constexpr (kAhead == 2)
-      if (r + 2ll * gridDim.x < p.tokens) load_row<XB, YB, T, NV>(p, r + 2ll * gridDim.x, after);
+      if (r + 2ll * gridDim.x < p.tokens) load_row<ONCE, T>(p, r + 2ll * gridDim.x, after);
     const float r_post = row.r_post, r_pre = row.r_pre;
     float xh[NV][8], d[NV][8];  // x' r_pre; dx' + r_pre w_pre dn
     float sums[3] = {0.0f, 0.0f, 0.0f};
@@ -265,7 +316,7 @@ __global__ __launch_bounds__(T) void block_norm_backward_kernel(NormArgs p) {
         if (p.dx_out) unpack8<XB>(row.dx[i], d[i]);
         if (p.y) {
           unpack8<YB>(row.y[i], a);
-          block_output<YB>(p, w_post, gate, row.gate[i], c, r_post, a);
+          block_output<YB>(p, w_post, gate, row.gate[i], i, r_post, a);
 #pragma unroll
           for (int q = 0; q < 8; ++q) a[q] *= p.alpha;
         }
@@ -273,16 +324,16 @@ __global__ __launch_bounds__(T) void block_norm_backward_kernel(NormArgs p) {
           float dn[8];
           unpack8<XB>(row.x[i], xh[i]);
           unpack8<YB>(row.dn[i], dn);
-          w_pre.get(c, f);
+          w_pre.get(i, f);
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             xh[i][q] = (xh[i][q] + a[q]) * r_pre;
-            s_pre[i][q] = fmaf(dn[q], xh[i][q], s_pre[i][q]);
             const float u = dn[q] * f[q];
             sums[0] = fmaf(u, xh[i][q], sums[0]);
             d[i][q] = fmaf(r_pre, u, d[i][q]);
             sums[2] = fmaf(a[q], xh[i][q], sums[2]);
           }
+          columns.add(0, i, dn, xh[i]);
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q) sums[1] = fmaf(a[q], d[i][q], sums[1]);
@@ -313,7 +364,7 @@ __global__ __launch_bounds__(T) void block_norm_backward_kernel(NormArgs p) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) dg[q] = d[i][q] * yh[q];
             if (p.w_post) {
-              w_post.get(c, f);
+              w_post.get(i, f);
 #pragma unroll
               for (int q = 0; q < 8; ++q) dg[q] *= f[q];
             }
@@ -322,15 +373,14 @@ __global__ __launch_bounds__(T) void block_norm_backward_kernel(NormArgs p) {
 #pragma unroll
             for (int q = 0; q < 8; ++q) d[i][q] *= f[q];
           }
-#pragma unroll
-          for (int q = 0; q < 8; ++q) s_post[i][q] = fmaf(d[i][q], yh[q], s_post[i][q]);
+          columns.add(1, i, d[i], yh);
           if (p.gate_c) {
-            gate.get(c, f);
+            gate.get(i, f);
 #pragma unroll
             for (int q = 0; q < 8; ++q) d[i][q] *= f[q];
           }
           if (p.w_post) {
-            w_post.get(c, f);
+            w_post.get(i, f);
 #pragma unroll
             for (int q = 0; q < 8; ++q) d[i][q] = r_post * fmaf(-c2, yh[q], d[i][q] * f[q]);
           }
@@ -342,15 +392,22 @@ __global__ __launch_bounds__(T) void block_norm_backward_kernel(NormArgs p) {
       row = next;
       if constexpr (kAhead == 2) next = after;
     } else {
-      if (more) load_row<XB, YB, T, NV>(p, r + gridDim.x, row);
+      if (more) load_row<ONCE, T>(p, r + gridDim.x, row);
     }
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = tid + T * i;
     if (c < p.pieces) {
-      if (p.w_pre) store8<false>(p.parts, blockIdx.x * static_cast<int64_t>(p.d) + 8ll * c, s_pre[i]);
-      if (p.y) store8<false>(p.parts, (static_cast<int64_t>(gridDim.x) + blockIdx.x) * p.d + 8ll * c, s_post[i]);
+      float v[8];
+      if (p.w_pre) {
+        columns.get(0, i, v);
+        store8<false>(p.parts, blockIdx.x * static_cast<int64_t>(p.d) + 8ll * c, v);
+      }
+      if (p.y) {
+        columns.get(1, i, v);
+        store8<false>(p.parts, (static_cast<int64_t>(gridDim.x) + blockIdx.x) * p.d + 8ll * c, v);
+      }
     }
   }
 }
@@ -446,30 +503,37 @@ int64_t backward_blocks(int64_t tokens, int64_t d) {
   return tokens < n ? tokens : n;
 }
 
-template <bool BWD, bool XB, bool YB, int T, int NV>
+template <bool BWD, bool XB, bool YB, bool ONCE, int T, int NV>
 hipError_t go(const NormArgs &p, int64_t blocks, hipStream_t stream) {
   if constexpr (BWD)
-    block_norm_backward_kernel<XB, YB, T, NV><<<dim3(static_cast<uint32_t>(blocks)), dim3(T), 0, stream>>>(p);
+    block_norm_backward_kernel<XB, YB, T, NV, ONCE><<<dim3(static_cast<uint32_t>(blocks)), dim3(T), 0, stream>>>(p);
   else
-    block_norm_kernel<XB, YB, T, NV><<<dim3(static_cast<uint32_t>(blocks)), dim3(T), 0, stream>>>(p);
+    block_norm_kernel<XB, YB, T, NV, ONCE><<<dim3(static_cast<uint32_t>(blocks)), dim3(T), 0, stream>>>(p);
   return hipGetLastError();
 }
 
-template <bool BWD, bool XB, bool YB>
+template <bool BWD, bool XB, bool YB, bool ONCE>
 hipError_t run(const NormArgs &p, int64_t blocks, hipStream_t stream) {
-  if (p.pieces <= 64) return go<BWD, XB, YB, 64, 1>(p, blocks, stream);
-  if (p.pieces <= 128) return go<BWD, XB, YB, 128, 1>(p, blocks, stream);
-  if (p.pieces <= 256) return go<BWD, XB, YB, 256, 1>(p, blocks, stream);
-  if (p.pieces <= 512) return go<BWD, XB, YB, 512, 1>(p, blocks, stream);
-  if (p.pieces <= 1024) return go<BWD, XB, YB, 512, 2>(p, blocks, stream);
-  return go<BWD, XB, YB, 512, 4>(p, blocks, stream);
+  if (p.pieces <= 64) return go<BWD, XB, YB, ONCE, 64, 1>(p, blocks, stream);
+  if (p.pieces <= 128) return go<BWD, XB, YB, ONCE, 128, 1>(p, blocks, stream);
+  if (p.pieces <= 256) return go<BWD, XB, YB, ONCE, 256, 1>(p, blocks, stream);
+  if (p.pieces <= 512) return go<BWD, XB, YB, ONCE, 512, 1>(p, blocks, stream);
+  if (p.pieces <= 1024) return go<BWD, XB, YB, ONCE, 512, 2>(p, blocks, stream);
+  return go<BWD, XB, YB, ONCE, 512, 4>(p, blocks, stream);
 }
 
+// Non-temporal loads where the forward pass's four matrices are too large for the cache: forward and backward of
+// 8192 x 4096 bf16 132 -> 121 us, 16384 x 4096 258 -> 223, 65536 x 512 148 -> 138; with
+// half the rows, 4096 x 4096, 63 -> 69.  Not for fp32, whose lanes read 32 bytes in two such loads (each half of a
+// line then comes from the L2 twice: 258 -> 267).
 template <bool BWD>
 hipError_t run_types(const BlockNormArgs &a, const NormArgs &p, int64_t blocks) {
-  if (a.x_dtype == 1)
-    return a.y_dtype == 1 ? run<BWD, true, true>(p, blocks, a.stream) : run<BWD, true, false>(p, blocks, a.stream);
-  return a.y_dtype == 1 ? run<BWD, false, true>(p, blocks, a.stream) : run<BWD, false, false>(p, blocks, a.stream);
+  const bool once = a.tokens * a.d * 8 >= kStreamBytes;
+  if (a.x_dtype == 1 && a.y_dtype == 1)
+    return once ? run<BWD, true, true, true>(p, blocks, a.stream) : run<BWD, true, true, false>(p, blocks, a.stream);
+  if (a.x_dtype == 1) return run<BWD, true, false, false>(p, blocks, a.stream);
+  return a.y_dtype == 1 ? run<BWD, false, true, false>(p, blocks, a.stream)
+                        : run<BWD, false, false, false>(p, blocks, a.stream);
 }
 
 }  // namespace

@@ -38,7 +38,6 @@ struct I8Args {
   uint8_t *c;
   int64_t ldc;
   int32_t tiles_n;
-  int32_t tiles_m;  // plain form
   int32_t groups;
   const int32_t *offsets;  // NULL: one group of M rows
   const int32_t *rows;     // NULL: row r of C is row r of A
@@ -61,16 +60,28 @@ struct TileRows {
   int64_t m0, m_end;
 };
 
-// Finds tile row `tm` among the groups' ceil(rows / BM) tile rows; false beyond the last.  Every lane of
-// the wave takes part and has the result.
-template <int BM>
+// Tile rows of a group of n rows, for tiles of BM rows: all of them, or only those of more than half a tile's rows,
+// or only those of less (a group has at most one).
+enum TileKind { kAllTiles, kFullTiles, kHalfTiles };
+template <int BM, TileKind KIND>
+__device__ __forceinline__ int32_t tile_rows(int64_t n) {
+  if (n <= 0) return 0;
+  const int32_t rest = static_cast<int32_t>(n % BM), whole = static_cast<int32_t>(n / BM);
+  if constexpr (KIND == kAllTiles) return whole + (rest > 0);
+  if constexpr (KIND == kFullTiles) return whole + (rest > BM / 2);
+  return rest > 0 && rest <= BM / 2;
+}
+
+// Finds tile row `tm` among the groups' tile rows; false beyond the last.  Every lane of the wave takes part
+// and has the result.
+template <int BM, TileKind KIND>
 __device__ __forceinline__ bool find_rows(const int32_t *offsets, int groups, int32_t tm, TileRows &out) {
   const int lane = threadIdx.x & 63;
   int32_t before = 0;
   for (int g0 = 0; g0 < groups; g0 += 64) {
     const int g = g0 + lane;
     const int32_t lo = g < groups ? offsets[g] : 0, hi = g < groups ? offsets[g + 1] : 0;
-    const int32_t n = hi > lo ? (hi - lo + BM - 1) / BM : 0;
+    const int32_t n = tile_rows<BM, KIND>(static_cast<int64_t>(hi) - lo);
     int32_t s = n;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
@@ -80,10 +91,10 @@ __device__ __forceinline__ bool find_rows(const int32_t *offsets, int groups, in
     const uint64_t past = __ballot(before + s > tm);
     if (past) {
       const int at = __builtin_ctzll(past);
-      const int32_t first = before + __shfl(s - n, at);
+      const int32_t first = before + __shfl(s - n, at), m_lo = __shfl(lo, at), m_hi = __shfl(hi, at);
       out.group = g0 + at;
-      out.m0 = __shfl(lo, at) + static_cast<int64_t>(tm - first) * BM;
-      out.m_end = __shfl(hi, at);
+      out.m0 = m_lo + static_cast<int64_t>(KIND == kHalfTiles ? (m_hi - m_lo) / BM : tm - first) * BM;
+      out.m_end = m_hi;
       return true;
     }
     before += __shfl(s, 63);
@@ -91,14 +102,13 @@ __device__ __forceinline__ bool find_rows(const int32_t *offsets, int groups, in
   return false;
 }
 // Tile rows of all groups.
-template <int BM>
-__device__ __forceinline__ int32_t count_rows(const int32_t *offsets, int groups) {
+template <int BM, TileKind KIND>
+__device__ __forceinline__ int32_t count_rows(const I8Args &p) {
+  if (!p.offsets) return tile_rows<BM, KIND>(p.M);
   const int lane = threadIdx.x & 63;
   int32_t n = 0;
-  for (int g = lane; g < groups; g += 64) {
-    const int32_t lo = offsets[g], hi = offsets[g + 1];
-    n += hi > lo ? (hi - lo + BM - 1) / BM : 0;
-  }
+  for (int g = lane; g < p.groups; g += 64)
+    n += tile_rows<BM, KIND>(static_cast<int64_t>(p.offsets[g + 1]) - p.offsets[g]);
 #pragma unroll
   for (int d = 32; d > 0; d /= 2) n += __shfl_xor(n, d);
   return __builtin_amdgcn_readfirstlane(n);
@@ -111,28 +121,20 @@ __device__ __forceinline__ int64_t a_row(const I8Args &p, int64_t r) {
   return s >= 0 && s < p.a_rows ? s : 0;
 }
 
-// The tiles of a launch, dealt so that each XCD (workgroup i runs on XCD i mod 8) gets a contiguous range of
-// them, walked in bands of tile rows (band_tile).
-struct Tiles {
-  int32_t rows, total, per;  // tile rows, tiles, tiles of an XCD
-};
-template <int BM>
-__device__ __forceinline__ Tiles all_tiles(const I8Args &p) {
-  Tiles w;
-  w.rows = p.offsets ? count_rows<BM>(p.offsets, p.groups) : p.tiles_m;
-  w.total = w.rows * p.tiles_n;
-  w.per = (w.total + 7) >> 3;
-  return w;
+// The number of workgroup `id` among `total` items (false beyond them), dealt so that each XCD (workgroup i runs on
+// XCD i mod 8) gets a contiguous range of them.
+__device__ __forceinline__ bool deal(int32_t id, int32_t total, int32_t &item) {
+  const int32_t per = (total + 7) >> 3;
+  item = (id & 7) * per + (id >> 3);
+  return (id >> 3) < per && item < total;
 }
-// The tile of workgroup number `id`; false where there is none.
-template <int BM>
-__device__ __forceinline__ bool find_tile(const I8Args &p, const Tiles &w, int32_t id, TileRows &t, int32_t &tn) {
-  const int32_t tile = (id & 7) * w.per + (id >> 3);
-  if ((id >> 3) >= w.per || tile >= w.total) return false;
+// Tile number `tile` of `rows` tile rows, walked in bands of tile rows (band_tile); false where there is none.
+template <int BM, TileKind KIND>
+__device__ __forceinline__ bool find_tile(const I8Args &p, int32_t rows, int32_t tile, TileRows &t, int32_t &tn) {
   int32_t tm;
-  band_tile(tile, p.tiles_n, w.rows, tm, tn);
+  band_tile(tile, p.tiles_n, rows, tm, tn);
   if (p.offsets) {
-    if (!find_rows<BM>(p.offsets, p.groups, tm, t)) return false;
+    if (!find_rows<BM, KIND>(p.offsets, p.groups, tm, t)) return false;
     t.group = __builtin_amdgcn_readfirstlane(t.group);
     t.m0 = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(t.m0));
     t.m_end = __builtin_amdgcn_readfirstlane(static_cast<int32_t>(t.m_end));
@@ -140,7 +142,7 @@ __device__ __forceinline__ bool find_tile(const I8Args &p, const Tiles &w, int32
     return t.m0 >= 0 && t.m0 < t.m_end;
   }
   t.group = 0;
-  t.m0 = static_cast<int64_t>(tm) * BM;
+  t.m0 = KIND == kHalfTiles ? p.M / BM * BM : static_cast<int64_t>(tm) * BM;
   t.m_end = p.M;
   return true;
 }
@@ -279,7 +281,9 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_int8_kernel(I8Args p) {
 
   TileRows t;
   int32_t tn;
-  if (!find_tile<TM>(p, all_tiles<TM>(p), blockIdx.x, t, tn)) return;
+  const int32_t rows = count_rows<TM, kAllTiles>(p);
+  int32_t tile;
+  if (!deal(blockIdx.x, rows * p.tiles_n, tile) || !find_tile<TM, kAllTiles>(p, rows, tile, t, tn)) return;
   const int64_t n0 = static_cast<int64_t>(tn) * TN;
   const uint8_t *const b = p.b + static_cast<int64_t>(t.group) * p.N * p.K;
 
@@ -395,9 +399,8 @@ constexpr int kBigLds = 3 * 384 * kStep;  // three stages of half tiles, or two 
 //
 // HALF: 128 x 256 tiles, each wave all 128 rows by 64 columns (eight MFMAs a sub-step): half the work where a
 // group's (or the matrix's) last tile row has at most 128 rows.  Such a tile has half the time a step to cover
-// its loads: three stages of 48 KB, loaded two to three steps ahead.  (32768 x 1536 x 4096 over 64 experts:
-// 256 us, against 183 us for one expert; the last, partly filled round is what is left.  Half tiles after all
-// full ones 247-262 us; lines fetched into the L2 some steps ahead 263-305 us.)
+// its loads: three stages of 48 KB, loaded two to three steps ahead.  (Lines fetched into the L2 some steps ahead, or
+// weights by non-temporal loads, were no faster.)
 template <bool OUT_BF16, bool HALF>
 __device__ __forceinline__ void big_tile(const I8Args &p, uint8_t *smem, const TileRows &t, int32_t tn) {
   constexpr int FN = HALF ? 2 : 4;                       // B fragments a wave
@@ -572,16 +575,40 @@ __device__ __forceinline__ void big_tile(const I8Args &p, uint8_t *smem, const T
   store_tile<4, FN, OUT_BF16>(p, acc, smem + wave * kRegion, t, n0 + wn, wm, lane);
 }
 
+// Full tiles that stay whole: all of them, or, where what exceeds whole rounds of 256 workgroups is at most a round of
+// half tiles, the whole rounds'.  Half tiles run last.  32768 x 1536 x 4096 over 64 experts (3.4 rounds): 256 us with half
+// tiles in between and none split, 245 so, against 183 for one expert; 16384 rows (1.9 rounds) 184 -> 150; plain 4096 x
+// 6144 x 4096 (1.5 rounds) 104 -> 92.
+__host__ __device__ inline int32_t kept_tiles(int32_t full, int32_t half) {
+  const int64_t halves = 2ll * full + half;
+  const int64_t whole = halves / 512 * 256;
+  return halves % 512 <= 256 && whole < full ? static_cast<int32_t>(whole) : full;
+}
+
 template <bool OUT_BF16>
 __global__ __launch_bounds__(kThreads, 1) void gemm_int8_big_kernel(I8Args p) {
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kBigLds];
   TileRows t;
   int32_t tn;
-  if (!find_tile<256>(p, all_tiles<256>(p), blockIdx.x, t, tn)) return;
-  if (t.m_end - t.m0 > 128)
-    big_tile<OUT_BF16, false>(p, smem, t, tn);
-  else
-    big_tile<OUT_BF16, true>(p, smem, t, tn);
+  const int32_t full_rows = count_rows<256, kFullTiles>(p), half_rows = count_rows<256, kHalfTiles>(p);
+  const int32_t full = full_rows * p.tiles_n, half = half_rows * p.tiles_n;
+  // the last round, in half tiles: where all of its work fits one round of them, the full tiles of it are split
+  const int32_t kept = kept_tiles(full, half), id = blockIdx.x, full_ids = (kept + 7) / 8 * 8;
+  int32_t item;
+  if (id < full_ids) {
+    if (deal(id, kept, item) && find_tile<256, kFullTiles>(p, full_rows, item, t, tn))
+      big_tile<OUT_BF16, false>(p, smem, t, tn);
+    return;
+  }
+  if (!deal(id - full_ids, half + 2 * (full - kept), item)) return;
+  if (item < half) {
+    if (!find_tile<256, kHalfTiles>(p, half_rows, item, t, tn)) return;
+  } else {
+    if (!find_tile<256, kFullTiles>(p, full_rows, kept + (item - half) / 2, t, tn)) return;
+    if ((item - half) & 1) t.m0 += 128;
+    if (t.m0 >= t.m_end) return;  // (a full tile has more than 128 rows, unless offsets pass the rows)
+  }
+  big_tile<OUT_BF16, true>(p, smem, t, tn);
 }
 
 // ---- few rows: weight streaming -------------------------------------------------------------------------
@@ -731,8 +758,8 @@ hipError_t run_tiles(const Int8GemmArgs &a, I8Args p, void (*bf16_kernel)(I8Args
   p.tiles_n = static_cast<int32_t>((a.N + TN - 1) / TN);
   // by expert: every group may have one partial tile row
   const int64_t rows = (a.M + TM - 1) / TM + (a.offsets ? a.num_groups : 0);
-  p.tiles_m = static_cast<int32_t>(rows);
-  const int64_t tiles = (rows * p.tiles_n + 7) / 8 * 8;
+  // (256-row tiles: both kinds are dealt in eights, and up to 128 full ones are split)
+  const int64_t tiles = (rows * p.tiles_n + 7) / 8 * 8 + (TM == 256 ? 8 + 128 : 0);
   if (tiles > kMaxTiles) return hipErrorInvalidValue;
   (a.c_dtype == 1 ? bf16_kernel : f32_kernel)<<<dim3(static_cast<uint32_t>(tiles)), dim3(kThreads), 0, a.stream>>>(p);
   return hipGetLastError();
@@ -753,7 +780,10 @@ int pick_tile(const Int8GemmArgs &a) {
   const double t64 = rounds(tiles(64)) * (0.21 * steps + 0.5) + 3.5;
   const bool one = tiles(128) <= 256;
   const double t128 = one ? 0.65 * steps + 4 : rounds(tiles(128)) * (0.5 * steps + 2) + 3;
-  const double t256 = rounds(tiles(256)) * (1.2 * steps + 6) + 6;
+  // (a last round of half tiles takes 0.62 of one: kept_tiles)
+  const int64_t last = tiles(256) % 256;
+  const double r256 = static_cast<double>(tiles(256) / 256) + (last == 0 ? 0.0 : last <= 128 ? 0.62 : 1.0);
+  const double t256 = r256 * (1.2 * steps + 6) + 6;
   // (a launch's tiles are bounded; larger tiles are fewer)
   const bool large = tiles(64) + (a.num_groups + 1) * ((a.N + 63) / 64) > kMaxTiles;
   if (large || (t256 < t128 && t256 < t64)) return 256;

@@ -1,5 +1,6 @@
 """The operators around the quantized products where their data is larger than the 256 MiB cache (they then read it
-with other loads), and block norms of rows above 4096 columns with several rows a workgroup.
+with other loads), block norms of rows above 4096 columns with several rows a workgroup, and 8-bit products of more
+than a round of 256 x 256 tiles.
 
 Tolerances are those of the small cases: a 32-bit sum of n products is within n x 2^-24 of their magnitudes, a bf16
 result adds one rounding; 8-bit products are exact."""
@@ -110,3 +111,24 @@ def test_weight_beyond_the_cache(M, N, K):
     got = nv.nvfp4_int8_gemm(a, b, F32).cpu()
     for cols in (slice(0, 70), slice(N - 70, N)):
         assert torch.equal(got[:, cols], _want(a.data, a.scales, b.data[cols], b.scales[cols], F32))
+
+
+@pytest.mark.parametrize("M,N,K", [(1999, 4000, 4096), (4500, 4096, 2064), (4096, 6100, 2048)])
+def test_product_with_a_last_round_of_half_tiles(M, N, K):
+    a, b = _weights(M, K, 1, 1), _weights(N, K, 1, 2)
+    got = nv.nvfp4_int8_gemm(a, b, BF16).cpu()
+    assert torch.equal(got, _want(a.data, a.scales, b.data, b.scales, BF16))
+
+
+@pytest.mark.parametrize("T,k,E,N,K,skew", [(1024, 8, 64, 1536, 2048, 0.7), (4096, 8, 8, 1000, 1024, 0.3), (4096, 8, 64, 1536, 1040, 1.0),
+                                            (1500, 2, 3, 4096, 2048, 0.0)])
+def test_experts_with_a_last_round_of_half_tiles(T, k, E, N, K, skew):
+    x, w = _weights(T, K, 1, 1), _weights(N, K, E, 2)
+    logits = torch.randn(T, E, device=DEV, generator=torch.Generator(device=DEV).manual_seed(3))
+    ids, _, plan = nv.nvfp4_moe_route(logits - skew * torch.log(1.0 + torch.arange(E, device=DEV)), k)
+    got = nv.nvfp4_int8_gemm(x, w, BF16, plan=plan, gather=True).cpu()
+    rows, off = plan.rows.long(), plan.offsets.cpu().tolist()
+    for e in range(E):
+        if off[e + 1] > off[e]:
+            src, r = rows[off[e]:off[e + 1]] // k, slice(e * N, (e + 1) * N)
+            assert torch.equal(got[off[e]:off[e + 1]], _want(x.data[src], x.scales[src], w.data[r], w.scales[r], BF16)), e

@@ -3,7 +3,8 @@
 // a row's columns and walks the token's slots, so the k loads of a lane are independent and a token's
 // own row (dout) is read once for all of its slots.  A token's sums run in the order of its slots.
 // 4096 tokens of 8 rows of 4096 bf16: the sum 55 us (302 MB, 5.5 TB/s), its gradient 101 us (570 MB, 5.6 TB/s); a
-// 1 GiB copy runs at 5.1 TB/s.  One to a few tokens: 4 us, the launch.
+// 1 GiB copy runs at 5.1 TB/s.  The gather 71 us (4.3 TB/s, nearly all writes).  16384 tokens of 8 rows of 512: gather 38
+// us, sum 24; of 128 fp32 19 and 13 (59 and 20 with a workgroup a row).  One to a few tokens: 4 us, the launch.
 #include "nvfp4_internal.h"
 #include "vec_io.hpp"
 
@@ -11,9 +12,8 @@ namespace nvfp4 {
 namespace {
 
 constexpr int kRowThreads = 256;
-// Workgroups of a launch; each walks its share of a larger problem (a grid of 2^32 threads or more does
-// not launch).
-constexpr int64_t kMaxBlocks = int64_t(1) << 20;
+// Workgroups along a launch's rows; each walks its share of a larger problem.
+constexpr int64_t kMaxBlocks = 65535;
 
 struct RowsArgs {
   const uint8_t *x;
@@ -22,15 +22,22 @@ struct RowsArgs {
   int64_t ld_dout;  // bytes
   int64_t tokens;
   int pieces;  // 16-byte pieces of a row
-  int col_blocks;
+  int lane_bits;  // gather, sum: 1 << lane_bits lanes a row (256 at most), so that short rows fill their workgroup
   const int32_t *pos, *rows;
   const float *weights;
   int k;
-  int64_t blocks;  // (row, column block) pairs, or tokens
   uint8_t *out;
   int64_t ldo;  // bytes
   float *dweights;
 };
+
+template <bool ONCE>
+__device__ __forceinline__ void store16(uint8_t *p, const uint4 &v) {
+  if constexpr (ONCE)
+    __builtin_nontemporal_store((vec_u32x4){v.x, v.y, v.z, v.w}, reinterpret_cast<vec_u32x4 *>(p));
+  else
+    *reinterpret_cast<uint4 *>(p) = v;
+}
 
 template <bool BF16>
 __device__ __forceinline__ void unpack16(const uint4 &v, float (&f)[BF16 ? 8 : 4]) {
@@ -58,27 +65,42 @@ __device__ __forceinline__ uint4 pack16(const float (&f)[BF16 ? 8 : 4]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// y[r] = x[rows[r] / k]; the dtype does not matter.
+// y[r] = x[rows[r] / k]; the dtype does not matter.  A lane moves its piece of kGatherRows rows at once.
+constexpr int kGatherRows = 4;
+template <bool ONCE>
 __global__ __launch_bounds__(kRowThreads) void gather_kernel(RowsArgs p) {
-  for (int64_t b = blockIdx.x; b < p.blocks; b += gridDim.x) {
-    const int64_t r = b / p.col_blocks;
-    const int c = static_cast<int>(b % p.col_blocks) * kRowThreads + threadIdx.x;
-    if (c >= p.pieces) continue;
-    const int64_t slot = p.rows[r];
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (slot >= 0 && slot < p.tokens * p.k) v = *reinterpret_cast<const uint4 *>(p.x + slot / p.k * p.ldx + 16ll * c);
-    *reinterpret_cast<uint4 *>(p.out + r * p.ldo + 16ll * c) = v;
+  const int c = blockIdx.x * kRowThreads + (threadIdx.x & ((1 << p.lane_bits) - 1));
+  if (c >= p.pieces) return;
+  const int64_t slots = p.tokens * p.k;
+  const int rows_at_once = kRowThreads >> p.lane_bits;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.y) * rows_at_once * kGatherRows + (threadIdx.x >> p.lane_bits); r0 < slots;
+       r0 += static_cast<int64_t>(gridDim.y) * rows_at_once * kGatherRows) {
+    uint4 v[kGatherRows];
+#pragma unroll
+    for (int u = 0; u < kGatherRows; ++u) {
+      const int64_t r = r0 + u * rows_at_once;
+      const uint32_t slot = r < slots ? static_cast<uint32_t>(p.rows[r]) : 0xFFFFFFFFu;
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (slot < static_cast<uint64_t>(slots))
+        v[u] = *reinterpret_cast<const uint4 *>(p.x + slot / static_cast<uint32_t>(p.k) * p.ldx + 16ll * c);
+    }
+#pragma unroll
+    for (int u = 0; u < kGatherRows; ++u) {
+      const int64_t r = r0 + u * rows_at_once;
+      if (r < slots) store16<ONCE>(p.out + r * p.ldo + 16ll * c, v[u]);
+    }
   }
 }
 
 template <bool BF16, bool ONCE>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(RowsArgs p) {
   constexpr int V = BF16 ? 8 : 4;
-  for (int64_t b = blockIdx.x; b < p.blocks; b += gridDim.x) {
-    const int64_t t = b / p.col_blocks;
-    const int c = static_cast<int>(b % p.col_blocks) * kRowThreads + threadIdx.x;
-    if (c >= p.pieces) continue;
-    const uint32_t slots = static_cast<uint32_t>(p.tokens * p.k);
+  const int c = blockIdx.x * kRowThreads + (threadIdx.x & ((1 << p.lane_bits) - 1));
+  if (c >= p.pieces) return;
+  const uint32_t slots = static_cast<uint32_t>(p.tokens * p.k);
+  const int rows_at_once = kRowThreads >> p.lane_bits;
+  for (int64_t t = static_cast<int64_t>(blockIdx.y) * rows_at_once + (threadIdx.x >> p.lane_bits); t < p.tokens;
+       t += static_cast<int64_t>(gridDim.y) * rows_at_once) {
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
@@ -110,14 +132,16 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(RowsArgs p) {
   }
 }
 
-// One workgroup a token; its lanes' partial dot products of eight slots at a time meet in LDS.
-template <bool BF16, bool ONCE>
+// LANES lanes a token, a wave or a workgroup; a workgroup's partial dot products of eight slots at a time meet in LDS.
+template <bool BF16, bool ONCE, int LANES>
 __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(RowsArgs p) {
-  constexpr int V = BF16 ? 8 : 4;
+  constexpr int V = BF16 ? 8 : 4, kTokens = kRowThreads / LANES;
   __shared__ float part[4][8];
   const int64_t slots = p.tokens * p.k;
   const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-  for (int64_t t = blockIdx.x; t < p.blocks; t += gridDim.x) {
+  const int first = threadIdx.x % LANES;
+  for (int64_t t = static_cast<int64_t>(blockIdx.x) * kTokens + threadIdx.x / LANES; t < p.tokens;
+       t += static_cast<int64_t>(gridDim.x) * kTokens) {
     const uint8_t *dout = p.dout + t * p.ld_dout;
     for (int j0 = 0; j0 < p.k; j0 += 8) {
       float dot[8], w[8];
@@ -133,7 +157,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(RowsArgs 
           w[j] = p.weights[t * p.k + j0 + j];
         }
       }
-      for (int c = threadIdx.x; c < p.pieces; c += kRowThreads) {
+      for (int c = first; c < p.pieces; c += LANES) {
         uint4 v[8];
         const uint4 dv = *reinterpret_cast<const uint4 *>(dout + 16ll * c);
 #pragma unroll
@@ -157,21 +181,28 @@ __global__ __launch_bounds__(kRowThreads) void combine_backward_kernel(RowsArgs 
         }
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float s = wave_sum(dot[j]);
-        if (lane == 0) part[wave][j] = s;
+      for (int j = 0; j < 8; ++j) dot[j] = wave_sum(dot[j]);
+      if constexpr (LANES == 64) {
+        float mine = dot[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) mine = lane == static_cast<uint32_t>(j) ? dot[j] : mine;
+        if (lane < 8 && j0 + static_cast<int>(lane) < p.k) p.dweights[t * p.k + j0 + lane] = mine;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (lane == 0) part[wave][j] = dot[j];
+        __syncthreads();
+        if (threadIdx.x < 8 && j0 + static_cast<int>(threadIdx.x) < p.k)
+          p.dweights[t * p.k + j0 + threadIdx.x] =
+              (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
+        __syncthreads();
       }
-      __syncthreads();
-      if (threadIdx.x < 8 && j0 + static_cast<int>(threadIdx.x) < p.k)
-        p.dweights[t * p.k + j0 + threadIdx.x] =
-            (part[0][threadIdx.x] + part[1][threadIdx.x]) + (part[2][threadIdx.x] + part[3][threadIdx.x]);
-      __syncthreads();
     }
-    // rows that no slot has: this workgroup looks after rows [t k, (t + 1) k)
+    // rows that no slot has: these lanes look after rows [t k, (t + 1) k)
     for (int j = 0; j < p.k; ++j) {
       const int64_t r = t * p.k + j;
       if (p.rows[r] < 0)
-        for (int c = threadIdx.x; c < p.pieces; c += kRowThreads)
+        for (int c = first; c < p.pieces; c += LANES)
           *reinterpret_cast<uint4 *>(p.out + r * p.ldo + 16ll * c) = make_uint4(0, 0, 0, 0);
     }
   }
@@ -186,7 +217,7 @@ RowsArgs rows_args(const MoeRowsArgs &a) {
   p.ld_dout = a.ld_dout * es;
   p.tokens = a.tokens;
   p.pieces = static_cast<int>(a.d * es / 16);
-  p.col_blocks = (p.pieces + kRowThreads - 1) / kRowThreads;
+  while (p.lane_bits < 8 && (1 << p.lane_bits) < p.pieces) ++p.lane_bits;
   p.pos = a.pos;
   p.rows = a.rows;
   p.weights = a.weights;
@@ -203,35 +234,47 @@ bool rows_once(const MoeRowsArgs &a) {
   return a.tokens * a.top_k * a.d * (a.dtype == 1 ? 2 : 4) >= kStreamBytes;
 }
 
-dim3 grid_of(const RowsArgs &p) { return dim3(static_cast<uint32_t>(p.blocks < kMaxBlocks ? p.blocks : kMaxBlocks)); }
+// A workgroup for every 256 columns and `rows` rows.
+dim3 grid_of(const RowsArgs &p, int64_t rows, int rows_a_group) {
+  const int64_t groups = (rows + rows_a_group - 1) / rows_a_group;
+  return dim3((p.pieces + kRowThreads - 1) / kRowThreads, static_cast<uint32_t>(groups < kMaxBlocks ? groups : kMaxBlocks));
+}
+
+// A wave a token up to 128 pieces, without barriers (16384 x 8 x 512 bf16 97 -> 55 us, 5.2 TB/s); at 512 pieces a workgroup
+// is faster (100 us against 109).
+template <bool BF16, bool ONCE>
+hipError_t run_backward(const RowsArgs &p, hipStream_t stream) {
+  const int64_t groups = p.pieces <= 128 ? (p.tokens + 3) / 4 : p.tokens;
+  const dim3 grid(static_cast<uint32_t>(groups < (1 << 20) ? groups : 1 << 20));
+  if (p.pieces <= 128)
+    combine_backward_kernel<BF16, ONCE, 64><<<grid, dim3(kRowThreads), 0, stream>>>(p);
+  else
+    combine_backward_kernel<BF16, ONCE, 256><<<grid, dim3(kRowThreads), 0, stream>>>(p);
+  return hipGetLastError();
+}
 
 }  // namespace
 
 hipError_t launch_moe_gather(const MoeRowsArgs &a) {
-  RowsArgs p = rows_args(a);
-  p.blocks = a.tokens * a.top_k * p.col_blocks;
-  gather_kernel<<<grid_of(p), dim3(kRowThreads), 0, a.stream>>>(p);
+  const RowsArgs p = rows_args(a);
+  auto *kernel = rows_once(a) ? gather_kernel<true> : gather_kernel<false>;
+  kernel<<<grid_of(p, a.tokens * a.top_k, (kRowThreads >> p.lane_bits) * kGatherRows), dim3(kRowThreads), 0, a.stream>>>(p);
   return hipGetLastError();
 }
 
 hipError_t launch_moe_combine(const MoeRowsArgs &a) {
-  RowsArgs p = rows_args(a);
-  p.blocks = a.tokens * p.col_blocks;
+  const RowsArgs p = rows_args(a);
   const bool once = rows_once(a);
   auto *kernel = a.dtype == 1 ? (once ? combine_kernel<true, true> : combine_kernel<true, false>)
                               : (once ? combine_kernel<false, true> : combine_kernel<false, false>);
-  kernel<<<grid_of(p), dim3(kRowThreads), 0, a.stream>>>(p);
+  kernel<<<grid_of(p, a.tokens, kRowThreads >> p.lane_bits), dim3(kRowThreads), 0, a.stream>>>(p);
   return hipGetLastError();
 }
 
 hipError_t launch_moe_combine_backward(const MoeRowsArgs &a) {
-  RowsArgs p = rows_args(a);
-  p.blocks = a.tokens;
-  const bool once = rows_once(a);
-  auto *kernel = a.dtype == 1 ? (once ? combine_backward_kernel<true, true> : combine_backward_kernel<true, false>)
-                              : (once ? combine_backward_kernel<false, true> : combine_backward_kernel<false, false>);
-  kernel<<<grid_of(p), dim3(kRowThreads), 0, a.stream>>>(p);
-  return hipGetLastError();
+  const RowsArgs p = rows_args(a);
+  if (rows_once(a)) return a.dtype == 1 ? run_backward<true, true>(p, a.stream) : run_backward<false, true>(p, a.stream);
+  return a.dtype == 1 ? run_backward<true, false>(p, a.stream) : run_backward<false, false>(p, a.stream);
 }
 
 }  // namespace nvfp4

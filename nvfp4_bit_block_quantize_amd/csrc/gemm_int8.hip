@@ -616,8 +616,8 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_int8_big_kernel(I8Args p) {
 // 16 MT rows of its expert: both pass through a deep LDS ring of whole 128-byte lines (direct loads, so
 // that the bytes in flight cost no registers), wave w multiplying weight rows [16 w, 16 w + 16) by all rows
 // (v_mfma_i32_16x16x64_i8; lane l: row l mod 16, bytes 16 (l / 16) of every 64).  Where that leaves compute
-// units without work (the plain form), the steps of K are split over grid.z, each split's integer sums go to the
-// workspace, and a second kernel adds and scales them.
+// units without work (the plain form), the steps of K are split over grid.y, each split's integer sums go to the
+// workspace, and a second kernel adds and scales them.  (By expert the grid's y is the expert and z its tile of rows.)
 template <int MT>
 struct Few {
   static constexpr int kRows = 16 * MT;
@@ -635,8 +635,8 @@ __global__ __launch_bounds__(kThreads) void gemm_int8_few_kernel(I8Args p) {
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t r16 = lane & 15u, g = lane >> 4;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 64;
-  const int32_t group = p.offsets ? blockIdx.z : 0;
-  int64_t m0 = static_cast<int64_t>(blockIdx.y) * F::kRows, m_end = p.M;
+  const int32_t group = p.offsets ? blockIdx.y : 0;
+  int64_t m0 = static_cast<int64_t>(blockIdx.z) * F::kRows, m_end = p.M;
   if (p.offsets) {
     const int64_t lo = p.offsets[group], hi = p.offsets[group + 1];
     m0 += lo;
@@ -645,7 +645,7 @@ __global__ __launch_bounds__(kThreads) void gemm_int8_few_kernel(I8Args p) {
   }
   // this split's steps
   const int32_t all = static_cast<int32_t>((p.K + kStep - 1) / kStep);
-  const int32_t kt0 = p.splits > 1 ? static_cast<int32_t>(blockIdx.z) * p.split_steps : 0;
+  const int32_t kt0 = p.splits > 1 ? static_cast<int32_t>(blockIdx.y) * p.split_steps : 0;
   const int32_t steps = p.splits > 1 ? min(p.split_steps, all - kt0) : all;
 
   const uint8_t *srcA[F::kA], *srcB[2];
@@ -724,7 +724,7 @@ __global__ __launch_bounds__(kThreads) void gemm_int8_few_kernel(I8Args p) {
     if (row >= m_end) continue;
     if (p.splits > 1) {
       // (the workspace's rows are padded to 64 columns)
-      *reinterpret_cast<intx4 *>(p.partial + (static_cast<int64_t>(blockIdx.z) * p.M + row) * p.partial_ld + col) = acc[i];
+      *reinterpret_cast<intx4 *>(p.partial + (static_cast<int64_t>(blockIdx.y) * p.M + row) * p.partial_ld + col) = acc[i];
       continue;
     }
     const float sa = p.a_scales[a_row(p, row)];
@@ -795,7 +795,8 @@ int pick_tile(const Int8GemmArgs &a) {
 template <int MT, bool ONCE>
 hipError_t run_few(const Int8GemmArgs &a, const I8Args &p, int64_t most) {
   const uint32_t tiles_n = static_cast<uint32_t>((a.N + 63) / 64), rows = static_cast<uint32_t>((most + 16 * MT - 1) / (16 * MT));
-  const dim3 grid(tiles_n, rows, a.offsets ? a.num_groups : p.splits);
+  // (rows last: further tiles of rows, which most experts do not have, start after all first ones)
+  const dim3 grid(tiles_n, a.offsets ? a.num_groups : p.splits, rows);
   if (a.c_dtype == 1)
     gemm_int8_few_kernel<MT, true, ONCE><<<grid, dim3(kThreads), 0, a.stream>>>(p);
   else
@@ -842,7 +843,10 @@ hipError_t launch_int8_gemm(const Int8GemmArgs &a) {
   const int splits = !a.offsets && a.workspace ? few_splits(a.M, a.N, a.K) : 1;
   // (from 65 to 128 rows the few-row kernel pays only where it splits K: 100 x 4096 x 14336 24.5 us against 36
   // in 64 x 64 tiles, but 100 x 1000 x 1008 9.2 against 5.8)
-  if (most <= 64 || splits > 1) {
+  // By expert also where an expert has at most 24 rows on average, whatever it could have (64 experts of 1536 x 4096, 8 a
+  // token: 65 tokens 90 -> 72 us, 128 tokens 93 -> 75, with falling loads 105 -> 83; 256 tokens, 32 rows each, 91 -> 82
+  // with equal loads but 90 -> 101 with falling ones).
+  if (most <= 64 || splits > 1 || (a.offsets && a.M <= 24ll * a.num_groups)) {
     const int steps = static_cast<int>((a.K + kStep - 1) / kStep);
     p.split_steps = (steps + splits - 1) / splits;
     p.splits = steps > 0 ? (steps + p.split_steps - 1) / p.split_steps : 1;
@@ -852,7 +856,7 @@ hipError_t launch_int8_gemm(const Int8GemmArgs &a) {
       constexpr bool kOnce = decltype(once)::value;
       if (most <= 16) return run_few<1, kOnce>(a, p, most);
       if (most <= 32) return run_few<2, kOnce>(a, p, most);
-      if (most <= 64) return run_few<4, kOnce>(a, p, most);
+      if (most <= 64 || a.offsets) return run_few<4, kOnce>(a, p, most);
       return run_few<8, kOnce>(a, p, most);
     };
     return a.num_groups * a.N * a.K >= kStreamBytes ? few(std::true_type{}) : few(std::false_type{});

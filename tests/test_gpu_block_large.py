@@ -1,6 +1,6 @@
 """The operators around the quantized products where their data is larger than the 256 MiB cache (they then read it
 with other loads), block norms of rows above 4096 columns with several rows a workgroup, and 8-bit products of more
-than a round of 256 x 256 tiles.
+than a round of 256 x 256 tiles or of few rows an expert.
 
 Tolerances are those of the small cases: a 32-bit sum of n products is within n x 2^-24 of their magnitudes, a bf16
 result adds one rounding; 8-bit products are exact."""
@@ -102,6 +102,22 @@ def test_experts_beyond_the_cache(T, k, N, K, dtype):
             src, r = rows[off[e]:off[e + 1]] // k, slice(e * N, (e + 1) * N)
             want = _want(x.data[src.to(DEV)], x.scales[src.to(DEV)], w.data[r], w.scales[r], dtype)
             assert torch.equal(got[off[e]:off[e + 1]], want), e
+
+
+@pytest.mark.parametrize("T,k,E,N,K", [(65, 3, 64, 130, 256), (300, 4, 64, 200, 144), (500, 2, 64, 64, 1024)])
+def test_few_rows_an_expert_of_many_tokens(T, k, E, N, K):
+    # one expert has nearly all tokens, so several tiles of rows of the kernel for few rows
+    x, w = _weights(T, K, 1, 1), _weights(N, K, E, 2)
+    logits = torch.randn(T, E, device=DEV, generator=torch.Generator(device=DEV).manual_seed(3))
+    logits[:, 5] += 6.0
+    _, _, plan = nv.nvfp4_moe_route(logits, k)
+    got = nv.nvfp4_int8_gemm(x, w, F32, plan=plan, gather=True).cpu()
+    rows, off = plan.rows.long(), plan.offsets.cpu().tolist()
+    assert off[6] - off[5] > 64 and T * k <= 24 * E
+    for e in range(E):
+        if off[e + 1] > off[e]:
+            src, r = rows[off[e]:off[e + 1]] // k, slice(e * N, (e + 1) * N)
+            assert torch.equal(got[off[e]:off[e + 1]], _want(x.data[src], x.scales[src], w.data[r], w.scales[r], F32)), e
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 66000, 4096), (30, 2100, 131056), (100, 4100, 65552)])

@@ -13,9 +13,9 @@
 // over the id's bits.  Up to 16 tokens (one chunk) the routing workgroup does all of it: one launch.
 //
 // What bounds them: the bytes are few (16384 tokens over 256 experts: 19 MB, 4 us), the choice is bound by
-// instructions, about 1500 a wave of four tokens at four cycles each on its SIMD.  16384 tokens, 8 of 256 experts:
-// 18.5 us with four of eight groups, sigmoid and bias, 15.5 without groups; 8192 tokens bf16, softmax 11.6, its
-// gradient 6.3; one token over 64 experts with the plan 4.8 us, of which the work is less than half.
+// instructions, 1217 a wave of four tokens at four cycles each on its SIMD.  16384 tokens, 8 of 256 experts:
+// 16.1 us with four of eight groups, sigmoid and bias, 12.2 without groups; 8192 tokens bf16, softmax 11.6, its
+// gradient 6.3; one token over 64 experts with the plan 4.3 us, of which the work is less than half.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -453,7 +453,7 @@ __device__ __forceinline__ void keep_groups(int (&key)[EPL], int *keys, const Ro
   if (W > 0) {
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-      m2 = max(m2, min(m1, key[j]));
+      m2 = max(min(m1, m2), min(max(m1, m2), key[j]));  // (the median of three: one instruction)
       m1 = max(m1, key[j]);
     }
     if (W > 1) merge_two<kXor1>(m1, m2);
@@ -517,6 +517,100 @@ __device__ __forceinline__ void keep_groups(int (&key)[EPL], int *keys, const Ro
   }
 }
 
+// The k best experts of the row in falling order, ties to the lower index: slot r to lane r mod 16, id_lo or id_hi.
+// k rounds of: the row's best key, the lowest lane that holds it, that lane's first expert with it.
+template <int EPL>
+__device__ __forceinline__ void choose_by_rounds(int (&key)[EPL], int k, uint32_t lane, int &id_lo, int &id_hi) {
+  const int l16 = lane & 15;
+  int best = key[0];
+#pragma unroll
+  for (int j = 1; j < EPL; ++j) best = max(best, key[j]);
+  for (int r = 0; r < k; ++r) {
+    const int m = row_max(best);
+    const uint32_t holds = static_cast<uint32_t>(__ballot(best == m) >> (lane & 48)) & 0xFFFFu;
+    const int owner = __ffs(holds) - 1;
+    // the lowest lane that holds the key closes it, and gets a bit for every expert of its that has it, the
+    // first expert's the highest.  In integer arithmetic, since a lane mask for every compare costs wait
+    // states: t is 0 for the key and -1 for a smaller one (other lanes want a key above all).
+    const int want = l16 == owner ? m : 2147483647;
+    int misses = 0;
+    best = kClosed;
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      int t = __builtin_elementwise_sub_sat(key[j], want) >> 31;
+      asm("" : "+v"(t));  // (else the compiler goes back to compares)
+      misses = (misses << 1) + t;
+      key[j] = (key[j] & t) | (kClosed & ~t);
+      best = max(best, key[j]);
+    }
+    const uint32_t hits = static_cast<uint32_t>(misses) + (EPL == 32 ? 0xFFFFFFFFu : (1u << (EPL & 31)) - 1u);
+    const uint32_t others = hits & ((1u << (31 - __clz(hits | 1u))) - 1u);
+    if (__ballot(others != 0 && m != kClosed)) {  // equal keys in one lane: all but the first come back
+#pragma unroll
+      for (int j = 0; j < EPL; ++j)
+        if ((others >> (EPL - 1 - j)) & 1u) key[j] = m;
+      best = others ? m : best;
+    }
+    const int at = __clz(hits) - (32 - EPL);
+    const int id = m != kClosed ? owner * EPL + __shfl(at, (lane & 48) + owner) : -1;
+    if (l16 == (r & 15)) {
+      if (r < 16)
+        id_lo = id;
+      else
+        id_hi = id;
+    }
+  }
+}
+
+// The same without closing keys: the owner's next best is its largest key below the one chosen, two instructions a
+// key, and the experts behind the keys are looked up for all slots at once.  False, with nothing chosen, where a lane
+// holds a chosen key twice (the rounds then start again): rare among fp32 scores, not among bf16 ones.
+// 16384 tokens, 8 of 256 experts in four of eight groups 18.6 -> 16.3 us, without groups 15.5 -> 12.2; 512
+// experts 28 -> 22.
+template <int EPL>
+__device__ __forceinline__ bool choose_unequal(const int (&key)[EPL], int k, uint32_t lane, int &id_lo, int &id_hi) {
+  const int l16 = lane & 15;
+  int best = key[0];
+#pragma unroll
+  for (int j = 1; j < EPL; ++j) best = max(best, key[j]);
+  int m_lo = kClosed, m_hi = kClosed, from_lo = 0, from_hi = 0;
+  for (int r = 0; r < k; ++r) {
+    const int m = row_max(best);
+    const uint32_t holds = static_cast<uint32_t>(__ballot(best == m) >> (lane & 48)) & 0xFFFFu;
+    const int owner = __ffs(holds) - 1;
+    // modulo 2^32, key - m is larger for every key below m than for the others, and rises with the key
+    uint32_t next = static_cast<uint32_t>(kClosed) - static_cast<uint32_t>(m);
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) next = max(next, static_cast<uint32_t>(key[j]) - static_cast<uint32_t>(m));
+    best = l16 == owner && m != kClosed ? static_cast<int>(next + static_cast<uint32_t>(m)) : best;
+    if (l16 == (r & 15)) {
+      if (r < 16) {
+        m_lo = m;
+        from_lo = owner;
+      } else {
+        m_hi = m;
+        from_hi = owner;
+      }
+    }
+  }
+  bool twice = false;
+  const auto expert_of = [&](int m, int from) {
+    uint32_t misses = 0;  // a bit for every expert of that lane with another key, the first expert's the highest
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      uint32_t other = min(static_cast<uint32_t>(__shfl(key[j], (lane & 48) + from) ^ m), 1u);
+      asm("" : "+v"(other));
+      misses = (misses << 1) + other;
+    }
+    const uint32_t hits = ~misses << (32 - EPL);
+    twice |= m != kClosed && (hits & (hits - 1)) != 0;
+    return m != kClosed ? from * EPL + __clz(hits) : -1;
+  };
+  id_lo = expert_of(m_lo, from_lo);
+  if (k > 16) id_hi = expert_of(m_hi, from_hi);
+  return __ballot(twice) == 0;
+}
+
 template <int EPL, bool BF16, bool SIGMOID>
 __global__ __launch_bounds__(kPlanThreads) void route_kernel(RouteArgs p) {
   constexpr int P = 16 * EPL;
@@ -569,44 +663,11 @@ __global__ __launch_bounds__(kPlanThreads) void route_kernel(RouteArgs p) {
     }
     if (p.group_k < p.G) keep_groups<EPL>(key, reinterpret_cast<int *>(area) + (threadIdx.x >> 4) * P, p, lane);
 
-    int best = key[0];
-#pragma unroll
-    for (int j = 1; j < EPL; ++j) best = max(best, key[j]);
     int id_lo = -1, id_hi = -1;  // slots l16 and 16 + l16
-    for (int r = 0; r < p.k; ++r) {
-      const int m = row_max(best);
-      const uint32_t holds = static_cast<uint32_t>(__ballot(best == m) >> (lane & 48)) & 0xFFFFu;
-      const int owner = __ffs(holds) - 1;
-      // the lowest lane that holds the key closes it, and gets a bit for every expert of its that has it, the
-      // first expert's the highest.  In integer arithmetic, since a lane mask for every compare costs wait
-      // states: t is 0 for the key and -1 for a smaller one (other lanes want a key above all).
-      const int want = l16 == owner ? m : 2147483647;
-      int misses = 0;
-      best = kClosed;
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) {
-        int t = __builtin_elementwise_sub_sat(key[j], want) >> 31;
-        asm("" : "+v"(t));  // (else the compiler goes back to compares)
-        misses = (misses << 1) + t;
-        key[j] = (key[j] & t) | (kClosed & ~t);
-        best = max(best, key[j]);
-      }
-      const uint32_t hits = static_cast<uint32_t>(misses) + (EPL == 32 ? 0xFFFFFFFFu : (1u << (EPL & 31)) - 1u);
-      const uint32_t others = hits & ((1u << (31 - __clz(hits | 1u))) - 1u);
-      if (__ballot(others != 0 && m != kClosed)) {  // equal keys in one lane: all but the first come back
-#pragma unroll
-        for (int j = 0; j < EPL; ++j)
-          if ((others >> (EPL - 1 - j)) & 1u) key[j] = m;
-        best = others ? m : best;
-      }
-      const int at = __clz(hits) - (32 - EPL);
-      const int id = m != kClosed ? owner * EPL + __shfl(at, (lane & 48) + owner) : -1;
-      if (l16 == (r & 15)) {
-        if (r < 16)
-          id_lo = id;
-        else
-          id_hi = id;
-      }
+    if constexpr (EPL >= 4 && !BF16) {
+      if (!choose_unequal<EPL>(key, p.k, lane, id_lo, id_hi)) choose_by_rounds<EPL>(key, p.k, lane, id_lo, id_hi);
+    } else {
+      choose_by_rounds<EPL>(key, p.k, lane, id_lo, id_hi);
     }
     // the chosen experts' scores, formed again from their logits (the same operations, the same bits)
     auto score_of = [&](int id) {

@@ -347,7 +347,8 @@ size_t nvfp4_int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
  * consecutive [N x K] weights and of b_scales' num_groups * N floats.  Rows of C from
  * offsets[num_groups] on are not written.  rows: nullable device int32[M] (a plan's rows): row r of C
  * then takes row rows[r] / row_div of a and a_scales (row_div = top_k reads a token's row for each of
- * its slots, without a gathered copy); rows outside a are read as row 0.  Without rows, M == a_rows.
+ * its slots, without a gathered copy); rows outside a are read as row 0.  Any rows may repeat, and an expert may have
+ * more rows than a has (a token that names it more than once).  Without rows, M == a_rows.
  * K % 16 == 0 and K < 2^17 (so that no sum overflows); N * K < 2^32 and, with rows, a_rows * K < 2^32;
  * M < 2^31; num_groups 1 .. 512 (else NVFP4_ERR_SHAPE); a and b 16-byte aligned, the other arrays
  * aligned to their element size.  workspace: nullable (the result is the same without it), device,

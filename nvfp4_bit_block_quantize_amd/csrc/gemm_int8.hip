@@ -627,22 +627,17 @@ struct Few {
   static constexpr int kStages = MT <= 2 ? 6 : MT == 4 ? 5 : 6;  // MT <= 4: two workgroups share a compute unit's LDS
 };
 
+// Rows [m0, m0 + kRows) of C, up to m_end, of one group.
 template <int MT, bool OUT_BF16, bool ONCE>
-__global__ __launch_bounds__(kThreads) void gemm_int8_few_kernel(I8Args p) {
+__device__ __forceinline__ void few_tile(const I8Args &p, uint8_t *smem, int32_t group, int64_t m0, int64_t m_end) {
   using F = Few<MT>;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[F::kStages * F::kStage];
-  const uint32_t lane = threadIdx.x & 63u;
-  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // (an opaque copy: what depends on the lane is not held in registers over further tiles)
+  uint32_t tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const uint32_t lane = tid & 63u;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const uint32_t r16 = lane & 15u, g = lane >> 4;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) * 64;
-  const int32_t group = p.offsets ? blockIdx.y : 0;
-  int64_t m0 = static_cast<int64_t>(blockIdx.z) * F::kRows, m_end = p.M;
-  if (p.offsets) {
-    const int64_t lo = p.offsets[group], hi = p.offsets[group + 1];
-    m0 += lo;
-    m_end = min(hi, p.M);
-    if (lo < 0 || m0 >= m_end) return;
-  }
   // this split's steps
   const int32_t all = static_cast<int32_t>((p.K + kStep - 1) / kStep);
   const int32_t kt0 = p.splits > 1 ? static_cast<int32_t>(blockIdx.y) * p.split_steps : 0;
@@ -732,6 +727,32 @@ __global__ __launch_bounds__(kThreads) void gemm_int8_few_kernel(I8Args p) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = static_cast<float>(acc[i][e]) * (sa * sb[min(col + e, p.N - 1)]);
     store4<OUT_BF16>(p, row, col, v);
+  }
+}
+
+template <int MT, bool OUT_BF16, bool ONCE>
+__global__ __launch_bounds__(kThreads) void gemm_int8_few_kernel(I8Args p) {
+  using F = Few<MT>;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[F::kStages * F::kStage];
+  const int32_t group = p.offsets ? blockIdx.y : 0;
+  int64_t m0 = static_cast<int64_t>(blockIdx.z) * F::kRows, m_end = p.M;
+  if (p.offsets) {
+    const int64_t lo = p.offsets[group], hi = p.offsets[group + 1];
+    m0 += lo;
+    m_end = min(hi, p.M);
+    if (lo < 0 || m0 >= m_end) return;
+  }
+  few_tile<MT, OUT_BF16, ONCE>(p, smem, group, m0, m_end);
+  // An expert's rows beyond the grid's (a token may name an expert more than once, so there can be more rows than tokens):
+  // this workgroup's further tiles of rows.  (The code of a tile twice: as one loop it took 1% more time where there is
+  // one tile.)
+  const int64_t further = static_cast<int64_t>(gridDim.z) * F::kRows;
+  for (m0 += further; m0 < m_end; m0 += further) {  // (the same in every wave)
+    // every wave is done with the stages
+    wait_vmcnt<0>();
+    wait_lgkmcnt0();
+    lds_barrier();
+    few_tile<MT, OUT_BF16, ONCE>(p, smem, group, m0, m_end);
   }
 }
 
@@ -838,7 +859,8 @@ hipError_t launch_int8_gemm(const Int8GemmArgs &a) {
   p.offsets = a.offsets;
   p.rows = a.rows;
   p.row_div = a.row_div;
-  // rows an expert can have
+  // rows an expert has at most where a token's experts differ: the kernel's tile and its grid.  (It takes any number of
+  // rows; those of a token that names an expert more than once come one tile after the other.)
   const int64_t most = a.rows && a.a_rows < a.M ? a.a_rows : a.M;
   const int splits = !a.offsets && a.workspace ? few_splits(a.M, a.N, a.K) : 1;
   // (from 65 to 128 rows the few-row kernel pays only where it splits K: 100 x 4096 x 14336 24.5 us against 36

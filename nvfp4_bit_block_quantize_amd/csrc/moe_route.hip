@@ -142,6 +142,12 @@ constexpr float kPlainMost = 0x1p125f, kPlainLeast = 0x1p-100f;
 // and 1 for a row without an open expert.
 __device__ __forceinline__ float softmax_score(float l, float top, float total) { return expf(l - top) / total; }
 __device__ __forceinline__ float sigmoid_score(float l) { return 1.0f / (1.0f + expf(-l)); }
+// s (1 - s).  For l >= 0 the complement is e s with e = exp(-l): 1 - s would lose it in the rounding of s (up to 1e-4 of
+// it at l = 8, all of it from 17 on).
+__device__ __forceinline__ float sigmoid_slope(float l) {
+  const float e = expf(-l), s = 1.0f / (1.0f + e);
+  return s * (l >= 0.0f ? e * s : 1.0f - s);
+}
 
 template <int EPL, bool SIGMOID>
 __device__ __forceinline__ void row_scores(const float (&l)[EPL], float (&s)[EPL], float &top, float &total) {
@@ -732,19 +738,21 @@ __device__ __forceinline__ uint32_t bf16_of(float v) {
 template <int EPL, bool BF16, bool SIGMOID>
 __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs p) {
   constexpr int P = 16 * EPL;
-  __shared__ float ds_lds[16][P];  // gradient of each expert's score, a row a token
+  __shared__ float ds_lds[16][P];  // gradient of each expert's score (sigmoid: of its logit), a row a token
   const uint32_t lane = threadIdx.x & 63u;
   const int l16 = lane & 15;
   const int64_t t = (p.first_block + blockIdx.x) * 16 + (threadIdx.x >> 4);
   const bool exists = t < p.tokens;
   const int64_t tr = exists ? t : p.tokens - 1;
   const uint8_t *row = p.logits + tr * p.row_bytes;
-  float l[EPL], s[EPL], top, total;
-  load_logits<EPL, BF16>(row, l16 * EPL, p.E, p.vec, l);
-  row_scores<EPL, SIGMOID>(l, s, top, total);
+  float l[EPL], s[EPL], top = 0.0f, total = 1.0f;
+  if constexpr (!SIGMOID) {
+    load_logits<EPL, BF16>(row, l16 * EPL, p.E, p.vec, l);
+    row_scores<EPL, false>(l, s, top, total);
+  }
 
-  // the row's slots l16 and 16 + l16: score and gradient
-  float picked[2] = {0.0f, 0.0f}, g[2] = {0.0f, 0.0f};
+  // the row's slots l16 and 16 + l16: score, slope (sigmoid) and gradient
+  float picked[2] = {0.0f, 0.0f}, slope[2] = {0.0f, 0.0f}, g[2] = {0.0f, 0.0f};
   int id[2] = {-1, -1};
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -755,6 +763,7 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs p) {
         const float v = load_logit<BF16>(row, e);
         id[h] = e;
         picked[h] = SIGMOID ? sigmoid_score(v) : softmax_score(v, top, total);
+        if (SIGMOID) slope[h] = sigmoid_slope(v);
         g[h] = p.dweights[tr * p.k + j] * p.scale;
       }
     }
@@ -770,6 +779,11 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs p) {
     if (id[1] < 0) g[1] = 0.0f;
     if (!SIGMOID) gs = row_sum(fmaf(g[0], picked[0], g[1] * picked[1]));
   }
+  // a sigmoid's gradient stays with its expert: it is formed here, and nothing is read for the others
+  if (SIGMOID) {
+    g[0] *= slope[0];
+    g[1] *= slope[1];
+  }
   float *ds = ds_lds[threadIdx.x >> 4];
 #pragma unroll
   for (int j = 0; j < EPL; ++j) ds[l16 * EPL + j] = 0.0f;
@@ -782,7 +796,10 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs p) {
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     const float v = ds[l16 * EPL + j];
-    d[j] = SIGMOID ? (v * s[j]) * (1.0f - s[j]) : s[j] * (v - gs);
+    if constexpr (SIGMOID)
+      d[j] = v;
+    else
+      d[j] = s[j] * (v - gs);
   }
   if (!exists) return;
   uint8_t *out = p.dlogits + t * p.out_row_bytes;

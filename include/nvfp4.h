@@ -241,7 +241,9 @@ int nvfp4_gemm_w4a16(const void *a, int a_dtype, int64_t m, int64_t lda, const n
  * (plain, for few tokens, and by expert), the sum of the experts' rows, and the norms before and after
  * a block.  They follow the conventions at the top of this file, except that routing accepts
  * infinities and NaN in its logits (see nvfp4_moe_route).  None of them uses floating-point atomics
- * across workgroups: the same input gives the same bits on every call. */
+ * across workgroups: the same input gives the same bits on every call.  A workspace has the size that the matching
+ * function gives for the call's own shape: a smaller problem may need the larger workspace (its sums run in more parts),
+ * so a workspace kept for several shapes has the largest of their sizes.  The calls cannot check it. */
 
 enum {
   NVFP4_ROUTE_SIGMOID = 1u << 0,    /* scores 1 / (1 + exp(-l)); without it, softmax over the experts  */

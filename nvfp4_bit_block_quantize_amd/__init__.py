@@ -438,9 +438,15 @@ def _empty_plan(tokens: int, top_k: int, experts: int, device) -> MoEPlan:
                    torch.empty((tokens, top_k), dtype=i32, device=device))
 
 
-def _moe_workspace(tokens: int, experts: int, top_k: int, device) -> Optional[torch.Tensor]:
-    size = lib().nvfp4_moe_workspace_size(tokens, experts, top_k)
-    return torch.empty(size // 4, dtype=torch.int32, device=device) if size else None
+def _scratch(where: str, workspace: Optional[torch.Tensor], size: int, like: torch.Tensor) -> Optional[torch.Tensor]:
+    """The caller's workspace if it has `size` bytes on the device of `like`; one of that size if there is none."""
+    if workspace is None:
+        return torch.empty(size // 4, dtype=torch.int32, device=like.device) if size else None
+    if size and (workspace.numel() * workspace.element_size() < size or not workspace.is_contiguous()
+                 or workspace.device != like.device):
+        raise ValueError(f"{where}: workspace must be contiguous and have {size} bytes on {like.device}, has "
+                         f"{workspace.numel() * workspace.element_size()} on {workspace.device}")
+    return workspace
 
 
 def nvfp4_moe_route(logits: torch.Tensor, top_k: int, flags: int = 0, bias: Optional[torch.Tensor] = None,
@@ -458,8 +464,7 @@ def nvfp4_moe_route(logits: torch.Tensor, top_k: int, flags: int = 0, bias: Opti
     plan = None
     if with_plan:
         plan = _empty_plan(T, max(top_k, 0), E, dev)
-        if workspace is None:
-            workspace = _moe_workspace(T, E, top_k, dev)
+        workspace = _scratch("nvfp4_moe_route", workspace, lib().nvfp4_moe_workspace_size(T, E, top_k), logits)
     st = lib().nvfp4_moe_route(logits.data_ptr(), _dtype_code(logits.dtype), T, E, ld, _addr(bias), num_groups, group_top_k,
                                top_k, flags, scale, ids.data_ptr(), weights.data_ptr(),
                                plan.offsets.data_ptr() if plan else None, plan.rows.data_ptr() if plan else None,
@@ -495,8 +500,7 @@ def nvfp4_moe_plan(ids: torch.Tensor, experts: int, workspace: Optional[torch.Te
     _want("nvfp4_moe_plan", "ids", ids, torch.int32, ids.shape, ids)
     T, k = ids.shape
     plan = _empty_plan(T, k, max(experts, 0), ids.device)
-    if workspace is None:
-        workspace = _moe_workspace(T, experts, k, ids.device)
+    workspace = _scratch("nvfp4_moe_plan", workspace, lib().nvfp4_moe_workspace_size(T, experts, k), ids)
     st = lib().nvfp4_moe_plan(ids.data_ptr(), T, k, experts, plan.offsets.data_ptr(), plan.rows.data_ptr(),
                               plan.pos.data_ptr(), _addr(workspace), _raw_stream(ids))
     _check(st, "nvfp4_moe_plan")
@@ -616,10 +620,8 @@ def nvfp4_int8_gemm(a: Int8Tensor, b: Int8Tensor, out_dtype: torch.dtype = torch
         raise ValueError(f"{where}: out must be [{M}, {b.rows}] on {ad.device}")
     else:
         ldc = _matrix(where, "out", out)
-    if workspace is None and plan is None:
-        size = lib().nvfp4_int8_gemm_workspace_size(M, b.rows, b.k)
-        if size:
-            workspace = torch.empty(size // 4, dtype=torch.int32, device=ad.device)
+    if plan is None:  # (by expert there is none)
+        workspace = _scratch(where, workspace, lib().nvfp4_int8_gemm_workspace_size(M, b.rows, b.k), ad)
     st = lib().nvfp4_int8_gemm(ad.data_ptr(), asc.data_ptr(), a.rows, bd.data_ptr(), bsc.data_ptr(), M, b.rows, b.k,
                                out.data_ptr(), _dtype_code(out.dtype), max(ldc, 1), b.groups, offsets, rows, div, _addr(workspace), _raw_stream(ad))
     _check(st, where)
@@ -695,8 +697,7 @@ def nvfp4_block_norm_backward(dx_out: Optional[torch.Tensor], dn: Optional[torch
     dw_post = torch.empty(D, dtype=torch.float32, device=dev) if w_post is not None else None
     dgate = torch.empty_like(gate) if gate is not None else None
     dw_pre = torch.empty(D, dtype=torch.float32, device=dev) if w_pre is not None else None
-    if workspace is None:
-        workspace = torch.empty(lib().nvfp4_block_norm_workspace_size(T, D) // 4, dtype=torch.float32, device=dev)
+    workspace = _scratch(where, workspace, lib().nvfp4_block_norm_workspace_size(T, D), x)
     st = lib().nvfp4_block_norm_backward(_addr(dx_out), _addr(dn), x.data_ptr(), _dtype_code(x.dtype), _addr(y),
                                          _dtype_code(y_dtype), T, D, _addr(w_post), _addr(gate), _addr(w_pre), alpha, flags,
                                          _addr(rstd_post), _addr(rstd_pre), dx.data_ptr(), _addr(dy), _addr(dw_post),

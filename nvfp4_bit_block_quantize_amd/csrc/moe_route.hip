@@ -126,8 +126,11 @@ __device__ __forceinline__ void load_logits(const uint8_t *row, int e0, int E, b
 
 // Correctly rounded 1 / x and e / total without the general division's range handling: the hardware's
 // reciprocal and one Newton step, then (Markstein) one corrected quotient, each with a fused remainder.  For
-// 1 <= x < 2^126 and, in the quotient, 1 <= total <= 512 and e = 0 or 2^-100 <= e <= 1 (`plain`): no step under-
-// or overflows there.  Elsewhere the general division.
+// 1 <= x <= 2^125 and, in the quotient, 1 <= total <= 512 and e = 0 or 2^-100 <= e <= 1: no step under-
+// or overflows there.  Elsewhere the general division, for a whole wave; the two give the same bits, so a token's
+// choice does not depend on the tokens beside it.  (The Newton step is correctly rounded for every x if its start is,
+// and for all but 32 significands if that is an ulp off.  The tests take those 32 through the keys: this chip's
+// reciprocal is right there too.)
 __device__ __forceinline__ float recip(float x) {
   const float r = __builtin_amdgcn_rcpf(x);
   return fmaf(fmaf(-x, r, 1.0f), r, r);

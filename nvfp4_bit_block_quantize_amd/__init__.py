@@ -399,8 +399,11 @@ class BlockNormGrads:
 
 
 def _raw_stream(t: torch.Tensor):
-    """The current stream of t's device, as a number (torch.cuda.current_stream builds an object first)."""
-    return torch._C._cuda_getCurrentRawStream(t.device.index) if t.is_cuda else None
+    """The current stream of t's device, as a number (torch.cuda.current_stream builds an object first).  A tensor in
+    host memory is refused: the kernels would read its address on the GPU."""
+    if not t.is_cuda:
+        raise NVFP4Error(NVFP4_ERR_UNSUPPORTED, f"tensors on {t.device}")
+    return torch._C._cuda_getCurrentRawStream(t.device.index)
 
 
 def _addr(t: Optional[torch.Tensor]):

@@ -288,7 +288,8 @@ int nvfp4_moe_route(const void *logits, int dtype, int64_t tokens, int64_t exper
  * itself has no gradient, and the bias none at all): dlogits [tokens x experts] in the logits' dtype
  * (leading dimension ldd), from dweights [tokens][top_k].  Scores are computed again from the logits.
  * flags (NVFP4_ROUTE_SIGMOID, NVFP4_ROUTE_RENORM; others ignored) and scale as in the forward call.
- * Slots whose id is not in [0, experts) have no gradient; a closed expert's gradient is 0. */
+ * Slots whose id is not in [0, experts) have no gradient; a closed expert's gradient is 0.  An expert with nearly all
+ * of the score keeps the precision of its (small) gradient: nothing is taken as a difference from one. */
 int nvfp4_moe_route_backward(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t ld,
                              const int32_t *ids, const float *dweights, int32_t top_k, uint32_t flags, float scale,
                              void *dlogits, int64_t ldd, void *hip_stream);

@@ -780,6 +780,15 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs p) {
     g[1] = (g[1] - mean) / sum;
     if (id[0] < 0) g[0] = 0.0f;
     if (id[1] < 0) g[1] = 0.0f;
+    // The slot that has most of the sum: its weight's distance from the mean is lost in the mean's rounding.  What the
+    // slots' g p add up to (mean 1e-20 / sum) gives it from the others.
+    const bool leads[2] = {2.0f * picked[0] > sum, 2.0f * picked[1] > sum};
+    if (__ballot(leads[0] || leads[1])) {
+      const float others = row_sum(fmaf(leads[0] ? 0.0f : g[0], picked[0], leads[1] ? 0.0f : g[1] * picked[1]));
+      const float left = fmaf(mean / sum, 1e-20f, -others);
+      if (leads[0]) g[0] = left / picked[0];
+      if (leads[1]) g[1] = left / picked[1];
+    }
     if (!SIGMOID) gs = row_sum(fmaf(g[0], picked[0], g[1] * picked[1]));
   }
   // a sigmoid's gradient stays with its expert: it is formed here, and nothing is read for the others
@@ -803,6 +812,17 @@ __global__ __launch_bounds__(256) void route_backward_kernel(RouteBwdArgs p) {
       d[j] = v;
     else
       d[j] = s[j] * (v - gs);
+  }
+  // Likewise the expert with a softmax score above one half: a row's gradients add up to zero.
+  if constexpr (!SIGMOID) {
+    if (__ballot(total < 2.0f)) {
+      float others = 0.0f;
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) others += s[j] > 0.5f ? 0.0f : d[j];
+      others = row_sum(others);
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) d[j] = s[j] > 0.5f ? -others : d[j];
+    }
   }
   if (!exists) return;
   uint8_t *out = p.dlogits + t * p.out_row_bytes;

@@ -342,7 +342,8 @@ size_t nvfp4_int8_gemm_workspace_size(int64_t M, int64_t N, int64_t K);
 /* Product of 8-bit integers with a scale for each token and each channel:
  *   C[i][j] = (a_scales[i] * b_scales[j]) * sum_k a[i][k] * b[j][k],
  * the sum exact in 32-bit integers, the scale product and its multiply in fp32, one rounding to a
- * bf16 C.  a: int8 [a_rows][K], b: int8 [N][K], both without padding; c [M x N], dtype NVFP4_F32 or
+ * bf16 C.  (The scale product comes first: where it is below 2^-126 C has its fewer bits, where it overflows
+ * C is infinite, or NaN for a sum of zero.)  a: int8 [a_rows][K], b: int8 [N][K], both without padding; c [M x N], dtype NVFP4_F32 or
  * NVFP4_BF16, leading dimension ldc >= N.  Values -128 are allowed.
  * Plain form (offsets NULL, num_groups 1, rows NULL): M == a_rows.
  * By expert: offsets is a DEVICE array of num_groups + 1 row offsets (a plan's offsets; offsets[0]

@@ -811,7 +811,8 @@ int pick_tile(const Int8GemmArgs &a) {
   return t128 < t64 ? (one ? 129 : 128) : 64;
 }
 
-// ONCE: the weights are too large for the cache, so they are read past it (8 tokens, 8 of 64 experts of 1536 x 4096,
+// ONCE: the weights are too large for the cache, so they are read past it.  All experts' bytes count, since which
+// experts a call reads is known on the device alone and over some calls they all are (8 tokens, 8 of 64 experts of 1536 x 4096,
 // 403 MB, about 40 of them read: 46 -> 40 us; 59 MB of weights with non-temporal loads 12.2 -> 13.1).
 template <int MT, bool ONCE>
 hipError_t run_few(const Int8GemmArgs &a, const I8Args &p, int64_t most) {

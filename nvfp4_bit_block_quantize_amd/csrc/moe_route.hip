@@ -12,10 +12,13 @@
 // counts of the chunks before it, then the slot's rank among its chunk's equal ids, found with ballots
 // over the id's bits.  Up to 16 tokens (one chunk) the routing workgroup does all of it: one launch.
 //
-// What bounds them: the bytes are few (16384 tokens over 256 experts: 19 MB, 4 us), the choice is bound by
-// instructions, 1217 a wave of four tokens at four cycles each on its SIMD.  16384 tokens, 8 of 256 experts:
-// 16.1 us with four of eight groups, sigmoid and bias, 12.2 without groups; 8192 tokens bf16, softmax 11.6, its
-// gradient 6.3; one token over 64 experts with the plan 4.3 us, of which the work is less than half.
+// What bounds them: the bytes are few (16384 tokens over 256 experts: 19 MB, 4 us).  The choice takes 1217 vector
+// instructions a wave of four tokens; with four waves a SIMD these are issued in 57% of its cycles and scalar ones in
+// 14%, while a wave by itself waits for 57% of its time (the rounds are a chain of exchanges, a ballot and a bit scan).
+// 16384 tokens, 8 of 256 experts: 16.1 to 16.9 us with four of eight groups, sigmoid and bias, 12.2 without groups;
+// 8192 tokens bf16, softmax 11.3 to 12.3, its gradient 6.2 to 6.5 (two waves a SIMD, vector instructions in 43% of the
+// cycles); the sigmoid's gradient 9.1 us for 16384 tokens of 256 experts in fp32;
+// one token over 64 experts with the plan 4.3 us, of which the work is less than half.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -157,6 +160,8 @@ __device__ __forceinline__ void row_scores(const float (&l)[EPL], float (&s)[EPL
   top = 0.0f;
   total = 1.0f;
   if constexpr (SIGMOID) {
+    // (a closed expert has an infinite s, and so has a lane's padding, so with masks and with any number of experts but
+    // 16, 32, .. 512 the wave takes the general division)
     float most = 0.0f;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {

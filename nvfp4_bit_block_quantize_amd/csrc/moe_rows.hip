@@ -2,8 +2,8 @@
 // the experts' rows, and its gradients.  All three move rows once (HBM-bound): a lane owns 16 bytes of
 // a row's columns and walks the token's slots, so the k loads of a lane are independent and a token's
 // own row (dout) is read once for all of its slots.  A token's sums run in the order of its slots.
-// 4096 tokens of 8 rows of 4096 bf16: the sum 55 us (302 MB, 5.5 TB/s), its gradient 101 us (570 MB, 5.6 TB/s); a
-// 1 GiB copy runs at 5.1 TB/s.  The gather 71 us (4.3 TB/s, nearly all writes).  16384 tokens of 8 rows of 512: gather 38
+// 4096 tokens of 8 rows of 4096 bf16: the sum 56 to 60 us (302 MB, 5.0 to 5.4 TB/s), its gradient 103 to
+// 107 us (570 MB, 5.3 to 5.5 TB/s); a 1 GiB copy runs at 5.1 TB/s.  The gather 71 us (4.3 TB/s, nearly all writes).  16384 tokens of 8 rows of 512: gather 38
 // us, sum 24; of 128 fp32 19 and 13 (59 and 20 with a workgroup a row).  One to a few tokens: 4 us, the launch.
 #include "nvfp4_internal.h"
 #include "vec_io.hpp"

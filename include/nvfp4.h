@@ -393,6 +393,67 @@ int nvfp4_block_norm_backward(const void *dx_out, const void *dn, const void *x,
                               const float *rstd_pre, void *dx, void *dy, float *dw_post, void *dgate, float *dw_pre,
                               void *workspace, void *hip_stream);
 
+/* ---- Fine-tuning beside the quantized products -----------------------------------------------------------
+ * What a step over frozen quantized weights needs next to the calls above: the routing's balance loss, and the
+ * norm and clipping of the gradients that the backward calls give.  Conventions as for the block above. */
+
+/* Bytes of device workspace nvfp4_moe_balance needs (0 for one sequence of up to 64 tokens: workspace may then be
+ * NULL).  Needs no initialisation; calls that may overlap must use distinct workspaces. */
+size_t nvfp4_moe_balance_workspace_size(int64_t tokens, int64_t experts, int64_t sequences);
+
+/* Balance loss of a routing, with the experts' counts.  The tokens form `sequences` equal consecutive sequences (1: the
+ * whole batch), each with a loss of its own:
+ *   counts[s][e] = slots of the sequence's tokens whose id is e  (an id given twice by a token counts twice)
+ *   live[s]      = N, its tokens with at least one id in [0, experts); other tokens (padding) enter nothing
+ *   p[t][e]      = exp(l - max l) / sum, or with NVFP4_ROUTE_SIGMOID s / (sum s + 1e-20), s = 1 / (1 + exp(-l));
+ *                  closed experts (a logit of -inf or NaN) have 0, other logits are capped at FLT_MAX, as in
+ *                  nvfp4_moe_route; a token without an open expert has zeros
+ *   probs[s][e]  = mean of p[t][e] over the N tokens (0 without tokens)
+ *   loss         = coef / sequences * sum_s sum_e (experts * counts[s][e] / (top_k * N)) * probs[s][e]
+ * logits [tokens x experts], ids [tokens][top_k] (a routing's) as for nvfp4_moe_route.  loss: device float[1]; counts:
+ * device int32 [sequences][experts]; probs: device float [sequences][experts]; live: device int32 [sequences].  Sums run
+ * in fp32 in one fixed order.  tokens a multiple of sequences, sequences 1 .. 65535, coef finite (else
+ * NVFP4_ERR_UNSUPPORTED); flags: NVFP4_ROUTE_SIGMOID, other routing flags are ignored. */
+int nvfp4_moe_balance(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t ld, const int32_t *ids,
+                      int32_t top_k, int64_t sequences, uint32_t flags, float coef, float *loss, int32_t *counts,
+                      float *probs, int32_t *live, void *workspace, void *hip_stream);
+
+/* Gradient of nvfp4_moe_balance's loss with respect to the logits, times *dloss (device float; NULL: 1), added to
+ * dlogits_in (nullable, the logits' dtype, leading dimension ld_in; e.g. nvfp4_moe_route_backward's result) with one
+ * rounding: dlogits [tokens x experts] in the logits' dtype, leading dimension ldd; it may be dlogits_in itself.  Counts
+ * have no gradient.  counts and live are the forward call's, or their sums over the ranks of a data-parallel job (then
+ * each rank has the gradient of the loss of all ranks' tokens with respect to its own logits).  Tokens without an id,
+ * and closed experts, get dlogits_in (or 0) unchanged.  An expert with nearly all of the score keeps the precision of its
+ * (small) gradient. */
+int nvfp4_moe_balance_backward(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t ld,
+                               const int32_t *ids, int32_t top_k, int64_t sequences, uint32_t flags, float coef,
+                               const int32_t *counts, const int32_t *live, const float *dloss, const void *dlogits_in,
+                               int64_t ld_in, void *dlogits, int64_t ldd, void *hip_stream);
+
+enum {
+  NVFP4_GRAD_MAX = 1u << 0 /* the largest magnitude instead of the square root of the sum of squares */
+};
+
+/* Bytes of device workspace nvfp4_grad_norm needs for `tensors` tensors of `elements` elements together. */
+size_t nvfp4_grad_workspace_size(int64_t tensors, int64_t elements);
+
+/* *norm (device float) = sqrt of the sum of squares over all elements of all tensors, or with NVFP4_GRAD_MAX their
+ * largest magnitude; NaN if any element is NaN, else infinite if any is.  (Infinities and NaN are accepted here and in
+ * nvfp4_grad_clip.)  Squares and sums are 64-bit numbers and added in one fixed order.  grads, counts, dtypes: HOST arrays of
+ * `tensors` entries, read before the call returns: device address (aligned to its element; contiguous elements),
+ * number of elements (0 .. 2^40) and NVFP4_F32 or NVFP4_BF16 of each tensor.  workspace: device,
+ * nvfp4_grad_workspace_size() bytes, 16-byte aligned. */
+int nvfp4_grad_norm(const void *const *grads, const int64_t *counts, const int32_t *dtypes, int64_t tensors,
+                    uint32_t flags, float *norm, void *workspace, void *hip_stream);
+
+/* outs[i] = grads[i] * min(1, max_norm / (*norm + eps)), the factor in fp32, one rounding to the tensor's dtype.  norm:
+ * device float, e.g. nvfp4_grad_norm's of these or of more tensors (all ranks').  Where *norm is infinite or NaN the factor
+ * is 1: the caller sees it in the norm.  outs: HOST array; outs[i] is grads[i] (in place; nothing is then written for a
+ * factor of 1) or does not overlap any tensor of the call; a tensor may not be given twice
+ * (NVFP4_ERR_UNSUPPORTED).  max_norm >= 0 and eps >= 0, not NaN, and not both zero (else NVFP4_ERR_UNSUPPORTED). */
+int nvfp4_grad_clip(const void *const *grads, void *const *outs, const int64_t *counts, const int32_t *dtypes,
+                    int64_t tensors, const float *norm, float max_norm, float eps, void *hip_stream);
+
 /* Static, human-readable text for a status code. */
 const char *nvfp4_status_string(int status);
 

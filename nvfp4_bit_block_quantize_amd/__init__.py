@@ -28,7 +28,8 @@ __all__ = [
     "NVFP4_ROUTE_SIGMOID", "NVFP4_ROUTE_RENORM", "NVFP4_ROUTE_GROUP_SUM2", "NVFP4_NORM_ONE_PLUS", "MoEPlan", "Int8Tensor",
     "BlockNorm", "BlockNormGrads", "nvfp4_moe_route", "nvfp4_moe_route_backward", "nvfp4_moe_plan", "nvfp4_moe_gather",
     "nvfp4_moe_combine", "nvfp4_moe_combine_backward", "nvfp4_int8_quantize", "nvfp4_int8_gemm", "nvfp4_block_norm",
-    "nvfp4_block_norm_backward",
+    "nvfp4_block_norm_backward", "NVFP4_GRAD_MAX", "MoEBalance", "nvfp4_moe_balance", "nvfp4_moe_balance_backward",
+    "nvfp4_grad_norm", "nvfp4_grad_clip",
 ]
 
 NVFP4_OK, NVFP4_ERR_NULL, NVFP4_ERR_SHAPE, NVFP4_ERR_ALIGN, NVFP4_ERR_UNSUPPORTED, NVFP4_ERR_HIP = range(6)
@@ -37,6 +38,7 @@ NVFP4_COLWISE, NVFP4_BLOCK2D, NVFP4_SR, NVFP4_FOUR_OVER_SIX = 1, 2, 4, 8
 NVFP4_TS_FOR_FOUR, NVFP4_SCALE_SEARCH = 16, 32
 NVFP4_ROUTE_SIGMOID, NVFP4_ROUTE_RENORM, NVFP4_ROUTE_GROUP_SUM2 = 1, 2, 4
 NVFP4_NORM_ONE_PLUS, NVFP4_NORM_TOKEN_GATE = 1, 2
+NVFP4_GRAD_MAX = 1
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -99,7 +101,14 @@ def lib():
                 ("nvfp4_block_norm", i, [P, i, P, i, i64, i64, P, P, P, f32, f32, u32, P, P, P, P, P]),
                 ("nvfp4_block_norm_workspace_size", size, [i64, i64]),
                 ("nvfp4_block_norm_backward", i,
-                 [P, P, P, i, P, i, i64, i64, P, P, P, f32, u32, P, P, P, P, P, P, P, P, P])):
+                 [P, P, P, i, P, i, i64, i64, P, P, P, f32, u32, P, P, P, P, P, P, P, P, P]),
+                ("nvfp4_moe_balance_workspace_size", size, [i64, i64, i64]),
+                ("nvfp4_moe_balance", i, [P, i, i64, i64, i64, P, i32, i64, u32, f32, P, P, P, P, P, P]),
+                ("nvfp4_moe_balance_backward", i,
+                 [P, i, i64, i64, i64, P, i32, i64, u32, f32, P, P, P, P, i64, P, i64, P]),
+                ("nvfp4_grad_workspace_size", size, [i64, i64]),
+                ("nvfp4_grad_norm", i, [P, P, P, i64, u32, P, P, P]),
+                ("nvfp4_grad_clip", i, [P, P, P, P, i64, P, f32, f32, P])):
             getattr(L, name).argtypes, getattr(L, name).restype = args, res
         L.nvfp4_status_string.argtypes = [ctypes.c_int]
         L.nvfp4_status_string.restype = ctypes.c_char_p
@@ -707,3 +716,136 @@ def nvfp4_block_norm_backward(dx_out: Optional[torch.Tensor], dn: Optional[torch
                                          _addr(dgate), _addr(dw_pre), _addr(workspace), _raw_stream(x))
     _check(st, where)
     return BlockNormGrads(dx, dy, dw_post, dgate, dw_pre)
+
+
+# ---- fine-tuning beside the quantized products ----------------------------------------------------------
+def _enqueue(name: str, like: torch.Tensor, *args):
+    """The library's call of this name on the current stream of `like`'s device, with that device current."""
+    stream = _raw_stream(like)
+    call = getattr(lib(), name)
+    if torch._C._cuda_getDevice() == like.device.index:
+        st = call(*args, stream)
+    else:
+        with torch.cuda.device(like.device):
+            st = call(*args, stream)
+    _check(st, name)
+
+
+@dataclass
+class MoEBalance:
+    """What nvfp4_moe_balance gives."""
+    loss: torch.Tensor    # float32 [1]
+    counts: torch.Tensor  # int32 [sequences, experts], slots of each expert
+    probs: torch.Tensor   # float32 [sequences, experts], mean probability of each expert
+    tokens: torch.Tensor  # int32 [sequences], tokens that have an expert
+
+
+def nvfp4_moe_balance(logits: torch.Tensor, ids: torch.Tensor, coef: float = 1.0, flags: int = 0, sequences: int = 1,
+                      workspace: Optional[torch.Tensor] = None) -> MoEBalance:
+    """Balance loss of a routing's ids [tokens, top_k] over its logits [tokens, experts], with the experts' counts, for
+    each of `sequences` equal consecutive sequences (see include/nvfp4.h)."""
+    where = "nvfp4_moe_balance"
+    ld = _matrix(where, "logits", logits)
+    T, E = logits.shape
+    _want(where, "ids", ids, torch.int32, (T, ids.shape[-1]), logits)
+    dev, S = logits.device, max(sequences, 1)
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
+    counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+    probs = torch.empty((S, E), dtype=torch.float32, device=dev)
+    live = torch.empty(S, dtype=torch.int32, device=dev)
+    workspace = _scratch(where, workspace, lib().nvfp4_moe_balance_workspace_size(T, E, sequences), logits)
+    _enqueue(where, logits, logits.data_ptr(), _dtype_code(logits.dtype), T, E, ld, ids.data_ptr(), ids.shape[1], sequences, flags,
+             coef, loss.data_ptr(), counts.data_ptr(), probs.data_ptr(), live.data_ptr(), _addr(workspace))
+    return MoEBalance(loss, counts, probs, live)
+
+
+def nvfp4_moe_balance_backward(logits: torch.Tensor, ids: torch.Tensor, balance: MoEBalance, coef: float = 1.0, flags: int = 0,
+                               dloss: Optional[torch.Tensor] = None, dlogits: Optional[torch.Tensor] = None,
+                               out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of nvfp4_moe_balance's loss with respect to the logits, times dloss (float32 [1]; None: 1) and added to
+    dlogits (None: 0), e.g. nvfp4_moe_route_backward's result.  out may be dlogits."""
+    where = "nvfp4_moe_balance_backward"
+    ld = _matrix(where, "logits", logits)
+    T, E = logits.shape
+    _want(where, "ids", ids, torch.int32, (T, ids.shape[-1]), logits)
+    S = balance.counts.shape[0]
+    _want(where, "balance.counts", balance.counts, torch.int32, (S, E), logits)
+    _want(where, "balance.tokens", balance.tokens, torch.int32, (S,), logits)
+    _want(where, "dloss", dloss, torch.float32, (1,), logits)
+    for name, t in (("dlogits", dlogits), ("out", out)):
+        if t is not None and (t.shape != logits.shape or t.dtype != logits.dtype or t.device != logits.device):
+            raise ValueError(f"{where}: {name} must match the logits")
+    ld_in = _matrix(where, "dlogits", dlogits) if dlogits is not None else 0
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    _enqueue(where, logits, logits.data_ptr(), _dtype_code(logits.dtype), T, E, ld, ids.data_ptr(), ids.shape[1], S, flags, coef,
+             balance.counts.data_ptr(), balance.tokens.data_ptr(), _addr(dloss), _addr(dlogits), ld_in, out.data_ptr(),
+             _matrix(where, "out", out))
+    return out
+
+
+def _dense(t: torch.Tensor) -> bool:
+    """Whether t's elements fill one range of memory, in whatever order of its dimensions."""
+    if t.is_contiguous():
+        return True
+    step = 1
+    for stride, size in sorted((st, n) for st, n in zip(t.stride(), t.shape) if n != 1):
+        if stride != step:
+            return False
+        step *= size
+    return True
+
+
+def _grad_list(where: str, grads: Sequence[torch.Tensor]):
+    """Host arrays of the tensors' addresses, element counts and types, and the number of elements of all."""
+    if isinstance(grads, torch.Tensor) or not len(grads):
+        raise ValueError(f"{where}: needs a list of at least one tensor")
+    n, at = len(grads), grads[0].get_device()
+    for t in grads:
+        if t.get_device() != at or t.layout is not torch.strided:
+            raise ValueError(f"{where}: all tensors must be strided tensors of one device")
+        if not _dense(t):
+            raise ValueError(f"{where}: a tensor of shape {list(t.shape)} has strides {list(t.stride())}, which leave gaps")
+    counts = [t.numel() for t in grads]
+    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in grads]), (ctypes.c_int64 * n)(*counts),
+            (ctypes.c_int32 * n)(*[_dtype_code(t.dtype) for t in grads]), n, sum(counts))
+
+
+def _grad_norm(where, grads, listed, flags, workspace):
+    addresses, counts, dtypes, n, elements = listed
+    first = grads[0]
+    norm = torch.empty(1, dtype=torch.float32, device=first.device)
+    workspace = _scratch(where, workspace, lib().nvfp4_grad_workspace_size(n, elements), first)
+    _enqueue("nvfp4_grad_norm", first, addresses, counts, dtypes, n, flags, norm.data_ptr(), _addr(workspace))
+    return norm
+
+
+def nvfp4_grad_norm(grads: Sequence[torch.Tensor], flags: int = 0, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Norm (float32 [1]) of all tensors of the list together (float32 / bfloat16, in any mixture): the square root of
+    the sum of squares, or with NVFP4_GRAD_MAX the largest magnitude."""
+    where = "nvfp4_grad_norm"
+    return _grad_norm(where, grads, _grad_list(where, grads), flags, workspace)
+
+
+def nvfp4_grad_clip(grads: Sequence[torch.Tensor], max_norm: float, flags: int = 0, eps: float = 1e-6,
+                    out: Optional[Sequence[torch.Tensor]] = None, norm: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Scale the tensors of the list, in place or into out, by min(1, max_norm / (norm + eps)); returns the norm
+    (float32 [1]), which is that of the list unless it is given (e.g. that of all ranks).  A norm that is infinite or NaN
+    leaves the gradients as they are."""
+    where = "nvfp4_grad_clip"
+    listed = _grad_list(where, grads)
+    addresses, counts, dtypes, n, _ = listed
+    outs = addresses
+    if out is not None:
+        if len(out) != n:
+            raise ValueError(f"{where}: out has {len(out)} tensors, the list {n}")
+        for o, t in zip(out, grads):
+            if o.shape != t.shape or o.dtype is not t.dtype or o.get_device() != t.get_device() or o.stride() != t.stride():
+                raise ValueError(f"{where}: out must match the list, tensor by tensor")
+        outs = (ctypes.c_void_p * n)(*[o.data_ptr() for o in out])
+    _want(where, "norm", norm, torch.float32, (1,), grads[0])
+    if norm is None:
+        norm = _grad_norm(where, grads, listed, flags, workspace)
+    _enqueue(where, grads[0], addresses, outs, counts, dtypes, n, norm.data_ptr(), max_norm, eps)
+    return norm

@@ -176,7 +176,45 @@ struct BlockNormArgs {
   hipStream_t stream;
 };
 
+struct MoeBalanceArgs {
+  const void *logits;
+  int dtype;
+  int64_t tokens, experts, ld, sequences;
+  const int32_t *ids;
+  int32_t top_k;
+  bool sigmoid;
+  float coef;
+  float *loss, *probs;       // forward
+  int32_t *counts, *live;    // forward: written; backward: read
+  const float *dloss;        // backward
+  const void *dlogits_in;
+  int64_t ld_in;
+  void *dlogits;
+  int64_t ldd;
+  void *workspace;
+  hipStream_t stream;
+};
+
+struct GradArgs {
+  const void *const *grads;  // host arrays
+  void *const *outs;
+  const int64_t *counts;
+  const int32_t *dtypes;
+  int64_t tensors;
+  bool max;
+  float max_norm, eps;
+  float *norm;  // norm: written; clip: read
+  double *workspace;
+  hipStream_t stream;
+};
+
 // Each returns hipSuccess or the launch error.
+hipError_t launch_moe_balance(const MoeBalanceArgs &a);
+hipError_t launch_moe_balance_backward(const MoeBalanceArgs &a);
+size_t moe_balance_workspace_bytes(int64_t tokens, int64_t experts, int64_t sequences);
+hipError_t launch_grad_norm(const GradArgs &a);
+hipError_t launch_grad_clip(const GradArgs &a);
+size_t grad_workspace_bytes(int64_t tensors, int64_t elements);
 hipError_t launch_moe_route(const MoeRouteArgs &a);
 hipError_t launch_moe_route_backward(const MoeRouteBackwardArgs &a);
 hipError_t launch_moe_plan(const int32_t *ids, int64_t slots, int64_t experts, int32_t *offsets, int32_t *rows,

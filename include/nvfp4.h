@@ -394,8 +394,64 @@ int nvfp4_block_norm_backward(const void *dx_out, const void *dn, const void *x,
                               void *workspace, void *hip_stream);
 
 /* ---- Fine-tuning beside the quantized products -----------------------------------------------------------
- * What a step over frozen quantized weights needs next to the calls above: the routing's balance loss, and the
- * norm and clipping of the gradients that the backward calls give.  Conventions as for the block above. */
+ * What serving and training steps over frozen quantized weights need next to the calls above: low-rank adapters beside
+ * a product, with their gradients, the routing's balance loss, and the norm and clipping of the gradients that the
+ * backward calls give.  Conventions as for the block above. */
+
+enum {
+  NVFP4_ADAPTER_GATHER = 1u << 0,  /* row r of c takes row rows[r] / row_div of x (a plan's rows, row_div its top_k) */
+  NVFP4_ADAPTER_BY_TOKEN = 1u << 1 /* x and c are in the tokens' own order: row r of the plan is row rows[r] of both  */
+};
+
+/* Bytes of device workspace of nvfp4_adapter / nvfp4_adapter_backward.  Needs no initialisation; calls that may overlap
+ * must use distinct workspaces. */
+size_t nvfp4_adapter_workspace_size(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters);
+size_t nvfp4_adapter_backward_workspace_size(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters);
+
+/* Low-rank adapters of many requests, or of many experts, beside a shared product whose result is base:
+ *   h[r] = A_g x[r],   c[r] = base[r] + scales[g] * B_g h[r]
+ * for the rows r of each adapter g.  Sums run in fp32; h enters the second product with at least 16 bits of precision for
+ * a bf16 c and 24 for an fp32 one; c is rounded once.
+ * x [x_rows x K] of x_dtype NVFP4_BF16 (else NVFP4_ERR_UNSUPPORTED), leading dimension ldx.  a: device bf16
+ * [adapters][rank][K], b: device bf16 [adapters][N][rank], scales: device float[adapters].
+ * offsets NULL: one adapter for all M == x_rows rows (adapters 1, flags 0; rows and pos are ignored).  Else a device plan,
+ * as nvfp4_moe_plan makes of each token's adapter (requests: top_k 1, an id outside [0, adapters) for none) or expert:
+ * rows offsets[g] .. offsets[g + 1] - 1 of its order have adapter g, and
+ *   flags 0:                 row r of x and of c is row r of this order (M == x_rows)
+ *   NVFP4_ADAPTER_GATHER:    row r of c takes row rows[r] / row_div of x
+ *   NVFP4_ADAPTER_BY_TOKEN:  row rows[r] of x and c (M == x_rows; rows distinct); pos [M]: the plan's (-1: no adapter)
+ * (not both flags).  Rows without an adapter are base's.  base [M x N] of c's dtype, leading dimension ldb; NULL: zeros.
+ * c [M x N], dtype NVFP4_F32 or NVFP4_BF16, leading dimension ldc; it may be base (in place), where rows without an
+ * adapter are then not touched; otherwise it overlaps no input.
+ * h: nullable device float [M][rank], the rows' h in the plan's order, for the backward call (rows behind
+ * offsets[adapters] are not written).
+ * rank a multiple of 8, 8 .. 128; adapters 1 .. 512; K a positive multiple of 8, K < 2^31; N >= 1, N < 2^31 (else
+ * NVFP4_ERR_SHAPE); a launch of 2^31 threads or more is refused (NVFP4_ERR_SHAPE: about 2^31 elements of c for few rows
+ * an adapter, 2^35 for many).  x, a, b and h 16-byte aligned, ldx a multiple of 8; base and c
+ * aligned to their elements.  workspace: device, nvfp4_adapter_workspace_size() bytes, 16-byte aligned. */
+int nvfp4_adapter(const void *x, int x_dtype, int64_t x_rows, int64_t ldx, const void *a, const void *b,
+                  const float *scales, int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters,
+                  const int32_t *offsets, const int32_t *rows, const int32_t *pos, int32_t row_div, uint32_t flags,
+                  const void *base, int64_t ldb, void *c, int c_dtype, int64_t ldc, float *h, void *workspace,
+                  void *hip_stream);
+
+/* Gradients of nvfp4_adapter from that of c, dc [M x N] (dc_dtype NVFP4_BF16, leading dimension lddc), its x, factors,
+ * scales, plan and h:
+ *   g[r] = scales[g] * B_g^T dc[r],  dx[r] = dx_base[r] + A_g^T g[r],  da_g = sum_r g[r] x[r]^T,
+ *   db_g = scales[g] * sum_r dc[r] h[r]^T
+ * dx [M x K] and dx_base (NULL: zeros; e.g. the shared product's own gradient) as c and base in the forward call, dtype
+ * dx_dtype.  da: device float [adapters][rank][K], db: device float [adapters][N][rank] (zeros for an adapter without
+ * rows).  base's gradient is dc itself.  Sums run in fp32 in one fixed order; g and h enter the second products with 24 bits.
+ * flags 0 or NVFP4_ADAPTER_BY_TOKEN (with NVFP4_ADAPTER_GATHER a row of x has several rows of c: gather the rows
+ * first, and sum their dx; NVFP4_ERR_UNSUPPORTED).  As nvfp4_adapter otherwise; N a multiple of 8 too, dc, da and db
+ * 16-byte aligned, lddc a multiple of 8.  dx may be dx_base, and otherwise overlaps no input.  workspace: device,
+ * nvfp4_adapter_backward_workspace_size() bytes, 16-byte aligned. */
+int nvfp4_adapter_backward(const void *dc, int dc_dtype, int64_t lddc, const void *x, int x_dtype, int64_t ldx,
+                           const void *a, const void *b, const float *scales, int64_t M, int64_t N, int64_t K,
+                           int32_t rank, int32_t adapters, const int32_t *offsets, const int32_t *rows,
+                           const int32_t *pos, uint32_t flags, const float *h, const void *dx_base, int64_t ldb,
+                           void *dx, int dx_dtype, int64_t lddx, float *da, float *db, void *workspace,
+                           void *hip_stream);
 
 /* Bytes of device workspace nvfp4_moe_balance needs (0 for one sequence of up to 64 tokens: workspace may then be
  * NULL).  Needs no initialisation; calls that may overlap must use distinct workspaces. */

@@ -29,7 +29,8 @@ __all__ = [
     "BlockNorm", "BlockNormGrads", "nvfp4_moe_route", "nvfp4_moe_route_backward", "nvfp4_moe_plan", "nvfp4_moe_gather",
     "nvfp4_moe_combine", "nvfp4_moe_combine_backward", "nvfp4_int8_quantize", "nvfp4_int8_gemm", "nvfp4_block_norm",
     "nvfp4_block_norm_backward", "NVFP4_GRAD_MAX", "MoEBalance", "nvfp4_moe_balance", "nvfp4_moe_balance_backward",
-    "nvfp4_grad_norm", "nvfp4_grad_clip",
+    "nvfp4_grad_norm", "nvfp4_grad_clip", "NVFP4_ADAPTER_GATHER", "NVFP4_ADAPTER_BY_TOKEN", "Adapters", "AdapterGrads",
+    "nvfp4_adapter", "nvfp4_adapter_backward",
 ]
 
 NVFP4_OK, NVFP4_ERR_NULL, NVFP4_ERR_SHAPE, NVFP4_ERR_ALIGN, NVFP4_ERR_UNSUPPORTED, NVFP4_ERR_HIP = range(6)
@@ -39,6 +40,7 @@ NVFP4_TS_FOR_FOUR, NVFP4_SCALE_SEARCH = 16, 32
 NVFP4_ROUTE_SIGMOID, NVFP4_ROUTE_RENORM, NVFP4_ROUTE_GROUP_SUM2 = 1, 2, 4
 NVFP4_NORM_ONE_PLUS, NVFP4_NORM_TOKEN_GATE = 1, 2
 NVFP4_GRAD_MAX = 1
+NVFP4_ADAPTER_GATHER, NVFP4_ADAPTER_BY_TOKEN = 1, 2
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB = None
@@ -106,6 +108,11 @@ def lib():
                 ("nvfp4_moe_balance", i, [P, i, i64, i64, i64, P, i32, i64, u32, f32, P, P, P, P, P, P]),
                 ("nvfp4_moe_balance_backward", i,
                  [P, i, i64, i64, i64, P, i32, i64, u32, f32, P, P, P, P, i64, P, i64, P]),
+                ("nvfp4_adapter_workspace_size", size, [i64, i64, i64, i32, i32]),
+                ("nvfp4_adapter_backward_workspace_size", size, [i64, i64, i64, i32, i32]),
+                ("nvfp4_adapter", i, [P, i, i64, i64, P, P, P, i64, i64, i64, i32, i32, P, P, P, i32, u32, P, i64, P, i, i64, P, P, P]),
+                ("nvfp4_adapter_backward", i,
+                 [P, i, i64, P, i, i64, P, P, P, i64, i64, i64, i32, i32, P, P, P, u32, P, P, i64, P, i, i64, P, P, P, P]),
                 ("nvfp4_grad_workspace_size", size, [i64, i64]),
                 ("nvfp4_grad_norm", i, [P, P, P, i64, u32, P, P, P]),
                 ("nvfp4_grad_clip", i, [P, P, P, P, i64, P, f32, f32, P])):
@@ -729,6 +736,110 @@ def _enqueue(name: str, like: torch.Tensor, *args):
         with torch.cuda.device(like.device):
             st = call(*args, stream)
     _check(st, name)
+
+
+@dataclass
+class Adapters:
+    """Low-rank factors of `count` adapters, one behind the other (adapters of lower rank are padded with zeros)."""
+    a: torch.Tensor       # bfloat16 [count*rank, k]
+    b: torch.Tensor       # bfloat16 [count*n, rank]
+    scales: torch.Tensor  # float32 [count], of each adapter's product
+    rank: int
+    k: int
+    n: int
+    count: int = 1
+
+
+@dataclass
+class AdapterGrads:
+    """What nvfp4_adapter_backward gives."""
+    dx: torch.Tensor
+    da: torch.Tensor  # float32 [count*rank, k]
+    db: torch.Tensor  # float32 [count*n, rank]
+
+
+def _adapter_inputs(where, x, w, plan, gather, by_token):
+    """(ldx, M, offsets, rows, pos, row_div, flags) of an adapter's call."""
+    bf16, ldx = torch.bfloat16, _matrix(where, "x", x)
+    if x.dtype is not bf16:
+        raise TypeError(f"{where}: x must be {bf16}, is {x.dtype}")
+    if x.shape[1] != w.k:
+        raise ValueError(f"{where}: x has K={x.shape[1]}, the adapters K={w.k}")
+    _want(where, "w.a", w.a, bf16, (w.count * w.rank, w.k), x)
+    _want(where, "w.b", w.b, bf16, (w.count * w.n, w.rank), x)
+    _want(where, "w.scales", w.scales, torch.float32, (w.count,), x)
+    T = x.shape[0]
+    if plan is None:
+        if gather or by_token or w.count != 1:
+            raise ValueError(f"{where}: more than one adapter needs a plan")
+        return ldx, T, None, None, None, 1, 0
+    if gather and by_token:
+        raise ValueError(f"{where}: rows are gathered or in the tokens' order, not both")
+    if plan.experts != w.count:
+        raise ValueError(f"{where}: the plan has {plan.experts} adapters, w {w.count}")
+    M = plan.rows.shape[0]
+    _want(where, "plan.offsets", plan.offsets, torch.int32, (w.count + 1,), x)
+    _want(where, "plan.rows", plan.rows, torch.int32, (T * plan.top_k if gather else T,), x)
+    if by_token:
+        _want(where, "plan.pos", plan.pos, torch.int32, (T, 1), x)
+        return ldx, M, plan.offsets.data_ptr(), plan.rows.data_ptr(), plan.pos.data_ptr(), 1, NVFP4_ADAPTER_BY_TOKEN
+    return (ldx, M, plan.offsets.data_ptr(), plan.rows.data_ptr(), None, plan.top_k if gather else 1,
+            NVFP4_ADAPTER_GATHER if gather else 0)
+
+
+def _beside(where, name, base, out, shape, dtype, like):
+    """(out, its leading dimension, base's) of a call that adds to base."""
+    ldb = 0
+    if base is not None:
+        if base.shape != shape or base.device != like.device:
+            raise ValueError(f"{where}: {name} must be {list(shape)} on {like.device}, is {list(base.shape)} on {base.device}")
+        ldb, dtype = _matrix(where, name, base), base.dtype
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=like.device), shape[1], ldb
+    if out.shape != shape or out.device != like.device or (base is not None and out.dtype is not dtype):
+        raise ValueError(f"{where}: out must be {list(shape)} like {name}")
+    return out, _matrix(where, "out", out), ldb
+
+
+def nvfp4_adapter(x: torch.Tensor, w: Adapters, base: Optional[torch.Tensor] = None, plan: Optional[MoEPlan] = None,
+                  gather: bool = False, by_token: bool = False, out_dtype: torch.dtype = torch.bfloat16, with_h: bool = False,
+                  out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None):
+    """base + scale * (x @ a^T) @ b^T with each row's own adapter (see include/nvfp4.h); returns the result, and with
+    with_h=True also h = x @ a^T (float32 [rows, rank], in the plan's order) for the backward call.  plan: of each token's
+    adapter (nvfp4_moe_plan of ids [tokens, 1]; by_token=True if x and base are in the tokens' own order) or
+    expert (x and base in the plan's order; gather=True if x has one row a token).  Without a plan w is one adapter for
+    all rows.  base None: zeros, the result in out_dtype.  out may be base."""
+    where = "nvfp4_adapter"
+    ldx, M, offsets, rows, pos, div, flags = _adapter_inputs(where, x, w, plan, gather, by_token)
+    out, ldc, ldb = _beside(where, "base", base, out, (M, w.n), out_dtype, x)
+    h = torch.empty((M, w.rank), dtype=torch.float32, device=x.device) if with_h else None
+    workspace = _scratch(where, workspace, lib().nvfp4_adapter_workspace_size(M, w.n, w.k, w.rank, w.count), x)
+    _enqueue(where, x, x.data_ptr(), _dtype_code(x.dtype), x.shape[0], max(ldx, w.k), w.a.data_ptr(), w.b.data_ptr(), w.scales.data_ptr(),
+             M, w.n, w.k, w.rank, w.count, offsets, rows, pos, div, flags, _addr(base), ldb, out.data_ptr(), _dtype_code(out.dtype),
+             ldc, _addr(h), _addr(workspace))
+    return (out, h) if with_h else out
+
+
+def nvfp4_adapter_backward(dout: torch.Tensor, x: torch.Tensor, w: Adapters, h: torch.Tensor, dx_base: Optional[torch.Tensor] = None,
+                           plan: Optional[MoEPlan] = None, by_token: bool = False, dx_dtype: torch.dtype = torch.bfloat16,
+                           dx: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> AdapterGrads:
+    """Gradients of nvfp4_adapter from that of its result (bfloat16), its inputs and its h: dx (added to dx_base, e.g.
+    the shared product's own; it may be dx_base) and float32 gradients of the factors.  With gathered rows gather x first."""
+    where = "nvfp4_adapter_backward"
+    ldx, M, offsets, rows, pos, _, flags = _adapter_inputs(where, x, w, plan, False, by_token)
+    if dout.dtype is not torch.bfloat16:
+        raise TypeError(f"{where}: dout must be {torch.bfloat16}, is {dout.dtype}")
+    if dout.shape != (M, w.n) or dout.device != x.device:
+        raise ValueError(f"{where}: dout must be [{M}, {w.n}] on {x.device}")
+    _want(where, "h", h, torch.float32, (M, w.rank), x)
+    dx, lddx, ldb = _beside(where, "dx_base", dx_base, dx, (M, w.k), dx_dtype, x)
+    da = torch.empty((w.count * w.rank, w.k), dtype=torch.float32, device=x.device)
+    db = torch.empty((w.count * w.n, w.rank), dtype=torch.float32, device=x.device)
+    workspace = _scratch(where, workspace, lib().nvfp4_adapter_backward_workspace_size(M, w.n, w.k, w.rank, w.count), x)
+    _enqueue(where, x, dout.data_ptr(), _dtype_code(dout.dtype), _matrix(where, "dout", dout), x.data_ptr(), _dtype_code(x.dtype), ldx,
+             w.a.data_ptr(), w.b.data_ptr(), w.scales.data_ptr(), M, w.n, w.k, w.rank, w.count, offsets, rows, pos, flags, h.data_ptr(),
+             _addr(dx_base), ldb, dx.data_ptr(), _dtype_code(dx.dtype), lddx, da.data_ptr(), db.data_ptr(), _addr(workspace))
+    return AdapterGrads(dx, da, db)
 
 
 @dataclass

@@ -35,7 +35,7 @@ def units():
     u = [(s, s + ".o", []) for s in ["nvfp4_api.cpp", "quantize.hip", "dequant.hip", "gemm.hip",
                                       "gemm_w4a16.hip", "transpose.hip", "block_api.cpp", "moe_route.hip",
                                       "moe_rows.hip", "int8_quantize.hip", "gemm_int8.hip", "block_norm.hip",
-                                      "tune_api.cpp", "moe_balance.hip", "grad.hip"]]
+                                      "tune_api.cpp", "moe_balance.hip", "grad.hip", "adapter.hip"]]
     for out in (0, 1, 2):
         for a2d in (0, 1):
             for b2d in (0, 1):

@@ -1,0 +1,947 @@
+// adapter.hip -- low-rank adapters of many requests (or experts) at once, beside a shared projection:
+//   h_r = A_g x_r,   c_r = base_r + s_g B_g h_r     (g: the adapter of row r)
+// and the gradients of x, A and B.  A [R x K] and B [N x R] of an adapter are bf16, R at most 128: all products run on
+// the bf16 matrix cores (v_mfma_f32_16x16x32_bf16: lane l holds row l & 15, elements 8 (l >> 4) .. + 7 of either operand,
+// and column l & 15, rows 4 (l >> 4) .. + 3 of the result).
+//
+// The long sums (h over K, dA and dB over the rows) stay in fp32.  Where h or its gradient g is an operand again, it is
+// taken as a sum of bf16 numbers, v = v0 + v1 (+ v2), each the rounding of what the ones before leave: 16 bits for a bf16
+// result, whose rounding is 2^-9, and 24, all that fp32 has, for fp32 results.  Such rows are kept as [M][3 R] bf16.
+//
+// Rows.  A plan's offsets live on the device: the launch has as many workgroups as any offsets could need (a partial
+// tile more for every adapter), and each finds its tile by a scan over the adapters' tile counts.
+#include "gemm_common.hpp"
+#include "nvfp4_internal.h"
+#include "vec_io.hpp"
+
+namespace nvfp4 {
+namespace {
+
+using namespace gemm;
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float floatx4 __attribute__((ext_vector_type(4)));
+typedef short short4v __attribute__((ext_vector_type(4)));
+
+// Where rows come from and go to (see MoEPlan): row r of the plan's order is row x_row(r) of x and row c_row(r) of c.
+struct Rows {
+  const int32_t *offsets;  // NULL: one adapter for all M rows
+  const int32_t *rows;     // NULL: row r itself
+  int32_t groups;
+  int32_t x_div;           // 0: x has rows in the plan's order; else x row = rows[r] / x_div
+  int32_t by_rows;         // c row = rows[r]
+  int64_t M, x_rows;
+};
+
+// What rows or columns that do not exist read.
+__device__ const uint4 kZeros = {0u, 0u, 0u, 0u};
+
+__device__ __forceinline__ int64_t x_row(const Rows &p, int64_t r) {
+  if (p.x_div == 0) return r;
+  const int64_t s = p.rows[r] / p.x_div;
+  return s >= 0 && s < p.x_rows ? s : -1;
+}
+__device__ __forceinline__ int64_t c_row(const Rows &p, int64_t r) {
+  if (!p.by_rows) return r;
+  const int64_t s = p.rows[r];
+  return s >= 0 && s < p.M ? s : -1;
+}
+
+// Tile `tm` of `size` rows among all adapters' tiles: its adapter and rows [m0, m_end), and how many tiles the adapter
+// has.  False beyond the last.  Every lane of the wave takes part and has the result.
+struct Tile {
+  int32_t group, tiles;
+  int64_t m0, m_end;
+};
+__device__ __forceinline__ bool find_tile(const Rows &p, int32_t size, int32_t tm, Tile &t) {
+  if (!p.offsets) {
+    t.group = 0;
+    t.tiles = static_cast<int32_t>((p.M + size - 1) / size);
+    t.m0 = static_cast<int64_t>(tm) * size;
+    t.m_end = min(t.m0 + size, p.M);
+    return t.m0 < p.M;
+  }
+  const int lane = threadIdx.x & 63;
+  int32_t before = 0;
+  for (int g0 = 0; g0 < p.groups; g0 += 64) {
+    const int g = g0 + lane;
+    const int32_t lo = g < p.groups ? p.offsets[g] : 0, hi = g < p.groups ? p.offsets[g + 1] : 0;
+    const int32_t n = hi > lo ? (hi - lo - 1) / size + 1 : 0;
+    int32_t s = n;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int32_t o = __shfl_up(s, d);
+      if (lane >= d) s += o;
+    }
+    const uint64_t past = __ballot(before + s > tm);
+    if (past) {
+      const int at = __builtin_ctzll(past);
+      const int32_t first = __builtin_amdgcn_readfirstlane(before + __shfl(s - n, at));
+      const int32_t m_lo = __builtin_amdgcn_readfirstlane(__shfl(lo, at)), m_hi = __builtin_amdgcn_readfirstlane(__shfl(hi, at));
+      t.group = g0 + at;
+      t.tiles = __builtin_amdgcn_readfirstlane(__shfl(n, at));
+      t.m0 = m_lo + static_cast<int64_t>(tm - first) * size;
+      t.m_end = min(min(t.m0 + size, static_cast<int64_t>(m_hi)), p.M);
+      return t.m0 >= 0 && t.m0 < t.m_end;
+    }
+    before += __builtin_amdgcn_readfirstlane(__shfl(s, 63));
+  }
+  return false;
+}
+
+__device__ __forceinline__ bf16x8 frag(const void *p) { return __builtin_bit_cast(bf16x8, *static_cast<const uint4 *>(p)); }
+__device__ __forceinline__ floatx4 mfma(const bf16x8 &a, const bf16x8 &b, const floatx4 &c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// Eight values as `parts` bf16 pieces each of which takes what the ones before leave.
+template <int PARTS>
+__device__ __forceinline__ void split8(float (&v)[8], uint4 (&out)[PARTS]) {
+#pragma unroll
+  for (int s = 0; s < PARTS; ++s) {
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      w[q] = pack_bf16(v[2 * q], v[2 * q + 1]);
+      v[2 * q] -= __uint_as_float(w[q] << 16);
+      v[2 * q + 1] -= __uint_as_float(w[q] & 0xFFFF0000u);
+    }
+    out[s] = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+// ---- rows x factor: part[split][r][q] = sum over the split's k of y[row(r)][k] f[g][q][k] --------------------
+struct ShrinkArgs {
+  Rows rows;
+  bool use_c_rows;       // y is indexed like c (a gradient), not like x
+  const uint8_t *y;
+  int64_t ldy;           // bytes
+  const uint8_t *f;      // [groups][R][K] bf16
+  int64_t K;
+  int32_t R;
+  int32_t splits, split_k;  // elements of K a split, a multiple of the step
+  float *part;           // [splits][M][R]
+};
+
+__device__ __forceinline__ int64_t y_row(const ShrinkArgs &p, int64_t r) {
+  return p.use_c_rows ? c_row(p.rows, r) : x_row(p.rows, r);
+}
+
+// Few rows an adapter: a workgroup has 16 rows and kFewK elements of K, a wave a quarter of these, all its loads in
+// flight at once; the waves' sums meet in LDS.
+constexpr int kFewWaveK = 128, kFewK = 4 * kFewWaveK;
+template <int RF>
+__global__ __launch_bounds__(256) void shrink_few_kernel(ShrinkArgs p) {
+  __shared__ floatx4 sums[4][RF][64];
+  const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, j = lane >> 4;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t tm = blockIdx.x / p.splits, split = blockIdx.x - tm * p.splits;
+  Tile t;
+  if (!find_tile(p.rows, 16, tm, t)) return;
+  const int64_t k0 = static_cast<int64_t>(split) * kFewK + wave * kFewWaveK + 8 * j;
+  const uint8_t *f = p.f + (static_cast<int64_t>(t.group) * p.R * p.K + k0) * 2;
+  uint4 a[RF][4], b[4];
+#pragma unroll
+  for (int u = 0; u < RF; ++u)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[u][i] = make_uint4(0, 0, 0, 0);
+      const int q = 16 * u + l16;
+      if (q < p.R && k0 + 32 * i < p.K) a[u][i] = *reinterpret_cast<const uint4 *>(f + (q * p.K + 32 * i) * 2);
+    }
+  const int64_t r = t.m0 + l16, y = r < t.m_end ? y_row(p, r) : -1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    b[i] = make_uint4(0, 0, 0, 0);
+    if (y >= 0 && k0 + 32 * i < p.K) b[i] = *reinterpret_cast<const uint4 *>(p.y + y * p.ldy + (k0 + 32 * i) * 2);
+  }
+  floatx4 acc[RF];
+#pragma unroll
+  for (int u = 0; u < RF; ++u) acc[u] = (floatx4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int u = 0; u < RF; ++u) acc[u] = mfma(__builtin_bit_cast(bf16x8, a[u][i]), __builtin_bit_cast(bf16x8, b[i]), acc[u]);
+#pragma unroll
+  for (int u = 0; u < RF; ++u) sums[wave][u][lane] = acc[u];
+  __syncthreads();
+  for (int u = wave; u < RF; u += 4) {
+    const floatx4 v = (sums[0][u][lane] + sums[1][u][lane]) + (sums[2][u][lane] + sums[3][u][lane]);
+    const int q = 16 * u + 4 * j;
+    if (r < t.m_end && q < p.R)
+      *reinterpret_cast<floatx4 *>(p.part + (static_cast<int64_t>(split) * p.rows.M + r) * p.R + q) = v;
+  }
+}
+
+// Many rows: a workgroup has 64 rows (a wave 16) and walks its split of K 64 elements (128 bytes of a row) a step through
+// a ring of LDS stages filled by direct loads.  16-byte chunk c of row r sits at c ^ ((r >> 1) & 7): the reads of a
+// fragment then cover all banks.
+constexpr int kManyRows = 64, kManyStep = 64, kManyStages = 4;
+__device__ __forceinline__ uint32_t swz(uint32_t r) { return (r >> 1) & 7u; }
+template <int RF>
+__global__ __launch_bounds__(256) void shrink_many_kernel(ShrinkArgs p) {
+  constexpr int kF = kManyRows * 128, kStage = kF + RF * 16 * 128;
+  constexpr int NF = (2 * RF + 3) / 4;  // loads of the factor a wave and step, eight rows each
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kManyStages * kStage];
+  const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, j = lane >> 4;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t tm = blockIdx.x / p.splits, split = blockIdx.x - tm * p.splits;
+  Tile t;
+  if (!find_tile(p.rows, kManyRows, tm, t)) return;
+  const uint8_t *const zeros = reinterpret_cast<const uint8_t *>(&kZeros);
+  const uint8_t *srcY[2], *srcF[NF];
+  uint32_t chunkY[2], chunkF[NF];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t R = 16 * wave + 8 * i + (lane >> 3);
+    chunkY[i] = ((lane & 7u) ^ swz(R)) * 8;
+    const int64_t r = t.m0 + R, y = r < t.m_end ? y_row(p, r) : -1;
+    srcY[i] = y >= 0 ? p.y + y * p.ldy : nullptr;
+  }
+#pragma unroll
+  for (int i = 0; i < NF; ++i) {
+    // (with fewer pieces than waves some waves fetch the same one)
+    const uint32_t R = 8 * ((wave + 4 * i) % (2 * RF)) + (lane >> 3);
+    chunkF[i] = ((lane & 7u) ^ swz(R)) * 8;
+    srcF[i] = R < static_cast<uint32_t>(p.R) ? p.f + (static_cast<int64_t>(t.group) * p.R + R) * p.K * 2 : nullptr;
+  }
+  const int64_t k_lo = static_cast<int64_t>(split) * p.split_k, k_hi = min(k_lo + p.split_k, p.K);
+  const int32_t steps = static_cast<int32_t>((k_hi - k_lo + kManyStep - 1) / kManyStep);
+  auto load = [&](int32_t kt) {
+    uint8_t *st = smem + (kt % kManyStages) * kStage;
+    const int64_t k = k_lo + static_cast<int64_t>(kt) * kManyStep;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t at = k + chunkY[i];
+      lds_load16(srcY[i] && at < k_hi ? srcY[i] + at * 2 : zeros, st + (16 * wave + 8 * i) * 128);
+    }
+#pragma unroll
+    for (int i = 0; i < NF; ++i) {
+      const int64_t at = k + chunkF[i];
+      lds_load16(srcF[i] && at < k_hi ? srcF[i] + at * 2 : zeros, st + kF + 8 * ((wave + 4 * i) % (2 * RF)) * 128);
+    }
+  };
+  constexpr int LPS = 2 + NF;
+#pragma unroll
+  for (int s = 0; s < kManyStages - 1; ++s) load(s);
+  floatx4 acc[RF];
+#pragma unroll
+  for (int u = 0; u < RF; ++u) acc[u] = (floatx4){0.0f, 0.0f, 0.0f, 0.0f};
+  for (int32_t kt = 0; kt < steps; ++kt) {
+    wait_vmcnt<(kManyStages - 2) * LPS>();
+    wait_lgkmcnt0();  // (this wave's reads of the stage that is filled next)
+    lds_barrier();
+    load(kt + kManyStages - 1);  // (beyond the last step: zeros, into a stage that nobody reads)
+    const uint8_t *st = smem + (kt % kManyStages) * kStage;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const uint32_t R = 16 * wave + l16;
+      const bf16x8 b = frag(st + R * 128 + ((4 * s + j) ^ swz(R)) * 16);
+#pragma unroll
+      for (int u = 0; u < RF; ++u) {
+        const uint32_t Q = 16 * u + l16;
+        acc[u] = mfma(frag(st + kF + Q * 128 + ((4 * s + j) ^ swz(Q)) * 16), b, acc[u]);
+      }
+    }
+  }
+  wait_vmcnt<0>();
+  const int64_t r = t.m0 + 16 * wave + l16;
+#pragma unroll
+  for (int u = 0; u < RF; ++u) {
+    const int q = 16 * u + 4 * j;
+    if (r < t.m_end && q < p.R)
+      *reinterpret_cast<floatx4 *>(p.part + (static_cast<int64_t>(split) * p.rows.M + r) * p.R + q) = acc[u];
+  }
+}
+
+// ---- sums of the splits, scaled and as bf16 pieces -----------------------------------------------------------
+struct FinishArgs {
+  Rows rows;
+  const float *part;  // [splits][M][R]
+  int32_t splits, R;
+  const float *scales;
+  float *h;           // nullable [M][R], unscaled
+  uint8_t *pieces;    // [M][3 R] bf16, of scale * h
+};
+// Eight columns of row r.
+__device__ __forceinline__ void sum_splits(const float *part, int64_t M, int32_t R, int32_t splits, int64_t r, int32_t q, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const floatx4 *at = reinterpret_cast<const floatx4 *>(part + (s * M + r) * R + q);
+    const floatx4 lo = at[0], hi = at[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] += lo[i];
+      v[4 + i] += hi[i];
+    }
+  }
+}
+__device__ __forceinline__ void store_h(float *h, int32_t R, int64_t r, int32_t q, const float (&v)[8]) {
+  floatx4 *at = reinterpret_cast<floatx4 *>(h + r * R + q);
+  at[0] = (floatx4){v[0], v[1], v[2], v[3]};
+  at[1] = (floatx4){v[4], v[5], v[6], v[7]};
+}
+constexpr int kFinishRows = 64;
+__device__ __forceinline__ void finish_tile(const FinishArgs &p, int32_t tm) {
+  Tile t;
+  if (!find_tile(p.rows, kFinishRows, tm, t)) return;
+  const int32_t RC = p.R / 8;
+  const float scale = p.scales[t.group];
+  for (int i = threadIdx.x; i < kFinishRows * RC; i += 256) {
+    const int64_t r = t.m0 + i / RC;
+    const int32_t rc = i % RC;
+    if (r >= t.m_end) break;
+    float v[8];
+    sum_splits(p.part, p.rows.M, p.R, p.splits, r, 8 * rc, v);
+    if (p.h) store_h(p.h, p.R, r, 8 * rc, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= scale;
+    uint4 w[3];
+    split8(v, w);
+    uint4 *out = reinterpret_cast<uint4 *>(p.pieces + r * (6 * p.R)) + rc;
+    out[0] = w[0];
+    out[RC] = w[1];
+    out[2 * RC] = w[2];
+  }
+}
+__global__ __launch_bounds__(256) void finish_kernel(FinishArgs p) { finish_tile(p, blockIdx.x); }
+
+// ---- rows + pieces x factor: c[row(r)][n] = base[row(r)][n] + sum_q piece[r][q] f[g][n][q] --------------------
+struct ExpandArgs {
+  Rows rows;
+  const int32_t *pos;     // by_rows: the row of each token (-1: none)
+  const uint8_t *f;       // [groups][N][R] bf16
+  int64_t N;
+  int32_t R;
+  const uint8_t *pieces;  // many rows
+  const float *part;      // few rows: [splits][M][R]
+  int32_t splits;
+  const float *scales;
+  float *h;               // few rows, nullable
+  const uint8_t *base;    // NULL: zeros
+  int64_t ldb;            // bytes
+  uint8_t *c;
+  int64_t ldc;            // bytes
+  bool vec;               // rows of base and c are aligned to 16 bytes and N fills whole pieces
+  int32_t tiles_n, tiles_m;  // a launch has tiles_n * (tiles_m + copy tiles) workgroups
+};
+
+template <bool BF16>
+__device__ __forceinline__ float element(const uint8_t *p, int64_t i) {
+  return BF16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(p)[i]) << 16)
+              : reinterpret_cast<const float *>(p)[i];
+}
+template <bool BF16>
+__device__ __forceinline__ void set_element(uint8_t *p, int64_t i, float v) {
+  if constexpr (BF16)
+    reinterpret_cast<uint16_t *>(p)[i] = static_cast<uint16_t>(pack_bf16(v, 0.0f));
+  else
+    reinterpret_cast<float *>(p)[i] = v;
+}
+
+// Rows without an adapter: c = base (or zeros), 64 rows and 256 columns a workgroup.
+template <bool BF16>
+__device__ void copy_rows(const ExpandArgs &p, int32_t tile, int64_t n0) {
+  constexpr int ES = BF16 ? 2 : 4, V = 16 / ES;
+  const int32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  int64_t covered = p.rows.offsets ? p.rows.offsets[p.rows.groups] : p.rows.M;
+  for (int i = wave; i < 64; i += 4) {
+    const int64_t r = static_cast<int64_t>(tile) * 64 + i;
+    if (r >= p.rows.M || (p.rows.by_rows ? p.pos[r] >= 0 : r < covered)) continue;
+    const uint8_t *from = p.base ? p.base + r * p.ldb : nullptr;
+    uint8_t *to = p.c + r * p.ldc;
+    if (p.vec) {
+      for (int64_t n = n0 + lane * V; n < min(n0 + 256, p.N); n += 64 * V)
+        *reinterpret_cast<uint4 *>(to + n * ES) = from ? *reinterpret_cast<const uint4 *>(from + n * ES) : make_uint4(0, 0, 0, 0);
+    } else {
+      for (int64_t n = n0 + lane; n < min(n0 + 256, p.N); n += 64) set_element<BF16>(to, n, from ? element<BF16>(from, n) : 0.0f);
+    }
+  }
+}
+
+// A workgroup has 16 TF rows and 256 columns, a wave 64 of these in four fragments: row 4 g + e of fragment f is column
+// 16 g + 4 f + e, so that a lane ends with 16 consecutive columns of its row.  NM products of 32 cover the pieces.
+// FEW: the pieces are formed here from the splits' sums, in LDS, not read.
+template <int NM, int TF, bool BF16, bool FEW>
+__global__ __launch_bounds__(256) void expand_kernel(ExpandArgs p) {
+  constexpr int ES = BF16 ? 2 : 4, PARTS = BF16 ? 2 : 3;
+  constexpr int kPitch = NM * 64 + 16;  // of a row of pieces in LDS (with the pad, rows start in different banks)
+  __shared__ __attribute__((aligned(16))) uint8_t staged[FEW ? 16 * TF * kPitch : 16];
+  const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, j = lane >> 4;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t tm = blockIdx.x / p.tiles_n, tn = blockIdx.x - tm * p.tiles_n;
+  if (tm >= p.tiles_m) return copy_rows<BF16>(p, tm - p.tiles_m, static_cast<int64_t>(tn) * 256);
+  Tile t;
+  if (!find_tile(p.rows, 16 * TF, tm, t)) return;
+  const int32_t RC = p.R / 8, chunks = PARTS * RC;
+  const int64_t n0 = static_cast<int64_t>(tn) * 256 + wave * 64;
+
+  // the factor's fragments
+  uint4 f[4][NM];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int64_t n = min(n0 + 16 * (l16 >> 2) + 4 * u + (l16 & 3), p.N - 1);
+    const uint8_t *row = p.f + (static_cast<int64_t>(t.group) * p.N + n) * p.R * 2;
+#pragma unroll
+    for (int i = 0; i < NM; ++i) {
+      const int32_t c = 4 * i + j;
+      f[u][i] = make_uint4(0, 0, 0, 0);
+      if (c < chunks) f[u][i] = *reinterpret_cast<const uint4 *>(row + (c % RC) * 16);
+    }
+  }
+  if constexpr (FEW) {
+    const float scale = p.scales[t.group];
+    for (int i = threadIdx.x; i < 16 * TF * RC; i += 256) {
+      const int32_t row = i / RC, rc = i % RC;
+      const int64_t r = t.m0 + row;
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+      if (r < t.m_end) {
+        sum_splits(p.part, p.rows.M, p.R, p.splits, r, 8 * rc, v);
+        if (p.h && tn == 0) store_h(p.h, p.R, r, 8 * rc, v);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] *= scale;
+      uint4 w[PARTS];
+      split8(v, w);
+#pragma unroll
+      for (int s = 0; s < PARTS; ++s) *reinterpret_cast<uint4 *>(staged + row * kPitch + (s * RC + rc) * 16) = w[s];
+    }
+    __syncthreads();
+  }
+  if (n0 >= p.N) return;
+
+  constexpr int NB = BF16 ? 2 : 4;  // 16-byte pieces of a lane's 16 columns
+  const int64_t n = n0 + 16 * j;
+#pragma unroll
+  for (int tf = 0; tf < TF; ++tf) {
+    const int64_t r = t.m0 + 16 * tf + l16;
+    if (t.m0 + 16 * tf >= t.m_end) break;
+    const int64_t cr = r < t.m_end ? c_row(p.rows, r) : -1;
+    uint4 b[NM];
+#pragma unroll
+    for (int i = 0; i < NM; ++i) {
+      const int32_t c = 4 * i + j;
+      b[i] = make_uint4(0, 0, 0, 0);
+      if (c < chunks) {
+        if constexpr (FEW)
+          b[i] = *reinterpret_cast<const uint4 *>(staged + (16 * tf + l16) * kPitch + c * 16);
+        else if (r < t.m_end)
+          b[i] = *reinterpret_cast<const uint4 *>(p.pieces + r * (6 * p.R) + c * 16);
+      }
+    }
+    floatx4 acc[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      acc[u] = (floatx4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < NM; ++i) acc[u] = mfma(__builtin_bit_cast(bf16x8, f[u][i]), __builtin_bit_cast(bf16x8, b[i]), acc[u]);
+    }
+    if (cr < 0) continue;
+    const uint8_t *from = p.base ? p.base + cr * p.ldb + n * ES : nullptr;
+    uint8_t *to = p.c + cr * p.ldc + n * ES;
+    if (p.vec) {
+#pragma unroll
+      for (int q = 0; q < NB; ++q) {
+        if (n + q * (16 / ES) >= p.N) break;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (from) v = *reinterpret_cast<const uint4 *>(from + 16 * q);
+        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (BF16) {
+            const int at = 8 * q + 2 * e;
+            w[e] = pack_bf16(__uint_as_float(w[e] << 16) + acc[at / 4][at % 4],
+                             __uint_as_float(w[e] & 0xFFFF0000u) + acc[at / 4][at % 4 + 1]);
+          } else {
+            w[e] = __float_as_uint(__uint_as_float(w[e]) + acc[q][e]);
+          }
+        }
+        *reinterpret_cast<uint4 *>(to + 16 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (n + e < p.N) set_element<BF16>(to, e, (from ? element<BF16>(from, e) : 0.0f) + acc[e / 4][e % 4]);
+    }
+  }
+}
+
+// ---- the factors' gradients: out[g][q][n] or out[g][n][q] = sum_r piece[r][q] y[row(r)][n] -----------------------
+struct OuterArgs {
+  Rows rows;
+  bool use_c_rows;
+  const uint8_t *y;
+  int64_t ldy;            // bytes
+  int64_t N;              // a multiple of 8
+  int32_t R;
+  const uint8_t *pieces;  // [M][3 R] bf16
+  bool n_major;           // out is [N][R], not [R][N]
+  int32_t chunk;          // rows of a workgroup, a multiple of 32
+  int32_t tiles_n;
+  float *part;            // [chunks][N R]
+  float *out;             // [groups][N R]
+};
+
+// A workgroup has `chunk` rows of one adapter and 256 columns of y, a wave 64 of these; 32 rows a step through LDS.  Both
+// operands lie with their rows (the contraction) outermost: fragments come from ds_read_b64_tr_b16, which gives a
+// lane four rows of one column.  32-byte unit u of row t of y sits at u ^ ((t & 3) | (t >> 1) & 4): the sixteen rows that
+// one read touches lie in different banks.
+constexpr int kOuterStep = 32, kOuterStages = 3, kMaxChunk = 1024;
+template <int RF>
+__global__ __launch_bounds__(256) void outer_kernel(OuterArgs p) {
+  constexpr int kY = kOuterStep * 512;
+  constexpr int NP = (kOuterStep * 6 * RF + 255) / 256;  // loads of pieces a wave and step (R = 16 RF at most)
+  constexpr int kStage = kY + NP * 4096;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[kOuterStages * kStage + 64];
+  __shared__ int32_t y_rows[kMaxChunk];  // the chunk's rows of y; -1 beyond the last
+  const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, j = lane >> 4;
+  const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int32_t tm = blockIdx.x / p.tiles_n, tn = blockIdx.x - tm * p.tiles_n;
+  Tile t;
+  if (!find_tile(p.rows, p.chunk, tm, t)) return;
+  const uint8_t *const zeros = reinterpret_cast<const uint8_t *>(&kZeros);
+  const int64_t n_wg = static_cast<int64_t>(tn) * 256;
+  const int32_t RC3 = 3 * p.R / 8;                 // 16-byte chunks of a row of pieces
+  const int32_t pitch = RC3 * 16;
+  const int32_t steps = static_cast<int32_t>((t.m_end - t.m0 + kOuterStep - 1) / kOuterStep);
+  for (int i = threadIdx.x; i < p.chunk; i += 256) {
+    const int64_t r = t.m0 + i;
+    y_rows[i] = static_cast<int32_t>(r < t.m_end ? (p.use_c_rows ? c_row(p.rows, r) : x_row(p.rows, r)) : -1);
+  }
+  __syncthreads();
+  // y: wave w loads rows [8 w, 8 w + 8), two a load; lane: row lane >> 5, position lane & 31
+  uint32_t col[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t T = 8 * wave + 2 * i + (lane >> 5);
+    const uint32_t u = ((lane & 31u) >> 1) ^ ((T & 3u) | ((T >> 1) & 4u));
+    col[i] = u * 16 + (lane & 1u) * 8;
+  }
+  int32_t prow[NP], pchunk[NP];
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    const int32_t at = (4 * i + wave) * 64 + lane;
+    prow[i] = at / RC3;
+    pchunk[i] = at - prow[i] * RC3;
+  }
+  auto load = [&](int32_t kt) {
+    uint8_t *st = smem + (kt % kOuterStages) * kStage;
+    const int64_t r0 = t.m0 + static_cast<int64_t>(kt) * kOuterStep;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int32_t at = kt * kOuterStep + 8 * wave + 2 * i + (lane >> 5), y = at < p.chunk ? y_rows[at] : -1;
+      const int64_t n = n_wg + col[i];
+      lds_load16(y >= 0 && n < p.N ? p.y + y * p.ldy + n * 2 : zeros, st + (8 * wave + 2 * i) * 512);
+    }
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int64_t r = r0 + prow[i];
+      lds_load16(prow[i] < kOuterStep && r < t.m_end ? p.pieces + r * pitch + pchunk[i] * 16 : zeros,
+                 st + kY + (4 * i + wave) * 1024);
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kOuterStages - 1; ++s) load(s);
+  floatx4 acc[RF][4];
+#pragma unroll
+  for (int u = 0; u < RF; ++u)
+#pragma unroll
+    for (int v = 0; v < 4; ++v) acc[u][v] = (floatx4){0.0f, 0.0f, 0.0f, 0.0f};
+  // Rows 8 j + 4 half + (l16 >> 2), elements 4 (l16 & 3) .. + 3 of a block of 16 columns: what this lane's address gives.
+  auto tr = [&](const uint8_t *at) {
+    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4v *)(at));
+  };
+  auto pair = [&](short4v lo, short4v hi) {
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  for (int32_t kt = 0; kt < steps; ++kt) {
+    wait_vmcnt<(kOuterStages - 2) * (4 + NP)>();
+    wait_lgkmcnt0();
+    lds_barrier();
+    load(kt + kOuterStages - 1);
+    uint8_t *st = smem + (kt % kOuterStages) * kStage;
+    bf16x8 y[4];
+    const uint32_t T = 8 * j + (l16 >> 2);  // (row T + 4 has the same swizzle)
+    const uint32_t sw = (T & 3u) | ((T >> 1) & 4u);
+#pragma unroll
+    for (int v = 0; v < 4; ++v) {
+      const uint8_t *at = st + T * 512 + ((4 * wave + v) ^ sw) * 32 + (l16 & 3u) * 8;
+      y[v] = pair(tr(at), tr(at + 4 * 512));
+    }
+#pragma unroll
+    for (int s = 0; s < 3; ++s)
+#pragma unroll
+      for (int u = 0; u < RF; ++u) {
+        const uint8_t *at = st + kY + T * pitch + (s * p.R + 16 * u + 4 * (l16 & 3u)) * 2;
+        const bf16x8 a = pair(tr(at), tr(at + 4 * pitch));
+#pragma unroll
+        for (int v = 0; v < 4; ++v) acc[u][v] = mfma(a, y[v], acc[u][v]);
+      }
+  }
+  wait_vmcnt<0>();
+  float *out = t.tiles == 1 ? p.out + static_cast<int64_t>(t.group) * p.N * p.R : p.part + static_cast<int64_t>(tm) * p.N * p.R;
+#pragma unroll
+  for (int v = 0; v < 4; ++v) {
+    const int64_t n = n_wg + 64 * wave + 16 * v + l16;
+    if (n >= p.N) continue;
+#pragma unroll
+    for (int u = 0; u < RF; ++u) {
+      const int q = 16 * u + 4 * j;
+      if (q >= p.R) continue;
+      if (p.n_major) {
+        *reinterpret_cast<floatx4 *>(out + n * p.R + q) = acc[u][v];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[(q + e) * p.N + n] = acc[u][v][e];
+      }
+    }
+  }
+}
+
+// Sums of an adapter's chunks in order; zeros for an adapter without rows.
+struct OuterSumArgs {
+  Rows rows;
+  int32_t chunk;
+  int64_t size;  // N R
+  int32_t blocks;  // workgroups an adapter
+  const float *part;
+  float *out;
+};
+constexpr int kOuterSumSize = 1024;
+__device__ __forceinline__ void outer_sum(const OuterSumArgs &p, int64_t id) {
+  const int32_t g = static_cast<int32_t>(id / p.blocks), lane = threadIdx.x & 63;
+  int32_t first = 0, n;
+  if (p.rows.offsets) {
+    for (int i = lane; i < g; i += 64) {
+      const int32_t rows = p.rows.offsets[i + 1] - p.rows.offsets[i];
+      first += rows > 0 ? (rows - 1) / p.chunk + 1 : 0;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) first += __shfl_xor(first, d);
+    const int32_t rows = p.rows.offsets[g + 1] - p.rows.offsets[g];
+    n = rows > 0 ? (rows - 1) / p.chunk + 1 : 0;
+  } else {
+    n = static_cast<int32_t>((p.rows.M + p.chunk - 1) / p.chunk);
+  }
+  if (n == 1) return;
+  const int64_t i = (id - static_cast<int64_t>(g) * p.blocks) * kOuterSumSize + threadIdx.x * 4;
+  if (i >= p.size) return;
+  floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int c = 0; c < n; ++c) v += *reinterpret_cast<const floatx4 *>(p.part + (static_cast<int64_t>(first) + c) * p.size + i);
+  *reinterpret_cast<floatx4 *>(p.out + g * p.size + i) = v;
+}
+__global__ __launch_bounds__(256) void outer_sum_kernel(OuterSumArgs a, OuterSumArgs b, int64_t blocks_a) {
+  if (blockIdx.x < blocks_a)
+    outer_sum(a, blockIdx.x);
+  else
+    outer_sum(b, blockIdx.x - blocks_a);
+}
+
+// ---- before a backward pass: transposed factors, and the pieces of h -------------------------------------------
+// out[g][c][r] = in[g][r][c], [rows x cols] bf16 with cols a multiple of 8 and one of the two at most 128; 64 x 64 tiles.
+struct TransposeArgs {
+  const uint16_t *in;
+  uint16_t *out;
+  int64_t rows, cols;
+  int32_t tiles_r, tiles_c;
+};
+__device__ void transpose_tile(const TransposeArgs &p, int64_t id, uint16_t (&lds)[64][66]) {
+  const int64_t per = static_cast<int64_t>(p.tiles_r) * p.tiles_c, g = id / per;
+  const int32_t in_g = static_cast<int32_t>(id - g * per), tr = in_g / p.tiles_c, tc = in_g - tr * p.tiles_c;
+  const int64_t r0 = tr * 64ll, c0 = tc * 64ll;
+  const uint16_t *in = p.in + g * p.rows * p.cols;
+  uint16_t *out = p.out + g * p.rows * p.cols;
+  const int32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int i = wave; i < 64; i += 4)
+    if (r0 + i < p.rows && c0 + lane < p.cols) lds[i][lane] = in[(r0 + i) * p.cols + c0 + lane];
+  __syncthreads();
+  for (int i = wave; i < 64; i += 4)
+    if (c0 + i < p.cols && r0 + lane < p.rows) out[(c0 + i) * p.rows + r0 + lane] = lds[lane][i];
+}
+__global__ __launch_bounds__(256) void adapter_prep_kernel(TransposeArgs a, int64_t blocks_a, TransposeArgs b, int64_t blocks_b,
+                                                           FinishArgs h) {
+  __shared__ uint16_t lds[64][66];
+  const int64_t id = blockIdx.x;
+  if (id < blocks_a)
+    transpose_tile(a, id, lds);
+  else if (id < blocks_a + blocks_b)
+    transpose_tile(b, id - blocks_a, lds);
+  else
+    finish_tile(h, static_cast<int32_t>(id - blocks_a - blocks_b));
+}
+
+// ---- launches ----------------------------------------------------------------------------------------------------
+Rows rows_of(const AdapterArgs &a) {
+  Rows p{};
+  p.offsets = a.offsets;
+  p.rows = a.rows;
+  p.groups = a.adapters;
+  p.x_div = a.by_token ? 1 : (a.gather ? a.row_div : 0);
+  p.by_rows = a.by_token;
+  p.M = a.M;
+  p.x_rows = a.x_rows;
+  return p;
+}
+// Tiles of `size` rows that any offsets could need.
+int64_t tiles_for(const AdapterArgs &a, int64_t size) {
+  if (!a.offsets) return (a.M + size - 1) / size;
+  return a.M / size + (a.adapters < a.M ? a.adapters : a.M);
+}
+
+// Few rows an adapter: 16 rows a tile.
+bool few_rows(int64_t M, int64_t adapters) { return M <= 256 || M <= 16 * adapters; }
+
+// Splits of K for many rows: workgroups for every compute unit, each with at least four steps.
+void many_splits(int64_t M, int64_t K, int32_t &splits, int32_t &split_k) {
+  const int64_t tiles = (M + kManyRows - 1) / kManyRows, steps = (K + kManyStep - 1) / kManyStep;
+  int64_t n = (768 + tiles - 1) / tiles;
+  if (n > steps / 4) n = steps / 4;
+  if (n > 8) n = 8;
+  if (n < 1) n = 1;
+  const int64_t per = (steps + n - 1) / n;
+  split_k = static_cast<int32_t>(per * kManyStep);
+  splits = static_cast<int32_t>((steps + per - 1) / per);
+}
+int32_t splits_for(int64_t M, int64_t adapters, int64_t K) {
+  if (few_rows(M, adapters)) return static_cast<int32_t>((K + kFewK - 1) / kFewK);
+  int32_t n, k;
+  many_splits(M, K, n, k);
+  return n;
+}
+
+template <int RF>
+hipError_t run_shrink(const ShrinkArgs &p, bool few, int64_t tiles, hipStream_t stream) {
+  const dim3 grid(static_cast<uint32_t>(tiles * p.splits));
+  if (few)
+    shrink_few_kernel<RF><<<grid, dim3(256), 0, stream>>>(p);
+  else
+    shrink_many_kernel<RF><<<grid, dim3(256), 0, stream>>>(p);
+  return hipGetLastError();
+}
+hipError_t run_shrink(const AdapterArgs &a, bool use_c_rows, const void *y, int64_t ldy, const void *f, int64_t K, float *part,
+                      int32_t &splits) {
+  ShrinkArgs p{};
+  p.rows = rows_of(a);
+  p.use_c_rows = use_c_rows;
+  p.y = static_cast<const uint8_t *>(y);
+  p.ldy = ldy * 2;
+  p.f = static_cast<const uint8_t *>(f);
+  p.K = K;
+  p.R = a.rank;
+  p.part = part;
+  const bool few = few_rows(a.M, a.adapters);
+  if (few) {
+    p.splits = static_cast<int32_t>((K + kFewK - 1) / kFewK);
+    p.split_k = kFewK;
+  } else {
+    many_splits(a.M, K, p.splits, p.split_k);
+  }
+  splits = p.splits;
+  const int64_t tiles = tiles_for(a, few ? 16 : kManyRows);
+  if (a.rank <= 16) return run_shrink<1>(p, few, tiles, a.stream);
+  if (a.rank <= 32) return run_shrink<2>(p, few, tiles, a.stream);
+  if (a.rank <= 64) return run_shrink<4>(p, few, tiles, a.stream);
+  return run_shrink<8>(p, few, tiles, a.stream);
+}
+
+template <int NM, bool BF16>
+hipError_t run_expand(const ExpandArgs &p, bool few, uint32_t groups, hipStream_t stream) {
+  if (few)
+    expand_kernel<NM, 1, BF16, true><<<dim3(groups), dim3(256), 0, stream>>>(p);
+  else
+    expand_kernel<NM, 4, BF16, false><<<dim3(groups), dim3(256), 0, stream>>>(p);
+  return hipGetLastError();
+}
+template <bool BF16>
+hipError_t run_expand(const ExpandArgs &p, bool few, uint32_t groups, hipStream_t stream) {
+  const int need = ((BF16 ? 2 : 3) * p.R / 8 + 3) / 4;
+  if (need <= 1) return run_expand<1, BF16>(p, few, groups, stream);
+  if (need <= 2) return run_expand<2, BF16>(p, few, groups, stream);
+  if (need <= 3) return run_expand<3, BF16>(p, few, groups, stream);
+  if (need <= 4) return run_expand<4, BF16>(p, few, groups, stream);
+  if (need <= 6) return run_expand<6, BF16>(p, few, groups, stream);
+  if constexpr (BF16) {
+    return run_expand<8, BF16>(p, few, groups, stream);
+  } else {
+    if (need <= 8) return run_expand<8, BF16>(p, few, groups, stream);
+    return run_expand<12, BF16>(p, few, groups, stream);
+  }
+}
+// `few`: part holds the splits' sums; else pieces are there.
+hipError_t run_expand(const AdapterArgs &a, const void *f, int64_t N, const uint8_t *pieces, const float *part, int32_t splits,
+                      float *h, const void *base, int64_t ldb, void *c, int64_t ldc, int dtype) {
+  ExpandArgs p{};
+  const int64_t es = dtype == 1 ? 2 : 4;
+  const bool few = pieces == nullptr;
+  p.rows = rows_of(a);
+  p.pos = a.pos;
+  p.f = static_cast<const uint8_t *>(f);
+  p.N = N;
+  p.R = a.rank;
+  p.pieces = pieces;
+  p.part = part;
+  p.splits = splits;
+  p.scales = a.scales;
+  p.h = h;
+  p.base = static_cast<const uint8_t *>(base);
+  p.ldb = ldb * es;
+  p.c = static_cast<uint8_t *>(c);
+  p.ldc = ldc * es;
+  p.vec = (reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(c) | static_cast<uintptr_t>(p.ldc) |
+           static_cast<uintptr_t>(base ? p.ldb : 0) | static_cast<uintptr_t>(N * es)) % 16 == 0;
+  p.tiles_n = static_cast<int32_t>((N + 255) / 256);
+  p.tiles_m = static_cast<int32_t>(tiles_for(a, few ? 16 : 64));
+  // rows without an adapter have to be written unless c is base
+  const int64_t copies = a.offsets && (base != c || ldb != ldc) ? (a.M + 63) / 64 : 0;
+  const uint32_t groups = static_cast<uint32_t>(p.tiles_n * (p.tiles_m + copies));
+  return dtype == 1 ? run_expand<true>(p, few, groups, a.stream) : run_expand<false>(p, few, groups, a.stream);
+}
+
+hipError_t run_finish(const AdapterArgs &a, const float *part, int32_t splits, float *h, uint8_t *pieces) {
+  FinishArgs p{rows_of(a), part, splits, a.rank, a.scales, h, pieces};
+  finish_kernel<<<dim3(static_cast<uint32_t>(tiles_for(a, kFinishRows))), dim3(256), 0, a.stream>>>(p);
+  return hipGetLastError();
+}
+
+// Rows of a workgroup of the factors' gradients: as many as leave about two workgroups a compute unit.
+int32_t outer_chunk(int64_t M, int64_t N) {
+  const int64_t tiles_n = (N + 255) / 256;
+  int64_t chunk = kMaxChunk;
+  while (chunk > 64 && tiles_n * (M / chunk) < 512) chunk /= 2;
+  return static_cast<int32_t>(chunk);
+}
+template <int RF>
+hipError_t run_outer(const OuterArgs &p, uint32_t groups, hipStream_t stream) {
+  outer_kernel<RF><<<dim3(groups), dim3(256), 0, stream>>>(p);
+  return hipGetLastError();
+}
+hipError_t run_outer(const AdapterArgs &a, bool use_c_rows, const void *y, int64_t ldy, int64_t N, const uint8_t *pieces, bool n_major,
+                     float *part, float *out) {
+  OuterArgs p{};
+  p.rows = rows_of(a);
+  p.use_c_rows = use_c_rows;
+  p.y = static_cast<const uint8_t *>(y);
+  p.ldy = ldy * 2;
+  p.N = N;
+  p.R = a.rank;
+  p.pieces = pieces;
+  p.n_major = n_major;
+  p.chunk = outer_chunk(a.M, N);
+  p.tiles_n = static_cast<int32_t>((N + 255) / 256);
+  p.part = part;
+  p.out = out;
+  const uint32_t groups = static_cast<uint32_t>(p.tiles_n * tiles_for(a, p.chunk));
+  if (a.rank <= 16) return run_outer<1>(p, groups, a.stream);
+  if (a.rank <= 32) return run_outer<2>(p, groups, a.stream);
+  if (a.rank <= 64) return run_outer<4>(p, groups, a.stream);
+  return run_outer<8>(p, groups, a.stream);
+}
+
+// The workspace's parts, each a multiple of 256 bytes.
+struct Layout {
+  size_t at = 0;
+  size_t take(int64_t bytes) {
+    const size_t here = at;
+    at += (static_cast<size_t>(bytes) + 255) / 256 * 256;
+    return here;
+  }
+};
+struct ForwardLayout {
+  size_t part, pieces, size;
+  ForwardLayout(int64_t M, int64_t K, int64_t R, int64_t adapters) {
+    Layout l;
+    part = l.take(splits_for(M, adapters, K) * M * R * 4);
+    pieces = few_rows(M, adapters) ? 0 : l.take(M * R * 6);
+    size = l.at;
+  }
+};
+struct BackwardLayout {
+  size_t at, bt, h_pieces, part, g_pieces, da_part, db_part, size;
+  BackwardLayout(const AdapterArgs &a) {
+    Layout l;
+    const int64_t factor = static_cast<int64_t>(a.adapters) * a.rank;
+    at = l.take(factor * a.K * 2);
+    bt = l.take(factor * a.N * 2);
+    h_pieces = l.take(a.M * a.rank * 6);
+    part = l.take(static_cast<int64_t>(splits_for(a.M, a.adapters, a.N)) * a.M * a.rank * 4);
+    g_pieces = l.take(a.M * a.rank * 6);
+    da_part = l.take(tiles_for(a, outer_chunk(a.M, a.K)) * a.K * a.rank * 4);
+    db_part = l.take(tiles_for(a, outer_chunk(a.M, a.N)) * a.N * a.rank * 4);
+    size = l.at;
+  }
+};
+
+}  // namespace
+
+size_t adapter_workspace_bytes(int64_t M, int64_t K, int32_t rank, int32_t adapters) {
+  return ForwardLayout(M, K, rank, adapters).size;
+}
+size_t adapter_backward_workspace_bytes(const AdapterArgs &a) { return BackwardLayout(a).size; }
+
+// (2^32 threads or more do not launch)
+bool adapter_launches(const AdapterArgs &a, bool backward) {
+  constexpr int64_t kMost = int64_t(1) << 23;
+  const int64_t widest = ((a.N > a.K ? a.N : a.K) + 255) / 256;
+  const bool few = few_rows(a.M, a.adapters);
+  const int64_t tiles = tiles_for(a, few ? 16 : 64) + (a.M + 63) / 64;
+  const int64_t splits = splits_for(a.M, a.adapters, backward ? a.N : a.K);
+  const int64_t sums = backward ? a.adapters * ((a.N + a.K) * a.rank / kOuterSumSize + 2) : 0;
+  const int64_t prep = backward ? a.adapters * ((a.rank + 63) / 64) * ((a.N + 63) / 64 + (a.K + 63) / 64) + tiles : 0;
+  return tiles * widest < kMost && tiles * splits < kMost && sums < kMost && prep < kMost &&
+         (!backward || widest * tiles_for(a, 64) < kMost);
+}
+
+hipError_t launch_adapter(const AdapterArgs &a) {
+  const ForwardLayout l(a.M, a.K, a.rank, a.adapters);
+  uint8_t *const w = static_cast<uint8_t *>(a.workspace);
+  float *const part = reinterpret_cast<float *>(w + l.part);
+  int32_t splits;
+  hipError_t e = run_shrink(a, false, a.x, a.ldx, a.a, a.K, part, splits);
+  if (e != hipSuccess) return e;
+  uint8_t *pieces = nullptr;
+  if (!few_rows(a.M, a.adapters)) {
+    pieces = w + l.pieces;
+    if ((e = run_finish(a, part, splits, a.h, pieces)) != hipSuccess) return e;
+  }
+  return run_expand(a, a.b, a.N, pieces, part, splits, a.h, a.base, a.ldb, a.c, a.ldc, a.c_dtype);
+}
+
+hipError_t launch_adapter_backward(const AdapterArgs &a) {
+  const BackwardLayout l(a);
+  uint8_t *const w = static_cast<uint8_t *>(a.workspace);
+  float *const part = reinterpret_cast<float *>(w + l.part), *const da_part = reinterpret_cast<float *>(w + l.da_part),
+              *const db_part = reinterpret_cast<float *>(w + l.db_part);
+  const Rows rows = rows_of(a);
+  hipError_t e;
+  if (a.M > 0) {  // A^T [K][R], B^T [R][N], and the pieces of s h
+    auto tiles = [](int64_t n) { return static_cast<int32_t>((n + 63) / 64); };
+    TransposeArgs ta{static_cast<const uint16_t *>(a.a), reinterpret_cast<uint16_t *>(w + l.at), a.rank, a.K, tiles(a.rank), tiles(a.K)};
+    TransposeArgs tb{static_cast<const uint16_t *>(a.b), reinterpret_cast<uint16_t *>(w + l.bt), a.N, a.rank, tiles(a.N), tiles(a.rank)};
+    FinishArgs h{rows, a.h, 1, a.rank, a.scales, nullptr, w + l.h_pieces};
+    const int64_t na = static_cast<int64_t>(a.adapters) * ta.tiles_r * ta.tiles_c, nb = static_cast<int64_t>(a.adapters) * tb.tiles_r * tb.tiles_c;
+    adapter_prep_kernel<<<dim3(static_cast<uint32_t>(na + nb + tiles_for(a, kFinishRows))), dim3(256), 0, a.stream>>>(ta, na, tb, nb, h);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (a.M > 0) {
+    int32_t splits;
+    if ((e = run_shrink(a, true, a.dc, a.lddc, w + l.bt, a.N, part, splits)) != hipSuccess) return e;
+    if ((e = run_finish(a, part, splits, nullptr, w + l.g_pieces)) != hipSuccess) return e;
+    if ((e = run_expand(a, w + l.at, a.K, w + l.g_pieces, nullptr, 0, nullptr, a.base, a.ldb, a.c, a.ldc, a.c_dtype)) != hipSuccess)
+      return e;
+    if ((e = run_outer(a, true, a.dc, a.lddc, a.N, w + l.h_pieces, true, db_part, a.db)) != hipSuccess) return e;
+    if ((e = run_outer(a, false, a.x, a.ldx, a.K, w + l.g_pieces, false, da_part, a.da)) != hipSuccess) return e;
+  }
+  OuterSumArgs sa{rows, outer_chunk(a.M, a.K), a.K * a.rank, 0, da_part, a.da}, sb{rows, outer_chunk(a.M, a.N), a.N * a.rank, 0, db_part, a.db};
+  sa.blocks = static_cast<int32_t>((sa.size + kOuterSumSize - 1) / kOuterSumSize);
+  sb.blocks = static_cast<int32_t>((sb.size + kOuterSumSize - 1) / kOuterSumSize);
+  const int64_t na = static_cast<int64_t>(a.adapters) * sa.blocks, nb = static_cast<int64_t>(a.adapters) * sb.blocks;
+  outer_sum_kernel<<<dim3(static_cast<uint32_t>(na + nb)), dim3(256), 0, a.stream>>>(sa, sb, na);
+  return hipGetLastError();
+}
+
+}  // namespace nvfp4

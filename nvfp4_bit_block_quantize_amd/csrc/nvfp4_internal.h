@@ -208,7 +208,35 @@ struct GradArgs {
   hipStream_t stream;
 };
 
+struct AdapterArgs {
+  const void *x;
+  int64_t x_rows, ldx;
+  const void *a, *b;    // bf16 [adapters][rank][K], [adapters][N][rank]
+  const float *scales;  // [adapters]
+  int64_t M, N, K;
+  int32_t rank, adapters;
+  const int32_t *offsets, *rows, *pos;  // device (offsets nullptr: one adapter)
+  int32_t row_div;
+  bool gather, by_token;
+  const void *base;  // forward: of c; backward: of dx
+  int64_t ldb;
+  void *c;           // forward: c; backward: dx
+  int64_t ldc;
+  int c_dtype;
+  float *h;          // forward: written (nullptr: not); backward: read
+  const void *dc;    // backward
+  int64_t lddc;
+  float *da, *db;
+  void *workspace;
+  hipStream_t stream;
+};
+
 // Each returns hipSuccess or the launch error.
+hipError_t launch_adapter(const AdapterArgs &a);
+hipError_t launch_adapter_backward(const AdapterArgs &a);
+size_t adapter_workspace_bytes(int64_t M, int64_t K, int32_t rank, int32_t adapters);
+size_t adapter_backward_workspace_bytes(const AdapterArgs &a);
+bool adapter_launches(const AdapterArgs &a, bool backward);
 hipError_t launch_moe_balance(const MoeBalanceArgs &a);
 hipError_t launch_moe_balance_backward(const MoeBalanceArgs &a);
 size_t moe_balance_workspace_bytes(int64_t tokens, int64_t experts, int64_t sequences);

@@ -1,5 +1,5 @@
-// tune_api.cpp -- C ABI front end of the operators of fine-tuning beside the quantized products (balance loss,
-// gradient norm and clipping): argument validation on the host, then the kernel launchers.  As in
+// tune_api.cpp -- C ABI front end of the operators of fine-tuning beside the quantized products (adapters,
+// balance loss, gradient norm and clipping): argument validation on the host, then the kernel launchers.  As in
 // nvfp4_api.cpp, validation never touches the GPU.
 #pragma GCC visibility push(default)
 #include "../../include/nvfp4.h"
@@ -19,6 +19,7 @@ namespace {
 constexpr int64_t kMaxSlots = int64_t(1) << 31;
 constexpr int64_t kMaxExperts = 512, kMaxSequences = 65535;
 constexpr int32_t kMaxTopK = 32;
+constexpr int32_t kMaxRank = 128;
 constexpr int64_t kMaxElements = int64_t(1) << 40, kMaxTensors = int64_t(1) << 20;
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -84,9 +85,134 @@ int check_overlap(const void *const *grads, void *const *outs, const int64_t *co
   return NVFP4_OK;
 }
 
+// What the forward and backward calls of an adapter share.  ldo, es: of the output and its dtype.
+int check_adapter(const nvfp4::AdapterArgs &a, int x_dtype, int out_dtype, uint32_t flags) {
+  if (x_dtype != NVFP4_BF16 || dtype_size(out_dtype) == 0 || (flags & ~(NVFP4_ADAPTER_GATHER | NVFP4_ADAPTER_BY_TOKEN)) ||
+      (a.gather && a.by_token))
+    return NVFP4_ERR_UNSUPPORTED;
+  if (a.M < 0 || a.M >= kMaxSlots || a.x_rows < 0 || a.x_rows >= kMaxSlots || a.N < 1 || a.N >= kMaxSlots || a.K < 8 ||
+      a.K >= kMaxSlots || a.K % 8 != 0 || a.rank < 8 || a.rank > kMaxRank || a.rank % 8 != 0 || a.adapters < 1 ||
+      a.adapters > kMaxExperts || a.ldx < a.K || product(a.x_rows, a.ldx) < 0)
+    return NVFP4_ERR_SHAPE;
+  if (!a.offsets && (a.adapters != 1 || flags)) return NVFP4_ERR_SHAPE;
+  if (a.gather ? a.row_div < 1 : a.x_rows != a.M) return NVFP4_ERR_SHAPE;
+  return NVFP4_OK;
+}
+// Their pointers, for M > 0.
+int check_adapter_pointers(const nvfp4::AdapterArgs &a, int out_dtype, size_t workspace_bytes) {
+  if ((a.x_rows > 0 && !a.x) || !a.a || !a.b || !a.scales || !a.c || (workspace_bytes > 0 && !a.workspace)) return NVFP4_ERR_NULL;
+  if ((a.gather || a.by_token) && !a.rows) return NVFP4_ERR_NULL;
+  if (a.by_token && !a.pos) return NVFP4_ERR_NULL;
+  const int es = dtype_size(out_dtype);
+  if (!aligned(a.x, 16) || a.ldx % 8 != 0 || !aligned(a.a, 16) || !aligned(a.b, 16) || !aligned(a.scales, 4) || !aligned(a.offsets, 4) ||
+      !aligned(a.rows, 4) || !aligned(a.pos, 4) || !aligned(a.base, es) || !aligned(a.c, es) || !aligned(a.h, 16) ||
+      !aligned(a.workspace, 16))
+    return NVFP4_ERR_ALIGN;
+  return NVFP4_OK;
+}
+
+nvfp4::AdapterArgs adapter_args(const void *x, int64_t x_rows, int64_t ldx, const void *a, const void *b, const float *scales,
+                                int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters, const int32_t *offsets,
+                                const int32_t *rows, const int32_t *pos, int32_t row_div, uint32_t flags) {
+  nvfp4::AdapterArgs p{};
+  p.x = x;
+  p.x_rows = x_rows;
+  p.ldx = ldx;
+  p.a = a;
+  p.b = b;
+  p.scales = scales;
+  p.M = M;
+  p.N = N;
+  p.K = K;
+  p.rank = rank;
+  p.adapters = adapters;
+  p.offsets = offsets;
+  p.rows = rows;
+  p.pos = pos;
+  p.row_div = row_div;
+  p.gather = flags & NVFP4_ADAPTER_GATHER;
+  p.by_token = flags & NVFP4_ADAPTER_BY_TOKEN;
+  return p;
+}
+
+// Whether a size is one that the workspace functions answer for.
+bool adapter_sizes(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters) {
+  return M >= 0 && M < kMaxSlots && N >= 1 && N < kMaxSlots && K >= 8 && K < kMaxSlots && rank >= 8 && rank <= kMaxRank && adapters >= 1 &&
+         adapters <= kMaxExperts;
+}
+
 }  // namespace
 
 extern "C" {
+
+size_t nvfp4_adapter_workspace_size(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters) {
+  return adapter_sizes(M, N, K, rank, adapters) ? (nvfp4::adapter_workspace_bytes(M, K, rank, adapters) + 15) / 16 * 16 : 0;
+}
+
+size_t nvfp4_adapter_backward_workspace_size(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters) {
+  if (!adapter_sizes(M, N, K, rank, adapters)) return 0;
+  // (with a plan as without one: more than one tile of rows may end early)
+  static const int32_t some = 0;
+  const nvfp4::AdapterArgs a = adapter_args(nullptr, M, K, nullptr, nullptr, nullptr, M, N, K, rank, adapters, &some, nullptr, nullptr, 1, 0);
+  return (nvfp4::adapter_backward_workspace_bytes(a) + 15) / 16 * 16;
+}
+
+int nvfp4_adapter(const void *x, int x_dtype, int64_t x_rows, int64_t ldx, const void *a, const void *b,
+                  const float *scales, int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters,
+                  const int32_t *offsets, const int32_t *rows, const int32_t *pos, int32_t row_div, uint32_t flags,
+                  const void *base, int64_t ldb, void *c, int c_dtype, int64_t ldc, float *h, void *workspace,
+                  void *hip_stream) {
+  nvfp4::AdapterArgs p = adapter_args(x, x_rows, ldx, a, b, scales, M, N, K, rank, adapters, offsets, rows, pos, row_div, flags);
+  int st = check_adapter(p, x_dtype, c_dtype, flags);
+  if (st != NVFP4_OK) return st;
+  if (ldc < N || product(M, ldc) < 0 || (base && (ldb < N || product(M, ldb) < 0)) || !nvfp4::adapter_launches(p, false)) return NVFP4_ERR_SHAPE;
+  if (base == c && base && ldb != ldc && M > 1) return NVFP4_ERR_SHAPE;
+  if (M == 0) return NVFP4_OK;
+  p.base = base;
+  p.ldb = ldb;
+  p.c = c;
+  p.ldc = ldc;
+  p.c_dtype = c_dtype == NVFP4_BF16 ? 1 : 0;
+  p.h = h;
+  p.workspace = workspace;
+  p.stream = static_cast<hipStream_t>(hip_stream);
+  if ((st = check_adapter_pointers(p, c_dtype, nvfp4::adapter_workspace_bytes(M, K, rank, adapters))) != NVFP4_OK) return st;
+  return status_of(nvfp4::launch_adapter(p));
+}
+
+int nvfp4_adapter_backward(const void *dc, int dc_dtype, int64_t lddc, const void *x, int x_dtype, int64_t ldx,
+                           const void *a, const void *b, const float *scales, int64_t M, int64_t N, int64_t K,
+                           int32_t rank, int32_t adapters, const int32_t *offsets, const int32_t *rows,
+                           const int32_t *pos, uint32_t flags, const float *h, const void *dx_base, int64_t ldb,
+                           void *dx, int dx_dtype, int64_t lddx, float *da, float *db, void *workspace,
+                           void *hip_stream) {
+  nvfp4::AdapterArgs p = adapter_args(x, M, ldx, a, b, scales, M, N, K, rank, adapters, offsets, rows, pos, 1, flags);
+  if (dc_dtype != NVFP4_BF16 || p.gather) return NVFP4_ERR_UNSUPPORTED;
+  int st = check_adapter(p, x_dtype, dx_dtype, flags);
+  if (st != NVFP4_OK) return st;
+  if (N % 8 != 0 || lddc < N || product(M, lddc) < 0 || lddx < K || product(M, lddx) < 0 ||
+      (dx_base && (ldb < K || product(M, ldb) < 0)) || (dx_base && dx_base == dx && ldb != lddx && M > 1) ||
+      !nvfp4::adapter_launches(p, true))
+    return NVFP4_ERR_SHAPE;
+  p.base = dx_base;
+  p.ldb = ldb;
+  p.c = dx;
+  p.ldc = lddx;
+  p.c_dtype = dx_dtype == NVFP4_BF16 ? 1 : 0;
+  p.h = const_cast<float *>(h);
+  p.dc = dc;
+  p.lddc = lddc;
+  p.da = da;
+  p.db = db;
+  p.workspace = workspace;
+  p.stream = static_cast<hipStream_t>(hip_stream);
+  if (!da || !db) return NVFP4_ERR_NULL;
+  if (!aligned(da, 16) || !aligned(db, 16)) return NVFP4_ERR_ALIGN;
+  if (M > 0 && (!dc || !h)) return NVFP4_ERR_NULL;
+  if (M > 0 && (st = check_adapter_pointers(p, dx_dtype, 1)) != NVFP4_OK) return st;
+  if (!aligned(dc, 16) || lddc % 8 != 0) return NVFP4_ERR_ALIGN;
+  return status_of(nvfp4::launch_adapter_backward(p));
+}
 
 size_t nvfp4_moe_balance_workspace_size(int64_t tokens, int64_t experts, int64_t sequences) {
   if (tokens < 0 || experts < 1 || experts > kMaxExperts || sequences < 1 || sequences > kMaxSequences) return 0;

@@ -87,18 +87,76 @@ def test_grad_clip():
     assert _clip(good, outs=[P + 4, P + 4096]) == UNSUPPORTED
 
 
+ADAPTER = dict(x=P, x_dtype=nv.NVFP4_BF16, x_rows=80, ldx=64, a=P, b=P, scales=P, M=80, N=40, K=64, rank=16, adapters=3, offsets=P,
+               rows=P, pos=P, row_div=1, flags=nv.NVFP4_ADAPTER_BY_TOKEN, base=P, ldb=40, c=P + 4096, c_dtype=nv.NVFP4_BF16, ldc=40, h=P,
+               workspace=P, stream=None)
+ABWD = dict(dc=P, dc_dtype=nv.NVFP4_BF16, lddc=40, x=P, x_dtype=nv.NVFP4_BF16, ldx=64, a=P, b=P, scales=P, M=80, N=40, K=64, rank=16,
+            adapters=3, offsets=P, rows=P, pos=P, flags=nv.NVFP4_ADAPTER_BY_TOKEN, h=P, dx_base=P, ldb=64, dx=P + 4096,
+            dx_dtype=nv.NVFP4_BF16, lddx=64, da=P, db=P, workspace=P, stream=None)
+BOTH = [(dict(x=None), NULL), (dict(a=None), NULL), (dict(b=None), NULL), (dict(scales=None), NULL), (dict(rows=None), NULL),
+        (dict(pos=None), NULL), (dict(workspace=None), NULL), (dict(x_dtype=nv.NVFP4_F32), UNSUPPORTED), (dict(flags=4), UNSUPPORTED),
+        (dict(flags=3), UNSUPPORTED), (dict(M=-1), SHAPE), (dict(N=0), SHAPE), (dict(K=0), SHAPE), (dict(K=60), SHAPE), (dict(ldx=56), SHAPE),
+        (dict(rank=0), SHAPE), (dict(rank=12), SHAPE), (dict(rank=136), SHAPE), (dict(adapters=0), SHAPE), (dict(adapters=513), SHAPE),
+        (dict(offsets=None), SHAPE), (dict(offsets=None, adapters=1), SHAPE), (dict(ldb=8), SHAPE), (dict(ldx=2**62), SHAPE),
+        (dict(M=2**31), SHAPE), (dict(x=P + 8), ALIGN), (dict(ldx=68), ALIGN), (dict(a=P + 8), ALIGN), (dict(b=P + 8), ALIGN),
+        (dict(scales=ODD), ALIGN), (dict(offsets=ODD), ALIGN), (dict(rows=ODD), ALIGN), (dict(pos=ODD), ALIGN), (dict(h=P + 8), ALIGN),
+        (dict(workspace=P + 8), ALIGN)]
+
+
+@pytest.mark.parametrize("changes,status", BOTH + [
+    (dict(c=None), NULL), (dict(c_dtype=2), UNSUPPORTED), (dict(ldc=39), SHAPE), (dict(x_rows=79), SHAPE), (dict(c=P, ldc=48), SHAPE),
+    (dict(flags=nv.NVFP4_ADAPTER_GATHER, row_div=0), SHAPE), (dict(c=P + 1), ALIGN), (dict(base=P + 1), ALIGN),
+    (dict(c=ODD, c_dtype=nv.NVFP4_F32), ALIGN), (dict(M=2**30, x_rows=2**30), SHAPE),
+    (dict(M=0, x_rows=0, x=None, base=None, c=None, h=None, workspace=None), OK)])
+def test_adapter(changes, status):
+    assert _call("nvfp4_adapter", ADAPTER, **changes) == status
+
+
+@pytest.mark.parametrize("changes,status", BOTH + [
+    (dict(dc=None), NULL), (dict(dx=None), NULL), (dict(da=None), NULL), (dict(db=None), NULL), (dict(h=None), NULL),
+    (dict(dc_dtype=nv.NVFP4_F32), UNSUPPORTED), (dict(flags=nv.NVFP4_ADAPTER_GATHER), UNSUPPORTED), (dict(dx_dtype=2), UNSUPPORTED),
+    (dict(N=44, lddc=48), SHAPE), (dict(lddc=32), SHAPE), (dict(lddx=56), SHAPE), (dict(dx=P, lddx=72), SHAPE), (dict(dc=P + 8), ALIGN),
+    (dict(lddc=44), ALIGN), (dict(da=P + 8), ALIGN), (dict(db=P + 8), ALIGN), (dict(M=2**30), SHAPE)])
+def test_adapter_backward(changes, status):
+    assert _call("nvfp4_adapter_backward", ABWD, **changes) == status
+
+
 def test_workspace_sizes():
     L = nv.lib()
     assert L.nvfp4_moe_balance_workspace_size(64, 64, 1) == 0 and L.nvfp4_moe_balance_workspace_size(65, 64, 1) > 0
     assert L.nvfp4_moe_balance_workspace_size(64, 64, 2) > 0 and L.nvfp4_moe_balance_workspace_size(64, 0, 1) == 0
     assert L.nvfp4_grad_workspace_size(1, 1) == 16 and L.nvfp4_grad_workspace_size(-1, 1) == 0
     assert L.nvfp4_grad_workspace_size(3, 1 << 40) <= 2048 * 8
+    assert L.nvfp4_adapter_workspace_size(4, 64, 512, 16, 2) >= 4 * 16 * 4 and L.nvfp4_adapter_workspace_size(4, 64, 512, 0, 2) == 0
+    assert L.nvfp4_adapter_backward_workspace_size(4, 64, 512, 16, 2) >= 2 * 2 * 16 * (64 + 512)
+    assert L.nvfp4_adapter_backward_workspace_size(-1, 64, 512, 16, 2) == 0
 
 
 def test_binding_refuses_wrong_tensors():
     f, i = torch.zeros(8, 64), torch.zeros(8, 4, dtype=torch.int32)
     b = nv.MoEBalance(torch.zeros(1), torch.zeros(1, 64, dtype=torch.int32), torch.zeros(1, 64), torch.zeros(1, dtype=torch.int32))
+    h, one = f.bfloat16(), torch.ones(1)
+    w = nv.Adapters(torch.zeros(16, 64).bfloat16(), torch.zeros(24, 16).bfloat16(), one, 16, 64, 24)
+    w2 = nv.Adapters(torch.zeros(32, 64).bfloat16(), torch.zeros(48, 16).bfloat16(), torch.ones(2), 16, 64, 24, 2)
+    z = torch.zeros(8, dtype=torch.int32)
+    plan = nv.MoEPlan(torch.zeros(3, dtype=torch.int32), z, z[:, None].contiguous())
+    r = torch.zeros(8, 16)
     for error, call in [
+            (TypeError, lambda: nv.nvfp4_adapter(f, w)),
+            (ValueError, lambda: nv.nvfp4_adapter(h[:, :32], w)),
+            (ValueError, lambda: nv.nvfp4_adapter(h.t(), w)),
+            (ValueError, lambda: nv.nvfp4_adapter(h, w2)),
+            (ValueError, lambda: nv.nvfp4_adapter(h, w, plan=plan)),
+            (ValueError, lambda: nv.nvfp4_adapter(h, w2, plan=plan, gather=True, by_token=True)),
+            (ValueError, lambda: nv.nvfp4_adapter(h[:7], w2, plan=plan)),
+            (ValueError, lambda: nv.nvfp4_adapter(h, w, f[:, :20])),
+            (ValueError, lambda: nv.nvfp4_adapter(h, w, f[:, :24], out=h[:, :24])),
+            (TypeError, lambda: nv.nvfp4_adapter(h, w, out_dtype=torch.float16)),
+            (nv.NVFP4Error, lambda: nv.nvfp4_adapter(h, w)),  # host memory
+            (TypeError, lambda: nv.nvfp4_adapter_backward(f[:, :24], h, w, r)),
+            (ValueError, lambda: nv.nvfp4_adapter_backward(h[:, :20], h, w, r)),
+            (ValueError, lambda: nv.nvfp4_adapter_backward(h[:, :24], h, w, r[:, :8])),
+            (nv.NVFP4Error, lambda: nv.nvfp4_adapter_backward(h[:, :24], h, w, r)),
             (TypeError, lambda: nv.nvfp4_moe_balance(f, i.long())),
             (TypeError, lambda: nv.nvfp4_moe_balance(f.double(), i)),
             (ValueError, lambda: nv.nvfp4_moe_balance(f, i[:7])),

@@ -64,3 +64,37 @@ def balance_backward(logits, ids, counts, tokens, coef, sigmoid, dloss=1.0):
     rel = (np.minimum(deep, 110.0) + E / 16 + 24) * U
     tol = np.abs(c) * p * slope * (2 * rel * (np.abs(n - ref) + spread) + 4 * U * ref * (1e-20 / (s.sum(axis=1, keepdims=True) + 1e-20) if sigmoid else 0.0))
     return grad, np.where(is_open, tol, 0.0) + 2.0 ** -126
+
+
+def adapter(x, a, b, scales, owner, base, x_rows):
+    """c [rows x N] in 64 bits, and the magnitudes its sums run over.  owner: the adapter of each row (-1: none); x_rows:
+    its row of x; a [L, R, K], b [L, N, R]."""
+    c, mag = base.copy(), np.abs(base)
+    h = np.zeros((len(owner), a.shape[1]))
+    for g in range(a.shape[0]):
+        at = np.flatnonzero(owner == g)
+        if len(at) == 0:
+            continue
+        rows = x[x_rows[at]]
+        h[at] = rows @ a[g].T
+        c[at] += scales[g] * (h[at] @ b[g].T)
+        mag[at] += np.abs(scales[g]) * ((np.abs(rows) @ np.abs(a[g]).T) @ np.abs(b[g]).T)
+    return c, h, mag
+
+
+def adapter_backward(dc, x, a, b, scales, owner, h, dx_base):
+    """(dx, da, db) and the magnitudes of their sums; x's rows are c's."""
+    dx, dxm = dx_base.copy(), np.abs(dx_base)
+    da, db, dam, dbm = np.zeros_like(a), np.zeros_like(b), np.zeros_like(a), np.zeros_like(b)
+    for g in range(a.shape[0]):
+        at = np.flatnonzero(owner == g)
+        if len(at) == 0:
+            continue
+        s = scales[g]
+        gr, gm = s * (dc[at] @ b[g]), np.abs(s) * (np.abs(dc[at]) @ np.abs(b[g]))
+        dx[at] += gr @ a[g]
+        dxm[at] += gm @ np.abs(a[g])
+        da[g], dam[g] = gr.T @ x[at], gm.T @ np.abs(x[at])
+        db[g] = s * (dc[at].T @ h[at])
+        dbm[g] = np.abs(s) * (np.abs(dc[at]).T @ (np.abs(x[at]) @ np.abs(a[g]).T))
+    return (dx, da, db), (dxm, dam, dbm)

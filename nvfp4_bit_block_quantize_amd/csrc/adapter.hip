@@ -127,12 +127,12 @@ __device__ __forceinline__ int64_t y_row(const ShrinkArgs &p, int64_t r) {
   return p.use_c_rows ? c_row(p.rows, r) : x_row(p.rows, r);
 }
 
-// Few rows an adapter: a workgroup has 16 rows and kFewK elements of K, a wave a quarter of these, all its loads in
+// Few rows an adapter: a workgroup has 16 rows and kFewK elements of K, a wave an eighth of these, all its loads in
 // flight at once; the waves' sums meet in LDS.
-constexpr int kFewWaveK = 128, kFewK = 4 * kFewWaveK;
+constexpr int kFewWaveK = 128, kFewWaves = 8, kFewK = kFewWaves * kFewWaveK;
 template <int RF>
-__global__ __launch_bounds__(256) void shrink_few_kernel(ShrinkArgs p) {
-  __shared__ floatx4 sums[4][RF][64];
+__global__ __launch_bounds__(64 * kFewWaves) void shrink_few_kernel(ShrinkArgs p) {
+  __shared__ floatx4 sums[kFewWaves][RF][64];
   const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, j = lane >> 4;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t tm = blockIdx.x / p.splits, split = blockIdx.x - tm * p.splits;
@@ -165,8 +165,10 @@ __global__ __launch_bounds__(256) void shrink_few_kernel(ShrinkArgs p) {
 #pragma unroll
   for (int u = 0; u < RF; ++u) sums[wave][u][lane] = acc[u];
   __syncthreads();
-  for (int u = wave; u < RF; u += 4) {
-    const floatx4 v = (sums[0][u][lane] + sums[1][u][lane]) + (sums[2][u][lane] + sums[3][u][lane]);
+  for (int u = wave; u < RF; u += kFewWaves) {
+    floatx4 v = sums[0][u][lane];
+#pragma unroll
+    for (int w = 1; w < kFewWaves; ++w) v += sums[w][u][lane];
     const int q = 16 * u + 4 * j;
     if (r < t.m_end && q < p.R)
       *reinterpret_cast<floatx4 *>(p.part + (static_cast<int64_t>(split) * p.rows.M + r) * p.R + q) = v;
@@ -283,6 +285,15 @@ __device__ __forceinline__ void store_h(float *h, int32_t R, int64_t r, int32_t 
   at[0] = (floatx4){v[0], v[1], v[2], v[3]};
   at[1] = (floatx4){v[4], v[5], v[6], v[7]};
 }
+// part[0] = the splits' sum, four values a thread.
+__global__ __launch_bounds__(256) void split_sum_kernel(float *part, int64_t size, int32_t splits) {
+  const int64_t i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 4;
+  if (i >= size) return;
+  floatx4 v = *reinterpret_cast<const floatx4 *>(part + i);
+#pragma unroll 8
+  for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const floatx4 *>(part + s * size + i);
+  *reinterpret_cast<floatx4 *>(part + i) = v;
+}
 constexpr int kFinishRows = 64;
 __device__ __forceinline__ void finish_tile(const FinishArgs &p, int32_t tm) {
   Tile t;
@@ -306,7 +317,6 @@ __device__ __forceinline__ void finish_tile(const FinishArgs &p, int32_t tm) {
     out[2 * RC] = w[2];
   }
 }
-__global__ __launch_bounds__(256) void finish_kernel(FinishArgs p) { finish_tile(p, blockIdx.x); }
 
 // ---- rows + pieces x factor: c[row(r)][n] = base[row(r)][n] + sum_q piece[r][q] f[g][n][q] --------------------
 struct ExpandArgs {
@@ -315,16 +325,16 @@ struct ExpandArgs {
   const uint8_t *f;       // [groups][N][R] bf16
   int64_t N;
   int32_t R;
-  const uint8_t *pieces;  // many rows
-  const float *part;      // few rows: [splits][M][R]
+  const float *part;      // [splits][M][R]
   int32_t splits;
   const float *scales;
-  float *h;               // few rows, nullable
+  float *h;               // nullable [M][R]: the splits' sums
+  uint8_t *pieces;        // nullable [M][3 R] bf16: of scale * sum
   const uint8_t *base;    // NULL: zeros
   int64_t ldb;            // bytes
   uint8_t *c;
   int64_t ldc;            // bytes
-  bool vec;               // rows of base and c are aligned to 16 bytes and N fills whole pieces
+  int32_t columns;        // of a workgroup, a multiple of 256
   int32_t tiles_n, tiles_m;  // a launch has tiles_n * (tiles_m + copy tiles) workgroups
 };
 
@@ -341,131 +351,181 @@ __device__ __forceinline__ void set_element(uint8_t *p, int64_t i, float v) {
     reinterpret_cast<float *>(p)[i] = v;
 }
 
-// Rows without an adapter: c = base (or zeros), 64 rows and 256 columns a workgroup.
+// How a wave meets rows of c, 64 columns (128 or 256 bytes) of each at a time: an instruction moves whole segments of
+// kRows rows, lane l the piece l % kPieces of row l / kPieces.  (Rows of 8192 x 14336 bf16 added to in 128-byte segments
+// run at 6.4 to 6.6 TB/s with non-temporal loads, in 64-byte ones, as the products' registers hold them, at 4.8.)
 template <bool BF16>
+struct Segment {
+  static constexpr int ES = BF16 ? 2 : 4, kValues = 16 / ES, kPieces = 64 / kValues, kRows = 64 / kPieces;
+};
+
+// Rows without an adapter: c = base (or zeros), 64 rows of a workgroup's columns.
+template <bool BF16, bool ONCE, bool VEC>
 __device__ void copy_rows(const ExpandArgs &p, int32_t tile, int64_t n0) {
-  constexpr int ES = BF16 ? 2 : 4, V = 16 / ES;
+  using S = Segment<BF16>;
+  constexpr int ES = S::ES, NI = 64 / S::kRows;
   const int32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  int64_t covered = p.rows.offsets ? p.rows.offsets[p.rows.groups] : p.rows.M;
-  for (int i = wave; i < 64; i += 4) {
-    const int64_t r = static_cast<int64_t>(tile) * 64 + i;
-    if (r >= p.rows.M || (p.rows.by_rows ? p.pos[r] >= 0 : r < covered)) continue;
-    const uint8_t *from = p.base ? p.base + r * p.ldb : nullptr;
-    uint8_t *to = p.c + r * p.ldc;
-    if (p.vec) {
-      for (int64_t n = n0 + lane * V; n < min(n0 + 256, p.N); n += 64 * V)
-        *reinterpret_cast<uint4 *>(to + n * ES) = from ? *reinterpret_cast<const uint4 *>(from + n * ES) : make_uint4(0, 0, 0, 0);
+  const int64_t n1 = min(n0 + p.columns, p.N);
+  const int64_t mine = static_cast<int64_t>(tile) * 64 + lane;
+  const bool bare = mine < p.rows.M && (p.rows.by_rows ? p.pos[mine] < 0 : mine >= p.rows.offsets[p.rows.groups]);
+  const uint64_t rows = __ballot(bare);
+  if (rows == 0) return;
+  const int32_t first = lane / S::kPieces, col = lane % S::kPieces * S::kValues;
+  for (int64_t n = n0 + 64 * wave + col; n < n1; n += 256) {
+    if constexpr (VEC) {
+      uint4 v[NI];
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int32_t r = S::kRows * i + first;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (p.base && (rows >> r & 1)) v[i] = load16<ONCE>(p.base + (static_cast<int64_t>(tile) * 64 + r) * p.ldb + n * ES);
+      }
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int32_t r = S::kRows * i + first;
+        if (rows >> r & 1) *reinterpret_cast<uint4 *>(p.c + (static_cast<int64_t>(tile) * 64 + r) * p.ldc + n * ES) = v[i];
+      }
     } else {
-      for (int64_t n = n0 + lane; n < min(n0 + 256, p.N); n += 64) set_element<BF16>(to, n, from ? element<BF16>(from, n) : 0.0f);
+      for (int i = 0; i < NI; ++i) {
+        const int32_t r = S::kRows * i + first;
+        const int64_t row = static_cast<int64_t>(tile) * 64 + r;
+        if (rows >> r & 1)
+          for (int64_t e = n; e < min(n + S::kValues, p.N); ++e)
+            set_element<BF16>(p.c + row * p.ldc, e, p.base ? element<BF16>(p.base + row * p.ldb, e) : 0.0f);
+      }
     }
   }
 }
 
-// A workgroup has 16 TF rows and 256 columns, a wave 64 of these in four fragments: row 4 g + e of fragment f is column
-// 16 g + 4 f + e, so that a lane ends with 16 consecutive columns of its row.  NM products of 32 cover the pieces.
-// FEW: the pieces are formed here from the splits' sums, in LDS, not read.
-template <int NM, int TF, bool BF16, bool FEW>
-__global__ __launch_bounds__(256) void expand_kernel(ExpandArgs p) {
-  constexpr int ES = BF16 ? 2 : 4, PARTS = BF16 ? 2 : 3;
+// A workgroup has 16 TF rows and walks its columns 256 at a time, a wave 64 of these in four fragments of the factor's
+// rows.  The rows' pieces are formed once, in LDS, from the splits' sums: part s of eight columns rc of a row is its chunk
+// s RCP + rc, RCP the power of two that holds R / 8, and NM products of 32 cover a row.  As RCP is a power of two, these take UF
+// different fragments of the factor, again and again for each part.  Sums leave through the wave's own LDS, 16 rows at a time, in
+// whole segments (see Segment).
+template <int RCP, int TF, bool BF16, bool ONCE, bool VEC>
+__global__ __launch_bounds__(256, RCP <= 4 ? 4 : RCP == 8 ? 3 : 2) void expand_kernel(ExpandArgs p) {
+  using S = Segment<BF16>;
+  constexpr int ES = S::ES, PARTS = BF16 ? 2 : 3, NI = 16 * TF / S::kRows;
+  constexpr int NM = (PARTS * RCP + 3) / 4, UF = RCP <= 4 ? 1 : RCP / 4;
   constexpr int kPitch = NM * 64 + 16;  // of a row of pieces in LDS (with the pad, rows start in different banks)
-  __shared__ __attribute__((aligned(16))) uint8_t staged[FEW ? 16 * TF * kPitch : 16];
+  __shared__ __attribute__((aligned(16))) uint8_t staged[16 * TF * kPitch];
+  __shared__ floatx4 turned[4][16 * 16];
+  __shared__ int32_t c_rows[16 * TF];  // -1: none
   const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, j = lane >> 4;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t tm = blockIdx.x / p.tiles_n, tn = blockIdx.x - tm * p.tiles_n;
-  if (tm >= p.tiles_m) return copy_rows<BF16>(p, tm - p.tiles_m, static_cast<int64_t>(tn) * 256);
+  const int64_t n_lo = static_cast<int64_t>(tn) * p.columns, n_hi = min(n_lo + p.columns, p.N);
+  if (tm >= p.tiles_m) return copy_rows<BF16, ONCE, VEC>(p, tm - p.tiles_m, n_lo);
   Tile t;
   if (!find_tile(p.rows, 16 * TF, tm, t)) return;
-  const int32_t RC = p.R / 8, chunks = PARTS * RC;
-  const int64_t n0 = static_cast<int64_t>(tn) * 256 + wave * 64;
-
-  // the factor's fragments
-  uint4 f[4][NM];
+  const int32_t RC = p.R / 8;
+  if (threadIdx.x < 16 * TF) {
+    const int64_t r = t.m0 + threadIdx.x;
+    c_rows[threadIdx.x] = static_cast<int32_t>(r < t.m_end ? c_row(p.rows, r) : -1);
+  }
+  const float scale = p.scales[t.group];
+  for (int i = threadIdx.x; i < 16 * TF * RCP; i += 256) {
+    const int32_t m = i / RCP, rc = i % RCP;
+    const int64_t r = t.m0 + m;
+    const bool real = r < t.m_end && rc < RC;
+    float v[8];
 #pragma unroll
-  for (int u = 0; u < 4; ++u) {
-    const int64_t n = min(n0 + 16 * (l16 >> 2) + 4 * u + (l16 & 3), p.N - 1);
-    const uint8_t *row = p.f + (static_cast<int64_t>(t.group) * p.N + n) * p.R * 2;
+    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+    if (real) {
+      sum_splits(p.part, p.rows.M, p.R, p.splits, r, 8 * rc, v);
+      if (p.h && tn == 0) store_h(p.h, p.R, r, 8 * rc, v);
+    }
 #pragma unroll
-    for (int i = 0; i < NM; ++i) {
-      const int32_t c = 4 * i + j;
-      f[u][i] = make_uint4(0, 0, 0, 0);
-      if (c < chunks) f[u][i] = *reinterpret_cast<const uint4 *>(row + (c % RC) * 16);
+    for (int e = 0; e < 8; ++e) v[e] *= scale;
+    uint4 w[3];
+    split8(v, w);
+#pragma unroll
+    for (int s = 0; s < PARTS; ++s) *reinterpret_cast<uint4 *>(staged + m * kPitch + (s * RCP + rc) * 16) = w[s];
+    if (p.pieces && tn == 0 && real) {
+      uint4 *out = reinterpret_cast<uint4 *>(p.pieces + r * (6 * p.R)) + rc;
+      out[0] = w[0];
+      out[RC] = w[1];
+      out[2 * RC] = w[2];
     }
   }
-  if constexpr (FEW) {
-    const float scale = p.scales[t.group];
-    for (int i = threadIdx.x; i < 16 * TF * RC; i += 256) {
-      const int32_t row = i / RC, rc = i % RC;
-      const int64_t r = t.m0 + row;
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-      if (r < t.m_end) {
-        sum_splits(p.part, p.rows.M, p.R, p.splits, r, 8 * rc, v);
-        if (p.h && tn == 0) store_h(p.h, p.R, r, 8 * rc, v);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= scale;
-      uint4 w[PARTS];
-      split8(v, w);
-#pragma unroll
-      for (int s = 0; s < PARTS; ++s) *reinterpret_cast<uint4 *>(staged + row * kPitch + (s * RC + rc) * 16) = w[s];
-    }
-    __syncthreads();
-  }
-  if (n0 >= p.N) return;
+  __syncthreads();
 
-  constexpr int NB = BF16 ? 2 : 4;  // 16-byte pieces of a lane's 16 columns
-  const int64_t n = n0 + 16 * j;
+  const uint32_t first = lane / S::kPieces, col = lane % S::kPieces * S::kValues;
+  floatx4 *const mine = turned[wave];
+  for (int64_t n0 = n_lo + 64 * wave; n0 < n_hi; n0 += 256) {
+    uint4 f[4][UF], b[NI];
+    const int64_t n = n0 + col;
+    if constexpr (VEC) {
 #pragma unroll
-  for (int tf = 0; tf < TF; ++tf) {
-    const int64_t r = t.m0 + 16 * tf + l16;
-    if (t.m0 + 16 * tf >= t.m_end) break;
-    const int64_t cr = r < t.m_end ? c_row(p.rows, r) : -1;
-    uint4 b[NM];
-#pragma unroll
-    for (int i = 0; i < NM; ++i) {
-      const int32_t c = 4 * i + j;
-      b[i] = make_uint4(0, 0, 0, 0);
-      if (c < chunks) {
-        if constexpr (FEW)
-          b[i] = *reinterpret_cast<const uint4 *>(staged + (16 * tf + l16) * kPitch + c * 16);
-        else if (r < t.m_end)
-          b[i] = *reinterpret_cast<const uint4 *>(p.pieces + r * (6 * p.R) + c * 16);
+      for (int i = 0; i < NI; ++i) {
+        const int64_t row = c_rows[S::kRows * i + first];
+        b[i] = make_uint4(0, 0, 0, 0);
+        if (p.base && row >= 0 && n < p.N) b[i] = load16<ONCE>(p.base + row * p.ldb + n * ES);
       }
     }
-    floatx4 acc[4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      acc[u] = (floatx4){0.0f, 0.0f, 0.0f, 0.0f};
+      const uint8_t *from = p.f + (static_cast<int64_t>(t.group) * p.N + min(n0 + 16 * u + l16, p.N - 1)) * p.R * 2;
 #pragma unroll
-      for (int i = 0; i < NM; ++i) acc[u] = mfma(__builtin_bit_cast(bf16x8, f[u][i]), __builtin_bit_cast(bf16x8, b[i]), acc[u]);
+      for (int i = 0; i < UF; ++i) {
+        const int32_t rc = (4 * i + j) % RCP;
+        f[u][i] = make_uint4(0, 0, 0, 0);
+        if (rc < RC) f[u][i] = *reinterpret_cast<const uint4 *>(from + rc * 16);
+      }
     }
-    if (cr < 0) continue;
-    const uint8_t *from = p.base ? p.base + cr * p.ldb + n * ES : nullptr;
-    uint8_t *to = p.c + cr * p.ldc + n * ES;
-    if (p.vec) {
 #pragma unroll
-      for (int q = 0; q < NB; ++q) {
-        if (n + q * (16 / ES) >= p.N) break;
+    for (int tf = 0; tf < TF; ++tf) {
+      bf16x8 x[NM];
+#pragma unroll
+      for (int i = 0; i < NM; ++i) {
         uint4 v = make_uint4(0, 0, 0, 0);
-        if (from) v = *reinterpret_cast<const uint4 *>(from + 16 * q);
-        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        if (PARTS * RCP == 4 * NM || 4 * i + static_cast<int32_t>(j) < PARTS * RCP)
+          v = *reinterpret_cast<const uint4 *>(staged + (16 * tf + l16) * kPitch + (4 * i + j) * 16);
+        x[i] = __builtin_bit_cast(bf16x8, v);
+      }
+      // column 16 u + 4 j of row l16 on: chunk 4 u + j of the row, at (4 u + j) ^ row
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (BF16) {
-            const int at = 8 * q + 2 * e;
-            w[e] = pack_bf16(__uint_as_float(w[e] << 16) + acc[at / 4][at % 4],
-                             __uint_as_float(w[e] & 0xFFFF0000u) + acc[at / 4][at % 4 + 1]);
-          } else {
-            w[e] = __float_as_uint(__uint_as_float(w[e]) + acc[q][e]);
+      for (int u = 0; u < 4; ++u) {
+        floatx4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int i = 0; i < NM; ++i) acc = mfma(__builtin_bit_cast(bf16x8, f[u][i % UF]), x[i], acc);
+        mine[16 * l16 + ((4 * u + j) ^ l16)] = acc;
+      }
+      // the wave reads back its own rows (LDS accesses of one wave complete in order)
+#pragma unroll
+      for (int k = 0; k < 16 / S::kRows; ++k) {
+        const int i = tf * (16 / S::kRows) + k;
+        const uint32_t m = S::kRows * k + first;
+        const int64_t row = c_rows[16 * tf + m];
+        float v[S::kValues];
+#pragma unroll
+        for (int q = 0; q < S::kValues / 4; ++q) {
+          const floatx4 four = mine[16 * m + ((col / 4 + q) ^ m)];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[4 * q + e] = four[e];
+        }
+        if constexpr (VEC) {
+          uint32_t w[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (BF16)
+              w[e] = pack_bf16(__uint_as_float(w[e] << 16) + v[2 * e], __uint_as_float(w[e] & 0xFFFF0000u) + v[2 * e + 1]);
+            else
+              w[e] = __float_as_uint(__uint_as_float(w[e]) + v[e]);
+          }
+          if (row >= 0 && n < p.N) *reinterpret_cast<uint4 *>(p.c + row * p.ldc + n * ES) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else if (row >= 0) {
+          // (a loop, to keep this rare path's code short)
+#pragma clang loop unroll(disable)
+          for (int e = 0; e < S::kValues && n + e < p.N; ++e) {
+            const float was = p.base ? element<BF16>(p.base + row * p.ldb, n + e) : 0.0f;
+            float d = v[0];
+#pragma unroll
+            for (int q = 1; q < S::kValues; ++q) d = e == q ? v[q] : d;
+            set_element<BF16>(p.c + row * p.ldc, n + e, was + d);
           }
         }
-        *reinterpret_cast<uint4 *>(to + 16 * q) = make_uint4(w[0], w[1], w[2], w[3]);
       }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        if (n + e < p.N) set_element<BF16>(to, e, (from ? element<BF16>(from, e) : 0.0f) + acc[e / 4][e % 4]);
     }
   }
 }
@@ -693,13 +753,21 @@ int64_t tiles_for(const AdapterArgs &a, int64_t size) {
   return a.M / size + (a.adapters < a.M ? a.adapters : a.M);
 }
 
+// Rows of a workgroup that adds to many rows of c: what a lane holds of base's rows is then the same for both types.
+template <bool BF16>
+constexpr int kExpandRows = BF16 ? 64 : 32;
+// Workgroups of the launch that adds to c, about: four a compute unit.
+constexpr int64_t kExpandGroups = 1024;
+
 // Few rows an adapter: 16 rows a tile.
 bool few_rows(int64_t M, int64_t adapters) { return M <= 256 || M <= 16 * adapters; }
 
-// Splits of K for many rows: workgroups for every compute unit, each with at least four steps.
-void many_splits(int64_t M, int64_t K, int32_t &splits, int32_t &split_k) {
+// Splits of K for many rows: workgroups for every compute unit, each with at least four steps.  Gathered rows come up
+// again for each of a token's experts: in eight splits, each XCD (workgroup i runs on XCD i mod 8) meets only its own
+// eighth of every row, which its L2 holds.
+void many_splits(int64_t M, int64_t K, bool gather, int32_t &splits, int32_t &split_k) {
   const int64_t tiles = (M + kManyRows - 1) / kManyRows, steps = (K + kManyStep - 1) / kManyStep;
-  int64_t n = (768 + tiles - 1) / tiles;
+  int64_t n = gather ? 8 : (768 + tiles - 1) / tiles;
   if (n > steps / 4) n = steps / 4;
   if (n > 8) n = 8;
   if (n < 1) n = 1;
@@ -707,10 +775,10 @@ void many_splits(int64_t M, int64_t K, int32_t &splits, int32_t &split_k) {
   split_k = static_cast<int32_t>(per * kManyStep);
   splits = static_cast<int32_t>((steps + per - 1) / per);
 }
-int32_t splits_for(int64_t M, int64_t adapters, int64_t K) {
+int32_t splits_for(int64_t M, int64_t adapters, int64_t K, bool gather) {
   if (few_rows(M, adapters)) return static_cast<int32_t>((K + kFewK - 1) / kFewK);
   int32_t n, k;
-  many_splits(M, K, n, k);
+  many_splits(M, K, gather, n, k);
   return n;
 }
 
@@ -718,7 +786,7 @@ template <int RF>
 hipError_t run_shrink(const ShrinkArgs &p, bool few, int64_t tiles, hipStream_t stream) {
   const dim3 grid(static_cast<uint32_t>(tiles * p.splits));
   if (few)
-    shrink_few_kernel<RF><<<grid, dim3(256), 0, stream>>>(p);
+    shrink_few_kernel<RF><<<grid, dim3(64 * kFewWaves), 0, stream>>>(p);
   else
     shrink_many_kernel<RF><<<grid, dim3(256), 0, stream>>>(p);
   return hipGetLastError();
@@ -739,7 +807,7 @@ hipError_t run_shrink(const AdapterArgs &a, bool use_c_rows, const void *y, int6
     p.splits = static_cast<int32_t>((K + kFewK - 1) / kFewK);
     p.split_k = kFewK;
   } else {
-    many_splits(a.M, K, p.splits, p.split_k);
+    many_splits(a.M, K, a.gather, p.splits, p.split_k);
   }
   splits = p.splits;
   const int64_t tiles = tiles_for(a, few ? 16 : kManyRows);
@@ -749,63 +817,72 @@ hipError_t run_shrink(const AdapterArgs &a, bool use_c_rows, const void *y, int6
   return run_shrink<8>(p, few, tiles, a.stream);
 }
 
-template <int NM, bool BF16>
-hipError_t run_expand(const ExpandArgs &p, bool few, uint32_t groups, hipStream_t stream) {
-  if (few)
-    expand_kernel<NM, 1, BF16, true><<<dim3(groups), dim3(256), 0, stream>>>(p);
+template <int RCP, bool BF16>
+hipError_t run_expand(const ExpandArgs &p, bool few, bool vec, uint32_t groups, hipStream_t stream) {
+  constexpr int TF = kExpandRows<BF16> / 16;
+  const bool once = p.base && 2 * p.rows.M * p.N * (BF16 ? 2 : 4) >= kStreamBytes;
+  if (!vec)
+    expand_kernel<RCP, 1, BF16, false, false><<<dim3(groups), dim3(256), 0, stream>>>(p);
+  else if (few)
+    expand_kernel<RCP, 1, BF16, false, true><<<dim3(groups), dim3(256), 0, stream>>>(p);
+  else if (once)
+    expand_kernel<RCP, TF, BF16, true, true><<<dim3(groups), dim3(256), 0, stream>>>(p);
   else
-    expand_kernel<NM, 4, BF16, false><<<dim3(groups), dim3(256), 0, stream>>>(p);
+    expand_kernel<RCP, TF, BF16, false, true><<<dim3(groups), dim3(256), 0, stream>>>(p);
   return hipGetLastError();
 }
 template <bool BF16>
-hipError_t run_expand(const ExpandArgs &p, bool few, uint32_t groups, hipStream_t stream) {
-  const int need = ((BF16 ? 2 : 3) * p.R / 8 + 3) / 4;
-  if (need <= 1) return run_expand<1, BF16>(p, few, groups, stream);
-  if (need <= 2) return run_expand<2, BF16>(p, few, groups, stream);
-  if (need <= 3) return run_expand<3, BF16>(p, few, groups, stream);
-  if (need <= 4) return run_expand<4, BF16>(p, few, groups, stream);
-  if (need <= 6) return run_expand<6, BF16>(p, few, groups, stream);
-  if constexpr (BF16) {
-    return run_expand<8, BF16>(p, few, groups, stream);
-  } else {
-    if (need <= 8) return run_expand<8, BF16>(p, few, groups, stream);
-    return run_expand<12, BF16>(p, few, groups, stream);
-  }
+hipError_t run_expand(const ExpandArgs &p, bool few, bool vec, uint32_t groups, hipStream_t stream) {
+  if (p.R <= 8) return run_expand<1, BF16>(p, few, vec, groups, stream);
+  if (p.R <= 16) return run_expand<2, BF16>(p, few, vec, groups, stream);
+  if (p.R <= 32) return run_expand<4, BF16>(p, few, vec, groups, stream);
+  if (p.R <= 64) return run_expand<8, BF16>(p, few, vec, groups, stream);
+  return run_expand<16, BF16>(p, few, vec, groups, stream);
 }
-// `few`: part holds the splits' sums; else pieces are there.
-hipError_t run_expand(const AdapterArgs &a, const void *f, int64_t N, const uint8_t *pieces, const float *part, int32_t splits,
-                      float *h, const void *base, int64_t ldb, void *c, int64_t ldc, int dtype) {
+hipError_t run_expand(const AdapterArgs &a, const void *f, int64_t N, float *part, int32_t splits, float *h, uint8_t *pieces,
+                      const void *base, int64_t ldb, void *c, int64_t ldc, int dtype) {
   ExpandArgs p{};
   const int64_t es = dtype == 1 ? 2 : 4;
-  const bool few = pieces == nullptr;
+  const bool few = few_rows(a.M, a.adapters);
   p.rows = rows_of(a);
   p.pos = a.pos;
   p.f = static_cast<const uint8_t *>(f);
   p.N = N;
   p.R = a.rank;
-  p.pieces = pieces;
   p.part = part;
   p.splits = splits;
   p.scales = a.scales;
   p.h = h;
+  p.pieces = pieces;
   p.base = static_cast<const uint8_t *>(base);
   p.ldb = ldb * es;
   p.c = static_cast<uint8_t *>(c);
   p.ldc = ldc * es;
-  p.vec = (reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(c) | static_cast<uintptr_t>(p.ldc) |
+  // rows of base and c aligned to 16 bytes, which N fills; else single elements, 16 rows a workgroup
+  const bool vec = (reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(c) | static_cast<uintptr_t>(p.ldc) |
            static_cast<uintptr_t>(base ? p.ldb : 0) | static_cast<uintptr_t>(N * es)) % 16 == 0;
-  p.tiles_n = static_cast<int32_t>((N + 255) / 256);
-  p.tiles_m = static_cast<int32_t>(tiles_for(a, few ? 16 : 64));
+  const int32_t tile_rows = few || !vec ? 16 : dtype == 1 ? kExpandRows<true> : kExpandRows<false>;
+  p.tiles_m = static_cast<int32_t>(tiles_for(a, tile_rows));
+  // as many steps of 256 columns a workgroup as leave kExpandGroups workgroups
+  const int64_t steps = (N + 255) / 256, tiles = (a.M + tile_rows - 1) / tile_rows;
+  const int64_t used = few && a.offsets ? (a.M < a.adapters ? a.M : a.adapters) : 0;  // at most so many tiles in use
+  int64_t each = steps * (tiles > used ? tiles : used) / kExpandGroups;
+  if (each < 1) each = 1;
+  if (each > steps) each = steps;
+  // the splits are summed first where each workgroup's own sums would read more than a quarter of what it moves of c
+  if (!few && splits > 1 && splits * p.R * 4 * 4 > each * 256 * 2 * es) {
+    const int64_t size = a.M * p.R;
+    split_sum_kernel<<<dim3(static_cast<uint32_t>((size + 1023) / 1024)), dim3(256), 0, a.stream>>>(part, size, splits);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    p.splits = 1;
+  }
+  p.columns = static_cast<int32_t>((steps + (steps + each - 1) / each - 1) / ((steps + each - 1) / each) * 256);
+  p.tiles_n = static_cast<int32_t>((N + p.columns - 1) / p.columns);
   // rows without an adapter have to be written unless c is base
-  const int64_t copies = a.offsets && (base != c || ldb != ldc) ? (a.M + 63) / 64 : 0;
+  const int64_t copies = a.offsets && base != c ? (a.M + 63) / 64 : 0;
   const uint32_t groups = static_cast<uint32_t>(p.tiles_n * (p.tiles_m + copies));
-  return dtype == 1 ? run_expand<true>(p, few, groups, a.stream) : run_expand<false>(p, few, groups, a.stream);
-}
-
-hipError_t run_finish(const AdapterArgs &a, const float *part, int32_t splits, float *h, uint8_t *pieces) {
-  FinishArgs p{rows_of(a), part, splits, a.rank, a.scales, h, pieces};
-  finish_kernel<<<dim3(static_cast<uint32_t>(tiles_for(a, kFinishRows))), dim3(256), 0, a.stream>>>(p);
-  return hipGetLastError();
+  return dtype == 1 ? run_expand<true>(p, few, vec, groups, a.stream) : run_expand<false>(p, few, vec, groups, a.stream);
 }
 
 // Rows of a workgroup of the factors' gradients: as many as leave about two workgroups a compute unit.
@@ -852,11 +929,12 @@ struct Layout {
   }
 };
 struct ForwardLayout {
-  size_t part, pieces, size;
+  size_t part, size;
   ForwardLayout(int64_t M, int64_t K, int64_t R, int64_t adapters) {
     Layout l;
-    part = l.take(splits_for(M, adapters, K) * M * R * 4);
-    pieces = few_rows(M, adapters) ? 0 : l.take(M * R * 6);
+    // (as large for gathered rows as for others)
+    const int64_t own = splits_for(M, adapters, K, false), gathered = splits_for(M, adapters, K, true);
+    part = l.take((own > gathered ? own : gathered) * M * R * 4);
     size = l.at;
   }
 };
@@ -868,7 +946,7 @@ struct BackwardLayout {
     at = l.take(factor * a.K * 2);
     bt = l.take(factor * a.N * 2);
     h_pieces = l.take(a.M * a.rank * 6);
-    part = l.take(static_cast<int64_t>(splits_for(a.M, a.adapters, a.N)) * a.M * a.rank * 4);
+    part = l.take(static_cast<int64_t>(splits_for(a.M, a.adapters, a.N, false)) * a.M * a.rank * 4);
     g_pieces = l.take(a.M * a.rank * 6);
     da_part = l.take(tiles_for(a, outer_chunk(a.M, a.K)) * a.K * a.rank * 4);
     db_part = l.take(tiles_for(a, outer_chunk(a.M, a.N)) * a.N * a.rank * 4);
@@ -888,8 +966,8 @@ bool adapter_launches(const AdapterArgs &a, bool backward) {
   constexpr int64_t kMost = int64_t(1) << 23;
   const int64_t widest = ((a.N > a.K ? a.N : a.K) + 255) / 256;
   const bool few = few_rows(a.M, a.adapters);
-  const int64_t tiles = tiles_for(a, few ? 16 : 64) + (a.M + 63) / 64;
-  const int64_t splits = splits_for(a.M, a.adapters, backward ? a.N : a.K);
+  const int64_t tiles = tiles_for(a, 16) + (a.M + 63) / 64;
+  const int64_t splits = splits_for(a.M, a.adapters, backward ? a.N : a.K, a.gather);
   const int64_t sums = backward ? a.adapters * ((a.N + a.K) * a.rank / kOuterSumSize + 2) : 0;
   const int64_t prep = backward ? a.adapters * ((a.rank + 63) / 64) * ((a.N + 63) / 64 + (a.K + 63) / 64) + tiles : 0;
   return tiles * widest < kMost && tiles * splits < kMost && sums < kMost && prep < kMost &&
@@ -901,14 +979,9 @@ hipError_t launch_adapter(const AdapterArgs &a) {
   uint8_t *const w = static_cast<uint8_t *>(a.workspace);
   float *const part = reinterpret_cast<float *>(w + l.part);
   int32_t splits;
-  hipError_t e = run_shrink(a, false, a.x, a.ldx, a.a, a.K, part, splits);
+  const hipError_t e = run_shrink(a, false, a.x, a.ldx, a.a, a.K, part, splits);
   if (e != hipSuccess) return e;
-  uint8_t *pieces = nullptr;
-  if (!few_rows(a.M, a.adapters)) {
-    pieces = w + l.pieces;
-    if ((e = run_finish(a, part, splits, a.h, pieces)) != hipSuccess) return e;
-  }
-  return run_expand(a, a.b, a.N, pieces, part, splits, a.h, a.base, a.ldb, a.c, a.ldc, a.c_dtype);
+  return run_expand(a, a.b, a.N, part, splits, a.h, nullptr, a.base, a.ldb, a.c, a.ldc, a.c_dtype);
 }
 
 hipError_t launch_adapter_backward(const AdapterArgs &a) {
@@ -930,8 +1003,7 @@ hipError_t launch_adapter_backward(const AdapterArgs &a) {
   if (a.M > 0) {
     int32_t splits;
     if ((e = run_shrink(a, true, a.dc, a.lddc, w + l.bt, a.N, part, splits)) != hipSuccess) return e;
-    if ((e = run_finish(a, part, splits, nullptr, w + l.g_pieces)) != hipSuccess) return e;
-    if ((e = run_expand(a, w + l.at, a.K, w + l.g_pieces, nullptr, 0, nullptr, a.base, a.ldb, a.c, a.ldc, a.c_dtype)) != hipSuccess)
+    if ((e = run_expand(a, w + l.at, a.K, part, splits, nullptr, w + l.g_pieces, a.base, a.ldb, a.c, a.ldc, a.c_dtype)) != hipSuccess)
       return e;
     if ((e = run_outer(a, true, a.dc, a.lddc, a.N, w + l.h_pieces, true, db_part, a.db)) != hipSuccess) return e;
     if ((e = run_outer(a, false, a.x, a.ldx, a.K, w + l.g_pieces, false, da_part, a.da)) != hipSuccess) return e;

@@ -110,10 +110,18 @@ __device__ __forceinline__ void split8(float (&v)[8], uint4 (&out)[PARTS]) {
   }
 }
 
+// Four rows of 16 columns (bf16, LDS), transposed: lane l16 of a group of 16 gives the address of elements 4 (l16 & 3) .. + 3
+// of row l16 >> 2 and gets column l16 of the four rows.  Two of them are a fragment.
+__device__ __forceinline__ short4v tr(const uint8_t *at) {
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4v *)(at));
+}
+__device__ __forceinline__ bf16x8 pair(const short4v &lo, const short4v &hi) {
+  return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+}
+
 // ---- rows x factor: part[split][r][q] = sum over the split's k of y[row(r)][k] f[g][q][k] --------------------
 struct ShrinkArgs {
   Rows rows;
-  bool use_c_rows;       // y is indexed like c (a gradient), not like x
   const uint8_t *y;
   int64_t ldy;           // bytes
   const uint8_t *f;      // [groups][R][K] bf16
@@ -122,10 +130,6 @@ struct ShrinkArgs {
   int32_t splits, split_k;  // elements of K a split, a multiple of the step
   float *part;           // [splits][M][R]
 };
-
-__device__ __forceinline__ int64_t y_row(const ShrinkArgs &p, int64_t r) {
-  return p.use_c_rows ? c_row(p.rows, r) : x_row(p.rows, r);
-}
 
 // Few rows an adapter: a workgroup has 16 rows and kFewK elements of K, a wave an eighth of these, all its loads in
 // flight at once; the waves' sums meet in LDS.
@@ -149,7 +153,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void shrink_few_kernel(ShrinkArgs p
       const int q = 16 * u + l16;
       if (q < p.R && k0 + 32 * i < p.K) a[u][i] = *reinterpret_cast<const uint4 *>(f + (q * p.K + 32 * i) * 2);
     }
-  const int64_t r = t.m0 + l16, y = r < t.m_end ? y_row(p, r) : -1;
+  const int64_t r = t.m0 + l16, y = r < t.m_end ? x_row(p.rows, r) : -1;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     b[i] = make_uint4(0, 0, 0, 0);
@@ -197,7 +201,7 @@ __global__ __launch_bounds__(256) void shrink_many_kernel(ShrinkArgs p) {
   for (int i = 0; i < 2; ++i) {
     const uint32_t R = 16 * wave + 8 * i + (lane >> 3);
     chunkY[i] = ((lane & 7u) ^ swz(R)) * 8;
-    const int64_t r = t.m0 + R, y = r < t.m_end ? y_row(p, r) : -1;
+    const int64_t r = t.m0 + R, y = r < t.m_end ? x_row(p.rows, r) : -1;
     srcY[i] = y >= 0 ? p.y + y * p.ldy : nullptr;
   }
 #pragma unroll
@@ -531,9 +535,9 @@ __global__ __launch_bounds__(256, RCP <= 4 ? 4 : RCP == 8 ? 3 : 2) void expand_k
 }
 
 // ---- the factors' gradients: out[g][q][n] or out[g][n][q] = sum_r piece[r][q] y[row(r)][n] -----------------------
+// and with a factor f in the same pass over y:  g_part[column tile][r][q] = sum over the tile's n of y[row(r)][n] f[g][n][q]
 struct OuterArgs {
   Rows rows;
-  bool use_c_rows;
   const uint8_t *y;
   int64_t ldy;            // bytes
   int64_t N;              // a multiple of 8
@@ -544,19 +548,29 @@ struct OuterArgs {
   int32_t tiles_n;
   float *part;            // [chunks][N R]
   float *out;             // [groups][N R]
+  const uint8_t *f;       // [groups][N][R] bf16
+  float *g_part;          // [tiles_n][M][R]
 };
 
-// A workgroup has `chunk` rows of one adapter and 256 columns of y, a wave 64 of these; 32 rows a step through LDS.  Both
-// operands lie with their rows (the contraction) outermost: fragments come from ds_read_b64_tr_b16, which gives a
-// lane four rows of one column.  32-byte unit u of row t of y sits at u ^ ((t & 3) | (t >> 1) & 4): the sixteen rows that
-// one read touches lie in different banks.
-constexpr int kOuterStep = 32, kOuterStages = 3, kMaxChunk = 1024;
+// A workgroup of eight waves has `chunk` rows of one adapter and 256 columns of y, a wave 32 of these; 32 rows a step through a
+// ring in LDS.  Both operands lie with their rows (the contraction) outermost: fragments come from ds_read_b64_tr_b16, which
+// gives a lane four rows of one column.  32-byte unit u of row t of y sits at u ^ ((t & 3) | (t >> 1) & 4): the sixteen rows
+// that one read touches lie in different banks.
+// The second product contracts over columns: f's fragments (again by transposed reads, from LDS before the rows' loop)
+// stay in registers, and each step the waves share out rows 0 to 15 and 16 to 31 with each fragment of f (of a rank of 16
+// there is one, and two waves take it).
+constexpr int kOuterStep = 32, kMaxChunk = 960, kOuterThreads = 512;
+// The ring's stages: two workgroups a compute unit share its 160 KB of LDS up to a rank of 32, else one has them.
 template <int RF>
-__global__ __launch_bounds__(256) void outer_kernel(OuterArgs p) {
-  constexpr int kY = kOuterStep * 512;
-  constexpr int NP = (kOuterStep * 6 * RF + 255) / 256;  // loads of pieces a wave and step (R = 16 RF at most)
-  constexpr int kStage = kY + NP * 4096;
-  __shared__ __attribute__((aligned(1024))) uint8_t smem[kOuterStages * kStage + 64];
+constexpr int kOuterStages = RF == 1 ? 4 : RF == 4 ? 5 : 3;
+template <int RF, bool G>
+__global__ __launch_bounds__(kOuterThreads) void outer_kernel(OuterArgs p) {
+  constexpr int S = kOuterStages<RF>;
+  constexpr int kY = kOuterStep * 512, kStage = kY + kOuterStep * 96 * RF;
+  // loads of pieces a step: 3 RF of 1 KB (R = 16 RF at most), NP for every wave and one more for the first `rest` waves
+  constexpr int NP = 3 * RF / 8;
+  constexpr uint32_t rest = 3 * RF % 8;
+  __shared__ __attribute__((aligned(1024))) uint8_t smem[S * kStage + 64];
   __shared__ int32_t y_rows[kMaxChunk];  // the chunk's rows of y; -1 beyond the last
   const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, j = lane >> 4;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -565,71 +579,89 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs p) {
   if (!find_tile(p.rows, p.chunk, tm, t)) return;
   const uint8_t *const zeros = reinterpret_cast<const uint8_t *>(&kZeros);
   const int64_t n_wg = static_cast<int64_t>(tn) * 256;
+  for (int i = threadIdx.x; i < p.chunk; i += kOuterThreads) {
+    const int64_t r = t.m0 + i;
+    y_rows[i] = static_cast<int32_t>(r < t.m_end ? x_row(p.rows, r) : -1);
+  }
+  constexpr int GF = G ? (RF + 3) / 4 : 1;  // fragments of f a wave
+  bf16x8 f[GF][8];
+  if constexpr (G) {
+    static_assert(256 * 32 * RF <= S * kStage, "f fits the ring");
+    const int32_t fp = p.R * 2, pieces = 256 * fp / 16;
+    const uint8_t *from = p.f + (static_cast<int64_t>(t.group) * p.N + n_wg) * fp;
+    const int32_t real = static_cast<int32_t>(min(static_cast<int64_t>(256), p.N - n_wg)) * fp / 16;
+    for (int32_t i = threadIdx.x; i < pieces; i += kOuterThreads)
+      *reinterpret_cast<uint4 *>(smem + i * 16) = i < real ? *reinterpret_cast<const uint4 *>(from + i * 16) : make_uint4(0, 0, 0, 0);
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < GF; ++v)
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        const int u = (4 * v + (wave >> 1)) % RF;
+        const uint8_t *at = smem + (32 * ks + 8 * j + (l16 >> 2)) * fp + (16 * u + 4 * (l16 & 3u)) * 2;
+        f[v][ks] = pair(tr(at), tr(at + 4 * fp));
+      }
+    wait_lgkmcnt0();
+  }
+  __syncthreads();  // (the ring takes f's place; y_rows are there)
   const int32_t RC3 = 3 * p.R / 8;                 // 16-byte chunks of a row of pieces
   const int32_t pitch = RC3 * 16;
   const int32_t steps = static_cast<int32_t>((t.m_end - t.m0 + kOuterStep - 1) / kOuterStep);
-  for (int i = threadIdx.x; i < p.chunk; i += 256) {
-    const int64_t r = t.m0 + i;
-    y_rows[i] = static_cast<int32_t>(r < t.m_end ? (p.use_c_rows ? c_row(p.rows, r) : x_row(p.rows, r)) : -1);
-  }
-  __syncthreads();
-  // y: wave w loads rows [8 w, 8 w + 8), two a load; lane: row lane >> 5, position lane & 31
-  uint32_t col[4];
+  // y: wave w loads rows [4 w, 4 w + 4), two a load; lane: row lane >> 5, position lane & 31
+  uint32_t col[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t T = 8 * wave + 2 * i + (lane >> 5);
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t T = 4 * wave + 2 * i + (lane >> 5);
     const uint32_t u = ((lane & 31u) >> 1) ^ ((T & 3u) | ((T >> 1) & 4u));
     col[i] = u * 16 + (lane & 1u) * 8;
   }
-  int32_t prow[NP], pchunk[NP];
+  int32_t prow[NP + 1], pchunk[NP + 1];
 #pragma unroll
-  for (int i = 0; i < NP; ++i) {
-    const int32_t at = (4 * i + wave) * 64 + lane;
+  for (int i = 0; i < NP + 1; ++i) {
+    const int32_t at = (8 * i + wave) * 64 + lane;
     prow[i] = at / RC3;
     pchunk[i] = at - prow[i] * RC3;
   }
   auto load = [&](int32_t kt) {
-    uint8_t *st = smem + (kt % kOuterStages) * kStage;
-    const int64_t r0 = t.m0 + static_cast<int64_t>(kt) * kOuterStep;
+    uint8_t *st = smem + (kt % S) * kStage;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int32_t at = kt * kOuterStep + 8 * wave + 2 * i + (lane >> 5), y = at < p.chunk ? y_rows[at] : -1;
+    for (int i = 0; i < 2; ++i) {
+      const int32_t at = kt * kOuterStep + 4 * wave + 2 * i + (lane >> 5), y = at < p.chunk ? y_rows[at] : -1;
       const int64_t n = n_wg + col[i];
-      lds_load16(y >= 0 && n < p.N ? p.y + y * p.ldy + n * 2 : zeros, st + (8 * wave + 2 * i) * 512);
+      lds_load16(y >= 0 && n < p.N ? p.y + y * p.ldy + n * 2 : zeros, st + (4 * wave + 2 * i) * 512);
     }
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
+    const int64_t r0 = t.m0 + static_cast<int64_t>(kt) * kOuterStep;
+    auto piece = [&](int i) {
       const int64_t r = r0 + prow[i];
-      lds_load16(prow[i] < kOuterStep && r < t.m_end ? p.pieces + r * pitch + pchunk[i] * 16 : zeros,
-                 st + kY + (4 * i + wave) * 1024);
-    }
+      lds_load16(prow[i] < kOuterStep && r < t.m_end ? p.pieces + r * pitch + pchunk[i] * 16 : zeros, st + kY + (8 * i + wave) * 1024);
+    };
+#pragma unroll
+    for (int i = 0; i < NP; ++i) piece(i);
+    if (rest > 0 && wave < rest) piece(NP);
   };
 #pragma unroll
-  for (int s = 0; s < kOuterStages - 1; ++s) load(s);
-  floatx4 acc[RF][4];
+  for (int s = 0; s < S - 1; ++s) load(s);
+  floatx4 acc[RF][2];
 #pragma unroll
   for (int u = 0; u < RF; ++u)
 #pragma unroll
-    for (int v = 0; v < 4; ++v) acc[u][v] = (floatx4){0.0f, 0.0f, 0.0f, 0.0f};
-  // Rows 8 j + 4 half + (l16 >> 2), elements 4 (l16 & 3) .. + 3 of a block of 16 columns: what this lane's address gives.
-  auto tr = [&](const uint8_t *at) {
-    return __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) short4v *)(at));
-  };
-  auto pair = [&](short4v lo, short4v hi) {
-    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
-  };
+    for (int v = 0; v < 2; ++v) acc[u][v] = (floatx4){0.0f, 0.0f, 0.0f, 0.0f};
   for (int32_t kt = 0; kt < steps; ++kt) {
-    wait_vmcnt<(kOuterStages - 2) * (4 + NP)>();
+    // (stores of the second product count too, and then a few of the later steps' loads are waited for)
+    if (rest > 0 && wave < rest)
+      wait_vmcnt<(S - 2) * (3 + NP)>();
+    else
+      wait_vmcnt<(S - 2) * (2 + NP)>();
     wait_lgkmcnt0();
     lds_barrier();
-    load(kt + kOuterStages - 1);
-    uint8_t *st = smem + (kt % kOuterStages) * kStage;
-    bf16x8 y[4];
+    load(kt + S - 1);
+    uint8_t *st = smem + (kt % S) * kStage;
+    bf16x8 y[2];
     const uint32_t T = 8 * j + (l16 >> 2);  // (row T + 4 has the same swizzle)
     const uint32_t sw = (T & 3u) | ((T >> 1) & 4u);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const uint8_t *at = st + T * 512 + ((4 * wave + v) ^ sw) * 32 + (l16 & 3u) * 8;
+    for (int v = 0; v < 2; ++v) {
+      const uint8_t *at = st + T * 512 + ((2 * wave + v) ^ sw) * 32 + (l16 & 3u) * 8;
       y[v] = pair(tr(at), tr(at + 4 * 512));
     }
 #pragma unroll
@@ -639,14 +671,32 @@ __global__ __launch_bounds__(256) void outer_kernel(OuterArgs p) {
         const uint8_t *at = st + kY + T * pitch + (s * p.R + 16 * u + 4 * (l16 & 3u)) * 2;
         const bf16x8 a = pair(tr(at), tr(at + 4 * pitch));
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[u][v] = mfma(a, y[v], acc[u][v]);
+        for (int v = 0; v < 2; ++v) acc[u][v] = mfma(a, y[v], acc[u][v]);
       }
+    if (G && (RF >= 4 || wave < 2 * RF)) {
+      const uint32_t tr_row = 16 * (wave & 1) + l16, sw2 = (tr_row & 3u) | ((tr_row >> 1) & 4u);
+      floatx4 g[GF];
+#pragma unroll
+      for (int v = 0; v < GF; ++v) g[v] = (floatx4){0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int ks = 0; ks < 8; ++ks) {
+        const bf16x8 b = frag(st + tr_row * 512 + ((2 * ks + (j >> 1)) ^ sw2) * 32 + (j & 1u) * 16);
+#pragma unroll
+        for (int v = 0; v < GF; ++v) g[v] = mfma(f[v][ks], b, g[v]);
+      }
+      const int64_t r = t.m0 + static_cast<int64_t>(kt) * kOuterStep + tr_row;
+#pragma unroll
+      for (int v = 0; v < GF; ++v) {
+        const int q = 16 * ((4 * v + (wave >> 1)) % RF) + 4 * j;
+        if (r < t.m_end && q < p.R) *reinterpret_cast<floatx4 *>(p.g_part + (static_cast<int64_t>(tn) * p.rows.M + r) * p.R + q) = g[v];
+      }
+    }
   }
   wait_vmcnt<0>();
   float *out = t.tiles == 1 ? p.out + static_cast<int64_t>(t.group) * p.N * p.R : p.part + static_cast<int64_t>(tm) * p.N * p.R;
 #pragma unroll
-  for (int v = 0; v < 4; ++v) {
-    const int64_t n = n_wg + 64 * wave + 16 * v + l16;
+  for (int v = 0; v < 2; ++v) {
+    const int64_t n = n_wg + 32 * wave + 16 * v + l16;
     if (n >= p.N) continue;
 #pragma unroll
     for (int u = 0; u < RF; ++u) {
@@ -702,7 +752,7 @@ __global__ __launch_bounds__(256) void outer_sum_kernel(OuterSumArgs a, OuterSum
     outer_sum(b, blockIdx.x - blocks_a);
 }
 
-// ---- before a backward pass: transposed factors, and the pieces of h -------------------------------------------
+// ---- before a backward pass: a transposed factor, and the pieces of h -------------------------------------------
 // out[g][c][r] = in[g][r][c], [rows x cols] bf16 with cols a multiple of 8 and one of the two at most 128; 64 x 64 tiles.
 struct TransposeArgs {
   const uint16_t *in;
@@ -723,16 +773,12 @@ __device__ void transpose_tile(const TransposeArgs &p, int64_t id, uint16_t (&ld
   for (int i = wave; i < 64; i += 4)
     if (c0 + i < p.cols && r0 + lane < p.rows) out[(c0 + i) * p.rows + r0 + lane] = lds[lane][i];
 }
-__global__ __launch_bounds__(256) void adapter_prep_kernel(TransposeArgs a, int64_t blocks_a, TransposeArgs b, int64_t blocks_b,
-                                                           FinishArgs h) {
+__global__ __launch_bounds__(256) void adapter_prep_kernel(TransposeArgs a, int64_t blocks_a, FinishArgs h) {
   __shared__ uint16_t lds[64][66];
-  const int64_t id = blockIdx.x;
-  if (id < blocks_a)
-    transpose_tile(a, id, lds);
-  else if (id < blocks_a + blocks_b)
-    transpose_tile(b, id - blocks_a, lds);
+  if (blockIdx.x < blocks_a)
+    transpose_tile(a, blockIdx.x, lds);
   else
-    finish_tile(h, static_cast<int32_t>(id - blocks_a - blocks_b));
+    finish_tile(h, static_cast<int32_t>(blockIdx.x - blocks_a));
 }
 
 // ---- launches ----------------------------------------------------------------------------------------------------
@@ -791,23 +837,21 @@ hipError_t run_shrink(const ShrinkArgs &p, bool few, int64_t tiles, hipStream_t 
     shrink_many_kernel<RF><<<grid, dim3(256), 0, stream>>>(p);
   return hipGetLastError();
 }
-hipError_t run_shrink(const AdapterArgs &a, bool use_c_rows, const void *y, int64_t ldy, const void *f, int64_t K, float *part,
-                      int32_t &splits) {
+hipError_t run_shrink(const AdapterArgs &a, float *part, int32_t &splits) {
   ShrinkArgs p{};
   p.rows = rows_of(a);
-  p.use_c_rows = use_c_rows;
-  p.y = static_cast<const uint8_t *>(y);
-  p.ldy = ldy * 2;
-  p.f = static_cast<const uint8_t *>(f);
-  p.K = K;
+  p.y = static_cast<const uint8_t *>(a.x);
+  p.ldy = a.ldx * 2;
+  p.f = static_cast<const uint8_t *>(a.a);
+  p.K = a.K;
   p.R = a.rank;
   p.part = part;
   const bool few = few_rows(a.M, a.adapters);
   if (few) {
-    p.splits = static_cast<int32_t>((K + kFewK - 1) / kFewK);
+    p.splits = static_cast<int32_t>((a.K + kFewK - 1) / kFewK);
     p.split_k = kFewK;
   } else {
-    many_splits(a.M, K, a.gather, p.splits, p.split_k);
+    many_splits(a.M, a.K, a.gather, p.splits, p.split_k);
   }
   splits = p.splits;
   const int64_t tiles = tiles_for(a, few ? 16 : kManyRows);
@@ -885,33 +929,32 @@ hipError_t run_expand(const AdapterArgs &a, const void *f, int64_t N, float *par
   return dtype == 1 ? run_expand<true>(p, few, vec, groups, a.stream) : run_expand<false>(p, few, vec, groups, a.stream);
 }
 
-// Rows of a workgroup of the factors' gradients: as many as leave about two workgroups a compute unit.
-int32_t outer_chunk(int64_t M, int64_t N) {
-  const int64_t tiles_n = (N + 255) / 256;
-  int64_t chunk = kMaxChunk;
-  while (chunk > 64 && tiles_n * (M / chunk) < 512) chunk /= 2;
-  return static_cast<int32_t>(chunk);
+// Rows of a workgroup of the factors' gradients: the workgroups are to come near a multiple of those that run at once, two a
+// compute unit or, of ranks above 32, one (for 56 column tiles and 8192 rows: 504 workgroups of 928 rows and not 896 of 512,
+// which leave a quarter of the second round idle), and have at least 64 rows.
+int32_t outer_chunk(int64_t M, int64_t N, int32_t rank) {
+  const int64_t tiles_n = (N + 255) / 256, slots = rank <= 32 ? 512 : 256;
+  int64_t rounds = 1, n;
+  do {
+    n = rounds++ * slots / tiles_n;
+  } while (n < 1 || (M + n - 1) / n > kMaxChunk);
+  const int64_t chunk = ((M + n - 1) / n + kOuterStep - 1) / kOuterStep * kOuterStep;
+  return static_cast<int32_t>(chunk < 64 ? 64 : chunk);
 }
 template <int RF>
 hipError_t run_outer(const OuterArgs &p, uint32_t groups, hipStream_t stream) {
-  outer_kernel<RF><<<dim3(groups), dim3(256), 0, stream>>>(p);
+  if (p.f)
+    outer_kernel<RF, true><<<dim3(groups), dim3(kOuterThreads), 0, stream>>>(p);
+  else
+    outer_kernel<RF, false><<<dim3(groups), dim3(kOuterThreads), 0, stream>>>(p);
   return hipGetLastError();
 }
-hipError_t run_outer(const AdapterArgs &a, bool use_c_rows, const void *y, int64_t ldy, int64_t N, const uint8_t *pieces, bool n_major,
-                     float *part, float *out) {
-  OuterArgs p{};
+hipError_t run_outer(const AdapterArgs &a, OuterArgs p) {
   p.rows = rows_of(a);
-  p.use_c_rows = use_c_rows;
-  p.y = static_cast<const uint8_t *>(y);
-  p.ldy = ldy * 2;
-  p.N = N;
+  p.ldy *= 2;
   p.R = a.rank;
-  p.pieces = pieces;
-  p.n_major = n_major;
-  p.chunk = outer_chunk(a.M, N);
-  p.tiles_n = static_cast<int32_t>((N + 255) / 256);
-  p.part = part;
-  p.out = out;
+  p.chunk = outer_chunk(a.M, p.N, a.rank);
+  p.tiles_n = static_cast<int32_t>((p.N + 255) / 256);
   const uint32_t groups = static_cast<uint32_t>(p.tiles_n * tiles_for(a, p.chunk));
   if (a.rank <= 16) return run_outer<1>(p, groups, a.stream);
   if (a.rank <= 32) return run_outer<2>(p, groups, a.stream);
@@ -939,17 +982,16 @@ struct ForwardLayout {
   }
 };
 struct BackwardLayout {
-  size_t at, bt, h_pieces, part, g_pieces, da_part, db_part, size;
+  size_t at, h_pieces, part, g_pieces, da_part, db_part, size;
   BackwardLayout(const AdapterArgs &a) {
     Layout l;
     const int64_t factor = static_cast<int64_t>(a.adapters) * a.rank;
     at = l.take(factor * a.K * 2);
-    bt = l.take(factor * a.N * 2);
     h_pieces = l.take(a.M * a.rank * 6);
-    part = l.take(static_cast<int64_t>(splits_for(a.M, a.adapters, a.N, false)) * a.M * a.rank * 4);
+    part = l.take((a.N + 255) / 256 * a.M * a.rank * 4);
     g_pieces = l.take(a.M * a.rank * 6);
-    da_part = l.take(tiles_for(a, outer_chunk(a.M, a.K)) * a.K * a.rank * 4);
-    db_part = l.take(tiles_for(a, outer_chunk(a.M, a.N)) * a.N * a.rank * 4);
+    da_part = l.take(tiles_for(a, outer_chunk(a.M, a.K, a.rank)) * a.K * a.rank * 4);
+    db_part = l.take(tiles_for(a, outer_chunk(a.M, a.N, a.rank)) * a.N * a.rank * 4);
     size = l.at;
   }
 };
@@ -967,9 +1009,9 @@ bool adapter_launches(const AdapterArgs &a, bool backward) {
   const int64_t widest = ((a.N > a.K ? a.N : a.K) + 255) / 256;
   const bool few = few_rows(a.M, a.adapters);
   const int64_t tiles = tiles_for(a, 16) + (a.M + 63) / 64;
-  const int64_t splits = splits_for(a.M, a.adapters, backward ? a.N : a.K, a.gather);
+  const int64_t splits = backward ? 1 : splits_for(a.M, a.adapters, a.K, a.gather);
   const int64_t sums = backward ? a.adapters * ((a.N + a.K) * a.rank / kOuterSumSize + 2) : 0;
-  const int64_t prep = backward ? a.adapters * ((a.rank + 63) / 64) * ((a.N + 63) / 64 + (a.K + 63) / 64) + tiles : 0;
+  const int64_t prep = backward ? a.adapters * ((a.rank + 63) / 64) * ((a.K + 63) / 64) + tiles : 0;
   return tiles * widest < kMost && tiles * splits < kMost && sums < kMost && prep < kMost &&
          (!backward || widest * tiles_for(a, 64) < kMost);
 }
@@ -979,7 +1021,7 @@ hipError_t launch_adapter(const AdapterArgs &a) {
   uint8_t *const w = static_cast<uint8_t *>(a.workspace);
   float *const part = reinterpret_cast<float *>(w + l.part);
   int32_t splits;
-  const hipError_t e = run_shrink(a, false, a.x, a.ldx, a.a, a.K, part, splits);
+  const hipError_t e = run_shrink(a, part, splits);
   if (e != hipSuccess) return e;
   return run_expand(a, a.b, a.N, part, splits, a.h, nullptr, a.base, a.ldb, a.c, a.ldc, a.c_dtype);
 }
@@ -991,24 +1033,39 @@ hipError_t launch_adapter_backward(const AdapterArgs &a) {
               *const db_part = reinterpret_cast<float *>(w + l.db_part);
   const Rows rows = rows_of(a);
   hipError_t e;
-  if (a.M > 0) {  // A^T [K][R], B^T [R][N], and the pieces of s h
-    auto tiles = [](int64_t n) { return static_cast<int32_t>((n + 63) / 64); };
-    TransposeArgs ta{static_cast<const uint16_t *>(a.a), reinterpret_cast<uint16_t *>(w + l.at), a.rank, a.K, tiles(a.rank), tiles(a.K)};
-    TransposeArgs tb{static_cast<const uint16_t *>(a.b), reinterpret_cast<uint16_t *>(w + l.bt), a.N, a.rank, tiles(a.N), tiles(a.rank)};
-    FinishArgs h{rows, a.h, 1, a.rank, a.scales, nullptr, w + l.h_pieces};
-    const int64_t na = static_cast<int64_t>(a.adapters) * ta.tiles_r * ta.tiles_c, nb = static_cast<int64_t>(a.adapters) * tb.tiles_r * tb.tiles_c;
-    adapter_prep_kernel<<<dim3(static_cast<uint32_t>(na + nb + tiles_for(a, kFinishRows))), dim3(256), 0, a.stream>>>(ta, na, tb, nb, h);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-  }
   if (a.M > 0) {
-    int32_t splits;
-    if ((e = run_shrink(a, true, a.dc, a.lddc, w + l.bt, a.N, part, splits)) != hipSuccess) return e;
-    if ((e = run_expand(a, w + l.at, a.K, part, splits, nullptr, w + l.g_pieces, a.base, a.ldb, a.c, a.ldc, a.c_dtype)) != hipSuccess)
+    // A^T [K][R], and the pieces of s h
+    auto tiles = [](int64_t n) { return static_cast<int32_t>((n + 63) / 64); };
+    const TransposeArgs ta{static_cast<const uint16_t *>(a.a), reinterpret_cast<uint16_t *>(w + l.at), a.rank, a.K, tiles(a.rank), tiles(a.K)};
+    const FinishArgs h{rows, a.h, 1, a.rank, a.scales, nullptr, w + l.h_pieces};
+    const int64_t na = static_cast<int64_t>(a.adapters) * ta.tiles_r * ta.tiles_c;
+    adapter_prep_kernel<<<dim3(static_cast<uint32_t>(na + tiles_for(a, kFinishRows))), dim3(256), 0, a.stream>>>(ta, na, h);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    // dB's parts and g's from one pass over dc; dx from g, and its pieces; dA's parts
+    OuterArgs o{};
+    o.y = static_cast<const uint8_t *>(a.dc);
+    o.ldy = a.lddc;
+    o.N = a.N;
+    o.pieces = w + l.h_pieces;
+    o.n_major = true;
+    o.part = db_part;
+    o.out = a.db;
+    o.f = static_cast<const uint8_t *>(a.b);
+    o.g_part = part;
+    if ((e = run_outer(a, o)) != hipSuccess) return e;
+    const int32_t tiles_n = static_cast<int32_t>((a.N + 255) / 256);
+    if ((e = run_expand(a, w + l.at, a.K, part, tiles_n, nullptr, w + l.g_pieces, a.base, a.ldb, a.c, a.ldc, a.c_dtype)) != hipSuccess)
       return e;
-    if ((e = run_outer(a, true, a.dc, a.lddc, a.N, w + l.h_pieces, true, db_part, a.db)) != hipSuccess) return e;
-    if ((e = run_outer(a, false, a.x, a.ldx, a.K, w + l.g_pieces, false, da_part, a.da)) != hipSuccess) return e;
+    o = {};
+    o.y = static_cast<const uint8_t *>(a.x);
+    o.ldy = a.ldx;
+    o.N = a.K;
+    o.pieces = w + l.g_pieces;
+    o.part = da_part;
+    o.out = a.da;
+    if ((e = run_outer(a, o)) != hipSuccess) return e;
   }
-  OuterSumArgs sa{rows, outer_chunk(a.M, a.K), a.K * a.rank, 0, da_part, a.da}, sb{rows, outer_chunk(a.M, a.N), a.N * a.rank, 0, db_part, a.db};
+  OuterSumArgs sa{rows, outer_chunk(a.M, a.K, a.rank), a.K * a.rank, 0, da_part, a.da}, sb{rows, outer_chunk(a.M, a.N, a.rank), a.N * a.rank, 0, db_part, a.db};
   sa.blocks = static_cast<int32_t>((sa.size + kOuterSumSize - 1) / kOuterSumSize);
   sb.blocks = static_cast<int32_t>((sb.size + kOuterSumSize - 1) / kOuterSumSize);
   const int64_t na = static_cast<int64_t>(a.adapters) * sa.blocks, nb = static_cast<int64_t>(a.adapters) * sb.blocks;

@@ -12,6 +12,7 @@ there is no fallback path.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 from dataclasses import dataclass
@@ -907,27 +908,40 @@ def _dense(t: torch.Tensor) -> bool:
     return True
 
 
+_DATA_PTR, _NUMEL, _DEVICE, _CONTIGUOUS = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.get_device, torch.Tensor.is_contiguous
+
+
+def _host(code: str, values):
+    """Host array of these numbers, and its address."""
+    a = array.array(code, values)
+    return a, a.buffer_info()[0]
+
+
 def _grad_list(where: str, grads: Sequence[torch.Tensor]):
-    """Host arrays of the tensors' addresses, element counts and types, and the number of elements of all."""
+    """Host arrays of the tensors' addresses, element counts and types, as (arrays, addresses, counts, contiguous): the walk
+    over hundreds of tensors is most of a small list's time, so each question is one map over all of them."""
     if isinstance(grads, torch.Tensor) or not len(grads):
         raise ValueError(f"{where}: needs a list of at least one tensor")
-    n, at = len(grads), grads[0].get_device()
-    for t in grads:
-        if t.get_device() != at or t.layout is not torch.strided:
-            raise ValueError(f"{where}: all tensors must be strided tensors of one device")
-        if not _dense(t):
-            raise ValueError(f"{where}: a tensor of shape {list(t.shape)} has strides {list(t.stride())}, which leave gaps")
-    counts = [t.numel() for t in grads]
-    return ((ctypes.c_void_p * n)(*[t.data_ptr() for t in grads]), (ctypes.c_int64 * n)(*counts),
-            (ctypes.c_int32 * n)(*[_dtype_code(t.dtype) for t in grads]), n, sum(counts))
+    if len(set(map(_DEVICE, grads))) != 1:
+        raise ValueError(f"{where}: all tensors must be on one device")
+    whole = all(map(_CONTIGUOUS, grads))
+    if not whole:
+        for t in grads:
+            if not _dense(t):
+                raise ValueError(f"{where}: a tensor of shape {list(t.shape)} has strides {list(t.stride())}, which leave gaps")
+    dtypes = [t.dtype for t in grads]
+    codes = {d: _dtype_code(d) for d in set(dtypes)}
+    counts = list(map(_NUMEL, grads))
+    arrays = (_host("Q", map(_DATA_PTR, grads)), _host("q", counts), _host("i", [codes[d] for d in dtypes]))
+    return arrays, counts, dtypes, whole
 
 
 def _grad_norm(where, grads, listed, flags, workspace):
-    addresses, counts, dtypes, n, elements = listed
-    first = grads[0]
+    (addresses, counts, dtypes), numbers, _, _ = listed
+    first, n = grads[0], len(numbers)
     norm = torch.empty(1, dtype=torch.float32, device=first.device)
-    workspace = _scratch(where, workspace, lib().nvfp4_grad_workspace_size(n, elements), first)
-    _enqueue("nvfp4_grad_norm", first, addresses, counts, dtypes, n, flags, norm.data_ptr(), _addr(workspace))
+    workspace = _scratch(where, workspace, lib().nvfp4_grad_workspace_size(n, sum(numbers)), first)
+    _enqueue("nvfp4_grad_norm", first, addresses[1], counts[1], dtypes[1], n, flags, norm.data_ptr(), _addr(workspace))
     return norm
 
 
@@ -946,17 +960,17 @@ def nvfp4_grad_clip(grads: Sequence[torch.Tensor], max_norm: float, flags: int =
     leaves the gradients as they are."""
     where = "nvfp4_grad_clip"
     listed = _grad_list(where, grads)
-    addresses, counts, dtypes, n, _ = listed
+    (addresses, counts, dtypes), numbers, types, whole = listed
     outs = addresses
     if out is not None:
-        if len(out) != n:
-            raise ValueError(f"{where}: out has {len(out)} tensors, the list {n}")
-        for o, t in zip(out, grads):
-            if o.shape != t.shape or o.dtype is not t.dtype or o.get_device() != t.get_device() or o.stride() != t.stride():
-                raise ValueError(f"{where}: out must match the list, tensor by tensor")
-        outs = (ctypes.c_void_p * n)(*[o.data_ptr() for o in out])
+        # (contiguous tensors are a row of elements, whatever their shapes)
+        if len(out) != len(numbers) or list(map(_NUMEL, out)) != numbers or [o.dtype for o in out] != types or \
+                set(map(_DEVICE, out)) != {grads[0].get_device()} or \
+                not (whole and all(map(_CONTIGUOUS, out)) or all(o.shape == t.shape and o.stride() == t.stride() for o, t in zip(out, grads))):
+            raise ValueError(f"{where}: out must match the list, tensor by tensor")
+        outs = _host("Q", map(_DATA_PTR, out))
     _want(where, "norm", norm, torch.float32, (1,), grads[0])
     if norm is None:
         norm = _grad_norm(where, grads, listed, flags, workspace)
-    _enqueue(where, grads[0], addresses, outs, counts, dtypes, n, norm.data_ptr(), max_norm, eps)
+    _enqueue(where, grads[0], addresses[1], outs[1], counts[1], dtypes[1], len(numbers), norm.data_ptr(), max_norm, eps)
     return norm

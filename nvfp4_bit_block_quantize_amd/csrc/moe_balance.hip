@@ -1,6 +1,6 @@
 // moe_balance.hip -- the balance loss of a routing, the counts it needs, and its gradient with respect to the logits.
 //
-// Sixteen lanes (one DPP row) own a token, lane i the experts [i EPL, (i + 1) EPL): a token's maximum and sum are
+// Sixteen lanes (one DPP row) own a token, each EPL of its experts: a token's maximum and sum are
 // four DPP steps each, and a wave takes four tokens at once.  A lane adds its experts' probabilities over the
 // workgroup's tokens in registers; rows, then waves, then workgroups meet in one fixed order.  Counts are integers
 // (LDS atomics, whose order does not show).  A second kernel, a workgroup a sequence, adds the workgroups' parts and
@@ -22,7 +22,8 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int kThreads = 256, kRows = kThreads / 16;  // tokens of a workgroup at once
+// Threads of a workgroup, and its tokens at once: the forward kernel leaves few partial sums, the backward one none.
+constexpr int kSumsThreads = 1024, kSumsRows = kSumsThreads / 16, kThreads = 256, kRows = kThreads / 16;
 constexpr int kMaxExperts = 512;
 constexpr float kNegInf = -__builtin_huge_valf(), kMaxLogit = 3.402823466e38f;
 constexpr float kTiny = 1e-20f;  // added to a sum of sigmoid scores
@@ -54,24 +55,36 @@ __device__ __forceinline__ int row_max(int v) {
   return v;
 }
 
-// A lane's EPL values of a row from element e0 on; `fill` beyond E.
+// A lane's EPL experts of a row of E <= 16 EPL: pieces of kPiece side by side, and the row's lanes side by side in each.
 template <int EPL, bool BF16>
-__device__ __forceinline__ void load_row(const uint8_t *row, int e0, int E, bool vec, float fill, float (&l)[EPL]) {
-  constexpr int BYTES = EPL * (BF16 ? 2 : 4);
-  if constexpr (BYTES % 16 == 0) {
-    if (vec && e0 + EPL <= E) {
-      constexpr int V = BF16 ? 8 : 4;
+struct Place {
+  static constexpr int kPiece = EPL < (BF16 ? 8 : 4) ? EPL : (BF16 ? 8 : 4);  // elements; 16 bytes where there are enough
+  static constexpr int kPieces = EPL / kPiece;
+  static constexpr bool kWide = kPiece * (BF16 ? 2 : 4) == 16;
+  // Expert of the lane's value i.
+  static __device__ __forceinline__ int of(int i, int l16) { return (i / kPiece * 16 + l16) * kPiece + i % kPiece; }
+};
+
+// The lane's values of a row; `fill` beyond E.  vec: the row is aligned to 16 bytes and E fills whole pieces.
+template <int EPL, bool BF16>
+__device__ __forceinline__ void load_row(const uint8_t *row, int l16, int E, bool vec, float fill, float (&l)[EPL]) {
+  using P = Place<EPL, BF16>;
+  if constexpr (P::kWide) {
+    if (vec) {
 #pragma unroll
-      for (int i = 0; i < BYTES / 16; ++i) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(row + e0 * (BF16 ? 2 : 4) + 16 * i);
+      for (int m = 0; m < P::kPieces; ++m) {
+        const int e0 = P::of(m * P::kPiece, l16);
+        const bool real = e0 < E;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (real) v = *reinterpret_cast<const uint4 *>(row + e0 * (BF16 ? 2 : 4));
         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if constexpr (BF16) {
-            l[V * i + 2 * q] = __uint_as_float(w[q] << 16);
-            l[V * i + 2 * q + 1] = __uint_as_float(w[q] & 0xFFFF0000u);
+            l[8 * m + 2 * q] = real ? __uint_as_float(w[q] << 16) : fill;
+            l[8 * m + 2 * q + 1] = real ? __uint_as_float(w[q] & 0xFFFF0000u) : fill;
           } else {
-            l[V * i + q] = __uint_as_float(w[q]);
+            l[4 * m + q] = real ? __uint_as_float(w[q]) : fill;
           }
         }
       }
@@ -79,70 +92,110 @@ __device__ __forceinline__ void load_row(const uint8_t *row, int e0, int E, bool
     }
   }
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    l[j] = fill;
-    if (e0 + j < E)
-      l[j] = BF16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[e0 + j]) << 16)
-                  : reinterpret_cast<const float *>(row)[e0 + j];
+  for (int i = 0; i < EPL; ++i) {
+    const int e = P::of(i, l16);
+    l[i] = fill;
+    if (e < E)
+      l[i] = BF16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[e]) << 16)
+                  : reinterpret_cast<const float *>(row)[e];
   }
 }
 template <int EPL, bool BF16>
-__device__ __forceinline__ void store_row(uint8_t *row, int e0, int E, bool vec, const float (&d)[EPL]) {
-  constexpr int BYTES = EPL * (BF16 ? 2 : 4);
-  if constexpr (BYTES % 16 == 0) {
-    if (vec && e0 + EPL <= E) {
+__device__ __forceinline__ void store_row(uint8_t *row, int l16, int E, bool vec, const float (&d)[EPL]) {
+  using P = Place<EPL, BF16>;
+  if constexpr (P::kWide) {
+    if (vec) {
 #pragma unroll
-      for (int i = 0; i < BYTES / 16; ++i) {
+      for (int m = 0; m < P::kPieces; ++m) {
+        const int e0 = P::of(m * P::kPiece, l16);
         uint32_t w[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if constexpr (BF16)
-            w[q] = pack_bf16(d[8 * i + 2 * q], d[8 * i + 2 * q + 1]);
+            w[q] = pack_bf16(d[8 * m + 2 * q], d[8 * m + 2 * q + 1]);
           else
-            w[q] = __float_as_uint(d[4 * i + q]);
+            w[q] = __float_as_uint(d[4 * m + q]);
         }
-        *reinterpret_cast<uint4 *>(row + e0 * (BF16 ? 2 : 4) + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+        if (e0 < E) *reinterpret_cast<uint4 *>(row + e0 * (BF16 ? 2 : 4)) = make_uint4(w[0], w[1], w[2], w[3]);
       }
       return;
     }
   }
 #pragma unroll
-  for (int j = 0; j < EPL; ++j)
-    if (e0 + j < E) {
+  for (int i = 0; i < EPL; ++i) {
+    const int e = P::of(i, l16);
+    if (e < E) {
       if constexpr (BF16)
-        reinterpret_cast<uint16_t *>(row)[e0 + j] = static_cast<uint16_t>(pack_bf16(d[j], 0.0f));
+        reinterpret_cast<uint16_t *>(row)[e] = static_cast<uint16_t>(pack_bf16(d[i], 0.0f));
       else
-        reinterpret_cast<float *>(row)[e0 + j] = d[j];
+        reinterpret_cast<float *>(row)[e] = d[i];
     }
+  }
+}
+// The lane's counts of a row of E (element by element unless four lie together in the lane and the row).
+template <int EPL, bool BF16>
+__device__ __forceinline__ void load_counts(const int32_t *row, int l16, int E, int (&n)[EPL]) {
+  using P = Place<EPL, BF16>;
+  if constexpr (P::kPiece >= 4) {
+    if (E % 4 == 0 && (reinterpret_cast<uintptr_t>(row) & 15u) == 0) {
+#pragma unroll
+      for (int i = 0; i < EPL; i += 4) {
+        const int e = P::of(i, l16);
+        int4 v = make_int4(0, 0, 0, 0);
+        if (e < E) v = *reinterpret_cast<const int4 *>(row + e);
+        n[i] = v.x;
+        n[i + 1] = v.y;
+        n[i + 2] = v.z;
+        n[i + 3] = v.w;
+      }
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < EPL; ++i) {
+    const int e = P::of(i, l16);
+    n[i] = e < E ? row[e] : 0;
+  }
 }
 
-// Probabilities of a token from its logits (closed experts: -inf or NaN; others capped at FLT_MAX).  l is left as the
-// logits in this form; `spare` is 1 - sum p (0 for a softmax).  Returns the largest logit.
-template <int EPL, bool SIGMOID>
-__device__ __forceinline__ float row_probs(float (&l)[EPL], float (&p)[EPL], float &spare) {
-  float top = kNegInf;
+// exp(x) for x <= 0, off by at most 4 x 2^-24 of itself: what the rounding of x / ln 2 leaves goes in by its first order.  (The
+// general function costs twice the instructions.)  -inf and NaN count as -200, whose exponential is zero in 32 bits.
+__device__ __forceinline__ float exp_of(float x) {
+  constexpr float kInvLn2 = 1.44269502e+00f, kLn2 = 6.93147182e-01f, kLn2Low = -1.90465421e-09f;
+  x = fmaxf(x, -200.0f);
+  const float t = x * kInvLn2;
+  const float left = fmaf(-t, kLn2Low, fmaf(-t, kLn2, x));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return fmaf(e, left, e);
+}
+
+// Scores of a token from its logits (closed experts: -inf or NaN; others capped at FLT_MAX), before their division by their
+// sum: p, and what divides them, `inv` (0 for a token without an open expert, or whose sum is zero).  l is left as the
+// logits in this form; `spare` is 1 - sum of the probabilities (0 for a softmax); slope (sigmoid): 1 - s.  Returns the
+// largest logit.  A closed expert's score comes out as zero by itself.
+template <int EPL, bool SIGMOID, bool SLOPE>
+__device__ __forceinline__ float row_scores(float (&l)[EPL], float (&p)[EPL], float (&slope)[EPL], float &inv, float &spare) {
+  float top = kNegInf, sum = 0.0f;
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
-    l[j] = l[j] > kNegInf ? fminf(l[j], kMaxLogit) : kNegInf;  // (NaN compares false)
-    top = fmaxf(top, l[j]);
+    l[j] = fminf(fmaxf(l[j], kNegInf), kMaxLogit);  // (the larger of NaN and -inf is -inf)
+    if (!SIGMOID || SLOPE) top = fmaxf(top, l[j]);
   }
-  top = row_max(top);
-  float sum = 0.0f;
+  if (!SIGMOID || SLOPE) top = row_max(top);
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     if constexpr (SIGMOID) {
-      const float e = expf(-fabsf(l[j]));
-      p[j] = l[j] == kNegInf ? 0.0f : (l[j] > 0.0f ? 1.0f : e) / (1.0f + e);
+      const float e = exp_of(-fabsf(l[j])), r = __builtin_amdgcn_rcpf(1.0f + e), er = e * r;
+      p[j] = l[j] > 0.0f ? r : er;
+      if (SLOPE) slope[j] = l[j] > 0.0f ? er : r;
     } else {
-      p[j] = l[j] == kNegInf ? 0.0f : expf(l[j] - top);
+      p[j] = exp_of(l[j] - top);
     }
     sum += p[j];
   }
   sum = row_sum(sum);
-  const float inv = SIGMOID ? 1.0f / (sum + kTiny) : (sum > 0.0f ? 1.0f / sum : 0.0f);
+  inv = SIGMOID ? 1.0f / (sum + kTiny) : (sum > 0.0f ? 1.0f / sum : 0.0f);
   spare = SIGMOID ? kTiny * inv : 0.0f;
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) p[j] *= inv;
   return top;
 }
 
@@ -157,7 +210,7 @@ struct BalanceArgs {
   float *part_probs;     // [sequences][blocks][E]
   int32_t *part_counts;  // the like
   int32_t *part_tokens;  // [sequences][blocks]
-  float *part_loss;      // [sequences]
+  float *part_loss;      // [sequences][workgroups of a sequence's sums]
   uint32_t *done;
   float *loss, *probs;
   int32_t *counts, *tokens;
@@ -193,53 +246,74 @@ __device__ __forceinline__ float seq_term(int count, float prob_sum, int tokens,
 
 // ONE: a single workgroup has all tokens and writes the results itself.
 template <int EPL, bool BF16, bool SIGMOID, bool ONE>
-__global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs p) {
-  constexpr int P = 16 * EPL;
+__global__ __launch_bounds__(kSumsThreads) void balance_kernel(BalanceArgs p) {
+  constexpr int P = 16 * EPL, kWaves = kSumsThreads / 64;
   __shared__ int32_t hist[P];
-  __shared__ float sums[4][P];
-  __shared__ int32_t live_count[4];
-  __shared__ float loss_part[4];
+  __shared__ float sums[kWaves][P];
+  __shared__ int32_t live_count[kWaves];
+  __shared__ float loss_part[kWaves];
   const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-  const int l16 = lane & 15, e0 = l16 * EPL;
+  const int l16 = lane & 15;
   const int64_t s = blockIdx.y, first = s * p.seq;
-  for (int e = threadIdx.x; e < P; e += kThreads) hist[e] = 0;
+  for (int e = threadIdx.x; e < P; e += kSumsThreads) hist[e] = 0;
   if (!ONE && blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.done = 0;
   __syncthreads();
   float acc[EPL];
 #pragma unroll
   for (int j = 0; j < EPL; ++j) acc[j] = 0.0f;
   int live = 0;
-  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kRows; t0 < p.seq; t0 += static_cast<int64_t>(p.blocks) * kRows) {
+  for (int64_t t0 = static_cast<int64_t>(blockIdx.x) * kSumsRows; t0 < p.seq; t0 += static_cast<int64_t>(p.blocks) * kSumsRows) {
     const int64_t i = t0 + (threadIdx.x >> 4);
     const bool exists = i < p.seq;
     const int64_t t = first + (exists ? i : p.seq - 1);
-    float l[EPL], q[EPL], spare;
-    load_row<EPL, BF16>(p.logits + t * p.row_bytes, e0, p.E, p.vec, kNegInf, l);
+    float l[EPL], q[EPL], none[EPL], inv, spare;
+    load_row<EPL, BF16>(p.logits + t * p.row_bytes, l16, p.E, p.vec, kNegInf, l);
     const bool on = row_ids(p.ids, t, p.k, p.E, l16, exists, hist);
-    row_probs<EPL, SIGMOID>(l, q, spare);
+    row_scores<EPL, SIGMOID, false>(l, q, none, inv, spare);
+    if (!on) inv = 0.0f;
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) acc[j] += on ? q[j] : 0.0f;
+    for (int j = 0; j < EPL; ++j) acc[j] = fmaf(q[j], inv, acc[j]);
     live += on;
   }
-  // the wave's four rows, then the waves
+  // The wave's four rows, then the waves.  A swap of two registers' halves and an add leave one's sum in either half.
+  if constexpr (EPL >= 4) {
 #pragma unroll
-  for (int j = 0; j < EPL; ++j) {
-    acc[j] += __shfl_xor(acc[j], 16);
-    acc[j] += __shfl_xor(acc[j], 32);
-    if (lane < 16) sums[wave][e0 + j] = acc[j];
+    for (int j = 0; j < EPL / 2; ++j) {
+      const auto v = __builtin_amdgcn_permlane32_swap(__float_as_uint(acc[j]), __float_as_uint(acc[j + EPL / 2]), false, false);
+      acc[j] = __uint_as_float(v[0]) + __uint_as_float(v[1]);
+    }
+#pragma unroll
+    for (int j = 0; j < EPL / 4; ++j) {
+      const auto v = __builtin_amdgcn_permlane16_swap(__float_as_uint(acc[j]), __float_as_uint(acc[j + EPL / 4]), false, false);
+      const float sum = __uint_as_float(v[0]) + __uint_as_float(v[1]);
+      const int mine = j + (lane & 32u ? EPL / 2 : 0) + (lane & 16u ? EPL / 4 : 0);
+      sums[wave][Place<EPL, BF16>::of(mine, l16)] = sum;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < EPL; ++j) {
+      acc[j] += __shfl_xor(acc[j], 16);
+      acc[j] += __shfl_xor(acc[j], 32);
+      if (lane < 16) sums[wave][Place<EPL, BF16>::of(j, l16)] = acc[j];
+    }
   }
   live += __shfl_xor(live, 16);
   live += __shfl_xor(live, 32);
   if (lane == 0) live_count[wave] = live;
   __syncthreads();
-  const int tokens = (live_count[0] + live_count[1]) + (live_count[2] + live_count[3]);
+  int tokens = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) tokens += live_count[w];
   const int64_t block = s * p.blocks + blockIdx.x;
   float loss = 0.0f;
-  for (int e = threadIdx.x; e < p.E; e += kThreads) {
-    const float sum = (sums[0][e] + sums[1][e]) + (sums[2][e] + sums[3][e]);
+  if (static_cast<int>(threadIdx.x) < p.E) {
+    const int e = threadIdx.x;
+    float sum = sums[0][e];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) sum += sums[w][e];
     if constexpr (ONE) {
       float prob;
-      loss += seq_term(hist[e], sum, tokens, p.E, p.k, prob);
+      loss = seq_term(hist[e], sum, tokens, p.E, p.k, prob);
       p.probs[e] = prob;
       p.counts[e] = hist[e];
     } else {
@@ -252,7 +326,9 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs p) {
     if (lane == 0) loss_part[wave] = loss;
     __syncthreads();
     if (threadIdx.x == 0) {
-      *p.loss = ((loss_part[0] + loss_part[1]) + (loss_part[2] + loss_part[3])) * p.scale;
+      loss = 0.0f;
+      for (int w = 0; w < kWaves; ++w) loss += loss_part[w];
+      *p.loss = loss * p.scale;
       *p.tokens = tokens;
     }
   } else if (threadIdx.x == 0) {
@@ -260,22 +336,24 @@ __global__ __launch_bounds__(kThreads) void balance_kernel(BalanceArgs p) {
   }
 }
 
-// A workgroup a sequence: 1024 / width threads an expert add the parts of every (1024 / width)-th workgroup.
-constexpr int kSumThreads = 1024;
-__global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(BalanceArgs p, int width) {
+// A workgroup has kSumColumns experts of a sequence, and every (1024 / kSumColumns)-th workgroup's part a thread.  The last
+// to finish adds the losses of all.
+constexpr int kSumThreads = 1024, kSumColumns = 32;
+__global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(BalanceArgs p) {
+  constexpr int kStep = kSumThreads / kSumColumns;
   __shared__ float sums[kSumThreads];
   __shared__ int32_t counts[kSumThreads];
-  __shared__ float loss_part[16];
   __shared__ int32_t token_part[16];
+  __shared__ float loss_part[16];
   __shared__ uint32_t arrived;
   const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
-  const int64_t s = blockIdx.x;
-  const int e = threadIdx.x & (width - 1), step = kSumThreads / width;
+  const int64_t s = blockIdx.y;
+  const int e = blockIdx.x * kSumColumns + threadIdx.x % kSumColumns;
   float sum = 0.0f;
   int count = 0, tokens = 0;
   if (e < p.E)
 #pragma unroll 4
-    for (int b = threadIdx.x / width; b < p.blocks; b += step) {
+    for (int b = threadIdx.x / kSumColumns; b < p.blocks; b += kStep) {
       sum += p.part_probs[(s * p.blocks + b) * p.E + e];
       count += p.part_counts[(s * p.blocks + b) * p.E + e];
     }
@@ -289,37 +367,31 @@ __global__ __launch_bounds__(kSumThreads) void balance_sum_kernel(BalanceArgs p,
   tokens = 0;
 #pragma unroll
   for (int w = 0; w < 16; ++w) tokens += token_part[w];
-  float loss = 0.0f;
-  if (static_cast<int>(threadIdx.x) < p.E) {
-    for (int g = 1; g < step; ++g) {
-      sum += sums[g * width + threadIdx.x];
-      count += counts[g * width + threadIdx.x];
+  if (wave == 0) {
+    float loss = 0.0f;
+    if (lane < kSumColumns && e < p.E) {
+#pragma unroll 8
+      for (int g = 1; g < kStep; ++g) {
+        sum += sums[g * kSumColumns + lane];
+        count += counts[g * kSumColumns + lane];
+      }
+      float prob;
+      loss = seq_term(count, sum, tokens, p.E, p.k, prob);
+      p.probs[s * p.E + e] = prob;
+      p.counts[s * p.E + e] = count;
     }
-    float prob;
-    loss = seq_term(count, sum, tokens, p.E, p.k, prob);
-    p.probs[s * p.E + threadIdx.x] = prob;
-    p.counts[s * p.E + threadIdx.x] = count;
-  }
-  loss = wave_sum(loss);
-  if (lane == 0) loss_part[wave] = loss;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    loss = 0.0f;
-    for (int w = 0; w < 16; ++w) loss += loss_part[w];
-    p.tokens[s] = tokens;
-    if (p.sequences == 1) {
-      *p.loss = loss * p.scale;
-    } else {
-      __hip_atomic_store(&p.part_loss[s], loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    loss = wave_sum(loss);
+    if (lane == 0) {
+      if (blockIdx.x == 0) p.tokens[s] = tokens;
+      __hip_atomic_store(&p.part_loss[s * gridDim.x + blockIdx.x], loss, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       arrived = __hip_atomic_fetch_add(p.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
     }
   }
-  if (p.sequences == 1) return;
   __syncthreads();
-  if (arrived != static_cast<uint32_t>(p.sequences) - 1) return;
-  // the last workgroup: every other one's loss is there
-  loss = 0.0f;
-  for (int64_t i = threadIdx.x; i < p.sequences; i += kSumThreads)
+  const uint32_t all = gridDim.x * gridDim.y;
+  if (arrived != all - 1) return;
+  float loss = 0.0f;
+  for (uint32_t i = threadIdx.x; i < all; i += kSumThreads)
     loss += __hip_atomic_load(&p.part_loss[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   loss = wave_sum(loss);
   if (lane == 0) loss_part[wave] = loss;
@@ -345,11 +417,10 @@ struct BalanceBwdArgs {
 
 template <int EPL, bool BF16, bool SIGMOID>
 __global__ __launch_bounds__(kThreads) void balance_backward_kernel(BalanceBwdArgs p) {
-  const int l16 = threadIdx.x & 15, e0 = l16 * EPL;
+  const int l16 = threadIdx.x & 15;
   const int64_t s = blockIdx.y, first = s * p.seq;
   int n[EPL];
-#pragma unroll
-  for (int j = 0; j < EPL; ++j) n[j] = e0 + j < p.E ? p.counts[s * p.E + e0 + j] : 0;
+  load_counts<EPL, BF16>(p.counts + s * p.E, l16, p.E, n);
   const int tokens = p.tokens[s];
   // (in 64 bits: N^2 may pass what 32 hold well)
   double c = tokens > 0 ? static_cast<double>(p.factor) / tokens / tokens : 0.0;
@@ -359,35 +430,35 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(BalanceBwdAr
     const int64_t i = t0 + (threadIdx.x >> 4);
     const bool exists = i < p.seq;
     const int64_t t = first + (exists ? i : p.seq - 1);
-    float l[EPL], q[EPL], d[EPL], spare;
-    load_row<EPL, BF16>(p.logits + t * p.row_bytes, e0, p.E, p.vec, kNegInf, l);
+    float l[EPL], q[EPL], slope[EPL], d[EPL], inv, spare;
+    load_row<EPL, BF16>(p.logits + t * p.row_bytes, l16, p.E, p.vec, kNegInf, l);
     if (p.din) {
-      load_row<EPL, BF16>(p.din + t * p.din_row_bytes, e0, p.E, p.vec_din, 0.0f, d);
+      load_row<EPL, BF16>(p.din + t * p.din_row_bytes, l16, p.E, p.vec_din, 0.0f, d);
     } else {
 #pragma unroll
       for (int j = 0; j < EPL; ++j) d[j] = 0.0f;
     }
     const bool on = row_ids(p.ids, t, p.k, p.E, l16, exists, nullptr);
-    const float top = row_probs<EPL, SIGMOID>(l, q, spare);
+    const float top = row_scores<EPL, SIGMOID, true>(l, q, slope, inv, spare);
     int ref = 0;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) ref = max(ref, l[j] == top ? n[j] : 0);
     ref = row_max(ref);
     float mean = 0.0f;  // of the counts, less ref
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) mean = fmaf(q[j], static_cast<float>(n[j] - ref), mean);
-    mean = row_sum(mean);
+    for (int j = 0; j < EPL; ++j) {
+      l[j] = static_cast<float>(n[j] - ref);
+      mean = fmaf(q[j], l[j], mean);
+    }
+    mean = row_sum(mean) * inv;
     if (SIGMOID) mean = fmaf(-spare, static_cast<float>(ref), mean);
+    const float factor = on ? cf * inv : 0.0f;
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
-      float g = cf * q[j] * (static_cast<float>(n[j] - ref) - mean);
-      if constexpr (SIGMOID) {
-        const float e = expf(-fabsf(l[j]));
-        g *= (l[j] > 0.0f ? e : 1.0f) / (1.0f + e);
-      }
-      if (on && l[j] != kNegInf) d[j] += g;
+      const float g = factor * q[j] * (l[j] - mean);
+      d[j] += SIGMOID ? g * slope[j] : g;
     }
-    if (exists) store_row<EPL, BF16>(p.out + t * p.out_row_bytes, e0, p.E, p.vec_out, d);
+    if (exists) store_row<EPL, BF16>(p.out + t * p.out_row_bytes, l16, p.E, p.vec_out, d);
   }
 }
 
@@ -396,16 +467,17 @@ int experts_per_lane(int64_t E) {
   while (16 * epl < E) epl *= 2;
   return epl;
 }
-bool rows_aligned16(const void *p, int64_t row_bytes) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && row_bytes % 16 == 0;
+// Whether rows of E elements of `es` bytes are 16-byte pieces.
+bool whole_pieces(const void *p, int64_t row_bytes, int64_t E, int es) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && row_bytes % 16 == 0 && E * es % 16 == 0;
 }
 
 // Tokens up to which one workgroup does all of it.
 constexpr int64_t kOneBlockTokens = 64;
 // Workgroups of a launch along the tokens, over all sequences.
 constexpr int64_t kForwardBlocks = 256, kBackwardBlocks = 2048;
-int64_t blocks_a_sequence(int64_t seq, int64_t sequences, int64_t most) {
-  const int64_t need = (seq + kRows - 1) / kRows, share = most / sequences;
+int64_t blocks_a_sequence(int64_t seq, int64_t sequences, int64_t rows, int64_t most) {
+  const int64_t need = (seq + rows - 1) / rows, share = most / sequences;
   const int64_t blocks = need < share ? need : share;
   return blocks > 1 ? blocks : 1;  // (without tokens a workgroup still writes zeros)
 }
@@ -413,9 +485,9 @@ template <int EPL, bool BF16, bool SIGMOID>
 hipError_t run_forward(const BalanceArgs &p, bool one, hipStream_t stream) {
   const dim3 grid(static_cast<uint32_t>(p.blocks), static_cast<uint32_t>(p.sequences));
   if (one)
-    balance_kernel<EPL, BF16, SIGMOID, true><<<grid, dim3(kThreads), 0, stream>>>(p);
+    balance_kernel<EPL, BF16, SIGMOID, true><<<grid, dim3(kSumsThreads), 0, stream>>>(p);
   else
-    balance_kernel<EPL, BF16, SIGMOID, false><<<grid, dim3(kThreads), 0, stream>>>(p);
+    balance_kernel<EPL, BF16, SIGMOID, false><<<grid, dim3(kSumsThreads), 0, stream>>>(p);
   return hipGetLastError();
 }
 template <int EPL>
@@ -431,14 +503,17 @@ hipError_t run_backward(const BalanceBwdArgs &p, int64_t sequences, bool bf16, b
   return hipGetLastError();
 }
 
+// Workgroups of a sequence's sums.
+int64_t sum_groups(int64_t experts) { return (experts + kSumColumns - 1) / kSumColumns; }
+
 bool one_block(int64_t tokens, int64_t sequences) { return sequences == 1 && tokens <= kOneBlockTokens; }
 
 }  // namespace
 
 size_t moe_balance_workspace_bytes(int64_t tokens, int64_t experts, int64_t sequences) {
   if (one_block(tokens, sequences)) return 0;
-  const int64_t blocks = sequences * blocks_a_sequence(tokens / sequences, sequences, kForwardBlocks);
-  return static_cast<size_t>(blocks * (2 * experts + 1) + sequences + 1) * 4;
+  const int64_t blocks = sequences * blocks_a_sequence(tokens / sequences, sequences, kSumsRows, kForwardBlocks);
+  return static_cast<size_t>(blocks * (2 * experts + 1) + sequences * sum_groups(experts) + 1) * 4;
 }
 
 hipError_t launch_moe_balance(const MoeBalanceArgs &a) {
@@ -450,7 +525,7 @@ hipError_t launch_moe_balance(const MoeBalanceArgs &a) {
   p.E = static_cast<int>(a.experts);
   p.k = a.top_k;
   p.sequences = static_cast<int>(a.sequences);
-  p.vec = rows_aligned16(a.logits, p.row_bytes);
+  p.vec = whole_pieces(a.logits, p.row_bytes, p.E, es);
   p.ids = a.ids;
   p.scale = a.coef / static_cast<float>(a.sequences);
   p.loss = a.loss;
@@ -458,14 +533,14 @@ hipError_t launch_moe_balance(const MoeBalanceArgs &a) {
   p.counts = a.counts;
   p.tokens = a.live;
   const bool one = one_block(a.tokens, a.sequences);
-  p.blocks = one ? 1 : static_cast<int>(blocks_a_sequence(p.seq, a.sequences, kForwardBlocks));
+  p.blocks = one ? 1 : static_cast<int>(blocks_a_sequence(p.seq, a.sequences, kSumsRows, kForwardBlocks));
   const int64_t blocks = p.sequences * static_cast<int64_t>(p.blocks);
   if (!one) {
     p.part_probs = static_cast<float *>(a.workspace);
     p.part_counts = reinterpret_cast<int32_t *>(p.part_probs + blocks * p.E);
     p.part_tokens = p.part_counts + blocks * p.E;
     p.part_loss = reinterpret_cast<float *>(p.part_tokens + blocks);
-    p.done = reinterpret_cast<uint32_t *>(p.part_loss + p.sequences);
+    p.done = reinterpret_cast<uint32_t *>(p.part_loss + p.sequences * sum_groups(p.E));
   }
   const bool bf16 = a.dtype == 1;
   hipError_t e;
@@ -478,9 +553,7 @@ hipError_t launch_moe_balance(const MoeBalanceArgs &a) {
     default: e = run_forward<32>(p, one, bf16, a.sigmoid, a.stream); break;
   }
   if (e != hipSuccess || one) return e;
-  int width = 64;
-  while (width < p.E) width *= 2;
-  balance_sum_kernel<<<dim3(static_cast<uint32_t>(p.sequences)), dim3(kSumThreads), 0, a.stream>>>(p, width);
+  balance_sum_kernel<<<dim3(static_cast<uint32_t>(sum_groups(p.E)), static_cast<uint32_t>(p.sequences)), dim3(kSumThreads), 0, a.stream>>>(p);
   return hipGetLastError();
 }
 
@@ -496,10 +569,10 @@ hipError_t launch_moe_balance_backward(const MoeBalanceArgs &a) {
   p.seq = a.tokens / a.sequences;
   p.E = static_cast<int>(a.experts);
   p.k = a.top_k;
-  p.blocks = static_cast<int>(blocks_a_sequence(p.seq, a.sequences, kBackwardBlocks));
-  p.vec = rows_aligned16(a.logits, p.row_bytes);
-  p.vec_din = rows_aligned16(a.dlogits_in, p.din_row_bytes);
-  p.vec_out = rows_aligned16(a.dlogits, p.out_row_bytes);
+  p.blocks = static_cast<int>(blocks_a_sequence(p.seq, a.sequences, kRows, kBackwardBlocks));
+  p.vec = whole_pieces(a.logits, p.row_bytes, p.E, es);
+  p.vec_din = whole_pieces(a.dlogits_in, p.din_row_bytes, p.E, es);
+  p.vec_out = whole_pieces(a.dlogits, p.out_row_bytes, p.E, es);
   p.ids = a.ids;
   p.counts = a.counts;
   p.tokens = a.live;

@@ -61,22 +61,29 @@ int check_grads(const void *const *grads, const int64_t *counts, const int32_t *
 }
 
 // Whether any two of the ranges of bytes that a clip reads or writes overlap, an in-place tensor being one range.
+struct Range {
+  uintptr_t lo, hi;
+};
+bool before(const Range &a, const Range &b) { return a.lo < b.lo; }
 int check_overlap(const void *const *grads, void *const *outs, const int64_t *counts, const int32_t *dtypes,
                   int64_t tensors) {
-  struct Range {
-    uintptr_t lo, hi;
-  };
   try {
-    std::vector<Range> all;
+    // (both lists are often in the order of their addresses already)
+    std::vector<Range> all, other;
     all.reserve(2 * tensors);
+    other.reserve(tensors);
     for (int64_t i = 0; i < tensors; ++i) {
       if (counts[i] == 0) continue;
       const uintptr_t bytes = static_cast<uintptr_t>(counts[i]) * dtype_size(dtypes[i]);
       const uintptr_t g = reinterpret_cast<uintptr_t>(grads[i]), o = reinterpret_cast<uintptr_t>(outs[i]);
       all.push_back({g, g + bytes});
-      if (o != g) all.push_back({o, o + bytes});
+      if (o != g) other.push_back({o, o + bytes});
     }
-    std::sort(all.begin(), all.end(), [](const Range &a, const Range &b) { return a.lo < b.lo; });
+    if (!std::is_sorted(all.begin(), all.end(), before)) std::sort(all.begin(), all.end(), before);
+    if (!std::is_sorted(other.begin(), other.end(), before)) std::sort(other.begin(), other.end(), before);
+    const size_t first = all.size();
+    all.insert(all.end(), other.begin(), other.end());
+    std::inplace_merge(all.begin(), all.begin() + first, all.end(), before);
     for (size_t i = 1; i < all.size(); ++i)
       if (all[i].lo < all[i - 1].hi) return NVFP4_ERR_UNSUPPORTED;
   } catch (const std::bad_alloc &) {

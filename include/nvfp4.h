@@ -403,7 +403,7 @@ enum {
   NVFP4_ADAPTER_BY_TOKEN = 1u << 1 /* x and c are in the tokens' own order: row r of the plan is row rows[r] of both  */
 };
 
-/* Bytes of device workspace of nvfp4_adapter / nvfp4_adapter_backward.  Needs no initialisation; calls that may overlap
+/* Bytes of device workspace of nvfp4_adapter / nvfp4_adapter_backward (0: it may be NULL).  Needs no initialisation; calls that may overlap
  * must use distinct workspaces. */
 size_t nvfp4_adapter_workspace_size(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters);
 size_t nvfp4_adapter_backward_workspace_size(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters);

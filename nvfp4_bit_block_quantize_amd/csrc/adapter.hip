@@ -331,6 +331,10 @@ struct ExpandArgs {
   int32_t R;
   const float *part;      // [splits][M][R]
   int32_t splits;
+  const uint8_t *x;       // OWN: as ShrinkArgs' y, f and K
+  int64_t ldx;            // bytes
+  const uint8_t *a;
+  int64_t K;
   const float *scales;
   float *h;               // nullable [M][R]: the splits' sums
   uint8_t *pieces;        // nullable [M][3 R] bf16: of scale * sum
@@ -377,17 +381,20 @@ __device__ void copy_rows(const ExpandArgs &p, int32_t tile, int64_t n0) {
   const int32_t first = lane / S::kPieces, col = lane % S::kPieces * S::kValues;
   for (int64_t n = n0 + 64 * wave + col; n < n1; n += 256) {
     if constexpr (VEC) {
-      uint4 v[NI];
+#pragma clang loop unroll(disable)
+      for (int i0 = 0; i0 < NI; i0 += 8) {
+        uint4 v[8];
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int32_t r = S::kRows * i + first;
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (p.base && (rows >> r & 1)) v[i] = load16<ONCE>(p.base + (static_cast<int64_t>(tile) * 64 + r) * p.ldb + n * ES);
-      }
+        for (int i = 0; i < 8; ++i) {
+          const int32_t r = S::kRows * (i0 + i) + first;
+          v[i] = make_uint4(0, 0, 0, 0);
+          if (p.base && (rows >> r & 1)) v[i] = load16<ONCE>(p.base + (static_cast<int64_t>(tile) * 64 + r) * p.ldb + n * ES);
+        }
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int32_t r = S::kRows * i + first;
-        if (rows >> r & 1) *reinterpret_cast<uint4 *>(p.c + (static_cast<int64_t>(tile) * 64 + r) * p.ldc + n * ES) = v[i];
+        for (int i = 0; i < 8; ++i) {
+          const int32_t r = S::kRows * (i0 + i) + first;
+          if (rows >> r & 1) *reinterpret_cast<uint4 *>(p.c + (static_cast<int64_t>(tile) * 64 + r) * p.ldc + n * ES) = v[i];
+        }
       }
     } else {
       for (int i = 0; i < NI; ++i) {
@@ -406,8 +413,9 @@ __device__ void copy_rows(const ExpandArgs &p, int32_t tile, int64_t n0) {
 // s RCP + rc, RCP the power of two that holds R / 8, and NM products of 32 cover a row.  As RCP is a power of two, these take UF
 // different fragments of the factor, again and again for each part.  Sums leave through the wave's own LDS, 16 rows at a time, in
 // whole segments (see Segment).
-template <int RCP, int TF, bool BF16, bool ONCE, bool VEC>
-__global__ __launch_bounds__(256, RCP <= 4 ? 4 : RCP == 8 ? 3 : 2) void expand_kernel(ExpandArgs p) {
+// OWN (16 rows): there are no splits; each workgroup forms its rows' h itself, a wave a quarter of K.
+template <int RCP, int TF, bool BF16, bool ONCE, bool VEC, bool OWN>
+__global__ __launch_bounds__(256, OWN ? 2 : RCP <= 8 ? 4 : 2) void expand_kernel(ExpandArgs p) {
   using S = Segment<BF16>;
   constexpr int ES = S::ES, PARTS = BF16 ? 2 : 3, NI = 16 * TF / S::kRows;
   constexpr int NM = (PARTS * RCP + 3) / 4, UF = RCP <= 4 ? 1 : RCP / 4;
@@ -415,6 +423,8 @@ __global__ __launch_bounds__(256, RCP <= 4 ? 4 : RCP == 8 ? 3 : 2) void expand_k
   __shared__ __attribute__((aligned(16))) uint8_t staged[16 * TF * kPitch];
   __shared__ floatx4 turned[4][16 * 16];
   __shared__ int32_t c_rows[16 * TF];  // -1: none
+  constexpr int RF = OWN ? (RCP + 1) / 2 : 1;
+  __shared__ floatx4 own[OWN ? 4 * 16 * 4 * RF : 1];  // [wave][row][16 RF values]
   const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, j = lane >> 4;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int32_t tm = blockIdx.x / p.tiles_n, tn = blockIdx.x - tm * p.tiles_n;
@@ -427,37 +437,9 @@ __global__ __launch_bounds__(256, RCP <= 4 ? 4 : RCP == 8 ? 3 : 2) void expand_k
     const int64_t r = t.m0 + threadIdx.x;
     c_rows[threadIdx.x] = static_cast<int32_t>(r < t.m_end ? c_row(p.rows, r) : -1);
   }
-  const float scale = p.scales[t.group];
-  for (int i = threadIdx.x; i < 16 * TF * RCP; i += 256) {
-    const int32_t m = i / RCP, rc = i % RCP;
-    const int64_t r = t.m0 + m;
-    const bool real = r < t.m_end && rc < RC;
-    float v[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-    if (real) {
-      sum_splits(p.part, p.rows.M, p.R, p.splits, r, 8 * rc, v);
-      if (p.h && tn == 0) store_h(p.h, p.R, r, 8 * rc, v);
-    }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= scale;
-    uint4 w[3];
-    split8(v, w);
-#pragma unroll
-    for (int s = 0; s < PARTS; ++s) *reinterpret_cast<uint4 *>(staged + m * kPitch + (s * RCP + rc) * 16) = w[s];
-    if (p.pieces && tn == 0 && real) {
-      uint4 *out = reinterpret_cast<uint4 *>(p.pieces + r * (6 * p.R)) + rc;
-      out[0] = w[0];
-      out[RC] = w[1];
-      out[2 * RC] = w[2];
-    }
-  }
-  __syncthreads();
-
   const uint32_t first = lane / S::kPieces, col = lane % S::kPieces * S::kValues;
-  floatx4 *const mine = turned[wave];
-  for (int64_t n0 = n_lo + 64 * wave; n0 < n_hi; n0 += 256) {
-    uint4 f[4][UF], b[NI];
+  uint4 f[4][UF], b[NI];
+  auto load = [&](int64_t n0) {
     const int64_t n = n0 + col;
     if constexpr (VEC) {
 #pragma unroll
@@ -477,8 +459,79 @@ __global__ __launch_bounds__(256, RCP <= 4 ? 4 : RCP == 8 ? 3 : 2) void expand_k
         if (rc < RC) f[u][i] = *reinterpret_cast<const uint4 *>(from + rc * 16);
       }
     }
+  };
+  const float scale = p.scales[t.group];
+  __syncthreads();  // c_rows
+  int64_t n0 = n_lo + 64 * wave;
+  if (TF == 1 && n0 < n_hi) load(n0);
+  if constexpr (OWN) {
+    const int64_t r = t.m0 + l16, y = r < t.m_end ? x_row(p.rows, r) : -1;
+    const uint8_t *a = p.a + static_cast<int64_t>(t.group) * p.R * p.K * 2;
+    floatx4 acc[RF];
+#pragma unroll
+    for (int u = 0; u < RF; ++u) acc[u] = (floatx4){0.0f, 0.0f, 0.0f, 0.0f};
+    // kBatch steps' loads in flight at once (steps are the same for every lane: matrix instructions want all)
+    constexpr int kBatch = 16 / RF;
+    const uint8_t *const zeros = reinterpret_cast<const uint8_t *>(&kZeros), *const x = p.x + (y >= 0 ? y : 0) * p.ldx;
+    for (int64_t k0 = 32 * wave; k0 < p.K; k0 += 128 * kBatch) {
+      uint4 v[kBatch], w[RF][kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int64_t k = k0 + 128 * i + 8 * j;
+        v[i] = *reinterpret_cast<const uint4 *>(y >= 0 && k < p.K ? x + k * 2 : zeros);
+#pragma unroll
+        for (int u = 0; u < RF; ++u)
+          w[u][i] = *reinterpret_cast<const uint4 *>(16 * u + static_cast<int>(l16) < p.R && k < p.K ? a + ((16 * u + l16) * p.K + k) * 2 : zeros);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+        for (int u = 0; u < RF; ++u) acc[u] = mfma(__builtin_bit_cast(bf16x8, w[u][i]), __builtin_bit_cast(bf16x8, v[i]), acc[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < RF; ++u) own[((wave * 16 + l16) * RF + u) * 4 + j] = acc[u];
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < 16 * TF * RCP; i += 256) {
+    const int32_t m = i / RCP, rc = i % RCP;
+    const int64_t r = t.m0 + m;
+    const bool real = r < t.m_end && rc < RC;
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = 0.0f;
+    if (real) {
+      if constexpr (OWN) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[e] += own[(w * 16 + m) * RF * 4 + 2 * rc + e / 4][e % 4];
+      } else {
+        sum_splits(p.part, p.rows.M, p.R, p.splits, r, 8 * rc, v);
+      }
+      if (p.h && tn == 0) store_h(p.h, p.R, r, 8 * rc, v);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] *= scale;
+    uint4 w[3];
+    split8(v, w);
+#pragma unroll
+    for (int s = 0; s < PARTS; ++s) *reinterpret_cast<uint4 *>(staged + m * kPitch + (s * RCP + rc) * 16) = w[s];
+    if (p.pieces && tn == 0 && real) {
+      uint4 *out = reinterpret_cast<uint4 *>(p.pieces + r * (6 * p.R)) + rc;
+      out[0] = w[0];
+      out[RC] = w[1];
+      out[2 * RC] = w[2];
+    }
+  }
+  __syncthreads();
+
+  floatx4 *const mine = turned[wave];
+  for (; n0 < n_hi; n0 += 256) {
+    const int64_t n = n0 + col;
+    if (TF > 1) load(n0);
 #pragma unroll
     for (int tf = 0; tf < TF; ++tf) {
+      if constexpr (RCP >= 4) asm volatile("" ::: "memory");  // (16 rows at a time: all rows' pieces in registers would spill)
       bf16x8 x[NM];
 #pragma unroll
       for (int i = 0; i < NM; ++i) {
@@ -531,6 +584,7 @@ __global__ __launch_bounds__(256, RCP <= 4 ? 4 : RCP == 8 ? 3 : 2) void expand_k
         }
       }
     }
+    if (TF == 1 && n0 + 256 < n_hi) load(n0 + 256);
   }
 }
 
@@ -802,8 +856,17 @@ int64_t tiles_for(const AdapterArgs &a, int64_t size) {
 // Rows of a workgroup that adds to many rows of c: what a lane holds of base's rows is then the same for both types.
 template <bool BF16>
 constexpr int kExpandRows = BF16 ? 64 : 32;
-// Workgroups of the launch that adds to c, about: four a compute unit.
-constexpr int64_t kExpandGroups = 1024;
+// Workgroups of the launch that adds to c, at least, where there is work for them (8192 x 14336 of rank 16: 1806 take 75 us, 903 87,
+// 7224 81; of rank 64 92, 108 and 99).
+constexpr int64_t kExpandGroups = 1536;
+
+// A few rows of low rank: one launch, in which each workgroup forms its rows' h by itself, as long as every workgroup has a
+// compute unit and A is read in about the time of a launch.  (One row of 4096 x 14336: see the figures at expand_kernel.)
+constexpr int32_t kOwnRank = 32;
+bool own_h(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters) {
+  const int64_t tiles = adapters == 1 ? (M + 15) / 16 : (M < adapters ? M : adapters) + M / 16;
+  return rank <= kOwnRank && rank * K <= (1 << 17) && tiles * ((N + 255) / 256) <= 256;
+}
 
 // Few rows an adapter: 16 rows a tile.
 bool few_rows(int64_t M, int64_t adapters) { return M <= 256 || M <= 16 * adapters; }
@@ -865,14 +928,23 @@ template <int RCP, bool BF16>
 hipError_t run_expand(const ExpandArgs &p, bool few, bool vec, uint32_t groups, hipStream_t stream) {
   constexpr int TF = kExpandRows<BF16> / 16;
   const bool once = p.base && 2 * p.rows.M * p.N * (BF16 ? 2 : 4) >= kStreamBytes;
-  if (!vec)
-    expand_kernel<RCP, 1, BF16, false, false><<<dim3(groups), dim3(256), 0, stream>>>(p);
-  else if (few)
-    expand_kernel<RCP, 1, BF16, false, true><<<dim3(groups), dim3(256), 0, stream>>>(p);
-  else if (once)
-    expand_kernel<RCP, TF, BF16, true, true><<<dim3(groups), dim3(256), 0, stream>>>(p);
-  else
-    expand_kernel<RCP, TF, BF16, false, true><<<dim3(groups), dim3(256), 0, stream>>>(p);
+  const dim3 grid(groups), threads(256);
+  if (p.a) {
+    if constexpr (RCP <= kOwnRank / 8) {
+      if (vec)
+        expand_kernel<RCP, 1, BF16, false, true, true><<<grid, threads, 0, stream>>>(p);
+      else
+        expand_kernel<RCP, 1, BF16, false, false, true><<<grid, threads, 0, stream>>>(p);
+    }
+  } else if (!vec) {
+    expand_kernel<RCP, 1, BF16, false, false, false><<<grid, threads, 0, stream>>>(p);
+  } else if (few) {
+    expand_kernel<RCP, 1, BF16, false, true, false><<<grid, threads, 0, stream>>>(p);
+  } else if (once) {
+    expand_kernel<RCP, TF, BF16, true, true, false><<<grid, threads, 0, stream>>>(p);
+  } else {
+    expand_kernel<RCP, TF, BF16, false, true, false><<<grid, threads, 0, stream>>>(p);
+  }
   return hipGetLastError();
 }
 template <bool BF16>
@@ -887,7 +959,7 @@ hipError_t run_expand(const AdapterArgs &a, const void *f, int64_t N, float *par
                       const void *base, int64_t ldb, void *c, int64_t ldc, int dtype) {
   ExpandArgs p{};
   const int64_t es = dtype == 1 ? 2 : 4;
-  const bool few = few_rows(a.M, a.adapters);
+  const bool few = !part || few_rows(a.M, a.adapters);
   p.rows = rows_of(a);
   p.pos = a.pos;
   p.f = static_cast<const uint8_t *>(f);
@@ -895,6 +967,12 @@ hipError_t run_expand(const AdapterArgs &a, const void *f, int64_t N, float *par
   p.R = a.rank;
   p.part = part;
   p.splits = splits;
+  if (!part) {
+    p.x = static_cast<const uint8_t *>(a.x);
+    p.ldx = a.ldx * 2;
+    p.a = static_cast<const uint8_t *>(a.a);
+    p.K = a.K;
+  }
   p.scales = a.scales;
   p.h = h;
   p.pieces = pieces;
@@ -911,7 +989,7 @@ hipError_t run_expand(const AdapterArgs &a, const void *f, int64_t N, float *par
   const int64_t steps = (N + 255) / 256, tiles = (a.M + tile_rows - 1) / tile_rows;
   const int64_t used = few && a.offsets ? (a.M < a.adapters ? a.M : a.adapters) : 0;  // at most so many tiles in use
   int64_t each = steps * (tiles > used ? tiles : used) / kExpandGroups;
-  if (each < 1) each = 1;
+  if (each < 1 || !part) each = 1;
   if (each > steps) each = steps;
   // the splits are summed first where each workgroup's own sums would read more than a quarter of what it moves of c
   if (!few && splits > 1 && splits * p.R * 4 * 4 > each * 256 * 2 * es) {
@@ -973,8 +1051,10 @@ struct Layout {
 };
 struct ForwardLayout {
   size_t part, size;
-  ForwardLayout(int64_t M, int64_t K, int64_t R, int64_t adapters) {
+  ForwardLayout(int64_t M, int64_t N, int64_t K, int32_t R, int32_t adapters) {
     Layout l;
+    part = size = 0;
+    if (own_h(M, N, K, R, adapters)) return;
     // (as large for gathered rows as for others)
     const int64_t own = splits_for(M, adapters, K, false), gathered = splits_for(M, adapters, K, true);
     part = l.take((own > gathered ? own : gathered) * M * R * 4);
@@ -998,8 +1078,8 @@ struct BackwardLayout {
 
 }  // namespace
 
-size_t adapter_workspace_bytes(int64_t M, int64_t K, int32_t rank, int32_t adapters) {
-  return ForwardLayout(M, K, rank, adapters).size;
+size_t adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters) {
+  return ForwardLayout(M, N, K, rank, adapters).size;
 }
 size_t adapter_backward_workspace_bytes(const AdapterArgs &a) { return BackwardLayout(a).size; }
 
@@ -1017,7 +1097,9 @@ bool adapter_launches(const AdapterArgs &a, bool backward) {
 }
 
 hipError_t launch_adapter(const AdapterArgs &a) {
-  const ForwardLayout l(a.M, a.K, a.rank, a.adapters);
+  if (own_h(a.M, a.N, a.K, a.rank, a.adapters))
+    return run_expand(a, a.b, a.N, nullptr, 0, a.h, nullptr, a.base, a.ldb, a.c, a.ldc, a.c_dtype);
+  const ForwardLayout l(a.M, a.N, a.K, a.rank, a.adapters);
   uint8_t *const w = static_cast<uint8_t *>(a.workspace);
   float *const part = reinterpret_cast<float *>(w + l.part);
   int32_t splits;

@@ -234,7 +234,7 @@ struct AdapterArgs {
 // Each returns hipSuccess or the launch error.
 hipError_t launch_adapter(const AdapterArgs &a);
 hipError_t launch_adapter_backward(const AdapterArgs &a);
-size_t adapter_workspace_bytes(int64_t M, int64_t K, int32_t rank, int32_t adapters);
+size_t adapter_workspace_bytes(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters);
 size_t adapter_backward_workspace_bytes(const AdapterArgs &a);
 bool adapter_launches(const AdapterArgs &a, bool backward);
 hipError_t launch_moe_balance(const MoeBalanceArgs &a);

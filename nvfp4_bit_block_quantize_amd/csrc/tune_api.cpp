@@ -153,7 +153,7 @@ bool adapter_sizes(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapte
 extern "C" {
 
 size_t nvfp4_adapter_workspace_size(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters) {
-  return adapter_sizes(M, N, K, rank, adapters) ? (nvfp4::adapter_workspace_bytes(M, K, rank, adapters) + 15) / 16 * 16 : 0;
+  return adapter_sizes(M, N, K, rank, adapters) ? (nvfp4::adapter_workspace_bytes(M, N, K, rank, adapters) + 15) / 16 * 16 : 0;
 }
 
 size_t nvfp4_adapter_backward_workspace_size(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters) {
@@ -183,7 +183,7 @@ int nvfp4_adapter(const void *x, int x_dtype, int64_t x_rows, int64_t ldx, const
   p.h = h;
   p.workspace = workspace;
   p.stream = static_cast<hipStream_t>(hip_stream);
-  if ((st = check_adapter_pointers(p, c_dtype, nvfp4::adapter_workspace_bytes(M, K, rank, adapters))) != NVFP4_OK) return st;
+  if ((st = check_adapter_pointers(p, c_dtype, nvfp4::adapter_workspace_bytes(M, N, K, rank, adapters))) != NVFP4_OK) return st;
   return status_of(nvfp4::launch_adapter(p));
 }
 

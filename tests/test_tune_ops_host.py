@@ -87,7 +87,7 @@ def test_grad_clip():
     assert _clip(good, outs=[P + 4, P + 4096]) == UNSUPPORTED
 
 
-ADAPTER = dict(x=P, x_dtype=nv.NVFP4_BF16, x_rows=80, ldx=64, a=P, b=P, scales=P, M=80, N=40, K=64, rank=16, adapters=3, offsets=P,
+ADAPTER = dict(x=P, x_dtype=nv.NVFP4_BF16, x_rows=80, ldx=64, a=P, b=P, scales=P, M=80, N=40, K=64, rank=48, adapters=3, offsets=P,
                rows=P, pos=P, row_div=1, flags=nv.NVFP4_ADAPTER_BY_TOKEN, base=P, ldb=40, c=P + 4096, c_dtype=nv.NVFP4_BF16, ldc=40, h=P,
                workspace=P, stream=None)
 ABWD = dict(dc=P, dc_dtype=nv.NVFP4_BF16, lddc=40, x=P, x_dtype=nv.NVFP4_BF16, ldx=64, a=P, b=P, scales=P, M=80, N=40, K=64, rank=16,
@@ -127,7 +127,7 @@ def test_workspace_sizes():
     assert L.nvfp4_moe_balance_workspace_size(64, 64, 2) > 0 and L.nvfp4_moe_balance_workspace_size(64, 0, 1) == 0
     assert L.nvfp4_grad_workspace_size(1, 1) == 16 and L.nvfp4_grad_workspace_size(-1, 1) == 0
     assert L.nvfp4_grad_workspace_size(3, 1 << 40) <= 2048 * 8
-    assert L.nvfp4_adapter_workspace_size(4, 64, 512, 16, 2) >= 4 * 16 * 4 and L.nvfp4_adapter_workspace_size(4, 64, 512, 0, 2) == 0
+    assert L.nvfp4_adapter_workspace_size(4, 64, 512, 64, 2) >= 4 * 64 * 4 and L.nvfp4_adapter_workspace_size(4, 64, 512, 0, 2) == 0
     assert L.nvfp4_adapter_backward_workspace_size(4, 64, 512, 16, 2) >= 2 * 2 * 16 * (64 + 512)
     assert L.nvfp4_adapter_backward_workspace_size(-1, 64, 512, 16, 2) == 0
 

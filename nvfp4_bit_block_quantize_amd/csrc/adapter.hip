@@ -614,11 +614,11 @@ struct OuterArgs {
 // stay in registers, and each step the waves share out rows 0 to 15 and 16 to 31 with each fragment of f (of a rank of 16
 // there is one, and two waves take it).
 constexpr int kOuterStep = 32, kMaxChunk = 960, kOuterThreads = 512;
-// The ring's stages: two workgroups a compute unit share its 160 KB of LDS up to a rank of 32, else one has them.
+// The ring's stages: two workgroups a compute unit share its 160 KB of LDS up to a rank of 64, above it one has them.
 template <int RF>
-constexpr int kOuterStages = RF == 1 ? 4 : RF == 4 ? 5 : 3;
+constexpr int kOuterStages = RF == 1 ? 4 : RF == 4 ? 2 : 3;
 template <int RF, bool G>
-__global__ __launch_bounds__(kOuterThreads) void outer_kernel(OuterArgs p) {
+__global__ __launch_bounds__(kOuterThreads, RF <= 4 ? 4 : 2) void outer_kernel(OuterArgs p) {
   constexpr int S = kOuterStages<RF>;
   constexpr int kY = kOuterStep * 512, kStage = kY + kOuterStep * 96 * RF;
   // loads of pieces a step: 3 RF of 1 KB (R = 16 RF at most), NP for every wave and one more for the first `rest` waves
@@ -660,6 +660,9 @@ __global__ __launch_bounds__(kOuterThreads) void outer_kernel(OuterArgs p) {
   __syncthreads();  // (the ring takes f's place; y_rows are there)
   const int32_t RC3 = 3 * p.R / 8;                 // 16-byte chunks of a row of pieces
   const int32_t pitch = RC3 * 16;
+  // 32-byte unit u of row t of the pieces sits at u + turn(t) modulo their number, where a row is whole units
+  const int32_t units = p.R % 16 == 0 ? 3 * p.R / 16 : 0;
+  auto turn = [](uint32_t row) { return static_cast<int32_t>(((row & 3u) >> 1) + ((row >> 3) & 1u) * 2u); };
   const int32_t steps = static_cast<int32_t>((t.m_end - t.m0 + kOuterStep - 1) / kOuterStep);
   // y: wave w loads rows [4 w, 4 w + 4), two a load; lane: row lane >> 5, position lane & 31
   uint32_t col[2];
@@ -675,6 +678,11 @@ __global__ __launch_bounds__(kOuterThreads) void outer_kernel(OuterArgs p) {
     const int32_t at = (8 * i + wave) * 64 + lane;
     prow[i] = at / RC3;
     pchunk[i] = at - prow[i] * RC3;
+    if (units) {
+      int32_t u = (pchunk[i] >> 1) - turn(prow[i]);
+      if (u < 0) u += units;
+      pchunk[i] = 2 * u + (pchunk[i] & 1);
+    }
   }
   auto load = [&](int32_t kt) {
     uint8_t *st = smem + (kt % S) * kStage;
@@ -711,7 +719,8 @@ __global__ __launch_bounds__(kOuterThreads) void outer_kernel(OuterArgs p) {
     load(kt + S - 1);
     uint8_t *st = smem + (kt % S) * kStage;
     bf16x8 y[2];
-    const uint32_t T = 8 * j + (l16 >> 2);  // (row T + 4 has the same swizzle)
+    const uint32_t T = 8 * j + (l16 >> 2);  // (row T + 4 has the same swizzle and turn)
+    const int32_t mine = turn(T);
     const uint32_t sw = (T & 3u) | ((T >> 1) & 4u);
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
@@ -722,7 +731,9 @@ __global__ __launch_bounds__(kOuterThreads) void outer_kernel(OuterArgs p) {
     for (int s = 0; s < 3; ++s)
 #pragma unroll
       for (int u = 0; u < RF; ++u) {
-        const uint8_t *at = st + kY + T * pitch + (s * p.R + 16 * u + 4 * (l16 & 3u)) * 2;
+        int32_t unit = s * (p.R / 16) + u + mine;
+        unit = unit >= units ? unit - units : unit;
+        const uint8_t *at = st + kY + T * pitch + (units ? unit * 32 : (s * p.R + 16 * u) * 2) + (l16 & 3u) * 8;
         const bf16x8 a = pair(tr(at), tr(at + 4 * pitch));
 #pragma unroll
         for (int v = 0; v < 2; ++v) acc[u][v] = mfma(a, y[v], acc[u][v]);
@@ -807,28 +818,45 @@ __global__ __launch_bounds__(256) void outer_sum_kernel(OuterSumArgs a, OuterSum
 }
 
 // ---- before a backward pass: a transposed factor, and the pieces of h -------------------------------------------
-// out[g][c][r] = in[g][r][c], [rows x cols] bf16 with cols a multiple of 8 and one of the two at most 128; 64 x 64 tiles.
+// out[g][c][r] = in[g][r][c], [rows x cols] bf16 with rows and cols multiples of 8; 64 x 64 tiles, 16 bytes a thread both ways.
 struct TransposeArgs {
   const uint16_t *in;
   uint16_t *out;
   int64_t rows, cols;
   int32_t tiles_r, tiles_c;
 };
-__device__ void transpose_tile(const TransposeArgs &p, int64_t id, uint16_t (&lds)[64][66]) {
+constexpr int kTurnPitch = 66;  // elements of a row in LDS: eight rows of one column lie in different banks
+__device__ void transpose_tile(const TransposeArgs &p, int64_t id, uint16_t (&lds)[64 * kTurnPitch]) {
   const int64_t per = static_cast<int64_t>(p.tiles_r) * p.tiles_c, g = id / per;
   const int32_t in_g = static_cast<int32_t>(id - g * per), tr = in_g / p.tiles_c, tc = in_g - tr * p.tiles_c;
   const int64_t r0 = tr * 64ll, c0 = tc * 64ll;
   const uint16_t *in = p.in + g * p.rows * p.cols;
   uint16_t *out = p.out + g * p.rows * p.cols;
-  const int32_t lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int i = wave; i < 64; i += 4)
-    if (r0 + i < p.rows && c0 + lane < p.cols) lds[i][lane] = in[(r0 + i) * p.cols + c0 + lane];
+#pragma unroll
+  for (int i = threadIdx.x; i < 512; i += 256) {
+    const int r = i / 8, c = i % 8 * 8;
+    if (r0 + r >= p.rows || c0 + c >= p.cols) continue;
+    const uint4 v = *reinterpret_cast<const uint4 *>(in + (r0 + r) * p.cols + c0 + c);
+    uint32_t *at = reinterpret_cast<uint32_t *>(&lds[r * kTurnPitch + c]);
+    at[0] = v.x;
+    at[1] = v.y;
+    at[2] = v.z;
+    at[3] = v.w;
+  }
   __syncthreads();
-  for (int i = wave; i < 64; i += 4)
-    if (c0 + i < p.cols && r0 + lane < p.rows) out[(c0 + i) * p.rows + r0 + lane] = lds[lane][i];
+#pragma unroll
+  for (int i = threadIdx.x; i < 512; i += 256) {
+    const int c = i / 8, r = i % 8 * 8;
+    if (r0 + r >= p.rows || c0 + c >= p.cols) continue;
+    uint32_t w[4];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      w[q] = lds[(r + 2 * q) * kTurnPitch + c] | static_cast<uint32_t>(lds[(r + 2 * q + 1) * kTurnPitch + c]) << 16;
+    *reinterpret_cast<uint4 *>(out + (c0 + c) * p.rows + r0 + r) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 __global__ __launch_bounds__(256) void adapter_prep_kernel(TransposeArgs a, int64_t blocks_a, FinishArgs h) {
-  __shared__ uint16_t lds[64][66];
+  __shared__ __attribute__((aligned(16))) uint16_t lds[64 * kTurnPitch];
   if (blockIdx.x < blocks_a)
     transpose_tile(a, blockIdx.x, lds);
   else
@@ -858,7 +886,7 @@ template <bool BF16>
 constexpr int kExpandRows = BF16 ? 64 : 32;
 // Workgroups of the launch that adds to c, at least, where there is work for them (8192 x 14336 of rank 16: 1806 take 75 us, 903 87,
 // 7224 81; of rank 64 92, 108 and 99).
-constexpr int64_t kExpandGroups = 1536;
+constexpr int64_t kExpandGroups = 1536, kFewGroups = 1024;
 
 // A few rows of low rank: one launch, in which each workgroup forms its rows' h by itself, as long as every workgroup has a
 // compute unit and A is read in about the time of a launch.  (One row of 4096 x 14336: see the figures at expand_kernel.)
@@ -988,7 +1016,7 @@ hipError_t run_expand(const AdapterArgs &a, const void *f, int64_t N, float *par
   // as many steps of 256 columns a workgroup as leave kExpandGroups workgroups
   const int64_t steps = (N + 255) / 256, tiles = (a.M + tile_rows - 1) / tile_rows;
   const int64_t used = few && a.offsets ? (a.M < a.adapters ? a.M : a.adapters) : 0;  // at most so many tiles in use
-  int64_t each = steps * (tiles > used ? tiles : used) / kExpandGroups;
+  int64_t each = steps * (tiles > used ? tiles : used) / (few ? kFewGroups : kExpandGroups);
   if (each < 1 || !part) each = 1;
   if (each > steps) each = steps;
   // the splits are summed first where each workgroup's own sums would read more than a quarter of what it moves of c
@@ -1008,16 +1036,21 @@ hipError_t run_expand(const AdapterArgs &a, const void *f, int64_t N, float *par
 }
 
 // Rows of a workgroup of the factors' gradients: the workgroups are to come near a multiple of those that run at once, two a
-// compute unit or, of ranks above 32, one (for 56 column tiles and 8192 rows: 504 workgroups of 928 rows and not 896 of 512,
-// which leave a quarter of the second round idle), and have at least 64 rows.
-int32_t outer_chunk(int64_t M, int64_t N, int32_t rank) {
-  const int64_t tiles_n = (N + 255) / 256, slots = rank <= 32 ? 512 : 256;
-  int64_t rounds = 1, n;
+// compute unit or, of ranks above 64, one (for 56 column tiles and 8192 rows: 504 workgroups of 928 rows and not 896 of 512,
+// which leave a quarter of the second round idle; each further adapter is counted as a partial tile).  Workgroups of few rows
+// write and read more partial sums than rows of y: four times the rank makes them equal, and from twice the rank on more
+// workgroups gain more (2047 rows of 4096 and rank 64: 24.6 us with at least 256 rows, 20.4 with 128).
+int32_t outer_chunk(int64_t M, int64_t N, int32_t rank, int32_t adapters) {
+  const int64_t tiles_n = (N + 255) / 256, slots = rank <= 64 ? 512 : 256;
+  int64_t rounds = 1, n, chunk;
   do {
-    n = rounds++ * slots / tiles_n;
-  } while (n < 1 || (M + n - 1) / n > kMaxChunk);
-  const int64_t chunk = ((M + n - 1) / n + kOuterStep - 1) / kOuterStep * kOuterStep;
-  return static_cast<int32_t>(chunk < 64 ? 64 : chunk);
+    n = rounds++ * slots / tiles_n - (adapters - 1);
+    if (n < 1) n = 1;
+    chunk = (M + n - 1) / n;
+  } while (chunk > kMaxChunk && rounds <= 64);
+  const int64_t least = 2 * rank > 64 ? 2 * rank : 64;
+  chunk = (chunk + kOuterStep - 1) / kOuterStep * kOuterStep;
+  return static_cast<int32_t>(chunk < least ? least : chunk > kMaxChunk ? kMaxChunk : chunk);
 }
 template <int RF>
 hipError_t run_outer(const OuterArgs &p, uint32_t groups, hipStream_t stream) {
@@ -1031,7 +1064,7 @@ hipError_t run_outer(const AdapterArgs &a, OuterArgs p) {
   p.rows = rows_of(a);
   p.ldy *= 2;
   p.R = a.rank;
-  p.chunk = outer_chunk(a.M, p.N, a.rank);
+  p.chunk = outer_chunk(a.M, p.N, a.rank, a.adapters);
   p.tiles_n = static_cast<int32_t>((p.N + 255) / 256);
   const uint32_t groups = static_cast<uint32_t>(p.tiles_n * tiles_for(a, p.chunk));
   if (a.rank <= 16) return run_outer<1>(p, groups, a.stream);
@@ -1070,8 +1103,8 @@ struct BackwardLayout {
     h_pieces = l.take(a.M * a.rank * 6);
     part = l.take((a.N + 255) / 256 * a.M * a.rank * 4);
     g_pieces = l.take(a.M * a.rank * 6);
-    da_part = l.take(tiles_for(a, outer_chunk(a.M, a.K, a.rank)) * a.K * a.rank * 4);
-    db_part = l.take(tiles_for(a, outer_chunk(a.M, a.N, a.rank)) * a.N * a.rank * 4);
+    da_part = l.take(tiles_for(a, outer_chunk(a.M, a.K, a.rank, a.adapters)) * a.K * a.rank * 4);
+    db_part = l.take(tiles_for(a, outer_chunk(a.M, a.N, a.rank, a.adapters)) * a.N * a.rank * 4);
     size = l.at;
   }
 };
@@ -1147,7 +1180,7 @@ hipError_t launch_adapter_backward(const AdapterArgs &a) {
     o.out = a.da;
     if ((e = run_outer(a, o)) != hipSuccess) return e;
   }
-  OuterSumArgs sa{rows, outer_chunk(a.M, a.K, a.rank), a.K * a.rank, 0, da_part, a.da}, sb{rows, outer_chunk(a.M, a.N, a.rank), a.N * a.rank, 0, db_part, a.db};
+  OuterSumArgs sa{rows, outer_chunk(a.M, a.K, a.rank, a.adapters), a.K * a.rank, 0, da_part, a.da}, sb{rows, outer_chunk(a.M, a.N, a.rank, a.adapters), a.N * a.rank, 0, db_part, a.db};
   sa.blocks = static_cast<int32_t>((sa.size + kOuterSumSize - 1) / kOuterSumSize);
   sb.blocks = static_cast<int32_t>((sb.size + kOuterSumSize - 1) / kOuterSumSize);
   const int64_t na = static_cast<int64_t>(a.adapters) * sa.blocks, nb = static_cast<int64_t>(a.adapters) * sb.blocks;

@@ -5,7 +5,8 @@
 One block is: the norm before it (fused with the previous block's output norm, gate and residual scale), the
 router's logits (a plain matrix product), nvfp4_moe_route with its plan, the experts' two products with their
 rows read through the plan, and nvfp4_moe_combine.  `train_step` runs the same block's router, sum and norms
-forward and backward, with the experts' products as fixed linear maps.
+forward and backward, with the experts' products as fixed linear maps.  `finetune_step` trains low-rank adapters beside the
+experts' frozen 8-bit products, and the router with its balance loss, and clips their gradients.
 """
 from __future__ import annotations
 
@@ -85,6 +86,57 @@ class MoEBlock:
         grads = nv.nvfp4_block_norm_backward(None, dn, x, y, f.rstd_post, f.rstd_pre, w_post=self.w_post, gate=self.gate,
                                              w_pre=self.w_pre, alpha=self.alpha)
         return out, grads, drouter, (ids, dn)
+
+    def add_adapters(self, rank=16, seed=1):
+        """An adapter for each expert's two products (of a trained one: neither factor is zero), and the products' transposes
+        for the gradients of their inputs, laid out once."""
+        g = torch.Generator(device=self.up.device).manual_seed(seed)
+        E, d, hidden = self.experts, self.d, self.hidden
+
+        def adapters(n, k):
+            a = (torch.randn(E * rank, k, generator=g, device=self.up.device) * k ** -0.5).to(torch.bfloat16)
+            b = (torch.randn(E * n, rank, generator=g, device=self.up.device) * 0.3 * rank ** -0.5).to(torch.bfloat16)
+            return nv.Adapters(a, b, torch.ones(E, device=self.up.device), rank, k, n, E)
+
+        self.up_adapters, self.down_adapters = adapters(2 * hidden, d), adapters(d, hidden)
+        turned = lambda w, n: w.view(E, n, -1).transpose(1, 2).reshape(-1, n).contiguous()
+        q, s = nv.nvfp4_int8_quantize(turned(self.up, 2 * hidden)), nv.nvfp4_int8_quantize(turned(self.down, d))
+        self.up8_t = nv.Int8Tensor(q.data, q.scales, d, 2 * hidden, E)
+        self.down8_t = nv.Int8Tensor(s.data, s.scales, hidden, d, E)
+
+    def finetune_step(self, x, y, dout, coef=0.01, max_norm=1.0):
+        """Loss sum(out * dout) + balance loss: (out, MoEBalance, gradient norm, clipped gradients of the down and up
+        adapters' factors and of the router, gradients of the norms)."""
+        f = nv.nvfp4_block_norm(x, y, w_post=self.w_post, gate=self.gate, w_pre=self.w_pre, alpha=self.alpha)
+        logits, ids, weights, plan = self.route(f.n)
+        balance = nv.nvfp4_moe_balance(logits, ids, coef, flags=self.route_flags)
+        rows = nv.nvfp4_moe_gather(f.n, plan)
+        u = nv.nvfp4_int8_gemm(nv.nvfp4_int8_quantize(rows), self.up8, plan=plan)
+        u, h_up = nv.nvfp4_adapter(rows, self.up_adapters, u, plan=plan, with_h=True, out=u)
+        a, b = u.float().split(self.hidden, dim=1)
+        s = torch.sigmoid(a)
+        z = (a * s * b).to(u.dtype)
+        v = nv.nvfp4_int8_gemm(nv.nvfp4_int8_quantize(z), self.down8, plan=plan)
+        v, h_down = nv.nvfp4_adapter(z, self.down_adapters, v, plan=plan, with_h=True, out=v)
+        out = nv.nvfp4_moe_combine(v, plan, weights)
+
+        dv, dweights = nv.nvfp4_moe_combine_backward(dout, v, plan, weights)
+        dz = nv.nvfp4_int8_gemm(nv.nvfp4_int8_quantize(dv), self.down8_t, plan=plan)
+        down = nv.nvfp4_adapter_backward(dv, z, self.down_adapters, h_down, dx_base=dz, plan=plan, dx=dz)
+        dz = down.dx.float()
+        du = torch.cat([dz * b * s * (1 + a * (1 - s)), dz * a * s], dim=1).to(u.dtype)
+        drows = nv.nvfp4_int8_gemm(nv.nvfp4_int8_quantize(du), self.up8_t, plan=plan)
+        up = nv.nvfp4_adapter_backward(du, rows, self.up_adapters, h_up, dx_base=drows, plan=plan, dx=drows)
+        dn = nv.nvfp4_moe_combine(up.dx, plan)
+        dlogits = nv.nvfp4_moe_route_backward(logits, ids, dweights, flags=self.route_flags, scale=self.scale)
+        dlogits = nv.nvfp4_moe_balance_backward(logits, ids, balance, coef, flags=self.route_flags, dlogits=dlogits, out=dlogits)
+        drouter = dlogits.t() @ f.n.float()
+        dn = (dn.float() + dlogits @ self.router.float()).to(f.n.dtype)
+        norms = nv.nvfp4_block_norm_backward(None, dn, x, y, f.rstd_post, f.rstd_pre, w_post=self.w_post, gate=self.gate,
+                                             w_pre=self.w_pre, alpha=self.alpha)
+        grads = [down.da, down.db, up.da, up.db, drouter]
+        norm = nv.nvfp4_grad_clip(grads, max_norm)
+        return out, balance, norm, grads, norms
 
     def plain(self, x, y):
         """The block in fp32 tensor operations, without any rounding of weights or activations."""

@@ -425,7 +425,7 @@ size_t nvfp4_adapter_backward_workspace_size(int64_t M, int64_t N, int64_t K, in
  * adapter are then not touched; otherwise it overlaps no input.
  * h: nullable device float [M][rank], the rows' h in the plan's order, for the backward call (rows behind
  * offsets[adapters] are not written).
- * rank a multiple of 8, 8 .. 128; adapters 1 .. 512; K a positive multiple of 8, K < 2^31; N >= 1, N < 2^31 (else
+ * rank a multiple of 8, 8 .. 128; adapters 1 .. 512; K a positive multiple of 8, N >= 1, both at most 2^24 (else
  * NVFP4_ERR_SHAPE); a launch of 2^31 threads or more is refused (NVFP4_ERR_SHAPE: about 2^34 elements of c).  x, a, b and h 16-byte aligned, ldx a multiple of 8; base and c
  * aligned to their elements.  workspace: device, nvfp4_adapter_workspace_size() bytes, 16-byte aligned. */
 int nvfp4_adapter(const void *x, int x_dtype, int64_t x_rows, int64_t ldx, const void *a, const void *b,

@@ -38,8 +38,9 @@ __device__ const uint4 kZeros = {0u, 0u, 0u, 0u};
 
 __device__ __forceinline__ int64_t x_row(const Rows &p, int64_t r) {
   if (p.x_div == 0) return r;
-  const int64_t s = p.rows[r] / p.x_div;
-  return s >= 0 && s < p.x_rows ? s : -1;
+  const int32_t slot = p.rows[r];
+  const int64_t s = slot / p.x_div;
+  return slot >= 0 && s < p.x_rows ? s : -1;
 }
 __device__ __forceinline__ int64_t c_row(const Rows &p, int64_t r) {
   if (!p.by_rows) return r;

@@ -20,6 +20,7 @@ constexpr int64_t kMaxSlots = int64_t(1) << 31;
 constexpr int64_t kMaxExperts = 512, kMaxSequences = 65535;
 constexpr int32_t kMaxTopK = 32;
 constexpr int32_t kMaxRank = 128;
+constexpr int64_t kMaxWidth = int64_t(1) << 24;
 constexpr int64_t kMaxElements = int64_t(1) << 40, kMaxTensors = int64_t(1) << 20;
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -97,8 +98,8 @@ int check_adapter(const nvfp4::AdapterArgs &a, int x_dtype, int out_dtype, uint3
   if (x_dtype != NVFP4_BF16 || dtype_size(out_dtype) == 0 || (flags & ~(NVFP4_ADAPTER_GATHER | NVFP4_ADAPTER_BY_TOKEN)) ||
       (a.gather && a.by_token))
     return NVFP4_ERR_UNSUPPORTED;
-  if (a.M < 0 || a.M >= kMaxSlots || a.x_rows < 0 || a.x_rows >= kMaxSlots || a.N < 1 || a.N >= kMaxSlots || a.K < 8 ||
-      a.K >= kMaxSlots || a.K % 8 != 0 || a.rank < 8 || a.rank > kMaxRank || a.rank % 8 != 0 || a.adapters < 1 ||
+  if (a.M < 0 || a.M >= kMaxSlots || a.x_rows < 0 || a.x_rows >= kMaxSlots || a.N < 1 || a.N > kMaxWidth || a.K < 8 ||
+      a.K > kMaxWidth || a.K % 8 != 0 || a.rank < 8 || a.rank > kMaxRank || a.rank % 8 != 0 || a.adapters < 1 ||
       a.adapters > kMaxExperts || a.ldx < a.K || product(a.x_rows, a.ldx) < 0)
     return NVFP4_ERR_SHAPE;
   if (!a.offsets && (a.adapters != 1 || flags)) return NVFP4_ERR_SHAPE;
@@ -144,7 +145,7 @@ nvfp4::AdapterArgs adapter_args(const void *x, int64_t x_rows, int64_t ldx, cons
 
 // Whether a size is one that the workspace functions answer for.
 bool adapter_sizes(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters) {
-  return M >= 0 && M < kMaxSlots && N >= 1 && N < kMaxSlots && K >= 8 && K < kMaxSlots && rank >= 8 && rank <= kMaxRank && adapters >= 1 &&
+  return M >= 0 && M < kMaxSlots && N >= 1 && N <= kMaxWidth && K >= 8 && K <= kMaxWidth && rank >= 8 && rank <= kMaxRank && adapters >= 1 &&
          adapters <= kMaxExperts;
 }
 

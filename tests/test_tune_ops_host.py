@@ -95,7 +95,7 @@ ABWD = dict(dc=P, dc_dtype=nv.NVFP4_BF16, lddc=40, x=P, x_dtype=nv.NVFP4_BF16, l
             dx_dtype=nv.NVFP4_BF16, lddx=64, da=P, db=P, workspace=P, stream=None)
 BOTH = [(dict(x=None), NULL), (dict(a=None), NULL), (dict(b=None), NULL), (dict(scales=None), NULL), (dict(rows=None), NULL),
         (dict(pos=None), NULL), (dict(workspace=None), NULL), (dict(x_dtype=nv.NVFP4_F32), UNSUPPORTED), (dict(flags=4), UNSUPPORTED),
-        (dict(flags=3), UNSUPPORTED), (dict(M=-1), SHAPE), (dict(N=0), SHAPE), (dict(K=0), SHAPE), (dict(K=60), SHAPE), (dict(ldx=56), SHAPE),
+        (dict(flags=3), UNSUPPORTED), (dict(M=-1), SHAPE), (dict(N=0), SHAPE), (dict(K=2**24 + 8, ldx=2**24 + 8), SHAPE), (dict(K=0), SHAPE), (dict(K=60), SHAPE), (dict(ldx=56), SHAPE),
         (dict(rank=0), SHAPE), (dict(rank=12), SHAPE), (dict(rank=136), SHAPE), (dict(adapters=0), SHAPE), (dict(adapters=513), SHAPE),
         (dict(offsets=None), SHAPE), (dict(offsets=None, adapters=1), SHAPE), (dict(ldb=8), SHAPE), (dict(ldx=2**62), SHAPE),
         (dict(M=2**31), SHAPE), (dict(x=P + 8), ALIGN), (dict(ldx=68), ALIGN), (dict(a=P + 8), ALIGN), (dict(b=P + 8), ALIGN),

@@ -189,6 +189,7 @@ template <int RF>
 __global__ __launch_bounds__(256) void shrink_many_kernel(ShrinkArgs p) {
   constexpr int kF = kManyRows * 128, kStage = kF + RF * 16 * 128;
   constexpr int NF = (2 * RF + 3) / 4;  // loads of the factor a wave and step, eight rows each
+  constexpr bool all = 2 * RF >= 4;     // (of a rank of 16 there are two, and two waves have one)
   __shared__ __attribute__((aligned(1024))) uint8_t smem[kManyStages * kStage];
   const uint32_t lane = threadIdx.x & 63u, l16 = lane & 15u, j = lane >> 4;
   const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -207,8 +208,7 @@ __global__ __launch_bounds__(256) void shrink_many_kernel(ShrinkArgs p) {
   }
 #pragma unroll
   for (int i = 0; i < NF; ++i) {
-    // (with fewer pieces than waves some waves fetch the same one)
-    const uint32_t R = 8 * ((wave + 4 * i) % (2 * RF)) + (lane >> 3);
+    const uint32_t R = 8 * (wave + 4 * i) + (lane >> 3);
     chunkF[i] = ((lane & 7u) ^ swz(R)) * 8;
     srcF[i] = R < static_cast<uint32_t>(p.R) ? p.f + (static_cast<int64_t>(t.group) * p.R + R) * p.K * 2 : nullptr;
   }
@@ -222,10 +222,11 @@ __global__ __launch_bounds__(256) void shrink_many_kernel(ShrinkArgs p) {
       const int64_t at = k + chunkY[i];
       lds_load16(srcY[i] && at < k_hi ? srcY[i] + at * 2 : zeros, st + (16 * wave + 8 * i) * 128);
     }
+    if (!all && wave >= 2) return;
 #pragma unroll
     for (int i = 0; i < NF; ++i) {
       const int64_t at = k + chunkF[i];
-      lds_load16(srcF[i] && at < k_hi ? srcF[i] + at * 2 : zeros, st + kF + 8 * ((wave + 4 * i) % (2 * RF)) * 128);
+      lds_load16(srcF[i] && at < k_hi ? srcF[i] + at * 2 : zeros, st + kF + 8 * (wave + 4 * i) * 128);
     }
   };
   constexpr int LPS = 2 + NF;
@@ -235,7 +236,10 @@ __global__ __launch_bounds__(256) void shrink_many_kernel(ShrinkArgs p) {
 #pragma unroll
   for (int u = 0; u < RF; ++u) acc[u] = (floatx4){0.0f, 0.0f, 0.0f, 0.0f};
   for (int32_t kt = 0; kt < steps; ++kt) {
-    wait_vmcnt<(kManyStages - 2) * LPS>();
+    if (!all && wave >= 2)
+      wait_vmcnt<(kManyStages - 2) * 2>();
+    else
+      wait_vmcnt<(kManyStages - 2) * LPS>();
     wait_lgkmcnt0();  // (this wave's reads of the stage that is filled next)
     lds_barrier();
     load(kt + kManyStages - 1);  // (beyond the last step: zeros, into a stage that nobody reads)

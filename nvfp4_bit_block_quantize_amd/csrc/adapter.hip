@@ -29,6 +29,7 @@ struct Rows {
   const int32_t *rows;     // NULL: row r itself
   int32_t groups;
   int32_t x_div;           // 0: x has rows in the plan's order; else x row = rows[r] / x_div
+  int32_t x_shift;         // of a power of two x_div, else -1 (a division takes some thirty instructions)
   int32_t by_rows;         // c row = rows[r]
   int64_t M, x_rows;
 };
@@ -39,7 +40,7 @@ __device__ const uint4 kZeros = {0u, 0u, 0u, 0u};
 __device__ __forceinline__ int64_t x_row(const Rows &p, int64_t r) {
   if (p.x_div == 0) return r;
   const int32_t slot = p.rows[r];
-  const int64_t s = slot / p.x_div;
+  const int64_t s = p.x_shift >= 0 ? slot >> p.x_shift : slot / p.x_div;
   return slot >= 0 && s < p.x_rows ? s : -1;
 }
 __device__ __forceinline__ int64_t c_row(const Rows &p, int64_t r) {
@@ -197,36 +198,43 @@ __global__ __launch_bounds__(256) void shrink_many_kernel(ShrinkArgs p) {
   Tile t;
   if (!find_tile(p.rows, kManyRows, tm, t)) return;
   const uint8_t *const zeros = reinterpret_cast<const uint8_t *>(&kZeros);
+  const int64_t k_lo = static_cast<int64_t>(split) * p.split_k, k_hi = min(k_lo + p.split_k, p.K);
+  const int32_t steps = static_cast<int32_t>((k_hi - k_lo + kManyStep - 1) / kManyStep);
+  // where the lane's next piece of each load lies, and what a step adds: rows that do not exist stay at the zeros
   const uint8_t *srcY[2], *srcF[NF];
-  uint32_t chunkY[2], chunkF[NF];
+  uint32_t stepY[2], stepF[NF], chunkY[2], chunkF[NF];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const uint32_t R = 16 * wave + 8 * i + (lane >> 3);
     chunkY[i] = ((lane & 7u) ^ swz(R)) * 8;
     const int64_t r = t.m0 + R, y = r < t.m_end ? x_row(p.rows, r) : -1;
-    srcY[i] = y >= 0 ? p.y + y * p.ldy : nullptr;
+    srcY[i] = y >= 0 ? p.y + y * p.ldy + (k_lo + chunkY[i]) * 2 : zeros;
+    stepY[i] = y >= 0 ? 2 * kManyStep : 0;
   }
 #pragma unroll
   for (int i = 0; i < NF; ++i) {
     const uint32_t R = 8 * (wave + 4 * i) + (lane >> 3);
     chunkF[i] = ((lane & 7u) ^ swz(R)) * 8;
-    srcF[i] = R < static_cast<uint32_t>(p.R) ? p.f + (static_cast<int64_t>(t.group) * p.R + R) * p.K * 2 : nullptr;
+    const bool real = R < static_cast<uint32_t>(p.R);
+    srcF[i] = real ? p.f + ((static_cast<int64_t>(t.group) * p.R + R) * p.K + k_lo + chunkF[i]) * 2 : zeros;
+    stepF[i] = real ? 2 * kManyStep : 0;
   }
-  const int64_t k_lo = static_cast<int64_t>(split) * p.split_k, k_hi = min(k_lo + p.split_k, p.K);
-  const int32_t steps = static_cast<int32_t>((k_hi - k_lo + kManyStep - 1) / kManyStep);
+  // loads of steps 0, 1, ... in turn; from the last on, whatever lies beyond the split reads zeros
+  const int32_t whole = static_cast<int32_t>((k_hi - k_lo) / kManyStep);
   auto load = [&](int32_t kt) {
     uint8_t *st = smem + (kt % kManyStages) * kStage;
-    const int64_t k = k_lo + static_cast<int64_t>(kt) * kManyStep;
+    const int64_t left = k_hi - k_lo - static_cast<int64_t>(kt) * kManyStep;
+    const bool cut = kt >= whole;  // (the same in every lane)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int64_t at = k + chunkY[i];
-      lds_load16(srcY[i] && at < k_hi ? srcY[i] + at * 2 : zeros, st + (16 * wave + 8 * i) * 128);
+      lds_load16(cut && static_cast<int64_t>(chunkY[i]) >= left ? zeros : srcY[i], st + (16 * wave + 8 * i) * 128);
+      srcY[i] += stepY[i];
     }
     if (!all && wave >= 2) return;
 #pragma unroll
     for (int i = 0; i < NF; ++i) {
-      const int64_t at = k + chunkF[i];
-      lds_load16(srcF[i] && at < k_hi ? srcF[i] + at * 2 : zeros, st + kF + 8 * (wave + 4 * i) * 128);
+      lds_load16(cut && static_cast<int64_t>(chunkF[i]) >= left ? zeros : srcF[i], st + kF + 8 * (wave + 4 * i) * 128);
+      srcF[i] += stepF[i];
     }
   };
   constexpr int LPS = 2 + NF;
@@ -875,6 +883,7 @@ Rows rows_of(const AdapterArgs &a) {
   p.rows = a.rows;
   p.groups = a.adapters;
   p.x_div = a.by_token ? 1 : (a.gather ? a.row_div : 0);
+  p.x_shift = p.x_div > 0 && (p.x_div & (p.x_div - 1)) == 0 ? __builtin_ctz(p.x_div) : -1;
   p.by_rows = a.by_token;
   p.M = a.M;
   p.x_rows = a.x_rows;

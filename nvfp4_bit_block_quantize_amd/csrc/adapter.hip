@@ -184,7 +184,7 @@ __global__ __launch_bounds__(64 * kFewWaves) void shrink_few_kernel(ShrinkArgs p
 // Many rows: a workgroup has 64 rows (a wave 16) and walks its split of K 64 elements (128 bytes of a row) a step through
 // a ring of LDS stages filled by direct loads.  16-byte chunk c of row r sits at c ^ ((r >> 1) & 7): the reads of a
 // fragment then cover all banks.
-constexpr int kManyRows = 64, kManyStep = 64, kManyStages = 4;
+constexpr int kManyRows = 64, kManyStep = 64, kManyStages = 3;
 __device__ __forceinline__ uint32_t swz(uint32_t r) { return (r >> 1) & 7u; }
 template <int RF>
 __global__ __launch_bounds__(256) void shrink_many_kernel(ShrinkArgs p) {

@@ -5,11 +5,17 @@
 // and column l & 15, rows 4 (l >> 4) .. + 3 of the result).
 //
 // The long sums (h over K, dA and dB over the rows) stay in fp32.  Where h or its gradient g is an operand again, it is
-// taken as a sum of bf16 numbers, v = v0 + v1 (+ v2), each the rounding of what the ones before leave: 16 bits for a bf16
-// result, whose rounding is 2^-9, and 24, all that fp32 has, for fp32 results.  Such rows are kept as [M][3 R] bf16.
+// taken as a sum of bf16 numbers, v = v0 + v1 (+ v2), each the rounding of what the ones before leave: to 2^-16 of it for a
+// bf16 result, whose own rounding is 2^-8, and to 2^-24, all that fp32 has, for fp32 results (with two pieces their error
+// was 1.2e-6 of the result, with three it is the sums' own 1e-7).  Such rows are kept as [M][3 R] bf16.
 //
 // Rows.  A plan's offsets live on the device: the launch has as many workgroups as any offsets could need (a partial
 // tile more for every adapter), and each finds its tile by a scan over the adapters' tile counts.
+//
+// What bounds it.  Ranks are small, so the rows of x, base, c and dc are nearly all of the bytes, and the products (two to
+// six R operations a byte) run under their loads up to a rank of 64.  8192 x 4096 x 14336 of rank 16, bf16: h 17.6 to
+// 21 us (67 MB), c 84 to 87 us (470 MB, 5.4 to 5.6 TB/s; a 1 GiB copy runs at 5.1); gradients 153 us (dc read once 82,
+// dx 30, x 20, the rest small).  Whole calls against the bytes at the copy's rate: forward 118 us (106), step 248 (191).
 #include "gemm_common.hpp"
 #include "nvfp4_internal.h"
 #include "vec_io.hpp"
@@ -134,7 +140,8 @@ struct ShrinkArgs {
 };
 
 // Few rows an adapter: a workgroup has 16 rows and kFewK elements of K, a wave an eighth of these, all its loads in
-// flight at once; the waves' sums meet in LDS.
+// flight at once; the waves' sums meet in LDS.  Latency: 48 rows of 4096, each with an adapter of rank 16, 5.2 us (6.7 MB);
+// 37 rows of 14336 and 16 adapters of rank 64 8.7 us (30 MB).
 constexpr int kFewWaveK = 128, kFewWaves = 8, kFewK = kFewWaves * kFewWaveK;
 template <int RF>
 __global__ __launch_bounds__(64 * kFewWaves) void shrink_few_kernel(ShrinkArgs p) {
@@ -183,7 +190,9 @@ __global__ __launch_bounds__(64 * kFewWaves) void shrink_few_kernel(ShrinkArgs p
 
 // Many rows: a workgroup has 64 rows (a wave 16) and walks its split of K 64 elements (128 bytes of a row) a step through
 // a ring of LDS stages filled by direct loads.  16-byte chunk c of row r sits at c ^ ((r >> 1) & 7): the reads of a
-// fragment then cover all banks.
+// fragment then cover all banks.  Two, three and four stages leave eight, five and four workgroups a compute unit at rank 16:
+// 32768 gathered rows of 4096 take 32.2, 33.6 and 35.5 us, 8192 rows 22.3, 21.3 and 21.3, 2047 of 14336 at rank 64 27.4,
+// 26.1 and 25.7.  The gathered rows (268 MB from the L2, 72% hits) take vector instructions for half of that time.
 constexpr int kManyRows = 64, kManyStep = 64, kManyStages = 3;
 __device__ __forceinline__ uint32_t swz(uint32_t r) { return (r >> 1) & 7u; }
 template <int RF>
@@ -273,15 +282,7 @@ __global__ __launch_bounds__(256) void shrink_many_kernel(ShrinkArgs p) {
   }
 }
 
-// ---- sums of the splits, scaled and as bf16 pieces -----------------------------------------------------------
-struct FinishArgs {
-  Rows rows;
-  const float *part;  // [splits][M][R]
-  int32_t splits, R;
-  const float *scales;
-  float *h;           // nullable [M][R], unscaled
-  uint8_t *pieces;    // [M][3 R] bf16, of scale * h
-};
+// ---- sums of the splits -----------------------------------------------------------------------------------------
 // Eight columns of row r.
 __device__ __forceinline__ void sum_splits(const float *part, int64_t M, int32_t R, int32_t splits, int64_t r, int32_t q, float (&v)[8]) {
 #pragma unroll
@@ -311,30 +312,6 @@ __global__ __launch_bounds__(256) void split_sum_kernel(float *part, int64_t siz
   for (int s = 1; s < splits; ++s) v += *reinterpret_cast<const floatx4 *>(part + s * size + i);
   *reinterpret_cast<floatx4 *>(part + i) = v;
 }
-constexpr int kFinishRows = 64;
-__device__ __forceinline__ void finish_tile(const FinishArgs &p, int32_t tm) {
-  Tile t;
-  if (!find_tile(p.rows, kFinishRows, tm, t)) return;
-  const int32_t RC = p.R / 8;
-  const float scale = p.scales[t.group];
-  for (int i = threadIdx.x; i < kFinishRows * RC; i += 256) {
-    const int64_t r = t.m0 + i / RC;
-    const int32_t rc = i % RC;
-    if (r >= t.m_end) break;
-    float v[8];
-    sum_splits(p.part, p.rows.M, p.R, p.splits, r, 8 * rc, v);
-    if (p.h) store_h(p.h, p.R, r, 8 * rc, v);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] *= scale;
-    uint4 w[3];
-    split8(v, w);
-    uint4 *out = reinterpret_cast<uint4 *>(p.pieces + r * (6 * p.R)) + rc;
-    out[0] = w[0];
-    out[RC] = w[1];
-    out[2 * RC] = w[2];
-  }
-}
-
 // ---- rows + pieces x factor: c[row(r)][n] = base[row(r)][n] + sum_q piece[r][q] f[g][n][q] --------------------
 struct ExpandArgs {
   Rows rows;
@@ -426,7 +403,10 @@ __device__ void copy_rows(const ExpandArgs &p, int32_t tile, int64_t n0) {
 // s RCP + rc, RCP the power of two that holds R / 8, and NM products of 32 cover a row.  As RCP is a power of two, these take UF
 // different fragments of the factor, again and again for each part.  Sums leave through the wave's own LDS, 16 rows at a time, in
 // whole segments (see Segment).
-// OWN (16 rows): there are no splits; each workgroup forms its rows' h itself, a wave a quarter of K.
+// OWN (16 rows): there are no splits; each workgroup forms its rows' h itself, a wave a quarter of K.  One row of 4096 x 14336,
+// rank 16: 9.6 us and 13.4 to 13.8 from Python, where two launches take 4.0 + 4.5 us and 17.2.
+// HBM-bound for many rows: see the top of the file for rank 16; 2047 x 14336 of rank 64 33 us (117 MB).  48 rows of 14336 with 48
+// adapters 8.8 us (25 MB).
 template <int RCP, int TF, bool BF16, bool ONCE, bool VEC, bool OWN>
 __global__ __launch_bounds__(256, OWN ? 2 : RCP <= 8 ? 4 : 2) void expand_kernel(ExpandArgs p) {
   using S = Segment<BF16>;
@@ -625,7 +605,9 @@ struct OuterArgs {
 // that one read touches lie in different banks.
 // The second product contracts over columns: f's fragments (again by transposed reads, from LDS before the rows' loop)
 // stay in registers, and each step the waves share out rows 0 to 15 and 16 to 31 with each fragment of f (of a rank of 16
-// there is one, and two waves take it).
+// there is one, and two waves take it).  Reading dc once for both costs 82 us where two passes took 130 (8192 x 14336, rank 16:
+// 235 MB, and 58 MB of g's parts written and read again); what of c the launch before left in the cache is written back
+// meanwhile.  x, 8192 x 4096: 20 us (3.4 TB/s).  From rank 64 on LDS reads and matrix instructions count: 2047 x 14336 28 us.
 constexpr int kOuterStep = 32, kMaxChunk = 960, kOuterThreads = 512;
 // The ring's stages: two workgroups a compute unit share its 160 KB of LDS up to a rank of 64, above it one has them.
 template <int RF>
@@ -868,12 +850,43 @@ __device__ void transpose_tile(const TransposeArgs &p, int64_t id, uint16_t (&ld
     *reinterpret_cast<uint4 *>(out + (c0 + c) * p.rows + r0 + r) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
-__global__ __launch_bounds__(256) void adapter_prep_kernel(TransposeArgs a, int64_t blocks_a, FinishArgs h) {
+// The pieces of scale * h, 64 rows a workgroup.
+struct PiecesArgs {
+  Rows rows;
+  const float *h;  // [M][R]
+  int32_t R;
+  const float *scales;
+  uint8_t *pieces;  // [M][3 R] bf16
+};
+constexpr int kPiecesRows = 64;
+__device__ __forceinline__ void pieces_tile(const PiecesArgs &p, int32_t tm) {
+  Tile t;
+  if (!find_tile(p.rows, kPiecesRows, tm, t)) return;
+  const int32_t RC = p.R / 8;
+  const float scale = p.scales[t.group];
+  for (int i = threadIdx.x; i < kPiecesRows * RC; i += 256) {
+    const int64_t r = t.m0 + i / RC;
+    const int32_t rc = i % RC;
+    if (r >= t.m_end) break;
+    const floatx4 *at = reinterpret_cast<const floatx4 *>(p.h + r * p.R + 8 * rc);
+    const floatx4 lo = at[0], hi = at[1];
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = (e < 4 ? lo[e] : hi[e - 4]) * scale;
+    uint4 w[3];
+    split8(v, w);
+    uint4 *out = reinterpret_cast<uint4 *>(p.pieces + r * (6 * p.R)) + rc;
+    out[0] = w[0];
+    out[RC] = w[1];
+    out[2 * RC] = w[2];
+  }
+}
+__global__ __launch_bounds__(256) void adapter_prep_kernel(TransposeArgs a, int64_t blocks_a, PiecesArgs h) {
   __shared__ __attribute__((aligned(16))) uint16_t lds[64 * kTurnPitch];
   if (blockIdx.x < blocks_a)
     transpose_tile(a, blockIdx.x, lds);
   else
-    finish_tile(h, static_cast<int32_t>(blockIdx.x - blocks_a));
+    pieces_tile(h, static_cast<int32_t>(blockIdx.x - blocks_a));
 }
 
 // ---- launches ----------------------------------------------------------------------------------------------------
@@ -903,7 +916,7 @@ constexpr int kExpandRows = BF16 ? 64 : 32;
 constexpr int64_t kExpandGroups = 1536, kFewGroups = 1024;
 
 // A few rows of low rank: one launch, in which each workgroup forms its rows' h by itself, as long as every workgroup has a
-// compute unit and A is read in about the time of a launch.  (One row of 4096 x 14336: see the figures at expand_kernel.)
+// compute unit and A is read in about the time of a launch.  (Figures: expand_kernel.)
 constexpr int32_t kOwnRank = 32;
 bool own_h(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters) {
   const int64_t tiles = adapters == 1 ? (M + 15) / 16 : (M < adapters ? M : adapters) + M / 16;
@@ -1166,9 +1179,9 @@ hipError_t launch_adapter_backward(const AdapterArgs &a) {
     // A^T [K][R], and the pieces of s h
     auto tiles = [](int64_t n) { return static_cast<int32_t>((n + 63) / 64); };
     const TransposeArgs ta{static_cast<const uint16_t *>(a.a), reinterpret_cast<uint16_t *>(w + l.at), a.rank, a.K, tiles(a.rank), tiles(a.K)};
-    const FinishArgs h{rows, a.h, 1, a.rank, a.scales, nullptr, w + l.h_pieces};
+    const PiecesArgs h{rows, a.h, a.rank, a.scales, w + l.h_pieces};
     const int64_t na = static_cast<int64_t>(a.adapters) * ta.tiles_r * ta.tiles_c;
-    adapter_prep_kernel<<<dim3(static_cast<uint32_t>(na + tiles_for(a, kFinishRows))), dim3(256), 0, a.stream>>>(ta, na, h);
+    adapter_prep_kernel<<<dim3(static_cast<uint32_t>(na + tiles_for(a, kPiecesRows))), dim3(256), 0, a.stream>>>(ta, na, h);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     // dB's parts and g's from one pass over dc; dx from g, and its pieces; dA's parts
     OuterArgs o{};

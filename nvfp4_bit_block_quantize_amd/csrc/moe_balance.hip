@@ -12,6 +12,11 @@
 //   sigmoid  dl_e = c p_e (1 - s_e) (n_e - sum_j p_j n_j),  p = s / (sum s + 1e-20)
 // Counts enter as differences (exact integers) from the count of the expert with the largest score: where one expert
 // has nearly all of the score its small gradient comes from the others' terms, and nothing cancels.
+//
+// What bounds them: 16384 x 256 in four sequences, sigmoid, fp32: forward 7.2 to 7.6 us (17 MB: 3.3 us at the rate of a large
+// copy) + the sums 4.5 to 5.4, gradient added to another 12.5 to 12.9 us (50 MB: 9.9).  The forward kernel issues about 350
+// vector instructions a lane, two of them a quarter as fast, of a launch in which every wave takes one group of tokens;
+// the sums are a launch and two dependent loads.  64 tokens of 64 experts: one launch of 2.9 us.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>

@@ -467,8 +467,8 @@ size_t nvfp4_moe_balance_workspace_size(int64_t tokens, int64_t experts, int64_t
  *   loss         = coef / sequences * sum_s sum_e (experts * counts[s][e] / (top_k * N)) * probs[s][e]
  * logits [tokens x experts], ids [tokens][top_k] (a routing's) as for nvfp4_moe_route.  loss: device float[1]; counts:
  * device int32 [sequences][experts]; probs: device float [sequences][experts]; live: device int32 [sequences].  Sums run
- * in fp32 in one fixed order.  tokens a multiple of sequences, sequences 1 .. 65535, coef finite (else
- * NVFP4_ERR_UNSUPPORTED); flags: NVFP4_ROUTE_SIGMOID, other routing flags are ignored. */
+ * in fp32 in one fixed order.  tokens a multiple of sequences, sequences 1 .. 65535 (else NVFP4_ERR_SHAPE), coef finite
+ * (else NVFP4_ERR_UNSUPPORTED); flags: NVFP4_ROUTE_SIGMOID, other routing flags are ignored. */
 int nvfp4_moe_balance(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t ld, const int32_t *ids,
                       int32_t top_k, int64_t sequences, uint32_t flags, float coef, float *loss, int32_t *counts,
                       float *probs, int32_t *live, void *workspace, void *hip_stream);
@@ -478,7 +478,7 @@ int nvfp4_moe_balance(const void *logits, int dtype, int64_t tokens, int64_t exp
  * rounding: dlogits [tokens x experts] in the logits' dtype, leading dimension ldd; it may be dlogits_in itself.  Counts
  * have no gradient.  counts and live are the forward call's, or their sums over the ranks of a data-parallel job (then
  * each rank has the gradient of the loss of all ranks' tokens with respect to its own logits).  Tokens without an id,
- * and closed experts, get dlogits_in (or 0) unchanged.  An expert with nearly all of the score keeps the precision of its
+ * and closed experts, get dlogits_in (or 0) unchanged, whatever *dloss is.  An expert with nearly all of the score keeps the precision of its
  * (small) gradient. */
 int nvfp4_moe_balance_backward(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t ld,
                                const int32_t *ids, int32_t top_k, int64_t sequences, uint32_t flags, float coef,

@@ -461,7 +461,8 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(BalanceBwdAr
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
       const float g = factor * q[j] * (l[j] - mean);
-      d[j] += SIGMOID ? g * slope[j] : g;
+      // (what has no score keeps dlogits_in also where dloss is infinite or NaN)
+      if (on && q[j] > 0.0f) d[j] += SIGMOID ? g * slope[j] : g;
     }
     if (exists) store_row<EPL, BF16>(p.out + t * p.out_row_bytes, l16, p.E, p.vec_out, d);
   }

@@ -202,6 +202,39 @@ def test_rows_without_an_adapter_are_not_read():
     assert not out[1][0][none].any() and not out[1][1][none].any()
 
 
+@pytest.mark.parametrize("T,K,N,R,L", [(3, 64, 48, 16, 2), (90, 520, 264, 24, 4), (700, 264, 328, 64, 3)])
+def test_no_numbers_stay_in_their_rows(T, K, N, R, L):
+    """Infinities and NaN of a token, or of an adapter's factors, reach no other token and no other adapter's gradients."""
+    w, *_ = _factors(L, R, K, N, 7)
+    ids = np.arange(T)[:, None] % L
+    plan, _ = _plan(ids, L)
+    x, dc, base = (torch.randn(T, n, device=DEV).to(BF16) for n in (K, N, N))
+    mine = torch.from_numpy(ids[:, 0] == 1).to(DEV)
+
+    def step(w, x, dc, base):
+        c, h = nv.nvfp4_adapter(x, w, base, plan=plan, by_token=True, with_h=True)
+        d = nv.nvfp4_adapter_backward(dc, x, w, h, plan=plan, by_token=True)
+        return c, d.dx, d.da.view(L, R, K), d.db.view(L, N, R)
+
+    clean = step(w, x, dc, base)
+    for bad in (float("inf"), float("nan")):
+        x2, dc2, base2 = x.clone(), dc.clone(), base.clone()
+        x2[1, 3], dc2[1, N - 1], base2[1, 5] = bad, bad, bad  # (token 1 has adapter 1)
+        dirty = step(w, x2, dc2, base2)
+        for p, q in zip(clean[:2], dirty[:2]):
+            assert torch.equal(p[2:], q[2:]) and torch.equal(p[0], q[0]) and not bool(torch.isfinite(q[1].float()).all())
+        for p, q in zip(clean[2:], dirty[2:]):
+            assert torch.equal(p[0], q[0]) and torch.equal(p[2:], q[2:])
+        a2, b2 = w.a.clone(), w.b.clone()
+        a2.view(L, R, K)[1] = bad
+        b2.view(L, N, R)[1] = bad
+        dirty = step(nv.Adapters(a2, b2, w.scales, R, K, N, L), x, dc, base)
+        for p, q in zip(clean[:2], dirty[:2]):
+            assert torch.equal(p[~mine], q[~mine]) and not bool(torch.isfinite(q[mine].float()).any())
+        for p, q in zip(clean[2:], dirty[2:]):
+            assert torch.equal(p[0], q[0]) and torch.equal(p[2:], q[2:])
+
+
 def test_no_rows():
     w, *_ = _factors(3, 16, 64, 32, 1)
     x = torch.empty(0, 64, dtype=BF16, device=DEV)

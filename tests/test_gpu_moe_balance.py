@@ -143,6 +143,22 @@ def test_added_in_place_with_strides_and_padding_untouched():
     assert torch.equal(whole[:, :4], wide[:, :4]) and torch.equal(whole[:, 4 + E:], wide[:, 4 + E:])
 
 
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_masked_places_of_a_loss_that_is_no_number(sigmoid, bad):
+    T, E, k = 37, 24, 2
+    logits, ids = _inputs(T, E, k, torch.float32, 11)
+    logits[:, 3] = -np.inf
+    logits[5, :] = np.nan
+    ids[7:9] = -1
+    flags = nv.NVFP4_ROUTE_SIGMOID if sigmoid else 0
+    b = nv.nvfp4_moe_balance(logits.to(DEV), ids.to(DEV), 1.0, flags=flags)
+    given = torch.randn(T, E).to(DEV)
+    d = nv.nvfp4_moe_balance_backward(logits.to(DEV), ids.to(DEV), b, 1.0, flags=flags, dloss=torch.tensor([bad]).to(DEV), dlogits=given)
+    assert torch.equal(d[:, 3], given[:, 3]) and torch.equal(d[5], given[5]) and torch.equal(d[7:9], given[7:9])
+    assert not torch.isfinite(d[0, 0]) and not torch.isfinite(d[36, 23])
+
+
 def test_counts_of_all_ranks():
     """Counts and tokens summed over two halves give each half its part of the whole batch's gradient."""
     logits, ids = _inputs(128, 24, 2, torch.float32, 21)

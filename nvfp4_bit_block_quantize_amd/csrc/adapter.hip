@@ -357,6 +357,21 @@ struct Segment {
   static constexpr int ES = BF16 ? 2 : 4, kValues = 16 / ES, kPieces = 64 / kValues, kRows = 64 / kPieces;
 };
 
+// A piece of a row of base or c; rows whose pieces lie at any element unless VEC.
+template <bool ONCE, bool VEC>
+__device__ __forceinline__ uint4 load_piece(const uint8_t *at) {
+  if constexpr (VEC) return load16<ONCE>(at);
+  const any_u32x4 v = *reinterpret_cast<const any_u32x4 *>(at);
+  return make_uint4(v.x, v.y, v.z, v.w);
+}
+template <bool VEC>
+__device__ __forceinline__ void store_piece(uint8_t *at, const uint4 &v) {
+  if constexpr (VEC)
+    *reinterpret_cast<uint4 *>(at) = v;
+  else
+    *reinterpret_cast<any_u32x4 *>(at) = (any_u32x4){v.x, v.y, v.z, v.w};
+}
+
 // Rows without an adapter: c = base (or zeros), 64 rows of a workgroup's columns.
 template <bool BF16, bool ONCE, bool VEC>
 __device__ void copy_rows(const ExpandArgs &p, int32_t tile, int64_t n0) {
@@ -370,7 +385,7 @@ __device__ void copy_rows(const ExpandArgs &p, int32_t tile, int64_t n0) {
   if (rows == 0) return;
   const int32_t first = lane / S::kPieces, col = lane % S::kPieces * S::kValues;
   for (int64_t n = n0 + 64 * wave + col; n < n1; n += 256) {
-    if constexpr (VEC) {
+    if (n + S::kValues <= p.N) {
 #pragma clang loop unroll(disable)
       for (int i0 = 0; i0 < NI; i0 += 8) {
         uint4 v[8];
@@ -378,20 +393,21 @@ __device__ void copy_rows(const ExpandArgs &p, int32_t tile, int64_t n0) {
         for (int i = 0; i < 8; ++i) {
           const int32_t r = S::kRows * (i0 + i) + first;
           v[i] = make_uint4(0, 0, 0, 0);
-          if (p.base && (rows >> r & 1)) v[i] = load16<ONCE>(p.base + (static_cast<int64_t>(tile) * 64 + r) * p.ldb + n * ES);
+          if (p.base && (rows >> r & 1)) v[i] = load_piece<ONCE, VEC>(p.base + (static_cast<int64_t>(tile) * 64 + r) * p.ldb + n * ES);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int32_t r = S::kRows * (i0 + i) + first;
-          if (rows >> r & 1) *reinterpret_cast<uint4 *>(p.c + (static_cast<int64_t>(tile) * 64 + r) * p.ldc + n * ES) = v[i];
+          if (rows >> r & 1) store_piece<VEC>(p.c + (static_cast<int64_t>(tile) * 64 + r) * p.ldc + n * ES, v[i]);
         }
       }
-    } else {
+    } else if constexpr (!VEC) {
+#pragma clang loop unroll(disable)
       for (int i = 0; i < NI; ++i) {
         const int32_t r = S::kRows * i + first;
         const int64_t row = static_cast<int64_t>(tile) * 64 + r;
         if (rows >> r & 1)
-          for (int64_t e = n; e < min(n + S::kValues, p.N); ++e)
+          for (int64_t e = n; e < p.N; ++e)
             set_element<BF16>(p.c + row * p.ldc, e, p.base ? element<BF16>(p.base + row * p.ldb, e) : 0.0f);
       }
     }
@@ -408,7 +424,7 @@ __device__ void copy_rows(const ExpandArgs &p, int32_t tile, int64_t n0) {
 // HBM-bound for many rows: see the top of the file for rank 16; 2047 x 14336 of rank 64 33 us (117 MB).  48 rows of 14336 with 48
 // adapters 8.8 us (25 MB).
 template <int RCP, int TF, bool BF16, bool ONCE, bool VEC, bool OWN>
-__global__ __launch_bounds__(256, OWN ? 2 : RCP <= 8 ? 4 : 2) void expand_kernel(ExpandArgs p) {
+__global__ __launch_bounds__(256, OWN || RCP > 8 ? 2 : VEC || TF == 1 ? 4 : 3) void expand_kernel(ExpandArgs p) {
   using S = Segment<BF16>;
   constexpr int ES = S::ES, PARTS = BF16 ? 2 : 3, NI = 16 * TF / S::kRows;
   constexpr int NM = (PARTS * RCP + 3) / 4, UF = RCP <= 4 ? 1 : RCP / 4;
@@ -434,13 +450,11 @@ __global__ __launch_bounds__(256, OWN ? 2 : RCP <= 8 ? 4 : 2) void expand_kernel
   uint4 f[4][UF], b[NI];
   auto load = [&](int64_t n0) {
     const int64_t n = n0 + col;
-    if constexpr (VEC) {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int64_t row = c_rows[S::kRows * i + first];
-        b[i] = make_uint4(0, 0, 0, 0);
-        if (p.base && row >= 0 && n < p.N) b[i] = load16<ONCE>(p.base + row * p.ldb + n * ES);
-      }
+    for (int i = 0; i < NI; ++i) {
+      const int64_t row = c_rows[S::kRows * i + first];
+      b[i] = make_uint4(0, 0, 0, 0);
+      if (p.base && row >= 0 && n + S::kValues <= p.N) b[i] = load_piece<ONCE, VEC>(p.base + row * p.ldb + n * ES);
     }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
@@ -554,7 +568,7 @@ __global__ __launch_bounds__(256, OWN ? 2 : RCP <= 8 ? 4 : 2) void expand_kernel
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[4 * q + e] = four[e];
         }
-        if constexpr (VEC) {
+        if (row >= 0 && n + S::kValues <= p.N) {
           uint32_t w[4] = {b[i].x, b[i].y, b[i].z, b[i].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
@@ -563,9 +577,9 @@ __global__ __launch_bounds__(256, OWN ? 2 : RCP <= 8 ? 4 : 2) void expand_kernel
             else
               w[e] = __float_as_uint(__uint_as_float(w[e]) + v[e]);
           }
-          if (row >= 0 && n < p.N) *reinterpret_cast<uint4 *>(p.c + row * p.ldc + n * ES) = make_uint4(w[0], w[1], w[2], w[3]);
-        } else if (row >= 0) {
-          // (a loop, to keep this rare path's code short)
+          store_piece<VEC>(p.c + row * p.ldc + n * ES, make_uint4(w[0], w[1], w[2], w[3]));
+        } else if (!VEC && row >= 0) {
+          // the last columns of a row (a loop, to keep this path's code short)
 #pragma clang loop unroll(disable)
           for (int e = 0; e < S::kValues && n + e < p.N; ++e) {
             const float was = p.base ? element<BF16>(p.base + row * p.ldb, n + e) : 0.0f;
@@ -992,7 +1006,10 @@ hipError_t run_expand(const ExpandArgs &p, bool few, bool vec, uint32_t groups, 
         expand_kernel<RCP, 1, BF16, false, false, true><<<grid, threads, 0, stream>>>(p);
     }
   } else if (!vec) {
-    expand_kernel<RCP, 1, BF16, false, false, false><<<grid, threads, 0, stream>>>(p);
+    if (few)
+      expand_kernel<RCP, 1, BF16, false, false, false><<<grid, threads, 0, stream>>>(p);
+    else
+      expand_kernel<RCP, TF, BF16, false, false, false><<<grid, threads, 0, stream>>>(p);
   } else if (few) {
     expand_kernel<RCP, 1, BF16, false, true, false><<<grid, threads, 0, stream>>>(p);
   } else if (once) {
@@ -1035,10 +1052,11 @@ hipError_t run_expand(const AdapterArgs &a, const void *f, int64_t N, float *par
   p.ldb = ldb * es;
   p.c = static_cast<uint8_t *>(c);
   p.ldc = ldc * es;
-  // rows of base and c aligned to 16 bytes, which N fills; else single elements, 16 rows a workgroup
+  // rows of base and c aligned to 16 bytes, which N fills; else pieces at any element, and each row's last by itself (whole
+  // calls of 8192 rows, rank 16, K 4096: 14336 columns 110 us, 14335 164, and 667 with all of them element by element)
   const bool vec = (reinterpret_cast<uintptr_t>(base) | reinterpret_cast<uintptr_t>(c) | static_cast<uintptr_t>(p.ldc) |
            static_cast<uintptr_t>(base ? p.ldb : 0) | static_cast<uintptr_t>(N * es)) % 16 == 0;
-  const int32_t tile_rows = few || !vec ? 16 : dtype == 1 ? kExpandRows<true> : kExpandRows<false>;
+  const int32_t tile_rows = few ? 16 : dtype == 1 ? kExpandRows<true> : kExpandRows<false>;
   p.tiles_m = static_cast<int32_t>(tiles_for(a, tile_rows));
   // as many steps of 256 columns a workgroup as leave kExpandGroups workgroups
   const int64_t steps = (N + 255) / 256, tiles = (a.M + tile_rows - 1) / tile_rows;

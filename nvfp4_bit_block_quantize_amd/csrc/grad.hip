@@ -43,9 +43,6 @@ constexpr int32_t kBf16 = 1;  // GradArgs::dtypes
 constexpr uint32_t kBf16Bit = 1u << 31;
 static_assert(sizeof(NormBatch) <= 4000 && sizeof(ClipBatch) <= 4000, "launch arguments");
 
-// 16 bytes at an address aligned to an element only.
-typedef uint32_t any_u32x4 __attribute__((ext_vector_type(4), aligned(2)));
-
 // A chunk: its tensor, first element and number of elements.
 struct Chunk {
   uint32_t tensor;

@@ -32,6 +32,9 @@ __device__ __forceinline__ uint4 load16(const uint8_t *p) {
   }
 }
 
+// 16 bytes at an address aligned to an element only.
+typedef uint32_t any_u32x4 __attribute__((ext_vector_type(4), aligned(2)));
+
 // Eight consecutive elements from element index i (a multiple of 8) on.
 template <bool BF16>
 struct Raw8 {

@@ -70,96 +70,130 @@ struct Place {
   static __device__ __forceinline__ int of(int i, int l16) { return (i / kPiece * 16 + l16) * kPiece + i % kPiece; }
 };
 
-// The lane's values of a row; `fill` beyond E.  vec: the row is aligned to 16 bytes and E fills whole pieces.
+template <bool BF16>
+__device__ __forceinline__ float load_one(const uint8_t *row, int e) {
+  return BF16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[e]) << 16)
+              : reinterpret_cast<const float *>(row)[e];
+}
+template <bool BF16>
+__device__ __forceinline__ void store_one(uint8_t *row, int e, float v) {
+  if constexpr (BF16)
+    reinterpret_cast<uint16_t *>(row)[e] = static_cast<uint16_t>(pack_bf16(v, 0.0f));
+  else
+    reinterpret_cast<float *>(row)[e] = v;
+}
+
+// The lane's values of a row: `load` asks for its pieces, and `values` gives them, `fill` beyond E (two steps, so that all of a
+// token's loads are under way before the first is waited for).  Pieces may lie at any element (the loads are the same); a row's
+// last one, if E ends within it, is read element by element: the others' number says in which of the lanes' pieces it is.  (Both
+// directions of 12010 x 317 bf16 and 14368 x 511 fp32 take 29 and 41 us so, 44 and 54 element by element; a path of its own for
+// rows of whole pieces would save these 2%.)
 template <int EPL, bool BF16>
-__device__ __forceinline__ void load_row(const uint8_t *row, int l16, int E, bool vec, float fill, float (&l)[EPL]) {
+struct Row {
   using P = Place<EPL, BF16>;
-  if constexpr (P::kWide) {
-    if (vec) {
+  any_u32x4 w[P::kPieces];
+  __device__ __forceinline__ void load(const uint8_t *row, int l16, int E) {
+    if constexpr (P::kWide) {
 #pragma unroll
       for (int m = 0; m < P::kPieces; ++m) {
         const int e0 = P::of(m * P::kPiece, l16);
-        const bool real = e0 < E;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (real) v = *reinterpret_cast<const uint4 *>(row + e0 * (BF16 ? 2 : 4));
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        w[m] = (any_u32x4){0, 0, 0, 0};
+        if (e0 + P::kPiece <= E) w[m] = *reinterpret_cast<const any_u32x4 *>(row + e0 * (BF16 ? 2 : 4));
+      }
+    }
+  }
+  __device__ __forceinline__ void values(const uint8_t *row, int l16, int E, float fill, float (&l)[EPL]) const {
+    if constexpr (P::kWide) {
+#pragma unroll
+      for (int m = 0; m < P::kPieces; ++m) {
+        const bool real = P::of(m * P::kPiece, l16) + P::kPiece <= E;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if constexpr (BF16) {
-            l[8 * m + 2 * q] = real ? __uint_as_float(w[q] << 16) : fill;
-            l[8 * m + 2 * q + 1] = real ? __uint_as_float(w[q] & 0xFFFF0000u) : fill;
+            l[8 * m + 2 * q] = real ? __uint_as_float(w[m][q] << 16) : fill;
+            l[8 * m + 2 * q + 1] = real ? __uint_as_float(w[m][q] & 0xFFFF0000u) : fill;
           } else {
-            l[4 * m + q] = real ? __uint_as_float(w[q]) : fill;
+            l[4 * m + q] = real ? __uint_as_float(w[m][q]) : fill;
           }
         }
       }
-      return;
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = P::of(i, l16);
-    l[i] = fill;
-    if (e < E)
-      l[i] = BF16 ? __uint_as_float(static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(row)[e]) << 16)
-                  : reinterpret_cast<const float *>(row)[e];
-  }
-}
-template <int EPL, bool BF16>
-__device__ __forceinline__ void store_row(uint8_t *row, int l16, int E, bool vec, const float (&d)[EPL]) {
-  using P = Place<EPL, BF16>;
-  if constexpr (P::kWide) {
-    if (vec) {
+      if (E % P::kPiece == 0) return;
 #pragma unroll
       for (int m = 0; m < P::kPieces; ++m) {
         const int e0 = P::of(m * P::kPiece, l16);
-        uint32_t w[4];
+        if (E / P::kPiece / 16 != m || e0 >= E || e0 + P::kPiece <= E) continue;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if constexpr (BF16)
-            w[q] = pack_bf16(d[8 * m + 2 * q], d[8 * m + 2 * q + 1]);
-          else
-            w[q] = __float_as_uint(d[4 * m + q]);
-        }
-        if (e0 < E) *reinterpret_cast<uint4 *>(row + e0 * (BF16 ? 2 : 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int i = 0; i < P::kPiece - 1; ++i)
+          if (e0 + i < E) l[P::kPiece * m + i] = load_one<BF16>(row, e0 + i);
       }
-      return;
+    } else {
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) {
+        const int e = P::of(i, l16);
+        l[i] = e < E ? load_one<BF16>(row, e) : fill;
+      }
     }
   }
+};
+template <int EPL, bool BF16>
+__device__ __forceinline__ void store_row(uint8_t *row, int l16, int E, const float (&d)[EPL]) {
+  using P = Place<EPL, BF16>;
+  if constexpr (P::kWide) {
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = P::of(i, l16);
-    if (e < E) {
-      if constexpr (BF16)
-        reinterpret_cast<uint16_t *>(row)[e] = static_cast<uint16_t>(pack_bf16(d[i], 0.0f));
-      else
-        reinterpret_cast<float *>(row)[e] = d[i];
+    for (int m = 0; m < P::kPieces; ++m) {
+      const int e0 = P::of(m * P::kPiece, l16);
+      any_u32x4 w;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if constexpr (BF16)
+          w[q] = pack_bf16(d[8 * m + 2 * q], d[8 * m + 2 * q + 1]);
+        else
+          w[q] = __float_as_uint(d[4 * m + q]);
+      }
+      if (e0 + P::kPiece <= E) *reinterpret_cast<any_u32x4 *>(row + e0 * (BF16 ? 2 : 4)) = w;
+    }
+    if (E % P::kPiece == 0) return;
+#pragma unroll
+    for (int m = 0; m < P::kPieces; ++m) {
+      const int e0 = P::of(m * P::kPiece, l16);
+      if (E / P::kPiece / 16 != m || e0 >= E || e0 + P::kPiece <= E) continue;
+#pragma unroll
+      for (int i = 0; i < P::kPiece - 1; ++i)
+        if (e0 + i < E) store_one<BF16>(row, e0 + i, d[P::kPiece * m + i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = P::of(i, l16);
+      if (e < E) store_one<BF16>(row, e, d[i]);
     }
   }
 }
-// The lane's counts of a row of E (element by element unless four lie together in the lane and the row).
+// The lane's counts of a row of E, four at a time where four lie together in the lane.
 template <int EPL, bool BF16>
 __device__ __forceinline__ void load_counts(const int32_t *row, int l16, int E, int (&n)[EPL]) {
   using P = Place<EPL, BF16>;
   if constexpr (P::kPiece >= 4) {
-    if (E % 4 == 0 && (reinterpret_cast<uintptr_t>(row) & 15u) == 0) {
 #pragma unroll
-      for (int i = 0; i < EPL; i += 4) {
-        const int e = P::of(i, l16);
-        int4 v = make_int4(0, 0, 0, 0);
-        if (e < E) v = *reinterpret_cast<const int4 *>(row + e);
-        n[i] = v.x;
-        n[i + 1] = v.y;
-        n[i + 2] = v.z;
-        n[i + 3] = v.w;
+    for (int i = 0; i < EPL; i += 4) {
+      const int e = P::of(i, l16);
+      any_u32x4 v = {0, 0, 0, 0};
+      if (e + 4 <= E) {
+        v = *reinterpret_cast<const any_u32x4 *>(row + e);
+      } else {
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+          if (e + q < E) v[q] = row[e + q];
       }
-      return;
-    }
-  }
 #pragma unroll
-  for (int i = 0; i < EPL; ++i) {
-    const int e = P::of(i, l16);
-    n[i] = e < E ? row[e] : 0;
+      for (int q = 0; q < 4; ++q) n[i + q] = static_cast<int>(v[q]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) {
+      const int e = P::of(i, l16);
+      n[i] = e < E ? row[e] : 0;
+    }
   }
 }
 
@@ -209,7 +243,6 @@ struct BalanceArgs {
   int64_t row_bytes;
   int64_t seq;  // tokens of a sequence
   int E, k, sequences, blocks;  // blocks: workgroups of a sequence
-  bool vec;
   const int32_t *ids;
   float scale;  // coef / sequences
   float *part_probs;     // [sequences][blocks][E]
@@ -272,8 +305,11 @@ __global__ __launch_bounds__(kSumsThreads) void balance_kernel(BalanceArgs p) {
     const bool exists = i < p.seq;
     const int64_t t = first + (exists ? i : p.seq - 1);
     float l[EPL], q[EPL], none[EPL], inv, spare;
-    load_row<EPL, BF16>(p.logits + t * p.row_bytes, l16, p.E, p.vec, kNegInf, l);
+    const uint8_t *const row = p.logits + t * p.row_bytes;
+    Row<EPL, BF16> raw;
+    raw.load(row, l16, p.E);
     const bool on = row_ids(p.ids, t, p.k, p.E, l16, exists, hist);
+    raw.values(row, l16, p.E, kNegInf, l);
     row_scores<EPL, SIGMOID, false>(l, q, none, inv, spare);
     if (!on) inv = 0.0f;
 #pragma unroll
@@ -414,7 +450,6 @@ struct BalanceBwdArgs {
   int64_t row_bytes, din_row_bytes, out_row_bytes;
   int64_t seq;
   int E, k, blocks;
-  bool vec, vec_din, vec_out;
   const int32_t *ids, *counts, *tokens;
   const float *dloss;  // NULL: 1
   float factor;        // coef E / (sequences k)
@@ -436,14 +471,12 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(BalanceBwdAr
     const bool exists = i < p.seq;
     const int64_t t = first + (exists ? i : p.seq - 1);
     float l[EPL], q[EPL], slope[EPL], d[EPL], inv, spare;
-    load_row<EPL, BF16>(p.logits + t * p.row_bytes, l16, p.E, p.vec, kNegInf, l);
-    if (p.din) {
-      load_row<EPL, BF16>(p.din + t * p.din_row_bytes, l16, p.E, p.vec_din, 0.0f, d);
-    } else {
-#pragma unroll
-      for (int j = 0; j < EPL; ++j) d[j] = 0.0f;
-    }
+    const uint8_t *const row = p.logits + t * p.row_bytes, *const given = p.din + t * p.din_row_bytes;
+    Row<EPL, BF16> raw, raw_d;
+    raw.load(row, l16, p.E);
+    if (p.din) raw_d.load(given, l16, p.E);
     const bool on = row_ids(p.ids, t, p.k, p.E, l16, exists, nullptr);
+    raw.values(row, l16, p.E, kNegInf, l);
     const float top = row_scores<EPL, SIGMOID, true>(l, q, slope, inv, spare);
     int ref = 0;
 #pragma unroll
@@ -458,13 +491,19 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(BalanceBwdAr
     mean = row_sum(mean) * inv;
     if (SIGMOID) mean = fmaf(-spare, static_cast<float>(ref), mean);
     const float factor = on ? cf * inv : 0.0f;
+    if (p.din) {
+      raw_d.values(given, l16, p.E, 0.0f, d);
+    } else {
+#pragma unroll
+      for (int j = 0; j < EPL; ++j) d[j] = 0.0f;
+    }
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
       const float g = factor * q[j] * (l[j] - mean);
       // (what has no score keeps dlogits_in also where dloss is infinite or NaN)
       if (on && q[j] > 0.0f) d[j] += SIGMOID ? g * slope[j] : g;
     }
-    if (exists) store_row<EPL, BF16>(p.out + t * p.out_row_bytes, l16, p.E, p.vec_out, d);
+    if (exists) store_row<EPL, BF16>(p.out + t * p.out_row_bytes, l16, p.E, d);
   }
 }
 
@@ -472,10 +511,6 @@ int experts_per_lane(int64_t E) {
   int epl = 1;
   while (16 * epl < E) epl *= 2;
   return epl;
-}
-// Whether rows of E elements of `es` bytes are 16-byte pieces.
-bool whole_pieces(const void *p, int64_t row_bytes, int64_t E, int es) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && row_bytes % 16 == 0 && E * es % 16 == 0;
 }
 
 // Tokens up to which one workgroup does all of it.
@@ -531,7 +566,6 @@ hipError_t launch_moe_balance(const MoeBalanceArgs &a) {
   p.E = static_cast<int>(a.experts);
   p.k = a.top_k;
   p.sequences = static_cast<int>(a.sequences);
-  p.vec = whole_pieces(a.logits, p.row_bytes, p.E, es);
   p.ids = a.ids;
   p.scale = a.coef / static_cast<float>(a.sequences);
   p.loss = a.loss;
@@ -576,9 +610,6 @@ hipError_t launch_moe_balance_backward(const MoeBalanceArgs &a) {
   p.E = static_cast<int>(a.experts);
   p.k = a.top_k;
   p.blocks = static_cast<int>(blocks_a_sequence(p.seq, a.sequences, kRows, kBackwardBlocks));
-  p.vec = whole_pieces(a.logits, p.row_bytes, p.E, es);
-  p.vec_din = whole_pieces(a.dlogits_in, p.din_row_bytes, p.E, es);
-  p.vec_out = whole_pieces(a.dlogits, p.out_row_bytes, p.E, es);
   p.ids = a.ids;
   p.counts = a.counts;
   p.tokens = a.live;

@@ -10,8 +10,10 @@
 // Gradient.  With counts n and c = coef dloss E / (S k N^2), N the sequence's tokens:
 //   softmax  dl_e = c p_e (n_e - sum_j p_j n_j)
 //   sigmoid  dl_e = c p_e (1 - s_e) (n_e - sum_j p_j n_j),  p = s / (sum s + 1e-20)
-// Counts enter as differences (exact integers) from the count of the expert with the largest score: where one expert
-// has nearly all of the score its small gradient comes from the others' terms, and nothing cancels.
+// Counts enter as differences (exact integers) from a reference count.  Where one expert has more than half of the score it
+// is that expert's: with nearly all of the score its small gradient comes from the others' terms, and nothing cancels.  Else
+// it is the integer next to sum_j p_j n_j: what the differences' own sum leaves is then of the size of the counts' spread.
+// (Taken from the likeliest expert's count everywhere, one token of 300 experts lost 7 bits: its 1 less 299/300 of it.)
 //
 // What bounds them: 16384 x 256 in four sequences, sigmoid, fp32: forward 7.2 to 7.6 us (17 MB: 3.3 us at the rate of a large
 // copy) + the sums 4.5 to 5.4, gradient added to another 12.5 to 12.9 us (50 MB: 9.9).  The forward kernel issues about 350
@@ -32,6 +34,7 @@ constexpr int kSumsThreads = 1024, kSumsRows = kSumsThreads / 16, kThreads = 256
 constexpr int kMaxExperts = 512;
 constexpr float kNegInf = -__builtin_huge_valf(), kMaxLogit = 3.402823466e38f;
 constexpr float kTiny = 1e-20f;  // added to a sum of sigmoid scores
+constexpr float kMaxCount = 2147483520.0f;  // the largest float below 2^31
 
 // Over the 16 lanes of a row, in every lane of it.
 __device__ __forceinline__ float row_sum(float v) {
@@ -210,17 +213,17 @@ __device__ __forceinline__ float exp_of(float x) {
 
 // Scores of a token from its logits (closed experts: -inf or NaN; others capped at FLT_MAX), before their division by their
 // sum: p, and what divides them, `inv` (0 for a token without an open expert, or whose sum is zero).  l is left as the
-// logits in this form; `spare` is 1 - sum of the probabilities (0 for a softmax); slope (sigmoid): 1 - s.  Returns the
-// largest logit.  A closed expert's score comes out as zero by itself.
+// logits in this form; `spare` is 1 - sum of the probabilities (0 for a softmax); slope (sigmoid): 1 - s.  Returns half of
+// the sum.  A closed expert's score comes out as zero by itself.
 template <int EPL, bool SIGMOID, bool SLOPE>
 __device__ __forceinline__ float row_scores(float (&l)[EPL], float (&p)[EPL], float (&slope)[EPL], float &inv, float &spare) {
   float top = kNegInf, sum = 0.0f;
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     l[j] = fminf(fmaxf(l[j], kNegInf), kMaxLogit);  // (the larger of NaN and -inf is -inf)
-    if (!SIGMOID || SLOPE) top = fmaxf(top, l[j]);
+    if (!SIGMOID) top = fmaxf(top, l[j]);
   }
-  if (!SIGMOID || SLOPE) top = row_max(top);
+  if (!SIGMOID) top = row_max(top);
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     if constexpr (SIGMOID) {
@@ -235,7 +238,7 @@ __device__ __forceinline__ float row_scores(float (&l)[EPL], float (&p)[EPL], fl
   sum = row_sum(sum);
   inv = SIGMOID ? 1.0f / (sum + kTiny) : (sum > 0.0f ? 1.0f / sum : 0.0f);
   spare = SIGMOID ? kTiny * inv : 0.0f;
-  return top;
+  return 0.5f * sum;
 }
 
 struct BalanceArgs {
@@ -477,12 +480,18 @@ __global__ __launch_bounds__(kThreads) void balance_backward_kernel(BalanceBwdAr
     if (p.din) raw_d.load(given, l16, p.E);
     const bool on = row_ids(p.ids, t, p.k, p.E, l16, exists, nullptr);
     raw.values(row, l16, p.E, kNegInf, l);
-    const float top = row_scores<EPL, SIGMOID, true>(l, q, slope, inv, spare);
-    int ref = 0;
+    const float half = row_scores<EPL, SIGMOID, true>(l, q, slope, inv, spare);
+    int ref = -1;
+    float mean = 0.0f;  // of the counts
 #pragma unroll
-    for (int j = 0; j < EPL; ++j) ref = max(ref, l[j] == top ? n[j] : 0);
+    for (int j = 0; j < EPL; ++j) {
+      ref = max(ref, q[j] > half ? n[j] : -1);
+      mean = fmaf(q[j], static_cast<float>(n[j]), mean);
+    }
     ref = row_max(ref);
-    float mean = 0.0f;  // of the counts, less ref
+    mean = row_sum(mean) * inv;
+    if (ref < 0) ref = static_cast<int>(fminf(rintf(mean), kMaxCount));
+    mean = 0.0f;  // of the counts, less ref
 #pragma unroll
     for (int j = 0; j < EPL; ++j) {
       l[j] = static_cast<float>(n[j] - ref);

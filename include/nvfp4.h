@@ -411,7 +411,8 @@ size_t nvfp4_adapter_backward_workspace_size(int64_t M, int64_t N, int64_t K, in
 /* Low-rank adapters of many requests, or of many experts, beside a shared product whose result is base:
  *   h[r] = A_g x[r],   c[r] = base[r] + scales[g] * B_g h[r]
  * for the rows r of each adapter g.  Sums run in fp32; h enters the second product with at least 16 bits of precision for
- * a bf16 c and 24 for an fp32 one; c is rounded once.
+ * a bf16 c and 24 for an fp32 one, an infinite h as itself; c is rounded once.  (A product of h, or of
+ * the gradients' g, with an infinite element of the other operand may be NaN instead of infinite.)
  * x [x_rows x K] of x_dtype NVFP4_BF16 (else NVFP4_ERR_UNSUPPORTED), leading dimension ldx.  a: device bf16
  * [adapters][rank][K], b: device bf16 [adapters][N][rank], scales: device float[adapters].
  * offsets NULL: one adapter for all M == x_rows rows (adapters 1, flags 0; rows and pos are ignored).  Else a device plan,

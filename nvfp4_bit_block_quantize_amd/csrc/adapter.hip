@@ -102,17 +102,36 @@ __device__ __forceinline__ floatx4 mfma(const bf16x8 &a, const bf16x8 &b, const 
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// Eight values as `parts` bf16 pieces each of which takes what the ones before leave.
+// Eight values as `parts` bf16 pieces each of which takes what the ones before leave.  An infinity is its first piece alone (what it
+// leaves would be NaN), and the first piece of a finite value that would round to one is the largest bf16 number.
+constexpr float kBf16Max = 0x1.FEp127f;
 template <int PARTS>
 __device__ __forceinline__ void split8(float (&v)[8], uint4 (&out)[PARTS]) {
+  float top = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[e]));
+  const bool over = top > kBf16Max;
 #pragma unroll
   for (int s = 0; s < PARTS; ++s) {
+    float piece[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) piece[e] = v[e];
+    if (s == 0 && over) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (fabsf(v[e]) > kBf16Max && !isinf(v[e])) piece[e] = copysignf(kBf16Max, v[e]);
+    }
     uint32_t w[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-      w[q] = pack_bf16(v[2 * q], v[2 * q + 1]);
+      w[q] = pack_bf16(piece[2 * q], piece[2 * q + 1]);
       v[2 * q] -= __uint_as_float(w[q] << 16);
       v[2 * q + 1] -= __uint_as_float(w[q] & 0xFFFF0000u);
+    }
+    if (s == 0 && over) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (isinf(piece[e])) v[e] = 0.0f;
     }
     out[s] = make_uint4(w[0], w[1], w[2], w[3]);
   }

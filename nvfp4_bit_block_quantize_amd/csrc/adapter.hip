@@ -805,10 +805,12 @@ __global__ __launch_bounds__(kOuterThreads, RF <= 4 ? 4 : 2) void outer_kernel(O
   }
 }
 
-// Sums of an adapter's chunks in order; zeros for an adapter without rows.
+// Sums of an adapter's chunks in order; zeros for an adapter without rows.  Only chunks that a workgroup of the launch before
+// had are read, whatever the offsets are: those among its tiles that start at one of the M rows.
 struct OuterSumArgs {
   Rows rows;
   int32_t chunk;
+  int64_t tiles;  // of the launch before
   int64_t size;  // N R
   int32_t blocks;  // workgroups an adapter
   const float *part;
@@ -817,25 +819,34 @@ struct OuterSumArgs {
 constexpr int kOuterSumSize = 1024;
 __device__ __forceinline__ void outer_sum(const OuterSumArgs &p, int64_t id) {
   const int32_t g = static_cast<int32_t>(id / p.blocks), lane = threadIdx.x & 63;
-  int32_t first = 0, n;
+  int64_t first = 0, lo = 0, n;
   if (p.rows.offsets) {
+    int32_t before = 0;
     for (int i = lane; i < g; i += 64) {
       const int32_t rows = p.rows.offsets[i + 1] - p.rows.offsets[i];
-      first += rows > 0 ? (rows - 1) / p.chunk + 1 : 0;
+      before += rows > 0 ? (rows - 1) / p.chunk + 1 : 0;
     }
 #pragma unroll
-    for (int d = 1; d < 64; d *= 2) first += __shfl_xor(first, d);
+    for (int d = 1; d < 64; d *= 2) before += __shfl_xor(before, d);
+    first = before;
+    lo = p.rows.offsets[g];
     const int32_t rows = p.rows.offsets[g + 1] - p.rows.offsets[g];
     n = rows > 0 ? (rows - 1) / p.chunk + 1 : 0;
   } else {
-    n = static_cast<int32_t>((p.rows.M + p.chunk - 1) / p.chunk);
+    n = (p.rows.M + p.chunk - 1) / p.chunk;
   }
-  if (n == 1) return;
+  // chunk c starts at row lo + c chunk and is tile first + c
+  const bool direct = n == 1;  // the result itself
+  int64_t c0 = lo < 0 ? (p.chunk - 1 - lo) / p.chunk : 0;
+  if (first < 0) n = 0;
+  n = min(n, min(p.tiles - first, (p.rows.M - lo + p.chunk - 1) / p.chunk));
+  if (direct && c0 == 0 && n == 1) return;
   const int64_t i = (id - static_cast<int64_t>(g) * p.blocks) * kOuterSumSize + threadIdx.x * 4;
   if (i >= p.size) return;
   floatx4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (!direct)
 #pragma unroll 4
-  for (int c = 0; c < n; ++c) v += *reinterpret_cast<const floatx4 *>(p.part + (static_cast<int64_t>(first) + c) * p.size + i);
+    for (int64_t c = c0; c < n; ++c) v += *reinterpret_cast<const floatx4 *>(p.part + (first + c) * p.size + i);
   *reinterpret_cast<floatx4 *>(p.out + g * p.size + i) = v;
 }
 __global__ __launch_bounds__(256) void outer_sum_kernel(OuterSumArgs a, OuterSumArgs b, int64_t blocks_a) {
@@ -1244,7 +1255,8 @@ hipError_t launch_adapter_backward(const AdapterArgs &a) {
     o.out = a.da;
     if ((e = run_outer(a, o)) != hipSuccess) return e;
   }
-  OuterSumArgs sa{rows, outer_chunk(a.M, a.K, a.rank, a.adapters), a.K * a.rank, 0, da_part, a.da}, sb{rows, outer_chunk(a.M, a.N, a.rank, a.adapters), a.N * a.rank, 0, db_part, a.db};
+  const int32_t ca = outer_chunk(a.M, a.K, a.rank, a.adapters), cb = outer_chunk(a.M, a.N, a.rank, a.adapters);
+  OuterSumArgs sa{rows, ca, tiles_for(a, ca), a.K * a.rank, 0, da_part, a.da}, sb{rows, cb, tiles_for(a, cb), a.N * a.rank, 0, db_part, a.db};
   sa.blocks = static_cast<int32_t>((sa.size + kOuterSumSize - 1) / kOuterSumSize);
   sb.blocks = static_cast<int32_t>((sb.size + kOuterSumSize - 1) / kOuterSumSize);
   const int64_t na = static_cast<int64_t>(a.adapters) * sa.blocks, nb = static_cast<int64_t>(a.adapters) * sb.blocks;

@@ -262,7 +262,8 @@ int nvfp4_moe_balance_backward(const void *logits, int dtype, int64_t tokens, in
                                int64_t ld_in, void *dlogits, int64_t ldd, void *hip_stream) {
   const int st = check_balance(logits, dtype, tokens, experts, ld, ids, top_k, sequences, flags, coef);
   if (st != NVFP4_OK) return st;
-  if (ldd < experts || product(tokens, ldd) < 0 || (dlogits_in && (ld_in < experts || product(tokens, ld_in) < 0)))
+  if (ldd < experts || product(tokens, ldd) < 0 || (dlogits_in && (ld_in < experts || product(tokens, ld_in) < 0)) ||
+      (dlogits_in && dlogits_in == dlogits && ld_in != ldd && tokens > 1))
     return NVFP4_ERR_SHAPE;
   if (tokens == 0) return NVFP4_OK;
   if (!counts || !live || !dlogits) return NVFP4_ERR_NULL;

@@ -1123,8 +1123,9 @@ int32_t outer_chunk(int64_t M, int64_t N, int32_t rank, int32_t adapters) {
     if (n < 1) n = 1;
     chunk = (M + n - 1) / n;
   } while (chunk > kMaxChunk && rounds <= 64);
-  const int64_t least = 2 * rank > 64 ? 2 * rank : 64;
-  chunk = (chunk + kOuterStep - 1) / kOuterStep * kOuterStep;
+  auto steps = [](int64_t rows) { return (rows + kOuterStep - 1) / kOuterStep * kOuterStep; };
+  const int64_t least = 2 * rank > 64 ? steps(2 * rank) : 64;
+  chunk = steps(chunk);
   return static_cast<int32_t>(chunk < least ? least : chunk > kMaxChunk ? kMaxChunk : chunk);
 }
 template <int RF>

@@ -215,6 +215,9 @@ __device__ __forceinline__ float exp_of(float x) {
 // sum: p, and what divides them, `inv` (0 for a token without an open expert, or whose sum is zero).  l is left as the
 // logits in this form; `spare` is 1 - sum of the probabilities (0 for a softmax); slope (sigmoid): 1 - s.  Returns half of
 // the sum.  A closed expert's score comes out as zero by itself.
+// A sigmoid's reciprocal is the hardware's, one unit off, and a Newton step: 0.1 us of the two kernels' 20 at 16384 x 256, where
+// the general division costs 1.7 for the same errors.  (Without it the gradient is off by 1.3e-7 of its norm and not 0.9e-7,
+// one token of 401 experts.)
 template <int EPL, bool SIGMOID, bool SLOPE>
 __device__ __forceinline__ float row_scores(float (&l)[EPL], float (&p)[EPL], float (&slope)[EPL], float &inv, float &spare) {
   float top = kNegInf, sum = 0.0f;
@@ -227,7 +230,8 @@ __device__ __forceinline__ float row_scores(float (&l)[EPL], float (&p)[EPL], fl
 #pragma unroll
   for (int j = 0; j < EPL; ++j) {
     if constexpr (SIGMOID) {
-      const float e = exp_of(-fabsf(l[j])), r = __builtin_amdgcn_rcpf(1.0f + e), er = e * r;
+      const float e = exp_of(-fabsf(l[j])), d = 1.0f + e, near = __builtin_amdgcn_rcpf(d);
+      const float r = fmaf(fmaf(-d, near, 1.0f), near, near), er = e * r;
       p[j] = l[j] > 0.0f ? r : er;
       if (SLOPE) slope[j] = l[j] > 0.0f ? er : r;
     } else {

@@ -403,16 +403,16 @@ enum {
   NVFP4_ADAPTER_BY_TOKEN = 1u << 1 /* x and c are in the tokens' own order: row r of the plan is row rows[r] of both  */
 };
 
-/* Bytes of device workspace of nvfp4_adapter / nvfp4_adapter_backward (0: it may be NULL).  Needs no initialisation; calls that may overlap
- * must use distinct workspaces. */
+/* Bytes of device workspace of nvfp4_adapter / nvfp4_adapter_backward (0: it may be NULL).  Needs no initialisation;
+ * calls that may overlap must use distinct workspaces. */
 size_t nvfp4_adapter_workspace_size(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters);
 size_t nvfp4_adapter_backward_workspace_size(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters);
 
 /* Low-rank adapters of many requests, or of many experts, beside a shared product whose result is base:
  *   h[r] = A_g x[r],   c[r] = base[r] + scales[g] * B_g h[r]
  * for the rows r of each adapter g.  Sums run in fp32; h enters the second product with at least 16 bits of precision for
- * a bf16 c and 24 for an fp32 one, an infinite h as itself; c is rounded once.  (A product of h, or of
- * the gradients' g, with an infinite element of the other operand may be NaN instead of infinite.)
+ * a bf16 c and 24 for an fp32 one, an infinite h as itself; c is rounded once.  (A product of h, or of the gradients' g,
+ * with an infinite element of the other operand may be NaN instead of infinite.)
  * x [x_rows x K] of x_dtype NVFP4_BF16 (else NVFP4_ERR_UNSUPPORTED), leading dimension ldx.  a: device bf16
  * [adapters][rank][K], b: device bf16 [adapters][N][rank], scales: device float[adapters].
  * offsets NULL: one adapter for all M == x_rows rows (adapters 1, flags 0; rows and pos are ignored).  Else a device plan,
@@ -427,8 +427,9 @@ size_t nvfp4_adapter_backward_workspace_size(int64_t M, int64_t N, int64_t K, in
  * h: nullable device float [M][rank], the rows' h in the plan's order, for the backward call (rows behind
  * offsets[adapters] are not written).
  * rank a multiple of 8, 8 .. 128; adapters 1 .. 512; K a positive multiple of 8, N >= 1, both at most 2^24 (else
- * NVFP4_ERR_SHAPE); a launch of 2^31 threads or more is refused (NVFP4_ERR_SHAPE: about 2^34 elements of c).  x, a, b and h 16-byte aligned, ldx a multiple of 8; base and c
- * aligned to their elements.  workspace: device, nvfp4_adapter_workspace_size() bytes, 16-byte aligned. */
+ * NVFP4_ERR_SHAPE); a launch of 2^23 workgroups or more is refused (NVFP4_ERR_SHAPE: about 2^34 elements of c).  x, a, b
+ * and h 16-byte aligned, ldx a multiple of 8; base and c aligned to their elements.  workspace: device,
+ * nvfp4_adapter_workspace_size() bytes, 16-byte aligned. */
 int nvfp4_adapter(const void *x, int x_dtype, int64_t x_rows, int64_t ldx, const void *a, const void *b,
                   const float *scales, int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters,
                   const int32_t *offsets, const int32_t *rows, const int32_t *pos, int32_t row_div, uint32_t flags,
@@ -441,7 +442,8 @@ int nvfp4_adapter(const void *x, int x_dtype, int64_t x_rows, int64_t ldx, const
  *   db_g = scales[g] * sum_r dc[r] h[r]^T
  * dx [M x K] and dx_base (NULL: zeros; e.g. the shared product's own gradient) as c and base in the forward call, dtype
  * dx_dtype.  da: device float [adapters][rank][K], db: device float [adapters][N][rank] (zeros for an adapter without
- * rows).  base's gradient is dc itself.  Sums run in fp32 in one fixed order; g and h enter the second products with 24 bits.
+ * rows).  base's gradient is dc itself.  Sums run in fp32 in one fixed order; g and h enter the second products with 24
+ * bits (of dx in bf16 with 16).
  * flags 0 or NVFP4_ADAPTER_BY_TOKEN (with NVFP4_ADAPTER_GATHER a row of x has several rows of c: gather the rows
  * first, and sum their dx; NVFP4_ERR_UNSUPPORTED).  As nvfp4_adapter otherwise; N a multiple of 8 too, dc, da and db
  * 16-byte aligned, lddc a multiple of 8.  dx may be dx_base, and otherwise overlaps no input.  workspace: device,
@@ -468,7 +470,9 @@ size_t nvfp4_moe_balance_workspace_size(int64_t tokens, int64_t experts, int64_t
  *   loss         = coef / sequences * sum_s sum_e (experts * counts[s][e] / (top_k * N)) * probs[s][e]
  * logits [tokens x experts], ids [tokens][top_k] (a routing's) as for nvfp4_moe_route.  loss: device float[1]; counts:
  * device int32 [sequences][experts]; probs: device float [sequences][experts]; live: device int32 [sequences].  Sums run
- * in fp32 in one fixed order.  tokens a multiple of sequences, sequences 1 .. 65535 (else NVFP4_ERR_SHAPE), coef finite
+ * in fp32 in one fixed order; a probability is within (|l - max l| + experts / 16 + 24) * 2^-24 of itself (a sigmoid's
+ * without the first term).
+ * tokens a multiple of sequences, sequences 1 .. 65535 (else NVFP4_ERR_SHAPE), coef finite
  * (else NVFP4_ERR_UNSUPPORTED); flags: NVFP4_ROUTE_SIGMOID, other routing flags are ignored. */
 int nvfp4_moe_balance(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t ld, const int32_t *ids,
                       int32_t top_k, int64_t sequences, uint32_t flags, float coef, float *loss, int32_t *counts,
@@ -476,11 +480,11 @@ int nvfp4_moe_balance(const void *logits, int dtype, int64_t tokens, int64_t exp
 
 /* Gradient of nvfp4_moe_balance's loss with respect to the logits, times *dloss (device float; NULL: 1), added to
  * dlogits_in (nullable, the logits' dtype, leading dimension ld_in; e.g. nvfp4_moe_route_backward's result) with one
- * rounding: dlogits [tokens x experts] in the logits' dtype, leading dimension ldd; it may be dlogits_in itself.  Counts
- * have no gradient.  counts and live are the forward call's, or their sums over the ranks of a data-parallel job (then
+ * rounding: dlogits [tokens x experts] in the logits' dtype, leading dimension ldd; it may be dlogits_in itself (ld_in ==
+ * ldd then, else NVFP4_ERR_SHAPE).  Counts have no gradient.  counts and live are the forward call's, or their sums over the ranks of a data-parallel job (then
  * each rank has the gradient of the loss of all ranks' tokens with respect to its own logits).  Tokens without an id,
- * and closed experts, get dlogits_in (or 0) unchanged, whatever *dloss is.  An expert with nearly all of the score keeps the precision of its
- * (small) gradient. */
+ * and closed experts, get dlogits_in (or 0) unchanged, whatever *dloss is.  An expert with nearly all of the score keeps
+ * the precision of its (small) gradient. */
 int nvfp4_moe_balance_backward(const void *logits, int dtype, int64_t tokens, int64_t experts, int64_t ld,
                                const int32_t *ids, int32_t top_k, int64_t sequences, uint32_t flags, float coef,
                                const int32_t *counts, const int32_t *live, const float *dloss, const void *dlogits_in,
@@ -494,8 +498,8 @@ enum {
 size_t nvfp4_grad_workspace_size(int64_t tensors, int64_t elements);
 
 /* *norm (device float) = sqrt of the sum of squares over all elements of all tensors, or with NVFP4_GRAD_MAX their
- * largest magnitude; NaN if any element is NaN, else infinite if any is.  (Infinities and NaN are accepted here and in
- * nvfp4_grad_clip.)  Squares and sums are 64-bit numbers and added in one fixed order.  grads, counts, dtypes: HOST arrays of
+ * largest magnitude; NaN if any element is NaN, else infinite if any is or the norm passes the largest fp32 number.
+ * (Infinities and NaN are accepted here and in nvfp4_grad_clip.)  Squares and sums are 64-bit numbers and added in one fixed order.  grads, counts, dtypes: HOST arrays of
  * `tensors` entries, read before the call returns: device address (aligned to its element; contiguous elements),
  * number of elements (0 .. 2^40) and NVFP4_F32 or NVFP4_BF16 of each tensor.  workspace: device,
  * nvfp4_grad_workspace_size() bytes, 16-byte aligned. */

@@ -815,15 +815,16 @@ def nvfp4_adapter(x: torch.Tensor, w: Adapters, base: Optional[torch.Tensor] = N
     out, ldc, ldb = _beside(where, "base", base, out, (M, w.n), out_dtype, x)
     h = torch.empty((M, w.rank), dtype=torch.float32, device=x.device) if with_h else None
     workspace = _scratch(where, workspace, lib().nvfp4_adapter_workspace_size(M, w.n, w.k, w.rank, w.count), x)
-    _enqueue(where, x, x.data_ptr(), _dtype_code(x.dtype), x.shape[0], max(ldx, w.k), w.a.data_ptr(), w.b.data_ptr(), w.scales.data_ptr(),
-             M, w.n, w.k, w.rank, w.count, offsets, rows, pos, div, flags, _addr(base), ldb, out.data_ptr(), _dtype_code(out.dtype),
-             ldc, _addr(h), _addr(workspace))
+    _enqueue(where, x, x.data_ptr(), _dtype_code(x.dtype), x.shape[0], max(ldx, w.k), w.a.data_ptr(), w.b.data_ptr(),
+             w.scales.data_ptr(), M, w.n, w.k, w.rank, w.count, offsets, rows, pos, div, flags, _addr(base), ldb,
+             out.data_ptr(), _dtype_code(out.dtype), ldc, _addr(h), _addr(workspace))
     return (out, h) if with_h else out
 
 
-def nvfp4_adapter_backward(dout: torch.Tensor, x: torch.Tensor, w: Adapters, h: torch.Tensor, dx_base: Optional[torch.Tensor] = None,
-                           plan: Optional[MoEPlan] = None, by_token: bool = False, dx_dtype: torch.dtype = torch.bfloat16,
-                           dx: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> AdapterGrads:
+def nvfp4_adapter_backward(dout: torch.Tensor, x: torch.Tensor, w: Adapters, h: torch.Tensor,
+                           dx_base: Optional[torch.Tensor] = None, plan: Optional[MoEPlan] = None, by_token: bool = False,
+                           dx_dtype: torch.dtype = torch.bfloat16, dx: Optional[torch.Tensor] = None,
+                           workspace: Optional[torch.Tensor] = None) -> AdapterGrads:
     """Gradients of nvfp4_adapter from that of its result (bfloat16), its inputs and its h: dx (added to dx_base, e.g.
     the shared product's own; it may be dx_base) and float32 gradients of the factors.  With gathered rows gather x first."""
     where = "nvfp4_adapter_backward"
@@ -837,9 +838,10 @@ def nvfp4_adapter_backward(dout: torch.Tensor, x: torch.Tensor, w: Adapters, h: 
     da = torch.empty((w.count * w.rank, w.k), dtype=torch.float32, device=x.device)
     db = torch.empty((w.count * w.n, w.rank), dtype=torch.float32, device=x.device)
     workspace = _scratch(where, workspace, lib().nvfp4_adapter_backward_workspace_size(M, w.n, w.k, w.rank, w.count), x)
-    _enqueue(where, x, dout.data_ptr(), _dtype_code(dout.dtype), _matrix(where, "dout", dout), x.data_ptr(), _dtype_code(x.dtype), ldx,
-             w.a.data_ptr(), w.b.data_ptr(), w.scales.data_ptr(), M, w.n, w.k, w.rank, w.count, offsets, rows, pos, flags, h.data_ptr(),
-             _addr(dx_base), ldb, dx.data_ptr(), _dtype_code(dx.dtype), lddx, da.data_ptr(), db.data_ptr(), _addr(workspace))
+    _enqueue(where, x, dout.data_ptr(), _dtype_code(dout.dtype), _matrix(where, "dout", dout), x.data_ptr(),
+             _dtype_code(x.dtype), ldx, w.a.data_ptr(), w.b.data_ptr(), w.scales.data_ptr(), M, w.n, w.k, w.rank, w.count,
+             offsets, rows, pos, flags, h.data_ptr(), _addr(dx_base), ldb, dx.data_ptr(), _dtype_code(dx.dtype), lddx,
+             da.data_ptr(), db.data_ptr(), _addr(workspace))
     return AdapterGrads(dx, da, db)
 
 
@@ -908,7 +910,8 @@ def _dense(t: torch.Tensor) -> bool:
     return True
 
 
-_DATA_PTR, _NUMEL, _DEVICE, _CONTIGUOUS = torch.Tensor.data_ptr, torch.Tensor.numel, torch.Tensor.get_device, torch.Tensor.is_contiguous
+_DATA_PTR, _NUMEL = torch.Tensor.data_ptr, torch.Tensor.numel
+_DEVICE, _CONTIGUOUS = torch.Tensor.get_device, torch.Tensor.is_contiguous
 
 
 def _host(code: str, values):
@@ -966,7 +969,8 @@ def nvfp4_grad_clip(grads: Sequence[torch.Tensor], max_norm: float, flags: int =
         # (contiguous tensors are a row of elements, whatever their shapes)
         if len(out) != len(numbers) or list(map(_NUMEL, out)) != numbers or [o.dtype for o in out] != types or \
                 set(map(_DEVICE, out)) != {grads[0].get_device()} or \
-                not (whole and all(map(_CONTIGUOUS, out)) or all(o.shape == t.shape and o.stride() == t.stride() for o, t in zip(out, grads))):
+                not (whole and all(map(_CONTIGUOUS, out)) or
+                     all(o.shape == t.shape and o.stride() == t.stride() for o, t in zip(out, grads))):
             raise ValueError(f"{where}: out must match the list, tensor by tensor")
         outs = _host("Q", map(_DATA_PTR, out))
     _want(where, "norm", norm, torch.float32, (1,), grads[0])

@@ -14,8 +14,9 @@
 //
 // What bounds it.  Ranks are small, so the rows of x, base, c and dc are nearly all of the bytes, and the products (two to
 // six R operations a byte) run under their loads up to a rank of 64.  8192 x 4096 x 14336 of rank 16, bf16: h 17.6 to
-// 21 us (67 MB), c 84 to 87 us (470 MB, 5.4 to 5.6 TB/s; a 1 GiB copy runs at 5.1); gradients 153 us (dc read once 82,
-// dx 30, x 20, the rest small).  Whole calls against the bytes at the copy's rate: forward 118 us (106), step 248 (191).
+// 21 us (67 MB), c 84 to 87 us (470 MB, 5.4 to 5.6 TB/s; a 1 GiB copy runs at 5.1 to 5.2, an elementwise pass over as much at
+// 6.2); gradients 153 us (dc read once 81, dx 30, x 20, the rest small).  Whole calls against the bytes at 6.2 TB/s: forward
+// 118 us (87), step 248 (157).
 #include "gemm_common.hpp"
 #include "nvfp4_internal.h"
 #include "vec_io.hpp"
@@ -102,8 +103,8 @@ __device__ __forceinline__ floatx4 mfma(const bf16x8 &a, const bf16x8 &b, const 
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// Eight values as `parts` bf16 pieces each of which takes what the ones before leave.  An infinity is its first piece alone (what it
-// leaves would be NaN), and the first piece of a finite value that would round to one is the largest bf16 number.
+// Eight values as PARTS bf16 pieces each of which takes what the ones before leave.  An infinity is its first piece alone
+// (what it leaves would be NaN), and the first piece of a finite value that would round to one is the largest bf16 number.
 constexpr float kBf16Max = 0x1.FEp127f;
 template <int PARTS>
 __device__ __forceinline__ void split8(float (&v)[8], uint4 (&out)[PARTS]) {
@@ -303,7 +304,8 @@ __global__ __launch_bounds__(256) void shrink_many_kernel(ShrinkArgs p) {
 
 // ---- sums of the splits -----------------------------------------------------------------------------------------
 // Eight columns of row r.
-__device__ __forceinline__ void sum_splits(const float *part, int64_t M, int32_t R, int32_t splits, int64_t r, int32_t q, float (&v)[8]) {
+__device__ __forceinline__ void sum_splits(const float *part, int64_t M, int32_t R, int32_t splits, int64_t r, int32_t q,
+                                           float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = 0.0f;
 #pragma unroll 4
@@ -412,7 +414,8 @@ __device__ void copy_rows(const ExpandArgs &p, int32_t tile, int64_t n0) {
         for (int i = 0; i < 8; ++i) {
           const int32_t r = S::kRows * (i0 + i) + first;
           v[i] = make_uint4(0, 0, 0, 0);
-          if (p.base && (rows >> r & 1)) v[i] = load_piece<ONCE, VEC>(p.base + (static_cast<int64_t>(tile) * 64 + r) * p.ldb + n * ES);
+          const int64_t row = static_cast<int64_t>(tile) * 64 + r;
+          if (p.base && (rows >> r & 1)) v[i] = load_piece<ONCE, VEC>(p.base + row * p.ldb + n * ES);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -507,7 +510,8 @@ __global__ __launch_bounds__(256, OWN || RCP > 8 ? 2 : VEC || TF == 1 ? 4 : 3) v
         v[i] = *reinterpret_cast<const uint4 *>(y >= 0 && k < p.K ? x + k * 2 : zeros);
 #pragma unroll
         for (int u = 0; u < RF; ++u)
-          w[u][i] = *reinterpret_cast<const uint4 *>(16 * u + static_cast<int>(l16) < p.R && k < p.K ? a + ((16 * u + l16) * p.K + k) * 2 : zeros);
+          w[u][i] = *reinterpret_cast<const uint4 *>(
+              16 * u + static_cast<int>(l16) < p.R && k < p.K ? a + ((16 * u + l16) * p.K + k) * 2 : zeros);
       }
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
@@ -673,7 +677,8 @@ __global__ __launch_bounds__(kOuterThreads, RF <= 4 ? 4 : 2) void outer_kernel(O
     const uint8_t *from = p.f + (static_cast<int64_t>(t.group) * p.N + n_wg) * fp;
     const int32_t real = static_cast<int32_t>(min(static_cast<int64_t>(256), p.N - n_wg)) * fp / 16;
     for (int32_t i = threadIdx.x; i < pieces; i += kOuterThreads)
-      *reinterpret_cast<uint4 *>(smem + i * 16) = i < real ? *reinterpret_cast<const uint4 *>(from + i * 16) : make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4 *>(smem + i * 16) =
+          i < real ? *reinterpret_cast<const uint4 *>(from + i * 16) : make_uint4(0, 0, 0, 0);
     __syncthreads();
 #pragma unroll
     for (int v = 0; v < GF; ++v)
@@ -723,7 +728,8 @@ __global__ __launch_bounds__(kOuterThreads, RF <= 4 ? 4 : 2) void outer_kernel(O
     const int64_t r0 = t.m0 + static_cast<int64_t>(kt) * kOuterStep;
     auto piece = [&](int i) {
       const int64_t r = r0 + prow[i];
-      lds_load16(prow[i] < kOuterStep && r < t.m_end ? p.pieces + r * pitch + pchunk[i] * 16 : zeros, st + kY + (8 * i + wave) * 1024);
+      lds_load16(prow[i] < kOuterStep && r < t.m_end ? p.pieces + r * pitch + pchunk[i] * 16 : zeros,
+                 st + kY + (8 * i + wave) * 1024);
     };
 #pragma unroll
     for (int i = 0; i < NP; ++i) piece(i);
@@ -781,7 +787,8 @@ __global__ __launch_bounds__(kOuterThreads, RF <= 4 ? 4 : 2) void outer_kernel(O
 #pragma unroll
       for (int v = 0; v < GF; ++v) {
         const int q = 16 * ((4 * v + (wave >> 1)) % RF) + 4 * j;
-        if (r < t.m_end && q < p.R) *reinterpret_cast<floatx4 *>(p.g_part + (static_cast<int64_t>(tn) * p.rows.M + r) * p.R + q) = g[v];
+        if (r < t.m_end && q < p.R)
+          *reinterpret_cast<floatx4 *>(p.g_part + (static_cast<int64_t>(tn) * p.rows.M + r) * p.R + q) = g[v];
       }
     }
   }
@@ -955,19 +962,25 @@ int64_t tiles_for(const AdapterArgs &a, int64_t size) {
 // Rows of a workgroup that adds to many rows of c: what a lane holds of base's rows is then the same for both types.
 template <bool BF16>
 constexpr int kExpandRows = BF16 ? 64 : 32;
-// Workgroups of the launch that adds to c, at least, where there is work for them (8192 x 14336 of rank 16: 1806 take 75 us, 903 87,
-// 7224 81; of rank 64 92, 108 and 99).
+// Workgroups of the launch that adds to c, at least, where there is work for them.  Whole calls of 8192 x 4096 x 14336, eight
+// adapters, replayed from a graph: rank 16 at 903 workgroups 131 us, 1806 113, 7224 107; rank 64 156, 139 and 135.
 constexpr int64_t kExpandGroups = 1536, kFewGroups = 1024;
 
 // A few rows of low rank: one launch, in which each workgroup forms its rows' h by itself, as long as every workgroup has a
-// compute unit and A is read in about the time of a launch.  (Figures: expand_kernel.)
+// compute unit and A is small.  From Python, where a call's own time counts, a token of 4096 x 14336 and rank 16 takes 13.4 us
+// so and 17.2 in two launches.  Replayed from a graph one launch gains up to a K of 1024 or so and loses from there on: 64 rows
+// of 1024 x 1024 6.5 us against 7.9, 256 of 512 x 512 6.3 against 7.8, 16 of 4096 x 4096 8.0 either way, the token above 9.2
+// against 7.8, one of 4096 x 4096 and rank 32 12.5 against 8.6, one of 14336 x 4096 and rank 8 16.6 against 8.5.
 constexpr int32_t kOwnRank = 32;
 bool own_h(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters) {
   const int64_t tiles = adapters == 1 ? (M + 15) / 16 : (M < adapters ? M : adapters) + M / 16;
   return rank <= kOwnRank && rank * K <= (1 << 17) && tiles * ((N + 255) / 256) <= 256;
 }
 
-// Few rows an adapter: 16 rows a tile.
+// Few rows an adapter: 16 rows a tile.  (K 4096, replayed from a graph, in tiles of 16 and of 64 rows: 512 rows of 32 adapters of
+// rank 16 18 and 24 us, 2048 of 128 39 and 55, 8000 of 512 182 and 182, of rank 64 170 and 184.  The rule counts the adapters
+// that there are; where a few of them have all rows, 1024 of 64 take 21 and 26 us, 8000 of 512 138 and 136, and of rank 64
+// 105 and 103; 2048 rows of 2 in 128 of rank 64 32 and 26.)
 bool few_rows(int64_t M, int64_t adapters) { return M <= 256 || M <= 16 * adapters; }
 
 // Splits of K for many rows: workgroups for every compute unit, each with at least four steps.  Gathered rows come up
@@ -1227,7 +1240,8 @@ hipError_t launch_adapter_backward(const AdapterArgs &a) {
   if (a.M > 0) {
     // A^T [K][R], and the pieces of s h
     auto tiles = [](int64_t n) { return static_cast<int32_t>((n + 63) / 64); };
-    const TransposeArgs ta{static_cast<const uint16_t *>(a.a), reinterpret_cast<uint16_t *>(w + l.at), a.rank, a.K, tiles(a.rank), tiles(a.K)};
+    const TransposeArgs ta{static_cast<const uint16_t *>(a.a), reinterpret_cast<uint16_t *>(w + l.at), a.rank, a.K,
+                           tiles(a.rank), tiles(a.K)};
     const PiecesArgs h{rows, a.h, a.rank, a.scales, w + l.h_pieces};
     const int64_t na = static_cast<int64_t>(a.adapters) * ta.tiles_r * ta.tiles_c;
     adapter_prep_kernel<<<dim3(static_cast<uint32_t>(na + tiles_for(a, kPiecesRows))), dim3(256), 0, a.stream>>>(ta, na, h);
@@ -1245,8 +1259,8 @@ hipError_t launch_adapter_backward(const AdapterArgs &a) {
     o.g_part = part;
     if ((e = run_outer(a, o)) != hipSuccess) return e;
     const int32_t tiles_n = static_cast<int32_t>((a.N + 255) / 256);
-    if ((e = run_expand(a, w + l.at, a.K, part, tiles_n, nullptr, w + l.g_pieces, a.base, a.ldb, a.c, a.ldc, a.c_dtype)) != hipSuccess)
-      return e;
+    e = run_expand(a, w + l.at, a.K, part, tiles_n, nullptr, w + l.g_pieces, a.base, a.ldb, a.c, a.ldc, a.c_dtype);
+    if (e != hipSuccess) return e;
     o = {};
     o.y = static_cast<const uint8_t *>(a.x);
     o.ldy = a.ldx;
@@ -1257,7 +1271,8 @@ hipError_t launch_adapter_backward(const AdapterArgs &a) {
     if ((e = run_outer(a, o)) != hipSuccess) return e;
   }
   const int32_t ca = outer_chunk(a.M, a.K, a.rank, a.adapters), cb = outer_chunk(a.M, a.N, a.rank, a.adapters);
-  OuterSumArgs sa{rows, ca, tiles_for(a, ca), a.K * a.rank, 0, da_part, a.da}, sb{rows, cb, tiles_for(a, cb), a.N * a.rank, 0, db_part, a.db};
+  OuterSumArgs sa{rows, ca, tiles_for(a, ca), a.K * a.rank, 0, da_part, a.da};
+  OuterSumArgs sb{rows, cb, tiles_for(a, cb), a.N * a.rank, 0, db_part, a.db};
   sa.blocks = static_cast<int32_t>((sa.size + kOuterSumSize - 1) / kOuterSumSize);
   sb.blocks = static_cast<int32_t>((sb.size + kOuterSumSize - 1) / kOuterSumSize);
   const int64_t na = static_cast<int64_t>(a.adapters) * sa.blocks, nb = static_cast<int64_t>(a.adapters) * sb.blocks;

@@ -7,7 +7,8 @@
 // is exact there and neither overflows nor vanishes, and the conversion and multiply-add still cost less than the
 // loads.  A workgroup leaves one partial result, and one workgroup adds these in order: the same bits on every call.
 // Eight bf16 tensors, 352 M elements: norm 107 to 110 us (704 MB, 6.5 TB/s: what of the last call's output the cache holds
-// costs no reads), clipping into other tensors 256 to 264 us (1.41 GB, 5.4 TB/s; a 1 GiB copy runs at 5.1).  160 fp32 tensors,
+// costs no reads), clipping into other tensors 256 to 264 us (1.41 GB, 5.4 TB/s; a 1 GiB copy runs at 5.1 to 5.2, an
+// elementwise pass at 6.2).  160 fp32 tensors,
 // 19 M elements: 15 + 2 + 25 us on the GPU; the walk over the list in Python and C takes 95.
 #include <hip/hip_runtime.h>
 

@@ -13,12 +13,13 @@
 // Counts enter as differences (exact integers) from a reference count.  Where one expert has more than half of the score it
 // is that expert's: with nearly all of the score its small gradient comes from the others' terms, and nothing cancels.  Else
 // it is the integer next to sum_j p_j n_j: what the differences' own sum leaves is then of the size of the counts' spread.
-// (Taken from the likeliest expert's count everywhere, one token of 300 experts lost 7 bits: its 1 less 299/300 of it.)
+// (From the likeliest expert's count everywhere, one token of 401 experts of equal scores had gradients off by 1.1e-5 of
+// themselves, 1 less 400/401; now 3e-8.)
 //
-// What bounds them: 16384 x 256 in four sequences, sigmoid, fp32: forward 7.2 to 7.6 us (17 MB: 3.3 us at the rate of a large
-// copy) + the sums 4.5 to 5.4, gradient added to another 12.5 to 12.9 us (50 MB: 9.9).  The forward kernel issues about 350
-// vector instructions a lane, two of them a quarter as fast, of a launch in which every wave takes one group of tokens;
-// the sums are a launch and two dependent loads.  64 tokens of 64 experts: one launch of 2.9 us.
+// What bounds them: 16384 x 256 in four sequences, sigmoid, fp32: forward 7.2 to 8.9 us (17 MB: 2.7 us at the 6.2 TB/s of a large
+// elementwise pass) + the sums 4.6 to 5.8, gradient added to another 12.5 to 13.2 us (50 MB: 8.1).  The forward kernel issues
+// about 350 vector instructions a lane, two of them a quarter as fast, of a launch in which every wave takes one group of
+// tokens; the sums are a launch and two dependent loads.  64 tokens of 64 experts: one launch of 2.7 to 3.0 us.
 #include <hip/hip_runtime.h>
 
 #include <cstdint>
@@ -606,7 +607,8 @@ hipError_t launch_moe_balance(const MoeBalanceArgs &a) {
     default: e = run_forward<32>(p, one, bf16, a.sigmoid, a.stream); break;
   }
   if (e != hipSuccess || one) return e;
-  balance_sum_kernel<<<dim3(static_cast<uint32_t>(sum_groups(p.E)), static_cast<uint32_t>(p.sequences)), dim3(kSumThreads), 0, a.stream>>>(p);
+  const dim3 grid(static_cast<uint32_t>(sum_groups(p.E)), static_cast<uint32_t>(p.sequences));
+  balance_sum_kernel<<<grid, dim3(kSumThreads), 0, a.stream>>>(p);
   return hipGetLastError();
 }
 

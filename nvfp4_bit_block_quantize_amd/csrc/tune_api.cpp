@@ -112,8 +112,8 @@ int check_adapter_pointers(const nvfp4::AdapterArgs &a, int out_dtype, size_t wo
   if ((a.gather || a.by_token) && !a.rows) return NVFP4_ERR_NULL;
   if (a.by_token && !a.pos) return NVFP4_ERR_NULL;
   const int es = dtype_size(out_dtype);
-  if (!aligned(a.x, 16) || a.ldx % 8 != 0 || !aligned(a.a, 16) || !aligned(a.b, 16) || !aligned(a.scales, 4) || !aligned(a.offsets, 4) ||
-      !aligned(a.rows, 4) || !aligned(a.pos, 4) || !aligned(a.base, es) || !aligned(a.c, es) || !aligned(a.h, 16) ||
+  if (!aligned(a.x, 16) || a.ldx % 8 != 0 || !aligned(a.a, 16) || !aligned(a.b, 16) || !aligned(a.scales, 4) ||
+      !aligned(a.offsets, 4) || !aligned(a.rows, 4) || !aligned(a.pos, 4) || !aligned(a.base, es) || !aligned(a.c, es) || !aligned(a.h, 16) ||
       !aligned(a.workspace, 16))
     return NVFP4_ERR_ALIGN;
   return NVFP4_OK;
@@ -145,8 +145,8 @@ nvfp4::AdapterArgs adapter_args(const void *x, int64_t x_rows, int64_t ldx, cons
 
 // Whether a size is one that the workspace functions answer for.
 bool adapter_sizes(int64_t M, int64_t N, int64_t K, int32_t rank, int32_t adapters) {
-  return M >= 0 && M < kMaxSlots && N >= 1 && N <= kMaxWidth && K >= 8 && K <= kMaxWidth && rank >= 8 && rank <= kMaxRank && adapters >= 1 &&
-         adapters <= kMaxExperts;
+  return M >= 0 && M < kMaxSlots && N >= 1 && N <= kMaxWidth && K >= 8 && K <= kMaxWidth && rank >= 8 && rank <= kMaxRank &&
+         adapters >= 1 && adapters <= kMaxExperts;
 }
 
 }  // namespace
@@ -161,7 +161,8 @@ size_t nvfp4_adapter_backward_workspace_size(int64_t M, int64_t N, int64_t K, in
   if (!adapter_sizes(M, N, K, rank, adapters)) return 0;
   // (with a plan as without one: more than one tile of rows may end early)
   static const int32_t some = 0;
-  const nvfp4::AdapterArgs a = adapter_args(nullptr, M, K, nullptr, nullptr, nullptr, M, N, K, rank, adapters, &some, nullptr, nullptr, 1, 0);
+  const nvfp4::AdapterArgs a =
+      adapter_args(nullptr, M, K, nullptr, nullptr, nullptr, M, N, K, rank, adapters, &some, nullptr, nullptr, 1, 0);
   return (nvfp4::adapter_backward_workspace_bytes(a) + 15) / 16 * 16;
 }
 
@@ -173,7 +174,8 @@ int nvfp4_adapter(const void *x, int x_dtype, int64_t x_rows, int64_t ldx, const
   nvfp4::AdapterArgs p = adapter_args(x, x_rows, ldx, a, b, scales, M, N, K, rank, adapters, offsets, rows, pos, row_div, flags);
   int st = check_adapter(p, x_dtype, c_dtype, flags);
   if (st != NVFP4_OK) return st;
-  if (ldc < N || product(M, ldc) < 0 || (base && (ldb < N || product(M, ldb) < 0)) || !nvfp4::adapter_launches(p, false)) return NVFP4_ERR_SHAPE;
+  if (ldc < N || product(M, ldc) < 0 || (base && (ldb < N || product(M, ldb) < 0)) || !nvfp4::adapter_launches(p, false))
+    return NVFP4_ERR_SHAPE;
   if (base == c && base && ldb != ldc && M > 1) return NVFP4_ERR_SHAPE;
   if (M == 0) return NVFP4_OK;
   p.base = base;
